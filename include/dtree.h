@@ -111,6 +111,12 @@ enum { DT_BF16 = 0, DT_F32 = 1 };
 #define DT_DEV_BESTFIRST 0x4        /* DARTree: TopB(S) was not a topologically
                                        ordered tree; the best-first heap over S
                                        was used (see dt_build_tree) */
+#define DT_DEV_BAD_CACHE 0x8        /* cache calls: a length, count, row index, page
+                                       id or position outside its range; the
+                                       request's part of the call was not done
+                                       (append) or its output is undefined
+                                       (attention), nothing outside the caller's
+                                       arrays was touched */
 #define DT_DEV_VIOLATION_SHIFT 8    /* DARTree: number of supertree edges whose
                                        child outscores its parent, saturating
                                        at 2^23-1, in bits 8..30 */
@@ -465,6 +471,134 @@ dt_status dt_saba_budget(const dt_saba_params* q, const dt_tree* tree, int32_t b
  *     them. */
 #define DT_NOALLOC_TABLE_BYTES (4u << 20)
 dt_status dt_select_dartree_noalloc(const dt_build_params* p, dt_tree* tree, dt_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The target model's side of a round.  A tree's rows attend to the verified
+ * context and to their root-to-node path ([DARTree] "Tree verification and
+ * DDTree", [DDTree] section 4.2); the walk accepts a path; the path's keys and
+ * values join the context; the emitted tokens' log-probabilities go to the
+ * user.  The three calls below do these steps around dt_tree_mask and
+ * dt_verify and take their outputs as they are.
+ *
+ * The context is kept in pages of e4m3 numbers with one scale for each (page,
+ * key head), for keys and values apart: an element is code * scale.  dt_kv_append
+ * writes scales that are powers of two: e4m3 is a floating format, so a finer
+ * scale would buy no precision, and a block whose scale grows is rescaled
+ * exactly (outside e4m3's subnormals).  dt_tree_attention takes any positive
+ * finite scale.  A scale that is NaN stands for a block that holds a value that
+ * is not finite: every row that attends to it becomes NaN. */
+typedef struct {
+    int32_t n_pages;      /* physical pages */
+    int32_t page;         /* tokens per page: 16, 32, 64 or 128 */
+    int32_t Hkv;          /* key heads */
+    int32_t D;            /* head size: 64 or 128 */
+    int32_t max_pages;    /* columns of the page table */
+    uint8_t* k;           /* [n_pages][Hkv][page][D] e4m3 codes, rotated; 16-byte aligned */
+    uint8_t* v;           /* the same for values */
+    float* k_scale;       /* [n_pages][Hkv] */
+    float* v_scale;       /* [n_pages][Hkv] */
+    const int32_t* table; /* [batch][max_pages] physical page of each logical page */
+    const int32_t* len;   /* [batch] tokens held; token j of a request lies in slot
+                             j % page of its logical page j / page */
+} dt_kv_cache;
+
+/* Position rotation: pair (a, b) of a head's first `rot` elements becomes
+ * (a cos - b sin, b cos + a sin) with entry [position][i] of the tables; pairs
+ * are (x[i], x[i + rot/2]), or (x[2i], x[2i+1]) when interleaved. */
+typedef struct {
+    const float* cos;     /* [max_pos][rot / 2] fp32, 16-byte aligned */
+    const float* sin;     /* the same */
+    int32_t max_pos;
+    int32_t rot;          /* a multiple of 16, <= D */
+    int32_t interleaved;  /* 0 or 1 */
+} dt_rope;
+
+/* Per-token head vectors, ptr[b * stride_b + n * stride_n + h * stride_h + d]
+ * (strides in elements, d dense), so that slices of a fused projection need no
+ * copy.  ptr and the strides in bytes are multiples of 16. */
+typedef struct {
+    const void* ptr;
+    int64_t stride_b, stride_n, stride_h;
+} dt_rows;
+
+/* Appends rows to the cache: row j < n_b of request b is token
+ * rows[b][j] (j when rows is NULL) of k and v, keys rotated to position
+ * len[b] + j, stored in slot len[b] + j.
+ *   k, v: [batch][M][Hkv][D] in dtype (DT_BF16 or DT_F32).
+ *   rope: NULL: keys are stored as they are.
+ *   rows: NULL or [batch][N] int32 in [0, M); entries from n_b on are not read
+ *         (dt_verify's acc_nodes with N = L + 1 is such an array).
+ *   N:    columns of rows (rows NULL: N <= M).
+ *   count: n_b = count[b] + count_add, in [0, N]; NULL: n_b = N (count_add is
+ *         ignored).  dt_verify's acc_len with count_add = 1 is the path with
+ *         its root.
+ *   len_out: NULL or [batch], gets len[b] + n_b (len[b] for a refused request);
+ *         may not be the cache's len, which the call only reads: every layer
+ *         appends at the same len.
+ * The scale of a (page, head) block is 2^e with the smallest e >= -48 such that
+ * the new rows' largest magnitude is at most 448 * 2^e; a block that already
+ * holds tokens keeps its scale when that is larger, and its codes are rescaled
+ * (to nearest, ties to even) when it is smaller.  Codes are the rotated fp32
+ * values over the scale, to nearest, ties to even.  Each fp32 step of the
+ * rotation rounds once (no contraction).
+ * A request whose len, count, rows, pages or positions are out of range is left
+ * alone and gets DT_DEV_BAD_CACHE in status[b] (OR-ed).  Pages being written
+ * must not appear twice in the table. */
+dt_status dt_kv_append(const dt_kv_cache* c, const dt_rope* rope, int32_t batch, int32_t M, int32_t dtype,
+                       const dt_rows* k, const dt_rows* v, const int32_t* rows, int32_t N, const int32_t* count,
+                       int32_t count_add, int32_t* len_out, int32_t* status, dt_stream_t stream);
+
+/* Attention of a tree's rows over the cached context and the tree itself.
+ * Row n < n_nodes[b] of query head h (key head h / (Hq / Hkv)) has position
+ * len[b] + pos[b][n]; it sees every cached token j < len[b] and those new rows
+ * m < n_nodes[b] whose bit (m % 32) of mask[b][n][m / 32] is set:
+ *   s = scale * <R(q_n), key>, key = cached key or R(k_m);
+ *   out[b][n][h] = sum exp(s - max) value / sum exp(s - max).
+ * A row that sees nothing, and every row n >= n_nodes[b], gets zeros.
+ *   q: [batch][M][Hq][D], k, v: [batch][M][Hkv][D] bf16, not rotated; what
+ *      masked rows of k and v hold (NaN included) does not matter; a row that
+ *      sees a new row with a value that is not finite becomes NaN.
+ *   mask: NULL (row n sees the new rows m <= n) or
+ *      [batch][M][ceil(M / 32)] as dt_tree_mask writes it.
+ *   pos: NULL (n) or [batch][M], as dt_tree_mask writes it with pos_offset 0.
+ *   n_nodes: NULL (M) or [batch] in [0, M].
+ *   scale > 0, finite; Hq a multiple of Hkv, Hq / Hkv <= 128.
+ *   out: [batch][M][Hq][D] bf16, dense, 16-byte aligned.
+ *   workspace: dt_tree_attention_workspace bytes of device memory, 16-byte
+ *      aligned, zeroed before its first use; the calls leave the part that has
+ *      to be zero as they found it, for any later shapes.  Calls that may run
+ *      at the same time need workspaces of their own.
+ * Products are taken in fp16 with fp32 accumulation (e4m3 codes are exact in
+ * fp16; q, new k and v are scaled by powers of two into its range); softmax
+ * statistics are fp32.
+ * A request whose len, n_nodes, pages or positions are out of range gets
+ * DT_DEV_BAD_CACHE in status[b] (OR-ed) and undefined output rows. */
+size_t dt_tree_attention_workspace(const dt_kv_cache* c, int32_t batch, int32_t M, int32_t Hq);
+dt_status dt_tree_attention(const dt_kv_cache* c, const dt_rope* rope, int32_t batch, int32_t M, int32_t Hq,
+                            const dt_rows* q, const dt_rows* k, const dt_rows* v, const uint32_t* mask,
+                            const int32_t* pos, const int32_t* n_nodes, float scale, void* out, void* workspace,
+                            size_t workspace_bytes, int32_t* status, dt_stream_t stream);
+
+/* Log-probabilities of given tokens ([Unit11] temperature 1), with the rank of
+ * the token, the entropy of the row and its best alternatives.
+ *   logits: [batch][M][V] in dtype, row m of request b at b * stride_b +
+ *      m * stride elements (stride >= V, stride_b >= 0); finite or -inf, one finite value per row at least (else logprob, entropy and
+ *      top_logprob of that row are NaN or infinite, ids and ranks unspecified).
+ *   rows:   NULL (row j, N <= M) or [batch][N]: entry j is about logits row
+ *      rows[b][j]; a negative entry is about no row: logprob, entropy and
+ *      top_logprob 0, rank and top_id -1; an entry >= M: the same with NaN.
+ *   tokens: [batch][N]; negative: no token (logprob 0, rank -1); >= V: logprob
+ *      NaN, rank -1.
+ *   logprob = x[token] - lse; entropy = lse - sum p x (nats);
+ *   rank = how many tokens come before it (larger logit, or an equal one and a
+ *      smaller id);
+ *   top_id, top_logprob: [batch][N][top] the `top` first tokens in that order,
+ *      0 <= top <= 32, top <= V (NULL when top is 0).
+ * logprob, entropy [batch][N] fp32; rank [batch][N] int32; each may be NULL. */
+#define DT_MAX_TOP 32
+dt_status dt_token_logprobs(const void* logits, int32_t dtype, int32_t batch, int32_t M, int32_t V, int64_t stride_b,
+                            int64_t stride, const int32_t* rows, const int32_t* tokens, int32_t N, int32_t top, float* logprob,
+                            float* entropy, int32_t* rank, int32_t* top_id, float* top_logprob, dt_stream_t stream);
 
 /* Test hook of the timeout path (failure detection without a GPU fault).
  * Every mbarrier wait in the library is bounded; when a bound runs out the

@@ -1,0 +1,69 @@
+// dt_cache.cuh -- device helpers of the paged e4m3 cache and its rotation.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "dt_device.cuh"
+
+// Eight consecutive elements as fp32 (16-byte aligned).
+DT_DI void dt_load8(const uint16_t* p, float (&x)[8]) { dt_vec_vals<uint16_t>(*(const uint4*)p, x); }
+DT_DI void dt_load8(const float* p, float (&x)[8]) {
+    const float4 a = ((const float4*)p)[0], b = ((const float4*)p)[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
+// Elements 8c .. 8c+7 of a head vector, rotated to position `at` (which must
+// lie in the tables).  The partner chunk of the split-halves form is read
+// again by the thread that owns it: both reads hit the same cache lines.
+template <typename T>
+DT_DI void dt_rotated8(const T* row, int c, const dt_rope& r, int at, float (&x)[8]) {
+    dt_load8(row + 8 * c, x);
+    if (8 * c >= r.rot) return;
+    const int half = r.rot >> 1;
+    const float* cs = r.cos + (size_t)at * half;
+    const float* sn = r.sin + (size_t)at * half;
+    if (r.interleaved) {
+        const float4 co = *(const float4*)(cs + 4 * c), si = *(const float4*)(sn + 4 * c);
+        const float cv[4] = {co.x, co.y, co.z, co.w}, sv[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i], b = x[2 * i + 1];
+            x[2 * i] = __fsub_rn(__fmul_rn(a, cv[i]), __fmul_rn(b, sv[i]));
+            x[2 * i + 1] = __fadd_rn(__fmul_rn(b, cv[i]), __fmul_rn(a, sv[i]));
+        }
+    } else {
+        const bool second = 8 * c >= half;
+        const int i0 = second ? 8 * c - half : 8 * c;
+        float y[8], cv[8], sv[8];
+        dt_load8(second ? row + i0 : row + 8 * c + half, y);
+        dt_load8(cs + i0, cv);
+        dt_load8(sn + i0, sv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float t = __fmul_rn(y[i], sv[i]);
+            x[i] = second ? __fadd_rn(__fmul_rn(x[i], cv[i]), t) : __fsub_rn(__fmul_rn(x[i], cv[i]), t);
+        }
+    }
+}
+
+// Two e4m3 codes (the low 16 bits) as an exact fp16 pair.
+DT_DI uint32_t dt_e4m3x2_to_f16x2(uint32_t codes) {
+    uint32_t d;
+    asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(d) : "r"(codes));
+    return d;
+}
+DT_DI float2 dt_e4m3x2_to_f32x2(uint32_t codes) {
+    const uint32_t h = dt_e4m3x2_to_f16x2(codes);
+    return __half22float2(*(const __half2*)&h);
+}
+// Two fp32 values to e4m3 (to nearest, ties to even, saturating): lo in the low byte.
+DT_DI uint32_t dt_f32x2_to_e4m3x2(float lo, float hi) {
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// 2^e for -126 <= e <= 127.
+DT_DI float dt_pow2(int e) { return __int_as_float((e + 127) << 23); }

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "dtree.h"
+
 // Launch configuration shared by every kernel: programmatic stream
 // serialisation (the kernel may start while its predecessor finishes; it
 // calls griddepcontrol.wait before reading inputs) and an optional cluster.
@@ -166,3 +168,39 @@ cudaError_t dt_kn6_launch(int batch, int L, int V, int dtype, int Mmax, int S, i
                           const float* target_lse, const void* draft,
                           const float* uniforms, int32_t* acc_nodes, int32_t* acc_len, int32_t* next_tok,
                           float* visited_lse, int32_t* status, const DtKn6Proposal* prop, cudaStream_t st);
+
+// Appending to the paged cache (kn10_append.cu).
+cudaError_t dt_kn10_launch(const dt_kv_cache& c, const dt_rope& rope, int batch, int M, int dtype, const dt_rows& k,
+                           const dt_rows& v, const int32_t* rows, int N, const int32_t* count, int count_add,
+                           int32_t* len_out, int32_t* status, cudaStream_t st);
+
+// Tree attention over the paged cache (kn11_attend.cu).
+struct DtAttend {
+    dt_kv_cache c;
+    dt_rope rope;  // rot = 0: none
+    int batch, M, Hq;
+    dt_rows q, k, v;
+    const uint32_t* mask;
+    const int32_t* pos;
+    const int32_t* n_nodes;
+    float scale;
+    void* out;
+    int32_t* status;
+};
+cudaError_t dt_kn11_launch(const DtAttend& a, cudaStream_t st);
+
+// Log-probabilities of given tokens (kn13_logprobs.cu).
+struct DtLogprobs {
+    const void* logits;
+    int dtype, batch, M, V;
+    long long stride_b, stride;
+    const int32_t* rows;
+    const int32_t* tokens;
+    int N, top;
+    float* logprob;
+    float* entropy;
+    int32_t* rank;
+    int32_t* top_id;
+    float* top_logprob;
+};
+cudaError_t dt_kn13_launch(const DtLogprobs& a, cudaStream_t st);

@@ -1,0 +1,154 @@
+// kn10_append.cu -- rotation, e4m3 quantisation and storing of new keys and
+// values in the paged cache (dt_kv_append).
+//
+// One CTA per (page touched, key head, keys or values, request): the block
+// that shares a scale.  Its new rows stay in registers between the two things
+// that need them: the largest magnitude, which fixes the scale 2^e, and the
+// codes x / 2^e.  Rows read once, codes written once.
+#include "dt_cache.cuh"
+#include "dt_launch.h"
+
+namespace {
+
+constexpr int NT = 256;
+constexpr int E_MIN = -48;  // smallest exponent of a block scale
+
+// Exponent of the scale for a block whose largest magnitude has these bits
+// (finite): the smallest e >= E_MIN with amax <= 448 * 2^e, 448 = 1.75 * 2^8.
+DT_DI int block_exponent(uint32_t amax_bits) {
+    const int x = (int)(amax_bits >> 23) - 127;
+    const int e = ((amax_bits & 0x7FFFFFu) <= 0x600000u) ? x - 8 : x - 7;
+    return max(e, E_MIN);
+}
+
+// Smallest e with scale <= 2^e (scale positive, finite, normal).
+DT_DI int scale_exponent(float scale) {
+    const uint32_t b = __float_as_uint(scale);
+    return (int)(b >> 23) - 127 + ((b & 0x7FFFFFu) ? 1 : 0);
+}
+
+template <typename T, int CH>  // CH: chunks of 8 elements a thread may own
+__global__ void __launch_bounds__(NT) kn10_kernel(dt_kv_cache c, dt_rope rope, int M, dt_rows kr, dt_rows vr,
+                                                  const int32_t* __restrict__ rows, int N,
+                                                  const int32_t* __restrict__ count, int count_add,
+                                                  int32_t* __restrict__ len_out, int32_t* __restrict__ status) {
+    __shared__ uint32_t red[NT / 32];
+    dt_pdl_trigger();
+    dt_pdl_wait();
+    const int tid = threadIdx.x, b = blockIdx.z, h = blockIdx.y;
+    const bool keys = (blockIdx.x & 1) == 0;
+    const int at = blockIdx.x >> 1;  // page touched, counted from the first one
+    const int len = c.len[b], n = count ? count[b] + count_add : N;
+    const int* table = c.table + (size_t)b * c.max_pages;
+    const long long cap = (long long)c.max_pages * c.page;
+    // every CTA of a request comes to the same verdict on it
+    bool bad = len < 0 || n < 0 || n > N || (long long)len + n > cap || (rope.rot && n > 0 && (long long)len + n > rope.max_pos);
+    if (!bad && n > 0) {
+        if (rows)
+            for (int j = tid; j < n; j += NT) bad |= (unsigned)rows[(size_t)b * N + j] >= (unsigned)M;
+        const int last = (len + n - 1) / c.page;
+        for (int p = len / c.page + tid; p <= last; p += NT) bad |= (unsigned)table[p] >= (unsigned)c.n_pages;
+    }
+    bad = __syncthreads_or(bad);
+    if (blockIdx.x == 0 && h == 0 && tid == 0) {
+        if (len_out) len_out[b] = bad ? len : len + n;
+        if (bad) atomicOr(&status[b], DT_DEV_BAD_CACHE);
+    }
+    if (bad || n == 0) return;
+    const int p = len / c.page + at;
+    const int lo = max(len, p * c.page), hi = min(len + n, (p + 1) * c.page);  // slots of new rows
+    if (lo >= hi) return;
+
+    const dt_rows& src = keys ? kr : vr;
+    const int cpr = c.D >> 3;  // chunks per row
+    const int m = (hi - lo) * cpr;
+    float x[CH][8];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int q = tid + i * NT;
+        if (q < m) {
+            const int j = lo - len + q / cpr, ch = q % cpr;
+            const int row = rows ? rows[(size_t)b * N + j] : j;
+            const T* ptr = (const T*)src.ptr + b * src.stride_b + row * src.stride_n + h * src.stride_h;
+            if (keys)
+                dt_rotated8(ptr, ch, rope, len + j, x[i]);
+            else
+                dt_load8(ptr + 8 * ch, x[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(x[i][e]) & 0x7FFFFFFFu);
+        }
+    }
+    amax = dt_warp_max_u32(amax);
+    if ((tid & 31) == 0) red[tid >> 5] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) amax = max(amax, red[w]);
+
+    const size_t blk = (size_t)table[p] * c.Hkv + h;
+    float* scale = (keys ? c.k_scale : c.v_scale) + blk;
+    uint8_t* codes = (keys ? c.k : c.v) + blk * c.page * c.D;
+    const bool held = lo > p * c.page;  // the block holds older tokens
+    int e = amax < 0x7F800000u ? block_exponent(amax) : 0;
+    bool nan = amax >= 0x7F800000u;
+    float old = 1.f;
+    if (held) {
+        old = *scale;
+        if (old > 0.f && old <= dt_pow2(120)) e = max(e, scale_exponent(old));
+        else nan = true;  // also a scale above any that a finite value gives
+    }
+    __syncthreads();  // every thread has read the scale
+    if (tid == 0) *scale = nan ? __int_as_float(0x7FC00000) : dt_pow2(e);
+    const float inv = dt_pow2(-e);  // -e in [-120, 48]
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int q = tid + i * NT;
+        if (q < m) {
+            uint2 w;
+            w.x = dt_f32x2_to_e4m3x2(__fmul_rn(x[i][0], inv), __fmul_rn(x[i][1], inv)) |
+                  dt_f32x2_to_e4m3x2(__fmul_rn(x[i][2], inv), __fmul_rn(x[i][3], inv)) << 16;
+            w.y = dt_f32x2_to_e4m3x2(__fmul_rn(x[i][4], inv), __fmul_rn(x[i][5], inv)) |
+                  dt_f32x2_to_e4m3x2(__fmul_rn(x[i][6], inv), __fmul_rn(x[i][7], inv)) << 16;
+            *(uint2*)(codes + (size_t)(lo - p * c.page) * c.D + 8 * q) = w;
+        }
+    }
+    if (held && !nan && dt_pow2(e) != old) {  // older codes to the larger scale
+        const float f = __fmul_rn(old, inv);
+        const int words = (lo - p * c.page) * c.D / 4;
+        for (int q = tid; q < words; q += NT) {
+            const uint32_t w = ((const uint32_t*)codes)[q];
+            const float2 a = dt_e4m3x2_to_f32x2(w & 0xFFFFu), d = dt_e4m3x2_to_f32x2(w >> 16);
+            ((uint32_t*)codes)[q] = dt_f32x2_to_e4m3x2(__fmul_rn(a.x, f), __fmul_rn(a.y, f)) |
+                                    dt_f32x2_to_e4m3x2(__fmul_rn(d.x, f), __fmul_rn(d.y, f)) << 16;
+        }
+    }
+}
+
+template <typename T, int CH>
+cudaError_t launch(const dt_kv_cache& c, const dt_rope& rope, int batch, int M, const dt_rows& k, const dt_rows& v,
+                   const int32_t* rows, int N, const int32_t* count, int count_add, int32_t* len_out, int32_t* status,
+                   cudaStream_t st) {
+    const int touched = (N + c.page - 2) / c.page + 1;  // pages that N rows may touch
+    DtLaunch lc(dim3(2 * touched, c.Hkv, batch), dim3(NT), 0, st);
+    return cudaLaunchKernelEx(&lc.cfg, kn10_kernel<T, CH>, c, rope, M, k, v, rows, N, count, count_add, len_out,
+                              status);
+}
+
+template <typename T>
+cudaError_t launch_ch(const dt_kv_cache& c, const dt_rope& rope, int batch, int M, const dt_rows& k, const dt_rows& v,
+                      const int32_t* rows, int N, const int32_t* count, int count_add, int32_t* len_out,
+                      int32_t* status, cudaStream_t st) {
+    // chunks of a block that new rows can fill, per thread
+    const int most = ((N < c.page ? N : c.page) * (c.D / 8) + NT - 1) / NT;
+    auto f = most <= 1 ? launch<T, 1> : most <= 2 ? launch<T, 2> : most <= 4 ? launch<T, 4> : launch<T, 8>;
+    return f(c, rope, batch, M, k, v, rows, N, count, count_add, len_out, status, st);
+}
+
+}  // namespace
+
+cudaError_t dt_kn10_launch(const dt_kv_cache& c, const dt_rope& rope, int batch, int M, int dtype, const dt_rows& k,
+                           const dt_rows& v, const int32_t* rows, int N, const int32_t* count, int count_add,
+                           int32_t* len_out, int32_t* status, cudaStream_t st) {
+    return (dtype == DT_BF16 ? launch_ch<uint16_t> : launch_ch<float>)(c, rope, batch, M, k, v, rows, N, count,
+                                                                       count_add, len_out, status, st);
+}

@@ -18,15 +18,18 @@ from . import build as _build
 DT_MODE = {"ddtree": 0, "dartree": 1, "talon": 2, "heap": 3}
 BUDGET_POLICY = {"topb": 0, "uniform": 1}
 DT_BF16, DT_F32 = 0, 1
-DT_DEV_BAD_TREE, DT_DEV_TIMEOUT, DT_DEV_BESTFIRST = 0x1, 0x2, 0x4
+DT_DEV_BAD_TREE, DT_DEV_TIMEOUT, DT_DEV_BESTFIRST, DT_DEV_BAD_CACHE = 0x1, 0x2, 0x4, 0x8
 DT_DEV_VIOLATION_SHIFT = 8
 DT_STAGE1_CLUSTER, DT_STAGE1_ROWS = 1, 2
 # acceptance rules of dt_verify_rule
 VERIFY_RULES = {"greedy": 0, "ratio": 1, "iter_residual": 2, "target_match": 3}
 MAX_NODES = 1025
 MAX_KC = 1024
+MAX_TOP = 32
+PAGE_SIZES = (16, 32, 64, 128)
 
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
 
 
@@ -52,6 +55,19 @@ class TreeStruct(ctypes.Structure):
     _fields_ = [("max_nodes", _i32), ("Kc", _i32), ("L", _i32), ("node_tok", _vp), ("parent", _vp),
                 ("depth", _vp), ("rank", _vp), ("score", _vp), ("n_nodes", _vp), ("lse", _vp),
                 ("cand_id", _vp), ("cand_lp", _vp), ("status", _vp)]
+
+
+class CacheStruct(ctypes.Structure):
+    _fields_ = [("n_pages", _i32), ("page", _i32), ("Hkv", _i32), ("D", _i32), ("max_pages", _i32), ("k", _vp),
+                ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("table", _vp), ("len", _vp)]
+
+
+class RopeStruct(ctypes.Structure):
+    _fields_ = [("cos", _vp), ("sin", _vp), ("max_pos", _i32), ("rot", _i32), ("interleaved", _i32)]
+
+
+class RowsStruct(ctypes.Structure):
+    _fields_ = [("ptr", _vp), ("stride_b", _i64), ("stride_n", _i64), ("stride_h", _i64)]
 
 
 _LIB = None
@@ -96,6 +112,17 @@ def lib():
         L.dt_select_dartree_noalloc.argtypes = [bp, tp, _vp]
         L.dt_test_wait_fault.restype = _i32
         L.dt_test_wait_fault.argtypes = [_i32, ctypes.c_int64]
+        cp, rp, xp = ctypes.POINTER(CacheStruct), ctypes.POINTER(RopeStruct), ctypes.POINTER(RowsStruct)
+        L.dt_kv_append.restype = _i32
+        L.dt_kv_append.argtypes = [cp, rp, _i32, _i32, _i32, xp, xp, _vp, _i32, _vp, _i32, _vp, _vp, _vp]
+        L.dt_tree_attention_workspace.restype = ctypes.c_size_t
+        L.dt_tree_attention_workspace.argtypes = [cp, _i32, _i32, _i32]
+        L.dt_tree_attention.restype = _i32
+        L.dt_tree_attention.argtypes = [cp, rp, _i32, _i32, _i32, xp, xp, xp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp,
+                                        ctypes.c_size_t, _vp, _vp]
+        L.dt_token_logprobs.restype = _i32
+        L.dt_token_logprobs.argtypes = [_vp, _i32, _i32, _i32, _i32, _i64, _i64, _vp, _vp, _i32, _i32, _vp, _vp,
+                                        _vp, _vp, _vp, _vp]
         L.dt_status_str.restype = ctypes.c_char_p
         L.dt_status_str.argtypes = [_i32]
         L.dt_version.restype = _i32
@@ -524,3 +551,206 @@ def saba_budget(tree, st, c_verify, c_fixed, B_min, B_max, budget, state, hidden
     _check(lib().dt_saba_budget(ctypes.byref(q), ctypes.byref(tree.struct()), batch, _ptr(hidden), Hd,
                                 _ptr(prev_acc_len), _ptr(st.ring), _ptr(st.count), _ptr(state), _ptr(budget),
                                 _stream(stream)), "dt_saba_budget")
+
+
+# ---------------------------------------------------------------------------
+# The target model's side of a round: paged e4m3 cache, tree attention over it,
+# and log-probabilities of what was emitted.
+# ---------------------------------------------------------------------------
+
+class PagedCache:
+    """Keys and values in pages of e4m3 numbers with a scale per (page, key head) (dt_kv_cache).
+
+    k, v: [n_pages, Hkv, page, D] uint8 (or float8_e4m3fn) codes; k_scale, v_scale: [n_pages, Hkv] fp32;
+    table: [batch, max_pages] int32; len: [batch] int32 tokens held.  The caller owns all of them and
+    assigns pages by writing `table`; reassigning an attribute needs a new PagedCache."""
+
+    def __init__(self, k, v, k_scale, v_scale, table, len):
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError("k and v must be [n_pages, Hkv, page, D] of one shape, got %s and %s"
+                             % (tuple(k.shape), tuple(v.shape)))
+        for t, name in ((k, "k"), (v, "v")):
+            _need(t, name=name)
+            if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+                raise TypeError("%s must be uint8 or float8_e4m3fn codes, got %s" % (name, t.dtype))
+        self.n_pages, self.Hkv, self.page, self.D = k.shape
+        _need(k_scale, torch.float32, "k_scale", numel=self.n_pages * self.Hkv)
+        _need(v_scale, torch.float32, "v_scale", numel=self.n_pages * self.Hkv)
+        _need(table, torch.int32, "table")
+        if table.dim() != 2:
+            raise ValueError("table must be [batch, max_pages], got %s" % (tuple(table.shape),))
+        self.batch, self.max_pages = table.shape
+        _need(len, torch.int32, "len", numel=self.batch)
+        self.k, self.v, self.k_scale, self.v_scale, self.table, self.len = k, v, k_scale, v_scale, table, len
+        self._struct = CacheStruct(self.n_pages, self.page, self.Hkv, self.D, self.max_pages, k.data_ptr(),
+                                   v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
+                                   len.data_ptr())
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def empty(cls, n_pages, page, Hkv, D, batch, max_pages, device="cuda"):
+        """A cache with nothing in it: every length 0, every table entry -1."""
+        u8 = dict(dtype=torch.uint8, device=device)
+        f32 = dict(dtype=torch.float32, device=device)
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.zeros((n_pages, Hkv, page, D), **u8), torch.zeros((n_pages, Hkv, page, D), **u8),
+                   torch.ones((n_pages, Hkv), **f32), torch.ones((n_pages, Hkv), **f32),
+                   torch.full((batch, max_pages), -1, **i32), torch.zeros((batch,), **i32))
+
+
+class Rope:
+    """Rotation tables (dt_rope): cos, sin [max_pos, rot / 2] fp32."""
+
+    def __init__(self, cos, sin, interleaved=False):
+        _need(cos, torch.float32, "cos")
+        _need(sin, torch.float32, "sin", numel=cos.numel())
+        if cos.dim() != 2 or cos.shape != sin.shape:
+            raise ValueError("cos and sin must be [max_pos, rot / 2], got %s and %s"
+                             % (tuple(cos.shape), tuple(sin.shape)))
+        self.cos, self.sin, self.interleaved = cos, sin, bool(interleaved)
+        self._struct = RopeStruct(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], int(self.interleaved))
+        self._ref = ctypes.byref(self._struct)
+
+
+def _head_rows(t, batch, M, H, D, name):
+    """dt_rows of [batch, M, H, D]: any strides with dense, 16-byte aligned head vectors."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.shape != (batch, M, H, D):
+        raise ValueError("%s must be %s, got %s" % (name, (batch, M, H, D), tuple(t.shape)))
+    sb, sn, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError("%s must be dense in its last dimension" % name)
+    return RowsStruct(t.data_ptr(), sb, sn, sh)
+
+
+def _need_status(status, batch):
+    return _need(status, torch.int32, "status", numel=batch)
+
+
+def kv_append(cache, k, v, rope=None, rows=None, count=None, count_add=0, len_out=None, status=None, stream=None):
+    """Append rows of k, v [batch, M, Hkv, D] to the cache (dt_kv_append): keys rotated to their
+    position on the way, both stored in e4m3.  rows [batch, N] int32 picks rows (the walk's acc_nodes),
+    count [batch] int32 + count_add says how many (its acc_len, 1); len_out [batch] gets the new lengths;
+    status [batch] int32 is OR-ed with DT_DEV_BAD_CACHE for a request that does not fit."""
+    batch, M = cache.batch, k.shape[1]
+    if k.dtype != v.dtype:
+        raise TypeError("k (%s) and v (%s) must share one dtype" % (k.dtype, v.dtype))
+    kr = _head_rows(k, batch, M, cache.Hkv, cache.D, "k")
+    vr = _head_rows(v, batch, M, cache.Hkv, cache.D, "v")
+    N = M
+    if rows is not None:
+        _need(rows, torch.int32, "rows")
+        if rows.dim() != 2 or rows.shape[0] != batch:
+            raise ValueError("rows must be [batch, N], got %s" % (tuple(rows.shape),))
+        N = rows.shape[1]
+    if count is not None:
+        _need(count, torch.int32, "count", numel=batch)
+    if len_out is not None:
+        _need(len_out, torch.int32, "len_out", numel=batch)
+    status = torch.zeros((batch,), dtype=torch.int32, device=k.device) if status is None else _need_status(status, batch)
+    _check(lib().dt_kv_append(cache._ref, rope._ref if rope is not None else None, batch, M, _dtype_code(k),
+                              ctypes.byref(kr), ctypes.byref(vr), _ptr(rows), N, _ptr(count), int(count_add),
+                              _ptr(len_out), _ptr(status), _stream(stream)), "dt_kv_append")
+    return status
+
+
+def attention_workspace(cache, M, Hq):
+    """Zeroed workspace of tree_attention calls on this cache with M rows and Hq query heads (or
+    fewer of either): (tensor, bytes).  Calls that may run at the same time need one each."""
+    n = int(lib().dt_tree_attention_workspace(cache._ref, cache.batch, M, Hq))
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=cache.k.device), n
+
+
+def tree_attention(cache, q, k, v, mask=None, pos=None, n_nodes=None, rope=None, scale=None, out=None, workspace=None,
+                   status=None, stream=None):
+    """Attention of the tree's rows over the cache and over the tree (dt_tree_attention).
+    q [batch, M, Hq, D], k, v [batch, M, Hkv, D] bf16, not rotated; mask, pos as dt_tree_mask writes
+    them with pos_offset 0 (None: a chain); returns out [batch, M, Hq, D] bf16."""
+    batch, M, Hq = cache.batch, q.shape[1], q.shape[2]
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t.dtype != torch.bfloat16:
+            raise TypeError("%s must be bfloat16, got %s" % (name, t.dtype))
+    qr = _head_rows(q, batch, M, Hq, cache.D, "q")
+    kr = _head_rows(k, batch, M, cache.Hkv, cache.D, "k")
+    vr = _head_rows(v, batch, M, cache.Hkv, cache.D, "v")
+    if mask is not None:
+        _need(mask, torch.int32, "mask", numel=batch * M * ((M + 31) // 32))
+    if pos is not None:
+        _need(pos, torch.int32, "pos", numel=batch * M)
+    if n_nodes is not None:
+        _need(n_nodes, torch.int32, "n_nodes", numel=batch)
+    if out is None:
+        out = torch.empty((batch, M, Hq, cache.D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _need(out, torch.bfloat16, "out", numel=batch * M * Hq * cache.D)
+    if status is None:
+        status = torch.zeros((batch,), dtype=torch.int32, device=q.device)
+    else:
+        _need_status(status, batch)
+    if workspace is None:
+        workspace = attention_workspace(cache, M, Hq)
+    ws, n = _need_workspace(workspace)
+    if scale is None:
+        scale = 1.0 / math.sqrt(cache.D)
+    _check(lib().dt_tree_attention(cache._ref, rope._ref if rope is not None else None, batch, M, Hq,
+                                   ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), _ptr(mask), _ptr(pos),
+                                   _ptr(n_nodes), scale, _ptr(out), _ptr(ws), n, _ptr(status), _stream(stream)),
+           "dt_tree_attention")
+    return out
+
+
+@dataclasses.dataclass
+class Logprobs:
+    """Outputs of token_logprobs: logprob, entropy [batch, N] fp32, rank [batch, N] int32, and
+    top_id int32, top_logprob fp32 [batch, N, top] (None when top is 0)."""
+    logprob: torch.Tensor
+    entropy: torch.Tensor
+    rank: torch.Tensor
+    top_id: torch.Tensor = None
+    top_logprob: torch.Tensor = None
+
+
+def alloc_logprobs(batch, N, top=0, device="cuda"):
+    f32 = dict(dtype=torch.float32, device=device)
+    i32 = dict(dtype=torch.int32, device=device)
+    o = Logprobs(torch.zeros((batch, N), **f32), torch.zeros((batch, N), **f32), torch.full((batch, N), -1, **i32))
+    if top > 0:
+        o.top_id, o.top_logprob = torch.full((batch, N, top), -1, **i32), torch.zeros((batch, N, top), **f32)
+    return o
+
+
+def token_logprobs(logits, tokens, top=0, rows=None, out=None, stream=None):
+    """Log-probability, rank and entropy for tokens [batch, N] int32 under rows of logits [batch, M, V]
+    (row j, or rows[b, j]), with the `top` best alternatives (dt_token_logprobs).  Negative entries
+    of rows or tokens are padding."""
+    if logits.dim() != 3 or not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor [batch, M, V]")
+    batch, M, V = logits.shape
+    sb, sm, sv = logits.stride()
+    if sv != 1 and V > 1 or sm < V and M > 1:
+        raise ValueError("logits must be dense in V and their rows apart, got strides %s" % (logits.stride(),))
+    _need(tokens, torch.int32, "tokens")
+    if tokens.dim() != 2 or tokens.shape[0] != batch:
+        raise ValueError("tokens must be [batch, N], got %s" % (tuple(tokens.shape),))
+    N = tokens.shape[1]
+    if rows is not None:
+        _need(rows, torch.int32, "rows")
+        if rows.shape != tokens.shape:
+            raise ValueError("rows must be shaped as tokens, got %s and %s" % (tuple(rows.shape), tuple(tokens.shape)))
+    if out is None:
+        out = alloc_logprobs(batch, N, top, logits.device)
+    else:
+        _need(out.logprob, torch.float32, "logprob", numel=batch * N)
+        _need(out.entropy, torch.float32, "entropy", numel=batch * N)
+        _need(out.rank, torch.int32, "rank", numel=batch * N)
+        if top > 0:
+            if out.top_id is None or out.top_logprob is None:
+                raise ValueError("out has no room for alternatives (alloc_logprobs(batch, N, top))")
+            _need(out.top_id, torch.int32, "top_id", numel=batch * N * top)
+            _need(out.top_logprob, torch.float32, "top_logprob", numel=batch * N * top)
+    _check(lib().dt_token_logprobs(_ptr(logits), _dtype_code(logits), batch, M, V, sb, max(sm, V), _ptr(rows),
+                                   _ptr(tokens), N, int(top), _ptr(out.logprob), _ptr(out.entropy), _ptr(out.rank),
+                                   _ptr(out.top_id) if top > 0 else None, _ptr(out.top_logprob) if top > 0 else None,
+                                   _stream(stream)), "dt_token_logprobs")
+    return out

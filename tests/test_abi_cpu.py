@@ -272,3 +272,83 @@ def test_binding_size_checks_reject_short_buffers_and_small_trees():
         dtree._need_batch(t, 3)
     with pytest.raises(ValueError):
         dtree._need(torch.zeros(4), name="cpu tensor")  # a host tensor never reaches a kernel
+
+
+def _cache(**kw):
+    f = dict(n_pages=4, page=16, Hkv=2, D=64, max_pages=2, k=0x1000, v=0x2000, k_scale=0x3000, v_scale=0x4000,
+             table=0x5000, len=0x6000)
+    f.update(kw)
+    return dtree.CacheStruct(*[f[n] for n, _ in dtree.CacheStruct._fields_])
+
+
+def _rope(**kw):
+    f = dict(cos=0x1000, sin=0x2000, max_pos=10, rot=32, interleaved=0)
+    f.update(kw)
+    return dtree.RopeStruct(*[f[n] for n, _ in dtree.RopeStruct._fields_])
+
+
+def _rows(**kw):
+    f = dict(ptr=0x1000, stride_b=1024, stride_n=128, stride_h=64)
+    f.update(kw)
+    return dtree.RowsStruct(*[f[n] for n, _ in dtree.RowsStruct._fields_])
+
+
+def _call_append(cache=None, rope=None, batch=1, M=3, dtype=0, k=None, rows=None, N=3, len_out=None, status=0x7000):
+    ref = ctypes.byref
+    return dtree.lib().dt_kv_append(ref(cache or _cache()), ref(rope) if rope else None, batch, M, dtype,
+                                    ref(k or _rows()), ref(_rows()), rows, N, None, 0, len_out, status, None)
+
+
+def _call_attention(cache=None, rope=None, batch=1, M=3, Hq=4, q=None, scale=1.0, out=0x8000, ws=0x9000, n=1 << 40,
+                    status=0x7000):
+    ref = ctypes.byref
+    return dtree.lib().dt_tree_attention(ref(cache or _cache()), ref(rope) if rope else None, batch, M, Hq,
+                                         ref(q or _rows()), ref(_rows()), ref(_rows()), None, None, None, scale, out,
+                                         ws, n, status, None)
+
+
+@pytest.mark.parametrize("call", [_call_append, _call_attention])
+@pytest.mark.parametrize("bad,rc", [
+    (dict(page=48), -1), (dict(page=0), -1), (dict(n_pages=0), -1), (dict(max_pages=0), -1), (dict(Hkv=0), -1),
+    (dict(D=0), -1), (dict(D=96), -2), (dict(max_pages=1 << 30), -2), (dict(k=None), -1), (dict(v=0x2008), -1),
+    (dict(v_scale=None), -1), (dict(table=None), -1), (dict(len=None), -1),
+])
+def test_target_calls_reject_invalid_caches(call, bad, rc):
+    assert call(cache=_cache(**bad)) == rc
+
+
+@pytest.mark.parametrize("call", [_call_append, _call_attention])
+@pytest.mark.parametrize("bad", [dict(rot=0), dict(rot=8), dict(rot=40), dict(rot=80), dict(max_pos=0), dict(cos=None),
+                                 dict(sin=0x2004), dict(interleaved=2)])
+def test_target_calls_reject_invalid_rotations(call, bad):
+    assert call(rope=_rope(**bad)) == -1
+
+
+def test_append_rejects_invalid_arguments():
+    for kw in (dict(batch=0), dict(M=0), dict(N=0), dict(N=4), dict(dtype=2), dict(status=None), dict(len_out=0x6000),
+               dict(k=_rows(ptr=None)), dict(k=_rows(ptr=0x1002)), dict(k=_rows(stride_n=100)),
+               dict(k=_rows(stride_b=-1024))):
+        assert _call_append(**kw) == -1, kw
+
+
+def test_attention_rejects_invalid_arguments():
+    nan, inf = float("nan"), float("inf")
+    for kw in (dict(batch=0), dict(M=0), dict(Hq=0), dict(Hq=3), dict(scale=0.0), dict(scale=-1.0), dict(scale=nan),
+               dict(scale=inf), dict(out=None), dict(out=0x8004), dict(status=None), dict(q=_rows(ptr=None)),
+               dict(q=_rows(stride_h=60))):
+        assert _call_attention(**kw) == -1, kw
+    assert _call_attention(Hq=2 * 129) == -2
+    need = dtree.lib().dt_tree_attention_workspace(ctypes.byref(_cache()), 1, 3, 4)
+    if need:
+        assert _call_attention(ws=None) == -1 and _call_attention(ws=0x9004) == -1 and _call_attention(n=need - 1) == -1
+
+
+def test_logprobs_reject_invalid_arguments():
+    def call(x=0x1000, dtype=0, batch=1, M=3, V=100, stride=100, tokens=0x2000, rows=None, N=3, top=0, top_id=None):
+        return dtree.lib().dt_token_logprobs(x, dtype, batch, M, V, 300, stride, rows, tokens, N, top, 0x3000, 0x4000,
+                                             0x5000, top_id, top_id, None)
+    for kw in (dict(x=None), dict(x=0x1001), dict(dtype=5), dict(batch=0), dict(M=0), dict(V=0), dict(stride=99),
+               dict(tokens=None), dict(N=0), dict(N=4), dict(top=-1), dict(top=33, top_id=0x6000), dict(top=1),
+               dict(V=5, top=6, top_id=0x6000)):
+        assert call(**kw) == -1, kw
+    assert call(V=dtree.lib() and (1 << 20), stride=1 << 20) == -2
