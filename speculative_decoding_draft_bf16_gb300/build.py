@@ -19,7 +19,7 @@ LIB = os.path.join(OUT, "libdtree.so")
 
 SOURCES = ["dt_abi.cu", "kn0_ceiling.cu", "kn1_candidates.cu", "kn1b_rows.cu", "kn2_ddtree.cu", "kn3_dartree.cu", "kn3n_norm.cu", "kn4_talon.cu",
            "kn5_mask.cu", "kn6_verify.cu", "kn7_heap.cu",
-           "kn9_saba.cu", "dt_abi_target.cu", "kn10_append.cu", "kn11_attend.cu", "kn13_logprobs.cu"]
+           "kn9_saba.cu", "dt_abi_target.cu", "kn10_append.cu", "kn11_attend.cu", "kn12_attend_tc.cu", "kn13_logprobs.cu"]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-ffp-contract=off", "--fmad=false",

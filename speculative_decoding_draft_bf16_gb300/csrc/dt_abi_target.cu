@@ -15,6 +15,19 @@ dt_status cuda_status(cudaError_t e) {
     return DT_ERR_CUDA;
 }
 
+// Rows per key head up to which attention streams the cache through registers.
+constexpr long long kStreamRows = 16;
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        return 152;
+    }
+    return n < 1024 ? n : 1024;
+}
+
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 dt_status check_cache(const dt_kv_cache* c, int32_t batch) {
@@ -68,8 +81,8 @@ dt_status dt_kv_append(const dt_kv_cache* c, const dt_rope* rope, int32_t batch,
 }
 
 size_t dt_tree_attention_workspace(const dt_kv_cache* c, int32_t batch, int32_t M, int32_t Hq) {
-    (void)c, (void)batch, (void)M, (void)Hq;
-    return 0;
+    if (check_cache(c, batch) != DT_OK || M < 1 || Hq < 1) return 0;
+    return dt_kn12_workspace(c->D, sm_count());
 }
 
 dt_status dt_tree_attention(const dt_kv_cache* c, const dt_rope* rope, int32_t batch, int32_t M, int32_t Hq,
@@ -88,7 +101,8 @@ dt_status dt_tree_attention(const dt_kv_cache* c, const dt_rope* rope, int32_t b
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return DT_ERR_INVALID_ARG;
     const dt_rope none = {nullptr, nullptr, 0, 0, 0};
     const DtAttend a{*c, rope ? *rope : none, batch, M, Hq, *q, *k, *v, mask, pos, n_nodes, scale, out, status};
-    return cuda_status(dt_kn11_launch(a, (cudaStream_t)stream));
+    if ((long long)M * (Hq / c->Hkv) <= kStreamRows) return cuda_status(dt_kn11_launch(a, (cudaStream_t)stream));
+    return cuda_status(dt_kn12_launch(a, workspace, sm_count(), (cudaStream_t)stream));
 }
 
 dt_status dt_token_logprobs(const void* logits, int32_t dtype, int32_t batch, int32_t M, int32_t V, int64_t stride_b,
