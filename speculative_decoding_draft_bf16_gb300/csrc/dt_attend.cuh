@@ -25,7 +25,7 @@ struct AtReq {  // one request
 template <int ROWS>
 struct AtPlan {
     // Cost of a tile of a block: blocks of more than half the rows cost two.
-    static DT_DI int weight(int rows) { return rows > ROWS / 2 ? 2 : 1; }
+    static DT_DI int weight(int rows) { return 1; }
     static DT_DI AtReq req(const DtAttend& a, int b) {
         AtReq r;
         const int len = a.c.len[b], n = a.n_nodes ? a.n_nodes[b] : a.M;
@@ -55,7 +55,7 @@ struct AtPlan {
         long long s = 0;
         if (a.mask) {
             const long long t = block_tiles(a, r, 0);
-            s = t * (2 * (r.nqb - 1) + weight(block_rows(a, r, r.nqb - 1)));
+            s = t * (weight(ROWS) * (r.nqb - 1) + weight(block_rows(a, r, r.nqb - 1)));
         } else {
             for (int qb = 0; qb < r.nqb; ++qb) s += (long long)block_tiles(a, r, qb) * weight(block_rows(a, r, qb));
         }

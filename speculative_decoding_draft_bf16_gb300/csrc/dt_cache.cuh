@@ -48,6 +48,45 @@ DT_DI void dt_rotated8(const T* row, int c, const dt_rope& r, int at, float (&x)
     }
 }
 
+// Two chunks of 8 elements of a head vector that rotate together, index p of
+// D / 16: split halves pair chunk p with chunk p + rot / 16; otherwise, and
+// past rot, neighbours.  c0, c1: which chunks they are.
+DT_DI void dt_pair_chunks(int p, const dt_rope& r, int& c0, int& c1) {
+    const bool halves = !r.interleaved && 16 * p < r.rot;
+    c0 = halves ? p : 2 * p;
+    c1 = halves ? p + (r.rot >> 4) : 2 * p + 1;
+}
+// Both chunks as fp32, rotated to position `at` (which must lie in the tables).
+template <typename T>
+DT_DI void dt_rotated_pair(const T* row, int p, const dt_rope& r, int at, float (&x)[8], float (&y)[8]) {
+    int c0, c1;
+    dt_pair_chunks(p, r, c0, c1);
+    dt_load8(row + 8 * c0, x);
+    dt_load8(row + 8 * c1, y);
+    if (16 * p >= r.rot) return;
+    float cv[8], sv[8];
+    const size_t o = (size_t)at * (r.rot >> 1) + 8 * p;
+    dt_load8(r.cos + o, cv);
+    dt_load8(r.sin + o, sv);
+    if (r.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i], b = x[2 * i + 1], c = y[2 * i], d = y[2 * i + 1];
+            x[2 * i] = __fsub_rn(__fmul_rn(a, cv[i]), __fmul_rn(b, sv[i]));
+            x[2 * i + 1] = __fadd_rn(__fmul_rn(b, cv[i]), __fmul_rn(a, sv[i]));
+            y[2 * i] = __fsub_rn(__fmul_rn(c, cv[4 + i]), __fmul_rn(d, sv[4 + i]));
+            y[2 * i + 1] = __fadd_rn(__fmul_rn(d, cv[4 + i]), __fmul_rn(c, sv[4 + i]));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float a = x[i], b = y[i];
+            x[i] = __fsub_rn(__fmul_rn(a, cv[i]), __fmul_rn(b, sv[i]));
+            y[i] = __fadd_rn(__fmul_rn(b, cv[i]), __fmul_rn(a, sv[i]));
+        }
+    }
+}
+
 // Two e4m3 codes (the low 16 bits) as an exact fp16 pair.
 DT_DI uint32_t dt_e4m3x2_to_f16x2(uint32_t codes) {
     uint32_t d;

@@ -29,30 +29,51 @@ namespace {
 constexpr int ROWS = 256;       // query rows of a block
 constexpr int TQ = 128;         // rows of a slot
 constexpr int NS = 256;         // softmax threads
-constexpr int NC = 128;         // converter threads
-constexpr int NT = NS + NC + 32;
+constexpr int NC = 128;         // converter threads for the keys, and as many for the values
+// Five warpgroups; in the last one a thread issues the MMAs, a thread of another
+// warp walks the CTA's share of the work and a third warp looks up pages.
+constexpr int NT = NS + 2 * NC + 128;
+// Registers per thread of the warpgroups (softmax, converters, MMA): over the
+// CTA they sum to what it is launched with, LAUNCH_REGS each.  No loop of a role may
+// spill: the shared memory in use leaves the L1 less than the spills need.
+constexpr int LAUNCH_REGS = 65536 / NT / 8 * 8;
+constexpr int REG_SOFT = 112, REG_CONV = 104, REG_MMA = 48;
+static_assert(NS * REG_SOFT + 2 * NC * REG_CONV + 128 * REG_MMA == NT * LAUNCH_REGS, "register split");
 constexpr int STAGES = 2;       // K and V tiles in shared memory, each
-constexpr int RING = 4;         // tiles whose scales are kept
+constexpr int RING = 8;         // tiles whose page ids and scales are kept
+constexpr int SEGS = 4;         // segments the walk may be ahead
 constexpr int ATOM = 4;         // tiles of the longest unit that is not split
-constexpr int MIN_SHARE = 4;    // least cost worth a CTA: two tiles of a full block
+constexpr int MIN_SHARE = 2;    // least cost worth a CTA: two tiles of a full block
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float HEADROOM = 5.f, LAZY = 8.f;
 
-struct Ring {
+struct __align__(16) Ring {
     float ks[8], lv[8], iv[8];  // key scale, log2 and inverse of the value scale per 16 tokens
-    uint32_t bad[4];            // new rows with a value that is not finite
+    uint32_t id[8];             // their pages
+    uint32_t bad[2][4];         // new rows with a key, a value that is not finite
+};
+
+// The tiles [t0, t1) of a unit (b, h, qb), from the walk to the roles.
+struct Seg {
+    int b, h, qb, t0, t1, nt;  // b < 0: no more
+    int rows, len, n, ctx;     // rows of the block; cached tokens, new rows, cached tiles
+    int first, segs;           // CTA of the unit's first tile, CTAs that share it
 };
 
 struct Shared {
     uint64_t kfull[STAGES], kfree[STAGES], vfull[STAGES], vfree[STAGES];
-    uint64_t sfull[2], pfull[2], ofull[2], qfull, scfull[RING];
+    uint64_t sfull[2], pfull[2], ofull[2], qfull, scfull[RING], idfull[RING], ringfree[RING];
     uint32_t tmem;
     int fail, last;
     AtShare share;
     Ring ring[RING];
     float qscale[ROWS];
+    int qpos[ROWS], kpos[AT_TILE];
+    long long qoff[ROWS];
     float mrg_m[TQ], mrg_l[TQ];
     uint32_t amax[2][NC / 32];
+    uint64_t segfull[SEGS], segfree[SEGS];
+    Seg seg[SEGS];
 };
 
 template <int D>
@@ -64,10 +85,58 @@ struct Lay {
 };
 
 // Bounded wait; once one has run out, later ones return at once.
-DT_DI void wait(uint64_t* bar, uint32_t phase, int* fail) {
-    if (*(volatile int*)fail) return;
-    if (!dt_mbar_wait(bar, phase)) *(volatile int*)fail = 1;
+DT_DI bool try_wait(uint64_t* bar, uint32_t phase) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(dt_smem_addr(bar)), "r"(phase)
+        : "memory");
+    return done;
 }
+DT_DI void wait(uint64_t* bar, uint32_t phase, int* fail) {
+    if (try_wait(bar, phase)) return;
+    const long long t0 = clock64();
+    while (!try_wait(bar, phase)) {
+        if (*(volatile int*)fail) return;
+        if (clock64() - t0 > DT_WAIT_BUDGET) {
+            *(volatile int*)fail = 1;
+            return;
+        }
+    }
+}
+
+// This warpgroup's registers per thread, from the LAUNCH_REGS it started with
+// (`dec` takes a lower count only, `inc` a higher one).
+template <int R>
+DT_DI void set_regs() {
+    static_assert(R >= 24 && R <= 256 && R % 8 == 0, "register count");
+    if constexpr (R > LAUNCH_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+    if constexpr (R < LAUNCH_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// The thread that walks the share, up to SEGS segments ahead of the roles.
+DT_DI void walk_share(const DtAttend& a, Shared* sh, int cta) {
+    AtWalk<ROWS, ATOM> u;
+    u.start(a, sh->share);
+    uint32_t i = 0;
+    for (bool more = true; more; ++i) {
+        more = u.next(a, sh->share, cta);
+        wait(&sh->segfree[i % SEGS], (i / SEGS + 1) & 1, &sh->fail);
+        Seg* s = &sh->seg[i % SEGS];
+        *s = more ? Seg{u.b, u.h, u.qb, u.t0, u.t1, u.nt, u.rows, u.r.len, u.r.n, u.r.ctx, u.first, u.segs} : Seg{-1};
+        dt_mbar_arrive(&sh->segfull[i % SEGS]);
+        if (more) u.step(a);
+    }
+}
+// Segment i of the share, or null after the last one.  Every thread of a role
+// gets each segment and releases it when it has read what it needs.
+DT_DI const Seg* get_segment(Shared* sh, uint32_t i) {
+    wait(&sh->segfull[i % SEGS], (i / SEGS) & 1, &sh->fail);
+    const Seg* s = &sh->seg[i % SEGS];
+    return sh->fail || s->b < 0 ? nullptr : s;
+}
+DT_DI void release_segment(Shared* sh, uint32_t i) { dt_mbar_arrive(&sh->segfree[i % SEGS]); }
 
 // 32-bit pair of fp16 from two fp32 (lo in the low half).
 DT_DI uint32_t f16x2(float lo, float hi) {
@@ -75,10 +144,26 @@ DT_DI uint32_t f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+DT_DI uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *(const uint32_t*)&v;
+}
 DT_DI float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+
+// Streamed codes: read once by this CTA, not kept in L1; zeros unless `in`.
+DT_DI uint4 ldg16_if(const void* p, bool in) {
+    uint4 v;
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
+        " @p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}\n"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((int)in)
+        : "memory");
+    return v;
 }
 
 // Byte offset of the 16-byte chunk c (8 fp16) of row r in a tile of D columns.
@@ -90,22 +175,15 @@ DT_DI void sts16(uint32_t addr, const uint32_t (&w)[4]) {
                  : "memory");
 }
 
-// Sixteen e4m3 codes to two fp16 chunks 2 * pc, 2 * pc + 1 of row r.  The lanes
-// of the upper 64 columns store their odd chunk first: the eight lanes of a
-// store phase then hit eight different 16-byte columns.
-template <int D>
-DT_DI void store_codes(uint32_t tile, int r, int pc, const uint4& q) {
-    uint32_t a[4], b[4];
-    a[0] = dt_e4m3x2_to_f16x2(q.x), a[1] = dt_e4m3x2_to_f16x2(q.x >> 16);
-    a[2] = dt_e4m3x2_to_f16x2(q.y), a[3] = dt_e4m3x2_to_f16x2(q.y >> 16);
-    b[0] = dt_e4m3x2_to_f16x2(q.z), b[1] = dt_e4m3x2_to_f16x2(q.z >> 16);
-    b[2] = dt_e4m3x2_to_f16x2(q.w), b[3] = dt_e4m3x2_to_f16x2(q.w >> 16);
-    const bool odd = D == 128 && pc >= 4;
-    uint32_t f[4], s[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = odd ? b[i] : a[i], s[i] = odd ? a[i] : b[i];
-    sts16(tile + chunk_at(r, 2 * pc + odd), f);
-    sts16(tile + chunk_at(r, 2 * pc + !odd), s);
+// Sixteen e4m3 codes to two fp16 chunks at a0 and a1.
+DT_DI void store_codes(uint32_t a0, uint32_t a1, const uint4& q) {
+    uint32_t w[4];
+    w[0] = dt_e4m3x2_to_f16x2(q.x), w[1] = dt_e4m3x2_to_f16x2(q.x >> 16);
+    w[2] = dt_e4m3x2_to_f16x2(q.y), w[3] = dt_e4m3x2_to_f16x2(q.y >> 16);
+    sts16(a0, w);
+    w[0] = dt_e4m3x2_to_f16x2(q.z), w[1] = dt_e4m3x2_to_f16x2(q.z >> 16);
+    w[2] = dt_e4m3x2_to_f16x2(q.w), w[3] = dt_e4m3x2_to_f16x2(q.w >> 16);
+    sts16(a1, w);
 }
 
 // log2 of a positive normal number, and its inverse: exact for powers of two.
@@ -114,211 +192,222 @@ DT_DI void scale_parts(float s, float& lg, float& inv) {
     inv = 1.0f / s;
 }
 
-template <int D>
-struct Conv {  // the converter warps
-    static constexpr int PPT = D / 16;        // 16-byte pieces of a token's codes
+// The converter warps of the keys (KEYS) or the values.
+template <int D, bool KEYS>
+struct Conv {
+    // A thread reads 16-byte piece `piece` (of D / 16) of token i * TPI + `tok`
+    // in iteration i.  Four lanes read half a row of 128 columns; eight lanes of
+    // a store phase then hold two tokens, whose chunks swizzle to eight
+    // different 16-byte columns.
+    static constexpr int PPT = D / 16;
     static constexpr int TPI = NC / PPT;      // tokens per iteration
+    static DT_DI int piece_of(int ct) { return D == 128 ? (ct & 3) + ((ct >> 4) & 1) * 4 : ct & 3; }
+    static DT_DI int tok_of(int ct) { return D == 128 ? ((ct >> 2) & 3) + (ct >> 5) * 4 : ct >> 2; }
     static constexpr int NI = AT_TILE / TPI;  // iterations per tile
+    static constexpr int BAR = KEYS ? 1 : 3, WHICH = KEYS ? 0 : 1;
     using L = Lay<D>;
 
-    // page ids of the tokens this thread reads of tile j (-1: none)
-    static DT_DI void pages(const DtAttend& a, const AtWalk<ROWS, ATOM>& u, int lp, int j, int ct, int (&id)[NI]) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int tok = j * AT_TILE + i * TPI + ct / PPT;
-            int p = -1;
-            if (tok < u.r.len) {
-                p = a.c.table[(size_t)u.b * a.c.max_pages + (tok >> lp)];
-                if ((unsigned)p >= (unsigned)a.c.n_pages) {
-                    atomicOr(&a.status[u.b], DT_DEV_BAD_CACHE);
-                    p = 0;
-                }
-            }
-            id[i] = p;
-        }
-    }
-    static DT_DI void codes(const DtAttend& a, const AtWalk<ROWS, ATOM>& u, const uint8_t* base, int lp, int j, int ct,
-                            const int (&id)[NI], uint4 (&q)[NI]) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int tok = j * AT_TILE + i * TPI + ct / PPT;
-            q[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (id[i] >= 0) {
-                const size_t row = (((size_t)id[i] * a.c.Hkv + u.h) << lp) + (tok & ((1 << lp) - 1));
-                q[i] = *(const uint4*)(base + row * D + (ct % PPT) * 16);
-            }
-        }
-    }
-    static DT_DI void store(uint32_t tile, int ct, const uint4 (&q)[NI]) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) store_codes<D>(tile, i * TPI + ct / PPT, ct % PPT, q[i]);
-        dt_fence_proxy_async_smem();
-    }
-    // scales of group ct (< 8) of tile j
-    static DT_DI void scales(const DtAttend& a, const AtWalk<ROWS, ATOM>& u, int lp, int j, int ct, float& ks, float& vs) {
-        const int tok = j * AT_TILE + ct * 16;
-        ks = vs = 1.f;
-        if (ct < 8 && tok < u.r.len) {
-            int p = a.c.table[(size_t)u.b * a.c.max_pages + (tok >> lp)];
-            if ((unsigned)p >= (unsigned)a.c.n_pages) p = 0;
-            ks = a.c.k_scale[(size_t)p * a.c.Hkv + u.h];
-            vs = a.c.v_scale[(size_t)p * a.c.Hkv + u.h];
-        }
+    static DT_DI void group_sync() { asm volatile("bar.sync %0, 128;" ::"n"(BAR) : "memory"); }
+
+    // Piece i of a tile: this thread's 16 bytes of token `tok`; zeros past len.
+    static DT_DI uint4 piece(const uint8_t* base, uint32_t page_bytes, int low, uint32_t id, int tok, int len) {
+        return ldg16_if(base + (size_t)id * page_bytes + (tok & low) * D, tok < len);
     }
 
-    // One tile of new rows, from row m0: keys rotated, both scaled by a power of
-    // two when their largest magnitude leaves fp16's comfortable range.
-    static DT_DI void fresh(const DtAttend& a, const AtWalk<ROWS, ATOM>& u, int m0, int ct, Shared* sh, Ring* ring,
-                            uint32_t kt, uint32_t vt, int stage, uint32_t kfree_ph, uint32_t vfree_ph, uint64_t* scfull) {
-        constexpr int CPR = D / 8;  // chunks per row
-        const int left = min(AT_TILE, u.r.n - m0);
-        const uint16_t* kp = (const uint16_t*)a.k.ptr + u.b * a.k.stride_b + u.h * a.k.stride_h;
-        const uint16_t* vp = (const uint16_t*)a.v.ptr + u.b * a.v.stride_b + u.h * a.v.stride_h;
-        if (ct < 4) ring->bad[ct] = 0u;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        uint32_t big[2] = {0u, 0u};
-        float x[8];
-        for (int i = ct; i < left * CPR; i += NC) {
-            const int m = m0 + i / CPR, c = i % CPR;
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                if (w == 0)
-                    dt_rotated8(kp + m * a.k.stride_n, c, a.rope, at_position(a, u.b, u.r.len, m), x);
-                else
-                    dt_load8(vp + m * a.v.stride_n + 8 * c, x);
+    // One tile of new rows, from row m0: keys rotated, scaled by a power of two
+    // when the largest magnitude leaves fp16's comfortable range.
+    static DT_DI void fresh(const DtAttend& a, const Seg& u, int m0, int ct, Shared* sh, Ring* ring, uint32_t tile) {
+        const int b = u.b, n = u.n, len = u.len, left = min(AT_TILE, n - m0);
+        const dt_rows& src = KEYS ? a.k : a.v;
+        const uint16_t* p = (const uint16_t*)src.ptr + b * src.stride_b + u.h * src.stride_h;
+        if (ct < 4) ring->bad[WHICH][ct] = 0u;
+        if (KEYS) sh->kpos[ct] = a.rope.rot && ct < left ? at_position(a, b, len, m0 + ct) : 0;
+        group_sync();
+        const int pr = ct % PPT;  // this thread's chunk pair of rows ct / PPT + i * TPI
+        int c0 = 2 * pr, c1 = 2 * pr + 1;
+        if (KEYS) dt_pair_chunks(pr, a.rope, c0, c1);
+        uint32_t big = 0u;
+        auto convert = [&](float f) {
+#pragma unroll 2
+            for (int i = 0; i < NI; ++i) {
+                const int r = ct / PPT + i * TPI;
+                const uint16_t* row = p + (m0 + min(r, left - 1)) * src.stride_n;
+                float x[8], y[8];
+                if (KEYS) {
+                    dt_rotated_pair(row, pr, a.rope, sh->kpos[min(r, left - 1)], x, y);
+                } else {
+                    dt_load8(row + 16 * pr, x);
+                    dt_load8(row + 16 * pr + 8, y);
+                }
                 bool bad = false;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const uint32_t v = __float_as_uint(x[e]) & 0x7FFFFFFFu;
-                    if (v >= 0x7F800000u) bad = true;
-                    else big[w] = max(big[w], v);
+                    const uint32_t v = __float_as_uint(x[e]) & 0x7FFFFFFFu, w = __float_as_uint(y[e]) & 0x7FFFFFFFu;
+                    const bool bx = v >= 0x7F800000u, by = w >= 0x7F800000u;
+                    bad |= bx | by;
+                    x[e] = bx || r >= left ? 0.f : x[e];
+                    y[e] = by || r >= left ? 0.f : y[e];
+                    big = max(big, max(__float_as_uint(x[e]) & 0x7FFFFFFFu, __float_as_uint(y[e]) & 0x7FFFFFFFu));
                 }
-                if (bad) atomicOr(&ring->bad[(m - m0) >> 5], 1u << ((m - m0) & 31));
+                if (bad && r < left) atomicOr(&ring->bad[WHICH][r >> 5], 1u << (r & 31));
+                uint32_t o[4], w[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    o[q] = f16x2(__fmul_rn(x[2 * q], f), __fmul_rn(x[2 * q + 1], f));
+                    w[q] = f16x2(__fmul_rn(y[2 * q], f), __fmul_rn(y[2 * q + 1], f));
+                }
+                sts16(tile + chunk_at(r, c0), o);
+                sts16(tile + chunk_at(r, c1), w);
             }
-        }
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            big[w] = dt_warp_max_u32(big[w]);
-            if ((ct & 31) == 0) sh->amax[w][ct >> 5] = big[w];
-        }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        int ex[2];
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            uint32_t v = 0;
-            for (int i = 0; i < NC / 32; ++i) v = max(v, sh->amax[w][i]);
-            // as they are in [2^-4, 2^15), else scaled to below 2^9; none or very small: 2^-57
-            const int e = (int)(v >> 23) - 127;
-            ex[w] = e >= -4 && e < 15 ? 0 : max(e - 8, -57);
-        }
+        };
+        convert(1.f);
+        big = dt_warp_max_u32(big);
+        if ((ct & 31) == 0) sh->amax[WHICH][ct >> 5] = big;
+        group_sync();
+        for (int i = 0; i < NC / 32; ++i) big = max(big, sh->amax[WHICH][i]);
+        // as they are in [2^-4, 2^15), else scaled to below 2^9; none or very small: 2^-57
+        int e = (int)(big >> 23) - 127;
+        e = e >= -4 && e < 15 ? 0 : max(e - 8, -57);
+        if (e != 0) convert(dt_pow2(-e));
         if (ct < 8) {
-            ring->ks[ct] = dt_pow2(ex[0]);
-            ring->lv[ct] = (float)ex[1];
-            ring->iv[ct] = dt_pow2(-ex[1]);
-        }
-        dt_mbar_arrive(scfull);
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            wait(w == 0 ? &sh->kfree[stage] : &sh->vfree[stage], w == 0 ? kfree_ph : vfree_ph, &sh->fail);
-            const float f = dt_pow2(-ex[w]);
-            for (int i = ct; i < AT_TILE * CPR; i += NC) {
-                const int r = i / CPR, c = i % CPR;
-                uint32_t o[4] = {0u, 0u, 0u, 0u};
-                if (r < left) {
-                    if (w == 0)
-                        dt_rotated8(kp + (m0 + r) * a.k.stride_n, c, a.rope, at_position(a, u.b, u.r.len, m0 + r), x);
-                    else
-                        dt_load8(vp + (m0 + r) * a.v.stride_n + 8 * c, x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x[e] = (__float_as_uint(x[e]) & 0x7FFFFFFFu) >= 0x7F800000u ? 0.f : __fmul_rn(x[e], f);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] = f16x2(x[2 * e], x[2 * e + 1]);
-                }
-                sts16((w == 0 ? kt : vt) + chunk_at(r, c), o);
+            if (KEYS) {
+                ring->ks[ct] = dt_pow2(e);
+            } else {
+                ring->lv[ct] = (float)e;
+                ring->iv[ct] = dt_pow2(-e);
             }
-            dt_fence_proxy_async_smem();
-            dt_mbar_arrive(w == 0 ? &sh->kfull[stage] : &sh->vfull[stage]);
         }
     }
 
-    static DT_DI void run(const DtAttend& a, unsigned char* sm, Shared* sh, int ct, int cta) {
+    static DT_DI void run(const DtAttend& a, unsigned char* sm, Shared* sh, int ct) {
         const int lp = 31 - __clz(a.c.page);
-        const uint32_t kt = dt_smem_addr(sm + L::K), vt = dt_smem_addr(sm + L::V);
-        AtWalk<ROWS, ATOM> u;
-        u.start(a, sh->share);
-        uint32_t g = 0;  // tiles done
-        for (; u.next(a, sh->share, cta); u.step(a)) {
-            uint4 kq[NI], vq[NI];
-            int id[NI];
-            float ks, vs;
-            const int cend = min(u.t1, u.r.ctx);
+        const uint32_t base = dt_smem_addr(sm + (KEYS ? L::K : L::V));
+        const uint32_t a0 = base + chunk_at(tok_of(ct), 2 * piece_of(ct)),
+                       a1 = base + chunk_at(tok_of(ct), 2 * piece_of(ct) + 1);
+        uint64_t* full = KEYS ? sh->kfull : sh->vfull;
+        uint64_t* free_ = KEYS ? sh->kfree : sh->vfree;
+        uint32_t g = 0, i = 0;  // tiles, segments done
+        for (const Seg* sg; (sg = get_segment(sh, i)) != nullptr; release_segment(sh, i++)) {
+            const Seg& u = *sg;
+            const int t1 = u.t1, cend = min(t1, u.ctx), len = u.len, low = a.c.page - 1;
+            const uint8_t* codes = (KEYS ? a.c.k : a.c.v) + (((size_t)u.h << lp) * D + piece_of(ct) * 16);
+            const uint32_t page_bytes = ((uint32_t)a.c.Hkv << lp) * D;
+            // The next tile's codes are loaded in two batches, each when this
+            // tile's have left its registers.  Page ids come from shared memory:
+            // loads that wait for loads would share their scoreboards.
+            uint4 q[NI];
+            auto load = [&](int j, uint32_t g, int i0) {
+                const Ring* ring = &sh->ring[g % RING];
+#pragma unroll
+                for (int i = i0; i < i0 + NI / 2; ++i) {
+                    const int r = tok_of(ct) + i * TPI;
+                    q[i] = piece(codes, page_bytes, low, ring->id[r >> 4], j * AT_TILE + r, len);
+                }
+            };
             int j = u.t0;
             if (j < cend) {
-                pages(a, u, lp, j, ct, id);
-                codes(a, u, a.c.k, lp, j, ct, id, kq);
-                codes(a, u, a.c.v, lp, j, ct, id, vq);
-                scales(a, u, lp, j, ct, ks, vs);
-                if (j + 1 < cend) pages(a, u, lp, j + 1, ct, id);
+                wait(&sh->idfull[g % RING], (g / RING) & 1, &sh->fail);
+                load(j, g, 0);
+                load(j, g, NI / 2);
             }
-            for (; j < cend; ++j, ++g) {
+            for (; j < t1; ++j, ++g) {
                 const int s = g % STAGES;
-                const uint32_t free_ph = (g / STAGES + 1) & 1;
-                Ring* ring = &sh->ring[g % RING];
-                wait(&sh->kfree[s], free_ph, &sh->fail);
-                if (ct < 8) {
-                    ring->ks[ct] = ks;
-                    scale_parts(vs, ring->lv[ct], ring->iv[ct]);
+                wait(&free_[s], (g / STAGES + 1) & 1, &sh->fail);
+                __syncwarp();
+                if (j < cend) {
+                    if (ct == 0) dt_mbar_arrive(&sh->scfull[g % RING]);
+                    const uint32_t o = s * L::TILE;
+                    const bool more = j + 1 < cend;
+                    if (more) wait(&sh->idfull[(g + 1) % RING], ((g + 1) / RING) & 1, &sh->fail);
+#pragma unroll
+                    for (int i0 = 0; i0 < NI; i0 += NI / 2) {
+#pragma unroll
+                        for (int i = i0; i < i0 + NI / 2; ++i)  // rows TPI apart, a multiple of 8, swizzle alike
+                            store_codes(a0 + o + i * (TPI * 128), a1 + o + i * (TPI * 128), q[i]);
+                        if (more) load(j + 1, g + 1, i0);
+                    }
+                } else {
+                    wait(&sh->idfull[g % RING], (g / RING) & 1, &sh->fail);  // the ring's slot is free
+                    fresh(a, u, (j - u.ctx) * AT_TILE, ct, sh, &sh->ring[g % RING], base + s * L::TILE);
+                    group_sync();
+                    if (ct == 0) dt_mbar_arrive(&sh->scfull[g % RING]);
                 }
-                dt_mbar_arrive(&sh->scfull[g % RING]);
-                store(kt + s * L::TILE, ct, kq);
-                dt_mbar_arrive(&sh->kfull[s]);
-                const bool more = j + 1 < cend;
-                if (more) {
-                    codes(a, u, a.c.k, lp, j + 1, ct, id, kq);
-                    scales(a, u, lp, j + 1, ct, ks, vs);
-                }
-                wait(&sh->vfree[s], free_ph, &sh->fail);
-                store(vt + s * L::TILE, ct, vq);
-                dt_mbar_arrive(&sh->vfull[s]);
-                if (more) {
-                    codes(a, u, a.c.v, lp, j + 1, ct, id, vq);
-                    if (j + 2 < cend) pages(a, u, lp, j + 2, ct, id);
-                }
-            }
-            for (; j < u.t1; ++j, ++g) {
-                const int s = g % STAGES;
-                const uint32_t free_ph = (g / STAGES + 1) & 1;
-                wait(&sh->kfree[s], free_ph, &sh->fail);  // and so the ring's slot
-                fresh(a, u, (j - u.r.ctx) * AT_TILE, ct, sh, &sh->ring[g % RING], kt + s * L::TILE, vt + s * L::TILE,
-                      s, free_ph, free_ph, &sh->scfull[g % RING]);
+                dt_fence_proxy_async_smem();
+                dt_mbar_arrive(&full[s]);
             }
         }
     }
 };
 
+// The warp that looks up pages and scales, four tiles at a time (eight lanes,
+// of 16 tokens each, to a tile), up to RING tiles ahead of their use, and asks
+// L2 for the codes.  A page id out of range is reported and reads another page.
+template <int D>
+DT_DI void look_up(const DtAttend& a, Shared* sh, int lane) {
+    const int lp = 31 - __clz(a.c.page), grp = lane & 7;
+    const uint32_t page_bytes = ((uint32_t)a.c.Hkv << lp) * D;
+    uint32_t g = 0, i = 0;
+    for (const Seg* sg; (sg = get_segment(sh, i)) != nullptr; release_segment(sh, i++)) {
+        const int t0 = sg->t0, nt = sg->t1 - t0, ctx = min(sg->t1, sg->ctx) - t0, len = sg->len, b = sg->b, h = sg->h;
+        const int* table = a.c.table + (size_t)b * a.c.max_pages;
+        for (int k = 0; k < nt; k += 4) {
+            const int t = k + (lane >> 3), tok = (t0 + t) * AT_TILE + grp * 16;
+            const bool in = t < ctx && tok < len;
+            uint32_t id = 0;
+            float ks = 1.f, vs = 1.f;
+            if (in) {
+                id = (uint32_t)table[tok >> lp];
+                if (id >= (uint32_t)a.c.n_pages) {
+                    atomicOr(&a.status[b], DT_DEV_BAD_CACHE);
+                    id = 0;
+                }
+                ks = a.c.k_scale[(size_t)id * a.c.Hkv + h];
+                vs = a.c.v_scale[(size_t)id * a.c.Hkv + h];
+                // the 16 tokens' codes: 16 D bytes of keys and of values
+                const size_t o = (size_t)id * page_bytes + ((size_t)h << lp) * D + (tok & (a.c.page - 1)) * D;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.k + o + c * 128));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.v + o + c * 128));
+                }
+            }
+            for (int d = 0; d < 4 && k + d < nt; ++d, ++g) {
+                wait(&sh->ringfree[g % RING], (g / RING + 1) & 1, &sh->fail);
+                if ((lane >> 3) == d && k + d < ctx) {
+                    Ring* ring = &sh->ring[g % RING];
+                    ring->id[grp] = id;
+                    ring->ks[grp] = ks;
+                    scale_parts(vs, ring->lv[grp], ring->iv[grp]);
+                }
+                __syncwarp();
+                if (lane == 0) dt_mbar_arrive(&sh->idfull[g % RING]);
+            }
+        }
+    }
+}
+
 // The MMA warp's one thread.
 template <int D>
-DT_DI void issue_all(const DtAttend& a, unsigned char* sm, Shared* sh, uint32_t tmem, int cta) {
+DT_DI void issue_all(unsigned char* sm, Shared* sh, uint32_t tmem) {
     using L = Lay<D>;
     constexpr uint32_t ID_S = dt_idesc_f16_f32(TQ, AT_TILE, false), ID_O = dt_idesc_f16_f32(TQ, D, true);
-    const uint32_t qb = dt_smem_addr(sm + L::Q), kb = dt_smem_addr(sm + L::K), vb = dt_smem_addr(sm + L::V);
-    AtWalk<ROWS, ATOM> u;
-    u.start(a, sh->share);
+    const uint32_t qd = dt_desc_lo(dt_smem_addr(sm + L::Q), 16), kd = dt_desc_lo(dt_smem_addr(sm + L::K), 16),
+                   vd = dt_desc_lo(dt_smem_addr(sm + L::V), L::HALF);
     uint32_t g0 = 0, seg = 0, pc[2] = {0u, 0u};
-    for (; u.next(a, sh->share, cta); u.step(a), ++seg) {
-        const bool dual = u.rows > TQ;  // two slots of rows; else two slots of tiles
-        const int nt = u.t1 - u.t0;
+    for (const Seg* u; (u = get_segment(sh, seg)) != nullptr; ++seg) {
+        const bool dual = u->rows > TQ;  // two slots of rows; else two slots of tiles
+        const int nt = u->t1 - u->t0;
+        release_segment(sh, seg);
         wait(&sh->qfull, seg & 1, &sh->fail);
         auto qk = [&](int s, int lt) {
             const uint32_t g = g0 + lt, st = g % STAGES;
             wait(&sh->kfull[st], (g / STAGES) & 1, &sh->fail);
             dt_tc_fence_after();
-            const uint32_t q = qb + (dual ? s : 0) * L::TILE, k = kb + st * L::TILE;
+            const uint32_t q = qd + (dual ? s : 0) * (L::TILE >> 4), k = kd + st * (L::TILE >> 4), d = tmem + s * AT_TILE;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t o = (kk >> 2) * L::HALF + (kk & 3) * 32;
-                dt_mma_bf16(tmem + s * AT_TILE, dt_desc_kmajor_sw128(q + o), dt_desc_kmajor_sw128(k + o), ID_S, kk > 0);
+                const uint32_t o = ((kk >> 2) * L::HALF + (kk & 3) * 32) >> 4;
+                dt_mma_ss_lo(d, q + o, k + o, ID_S, kk > 0);
             }
             dt_mma_commit(&sh->sfull[s]);
             if (!dual || s == 1) dt_mma_commit(&sh->kfree[st]);
@@ -328,27 +417,23 @@ DT_DI void issue_all(const DtAttend& a, unsigned char* sm, Shared* sh, uint32_t 
             wait(&sh->pfull[s], pc[s]++ & 1, &sh->fail);
             wait(&sh->vfull[st], (g / STAGES) & 1, &sh->fail);
             dt_tc_fence_after();
-            const uint32_t v = vb + st * L::TILE;
+            const uint32_t v = vd + st * (L::TILE >> 4), p = tmem + s * AT_TILE, d = tmem + 2 * AT_TILE + s * D;
 #pragma unroll
             for (int kk = 0; kk < AT_TILE / 16; ++kk)
-                dt_mma_f16_ts(tmem + 2 * AT_TILE + s * D, tmem + s * AT_TILE + kk * 8,
-                              dt_desc_mnmajor_sw128(v + kk * 2048, L::HALF), ID_O, !first || kk > 0);
-            if (!dual || s == 1) dt_mma_commit(&sh->vfree[st]);
+                dt_mma_ts_lo(d, p + kk * 8, v + kk * (2048 >> 4), ID_O, !first || kk > 0);
+            if (!dual || s == 1) {
+                dt_mma_commit(&sh->vfree[st]);
+                dt_mma_commit(&sh->ringfree[g % RING]);
+            }
             if (last) dt_mma_commit(&sh->ofull[s]);
         };
-        const int hop = dual ? 1 : 2;
-        qk(0, 0);
-        if (dual) qk(1, 0);
-        else if (nt > 1) qk(1, 1);
-        for (int lt = 0; lt < nt; lt += hop) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int t = dual ? lt : lt + s;
-                if (t < nt) {
-                    pv(s, t, lt == 0, t + hop >= nt);
-                    if (t + hop < nt) qk(s, t + hop);
-                }
-            }
+        // slot s = i & 1 step by step: its product with V, then its next scores
+        const int hop = dual ? 1 : 2, steps = dual ? 2 * nt : nt + (nt & 1);
+#pragma unroll 1
+        for (int i = -2; i < steps; ++i) {
+            const int s = i & 1, t = dual ? i >> 1 : i;  // i < 0: the tile before the slot's first
+            if (i >= 0 && t < nt) pv(s, t, i < 2, t + hop >= nt);
+            if (t + hop < nt) qk(s, t + hop);
         }
         g0 += nt;
     }
@@ -360,74 +445,186 @@ struct Soft {
     using L = Lay<D>;
 
     // The block's rows, rotated, scaled by a power of two and converted.
-    static DT_DI void queries(const DtAttend& a, const AtWalk<ROWS, ATOM>& u, unsigned char* sm, Shared* sh, int tid) {
-        constexpr int CPR = D / 8, RPI = NS / CPR;
-        const int G = a.Hq / a.c.Hkv;
+    static DT_DI void queries(const DtAttend& a, const Seg& u, unsigned char* sm, Shared* sh, int tid) {
+        constexpr int PPR = D / 16, RPI = NS / PPR, U = 2;  // chunk pairs per row, rows per pass
+        const uint32_t G = a.Hq / a.c.Hkv;
         const int tiles = u.rows > TQ ? 2 : 1;
         const uint32_t qb = dt_smem_addr(sm + L::Q);
-        const int c = tid % CPR;
-        for (int r = tid / CPR; r < tiles * TQ; r += RPI) {
-            float x[8] = {};
-            if (r < u.rows) {
-                const long long row = (long long)u.qb * ROWS + r;
-                const int n = (int)(row / G), h = u.h * G + (int)(row % G);
-                const uint16_t* p = (const uint16_t*)a.q.ptr + u.b * a.q.stride_b + n * a.q.stride_n + h * a.q.stride_h;
-                dt_rotated8(p, c, a.rope, at_position(a, u.b, u.r.len, n), x);
+        const int pr = tid % PPR;
+        int c0, c1;
+        dt_pair_chunks(pr, a.rope, c0, c1);
+        {
+            const uint32_t row = (uint32_t)u.qb * ROWS + min(tid, u.rows - 1), n = row / G;
+            sh->qpos[tid] = a.rope.rot ? at_position(a, u.b, u.len, (int)n) : 0;
+            sh->qoff[tid] = n * a.q.stride_n + (row % G) * a.q.stride_h;
+        }
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+        const uint16_t* base = (const uint16_t*)a.q.ptr + u.b * a.q.stride_b + (size_t)u.h * G * a.q.stride_h;
+#pragma unroll 1
+        for (int r0 = tid / PPR; r0 < tiles * TQ; r0 += U * RPI) {
+            float x[U][8], y[U][8];
+#pragma unroll
+            for (int k = 0; k < U; ++k)  // U rows in flight
+                dt_rotated_pair(base + sh->qoff[r0 + k * RPI], pr, a.rope, sh->qpos[r0 + k * RPI], x[k], y[k]);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int r = r0 + k * RPI;
+                uint32_t big = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (r >= u.rows) x[k][e] = y[k][e] = 0.f;
+                    big = max(big, max(__float_as_uint(x[k][e]) & 0x7FFFFFFFu, __float_as_uint(y[k][e]) & 0x7FFFFFFFu));
+                }
+#pragma unroll
+                for (int o = PPR / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+                int ex = (int)(big >> 23) - 127;  // largest magnitude in [2^ex, 2^(ex+1))
+                ex = big >= 0x7F800000u ? 0 : max(ex, -100);
+                const float f = dt_pow2(-ex);
+                uint32_t w[4], z[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = f16x2(__fmul_rn(x[k][2 * e], f), __fmul_rn(x[k][2 * e + 1], f));
+                    z[e] = f16x2(__fmul_rn(y[k][2 * e], f), __fmul_rn(y[k][2 * e + 1], f));
+                }
+                sts16(qb + (r / TQ) * L::TILE + chunk_at(r % TQ, c0), w);
+                sts16(qb + (r / TQ) * L::TILE + chunk_at(r % TQ, c1), z);
+                if (pr == 0) sh->qscale[r] = __fmul_rn(__fmul_rn(a.scale, LOG2E), dt_pow2(ex));
             }
-            uint32_t big = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) big = max(big, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-#pragma unroll
-            for (int o = CPR / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-            int ex = (int)(big >> 23) - 127;  // largest magnitude in [2^ex, 2^(ex+1))
-            ex = big >= 0x7F800000u ? 0 : max(ex, -100);
-            const float f = dt_pow2(-ex);
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = f16x2(__fmul_rn(x[2 * e], f), __fmul_rn(x[2 * e + 1], f));
-            sts16(qb + (r / TQ) * L::TILE + chunk_at(r % TQ, c), w);
-            if (c == 0) sh->qscale[r] = __fmul_rn(__fmul_rn(a.scale, LOG2E), dt_pow2(ex));
         }
         dt_fence_proxy_async_smem();
         dt_mbar_arrive(&sh->qfull);
     }
 
     // The row's mask words of a tile that is not wholly visible.
-    static DT_DI void mask_words(const DtAttend& a, const AtWalk<ROWS, ATOM>& u, int t, int row, uint32_t (&mk)[4]) {
+    static DT_DI void mask_words(const DtAttend& a, const Seg& u, int t, int row, uint32_t (&mk)[4]) {
         const int G = a.Hq / a.c.Hkv;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (t < u.r.ctx) {
-                const int left = u.r.len - t * AT_TILE - 32 * i;
+            if (t < u.ctx) {
+                const int left = u.len - t * AT_TILE - 32 * i;
                 mk[i] = left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
             } else {
-                const long long rr = (long long)u.qb * ROWS + row;
-                mk[i] = row < u.rows ? at_mask_word(a, u.b, (int)(rr / G), (t - u.r.ctx) * AT_TILE + 32 * i, u.r.n) : 0u;
+                const uint32_t node = ((uint32_t)u.qb * ROWS + row) / (uint32_t)G;
+                mk[i] = row < u.rows ? at_mask_word(a, u.b, (int)node, (t - u.ctx) * AT_TILE + 32 * i, u.n) : 0u;
             }
         }
     }
+    template <bool MASKED>
+    static DT_DI void blank(uint32_t (&x)[64], uint32_t lo, uint32_t hi) {
+        if constexpr (MASKED) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+                if (!(((i < 32 ? lo : hi) >> (i & 31)) & 1)) x[i] = 0xFF800000u;  // -infinity
+        }
+    }
 
-    static DT_DI void run(const DtAttend& a, unsigned char* sm, Shared* sh, uint32_t tmem, int tid, int cta, int ctas,
+    // One tile of a row: its scores at ts become probabilities in place, the
+    // running reference m and sum l move on, and O is rescaled when it has sums.
+    // The two halves of a tile share their code: five roles share the
+    // instruction cache.
+    template <bool MASKED>
+    static DT_DI void tile(const Ring* ring, uint32_t ts, uint32_t to, bool has_o, float rowc, const uint32_t (&mk)[4],
+                           float& m, float& l) {
+        const float NEG_INF = -__int_as_float(0x7F800000);
+        uint32_t x[64];
+        // pass 1: the largest score + log2 of its value scale
+        float mx = NEG_INF;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+            dt_tmem_ld64(ts + 64 * c, x);
+            blank<MASKED>(x, c ? mk[2] : mk[0], c ? mk[3] : mk[1]);
+            const float4 ks = *(const float4*)(ring->ks + 4 * c), lv = *(const float4*)(ring->lv + 4 * c);
+            const float k4[4] = {ks.x, ks.y, ks.z, ks.w}, l4[4] = {lv.x, lv.y, lv.z, lv.w};
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                float q0 = __uint_as_float(x[16 * h]), q1 = __uint_as_float(x[16 * h + 1]);
+#pragma unroll
+                for (int i = 2; i < 14; i += 4) {
+                    q0 = max3(q0, __uint_as_float(x[16 * h + i]), __uint_as_float(x[16 * h + i + 1]));
+                    q1 = max3(q1, __uint_as_float(x[16 * h + i + 2]), __uint_as_float(x[16 * h + i + 3]));
+                }
+                q0 = max3(q0, __uint_as_float(x[16 * h + 14]), __uint_as_float(x[16 * h + 15]));
+                mx = fmaxf(mx, __fmaf_rn(fmaxf(q0, q1), __fmul_rn(rowc, k4[h]), l4[h]));
+            }
+        }
+        // a maximum that has grown moves the reference; rows of a warp do so together
+        const bool grown = mx > m + (HEADROOM + LAZY);
+        if (__any_sync(0xffffffffu, grown)) {
+            const float to_m = grown ? mx - HEADROOM : m;
+            const float f = grown ? dt_ex2_approx(m - to_m) : 1.f;  // m = -inf: 0
+            m = to_m;
+            l = __fmul_rn(l, f);
+            if (has_o) {
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t o[16];
+                    dt_tmem_ld16_async(to + 16 * c, o);
+                    dt_tmem_ld_wait(o);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__fmul_rn(__uint_as_float(o[i]), f));
+                    dt_tmem_st16(to + 16 * c, o);
+                }
+                dt_tmem_st_wait();
+            }
+        }
+        const float mu = m == NEG_INF ? 0.f : m;
+        // pass 2: probabilities, over the columns already read
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+            dt_tmem_ld64(ts + 64 * c, x);
+            blank<MASKED>(x, c ? mk[2] : mk[0], c ? mk[3] : mk[1]);
+            const float4 ks = *(const float4*)(ring->ks + 4 * c), lv = *(const float4*)(ring->lv + 4 * c),
+                         iv = *(const float4*)(ring->iv + 4 * c);
+            const float k4[4] = {ks.x, ks.y, ks.z, ks.w}, l4[4] = {lv.x, lv.y, lv.z, lv.w},
+                        i4[4] = {iv.x, iv.y, iv.z, iv.w};
+#pragma unroll
+            for (int h = 0; h < 4; h += 2) {
+                uint32_t p[16];
+#pragma unroll
+                for (int g = h; g < h + 2; ++g) {
+                    const float ka = __fmul_rn(rowc, k4[g]), kb = __fsub_rn(l4[g], mu);
+                    const unsigned long long ka2 = dt_f2_pack(ka, ka), kb2 = dt_f2_pack(kb, kb);
+                    unsigned long long sum = dt_f2_pack(0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        float e0, e1;
+                        dt_f2_unpack(dt_f2_fma(dt_f2_pack(__uint_as_float(x[16 * g + i]), __uint_as_float(x[16 * g + i + 1])),
+                                               ka2, kb2), e0, e1);
+                        e0 = dt_ex2_approx(e0);
+                        e1 = dt_ex2_approx(e1);
+                        sum = dt_f2_add(sum, dt_f2_pack(e0, e1));
+                        p[8 * (g - h) + i / 2] = f16x2(e0, e1);
+                    }
+                    float s0, s1;
+                    dt_f2_unpack(sum, s0, s1);
+                    l = __fmaf_rn(__fadd_rn(s0, s1), i4[g], l);
+                }
+                dt_tmem_st16(ts + 32 * c + 8 * h, p);
+            }
+        }
+        dt_tmem_st_wait();
+    }
+
+    static DT_DI void run(const DtAttend& a, unsigned char* sm, Shared* sh, uint32_t tmem, int tid, int cta,
                           float* part, int* counters) {
         const int s = tid / TQ, w4 = (tid >> 5) & 3;
         const float NEG_INF = -__int_as_float(0x7F800000);
         const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
         const uint32_t ts = tmem + s * AT_TILE + lanes, to = tmem + 2 * AT_TILE + s * D + lanes;
-        AtWalk<ROWS, ATOM> u;
-        u.start(a, sh->share);
-        uint32_t g0 = 0, seg = 0, sc = 0, oc = 0;
-        for (; u.next(a, sh->share, cta); u.step(a), ++seg) {
-            const bool dual = u.rows > TQ;
-            const int nt = u.t1 - u.t0;
-            const int row = dual ? tid : tid % TQ;  // within the block
+        uint32_t g0 = 0, sc = 0, oc = 0, seg = 0;
+        for (const Seg* sg; (sg = get_segment(sh, seg)) != nullptr; release_segment(sh, seg++)) {
+            const Seg& u = *sg;
             // every product of the last segment has read its queries
             asm volatile("bar.sync 2, 256;" ::: "memory");
+            const bool dual = u.rows > TQ;
+            const int nt = u.t1 - u.t0, hop = dual ? 1 : 2, len = u.len;
+            const int row = dual ? tid : tid % TQ;  // within the block
             queries(a, u, sm, sh, tid);
             asm volatile("bar.sync 2, 256;" ::: "memory");
             const float rowc = sh->qscale[row];
             float m = NEG_INF, l = 0.f;
             bool poison = false;
-            for (int lt = dual ? 0 : s; lt < nt; lt += dual ? 1 : 2) {
+            for (int lt = dual ? 0 : s; lt < nt; lt += hop) {
                 const uint32_t g = g0 + lt;
                 const Ring* ring = &sh->ring[g % RING];
                 wait(&sh->sfull[s], sc++ & 1, &sh->fail);
@@ -435,93 +632,17 @@ struct Soft {
                 __syncwarp();
                 dt_tc_fence_after();
                 const int t = u.t0 + lt;
-                const bool masked = (t + 1) * AT_TILE > u.r.len;
-                uint32_t mk[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-                if (masked) {
+                uint32_t mk[4];
+                if ((t + 1) * AT_TILE > len) {
                     mask_words(a, u, t, row, mk);
-                    if (t >= u.r.ctx) {
+                    if (t >= u.ctx) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) poison |= (mk[i] & ring->bad[i]) != 0u;
+                        for (int i = 0; i < 4; ++i) poison |= (mk[i] & (ring->bad[0][i] | ring->bad[1][i])) != 0u;
                     }
+                    tile<true>(ring, ts, to, lt >= hop, rowc, mk, m, l);
+                } else {
+                    tile<false>(ring, ts, to, lt >= hop, rowc, mk, m, l);
                 }
-                // pass 1: the largest score
-                float mx = NEG_INF;
-                uint32_t v[2][32];
-                dt_tmem_ld32_async(ts, v[0]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    dt_tmem_ld_wait(v[c & 1]);
-                    if (c < 3) dt_tmem_ld32_async(ts + 32 * (c + 1), v[(c + 1) & 1]);
-                    uint32_t(&x)[32] = v[c & 1];
-                    if (masked) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!((mk[c] >> i) & 1)) x[i] = __float_as_uint(NEG_INF);
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float q = __uint_as_float(x[16 * h]);
-#pragma unroll
-                        for (int i = 1; i < 15; i += 2)
-                            q = max3(q, __uint_as_float(x[16 * h + i]), __uint_as_float(x[16 * h + i + 1]));
-                        q = fmaxf(q, __uint_as_float(x[16 * h + 15]));
-                        mx = fmaxf(mx, __fmaf_rn(q, __fmul_rn(rowc, ring->ks[2 * c + h]), ring->lv[2 * c + h]));
-                    }
-                }
-                // a maximum that has grown moves the reference; rows of a warp do so together
-                const bool grown = mx > m + (HEADROOM + LAZY);
-                if (__any_sync(0xffffffffu, grown)) {
-                    const float to_m = grown ? mx - HEADROOM : m;
-                    const float f = grown ? dt_ex2_approx(m - to_m) : 1.f;  // m = -inf: 0
-                    m = to_m;
-                    l = __fmul_rn(l, f);
-                    if (lt >= (dual ? 1 : 2)) {  // there is something in O
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            dt_tmem_ld32_async(to + 32 * c, v[0]);
-                            dt_tmem_ld_wait(v[0]);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[0][i] = __float_as_uint(__fmul_rn(__uint_as_float(v[0][i]), f));
-                            dt_tmem_st32(to + 32 * c, v[0]);
-                        }
-                    }
-                }
-                const float mu = m == NEG_INF ? 0.f : m;
-                // pass 2: probabilities, over the columns already read
-                dt_tmem_ld32_async(ts, v[0]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    dt_tmem_ld_wait(v[c & 1]);
-                    if (c < 3) dt_tmem_ld32_async(ts + 32 * (c + 1), v[(c + 1) & 1]);
-                    uint32_t(&x)[32] = v[c & 1];
-                    if (masked) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!((mk[c] >> i) & 1)) x[i] = __float_as_uint(NEG_INF);
-                    }
-                    uint32_t p[16];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float ka = __fmul_rn(rowc, ring->ks[2 * c + h]), kb = __fsub_rn(ring->lv[2 * c + h], mu);
-                        const unsigned long long ka2 = dt_f2_pack(ka, ka), kb2 = dt_f2_pack(kb, kb);
-                        unsigned long long sum = dt_f2_pack(0.f, 0.f);
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            float e0, e1;
-                            dt_f2_unpack(dt_f2_fma(dt_f2_pack(__uint_as_float(x[16 * h + i]), __uint_as_float(x[16 * h + i + 1])),
-                                                   ka2, kb2), e0, e1);
-                            e0 = dt_ex2_approx(e0);
-                            e1 = dt_ex2_approx(e1);
-                            sum = dt_f2_add(sum, dt_f2_pack(e0, e1));
-                            p[8 * h + i / 2] = f16x2(e0, e1);
-                        }
-                        float s0, s1;
-                        dt_f2_unpack(sum, s0, s1);
-                        l = __fmaf_rn(__fadd_rn(s0, s1), ring->iv[2 * c + h], l);
-                    }
-                    dt_tmem_st16(ts + 16 * c, p);
-                }
-                dt_tmem_st_wait();
                 dt_tc_fence_before();
                 dt_mbar_arrive(&sh->pfull[s]);
             }
@@ -545,14 +666,14 @@ struct Soft {
                     sh->mrg_l[row] = l;
                     if (any) {
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t v[32];
-                            dt_tmem_ld32_async(to + 32 * c, v);
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t v[16];
+                            dt_tmem_ld16_async(to + 16 * c, v);
                             dt_tmem_ld_wait(v);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
+                            for (int i = 0; i < 4; ++i) {
                                 const uint32_t q[4] = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-                                sts16(xb + (((8 * c + i) ^ (row & 7)) << 4), q);
+                                sts16(xb + (((4 * c + i) ^ (row & 7)) << 4), q);
                             }
                         }
                     }
@@ -570,51 +691,40 @@ struct Soft {
             if (dual || s == 0) {
                 const float inv = l == 0.f ? 0.f : 1.0f / l;
                 const float w0 = whole ? __fmul_rn(f0, inv) : f0, w1 = whole ? __fmul_rn(f1, inv) : f1;
-                const int G = a.Hq / a.c.Hkv;
-                const long long rr = (long long)u.qb * ROWS + row;
-                uint16_t* out = (uint16_t*)a.out + (((size_t)u.b * a.M + rr / G) * a.Hq + u.h * G + rr % G) * D;
+                uint16_t* out = out_row(a, u, row);
                 if (!whole) {
                     my[row] = m;
                     my[ROWS + row] = l;
                 }
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t v[32];
-                    dt_tmem_ld32_async(to + 32 * c, v);
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t v[16];
+                    dt_tmem_ld16_async(to + 16 * c, v);
                     dt_tmem_ld_wait(v);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
                         if (!dual && nt > 1) {
-                            const uint32_t ad = xb + (((8 * c + i) ^ (row & 7)) << 4);
+                            const uint32_t ad = xb + (((4 * c + i) ^ (row & 7)) << 4);
                             asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                                          : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w) : "r"(ad));
                         }
-                        float x[4];
-                        x[0] = __fmaf_rn(__uint_as_float(v[4 * i]), w0, __fmul_rn(y.x, w1));
-                        x[1] = __fmaf_rn(__uint_as_float(v[4 * i + 1]), w0, __fmul_rn(y.y, w1));
-                        x[2] = __fmaf_rn(__uint_as_float(v[4 * i + 2]), w0, __fmul_rn(y.z, w1));
-                        x[3] = __fmaf_rn(__uint_as_float(v[4 * i + 3]), w0, __fmul_rn(y.w, w1));
+                        const float z[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) v[4 * i + e] = __float_as_uint(x[e]);
+                        for (int e = 0; e < 4; ++e)
+                            v[4 * i + e] = __float_as_uint(__fmaf_rn(__uint_as_float(v[4 * i + e]), w0, __fmul_rn(z[e], w1)));
                     }
                     if (row < u.rows) {
                         if (whole) {
+                            uint32_t o[8];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t o[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * e]),
-                                                                                    __uint_as_float(v[8 * i + 2 * e + 1]));
-                                    o[e] = *(const uint32_t*)&b2;
-                                }
-                                *(uint4*)(out + 32 * c + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
-                            }
+                            for (int e = 0; e < 8; ++e) o[e] = bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+                            *(uint4*)(out + 16 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *(uint4*)(out + 16 * c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                *(uint4*)(my + 2 * ROWS + (size_t)row * D + 32 * c + 4 * i) =
+                            for (int i = 0; i < 4; ++i)
+                                *(uint4*)(my + 2 * ROWS + (size_t)row * D + 16 * c + 4 * i) =
                                     make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                         }
                     }
@@ -632,41 +742,72 @@ struct Soft {
                     __threadfence();
                 }
                 asm volatile("bar.sync 2, 256;" ::: "memory");
-                if (sh->last) join(a, u, part, tid);
+                if (sh->last) join(a, sm, u, part, tid);
             }
         }
     }
 
-    static DT_DI void join(const DtAttend& a, const AtWalk<ROWS, ATOM>& u, const float* part, int tid) {
-        constexpr int CPR = D / 8, RPI = NS / CPR;  // 8 columns per thread
+    static DT_DI uint16_t* out_row(const DtAttend& a, const Seg& u, int r) {
+        const uint32_t G = a.Hq / a.c.Hkv, rr = (uint32_t)u.qb * ROWS + r;
+        return (uint16_t*)a.out + (((size_t)u.b * a.M + rr / G) * a.Hq + u.h * G + rr % G) * D;
+    }
+
+    // Joins the parts of a unit: O = sum O_i 2^(m_i - M), l likewise.  The
+    // weights go to shared memory (the query tiles) first, P parts at a time,
+    // so that the loads of a row's parts do not wait on each other.
+    static DT_DI void join(const DtAttend& a, unsigned char* sm, const Seg& u, float* part, int tid) {
+        constexpr int CPR = D / 8, RPI = NS / CPR, P = 16;  // 8 columns per thread
         const float NEG_INF = -__int_as_float(0x7F800000);
-        const int G = a.Hq / a.c.Hkv, c = tid % CPR;
-        auto slot = [&](int i) { return part + (size_t)(2 * (u.first + i) + (i == 0)) * ROWS * (D + 2); };
-        for (int r = tid / CPR; r < u.rows; r += RPI) {
-            float M = NEG_INF, l = 0.f, x[8] = {};
-            for (int i = 0; i < u.segs; ++i) M = fmaxf(M, __ldcg(slot(i) + r));
-            for (int i = 0; i < u.segs; ++i) {
-                const float* p = slot(i);
-                const float mi = __ldcg(p + r);
-                const float f = mi == NEG_INF ? 0.f : dt_ex2_approx(mi - M);
-                l = __fmaf_rn(__ldcg(p + ROWS + r), f, l);
-                const float4* o = (const float4*)(p + 2 * ROWS + (size_t)r * D + 8 * c);
-                const float4 y = __ldcg(o), z = __ldcg(o + 1);
-                x[0] = __fmaf_rn(y.x, f, x[0]), x[1] = __fmaf_rn(y.y, f, x[1]);
-                x[2] = __fmaf_rn(y.z, f, x[2]), x[3] = __fmaf_rn(y.w, f, x[3]);
-                x[4] = __fmaf_rn(z.x, f, x[4]), x[5] = __fmaf_rn(z.y, f, x[5]);
-                x[6] = __fmaf_rn(z.z, f, x[6]), x[7] = __fmaf_rn(z.w, f, x[7]);
+        const int c = tid % CPR, first = u.first, segs = u.segs, rows = u.rows;
+        float* wt = (float*)(sm + L::Q);  // [P][ROWS]
+        auto slot = [&](int i) { return part + (size_t)(2 * (first + i) + (i == 0)) * ROWS * (D + 2); };
+        float M = NEG_INF, l = 0.f;  // of row tid
+        if (tid < rows) {
+#pragma unroll 4
+            for (int i = 0; i < segs; ++i) M = fmaxf(M, __ldcg(slot(i) + tid));
+#pragma unroll 4
+            for (int i = 0; i < segs; ++i) {
+                const float mi = __ldcg(slot(i) + tid);
+                l = __fmaf_rn(__ldcg(slot(i) + ROWS + tid), mi == NEG_INF ? 0.f : dt_ex2_approx(mi - M), l);
             }
-            const float inv = l == 0.f ? 0.f : 1.0f / l;
-            const long long rr = (long long)u.qb * ROWS + r;
-            uint16_t* out = (uint16_t*)a.out + (((size_t)u.b * a.M + rr / G) * a.Hq + u.h * G + rr % G) * D + 8 * c;
-            uint32_t o[4];
+        }
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        for (int i0 = 0; i0 < segs; i0 += P) {
+            // weight of part i for each row, 1 / l included; past the last part 0
+            asm volatile("bar.sync 2, 256;" ::: "memory");
+            for (int i = 0; i < P; ++i) {
+                const float mi = tid < rows && i0 + i < segs ? __ldcg(slot(i0 + i) + tid) : NEG_INF;
+                wt[i * ROWS + tid] = mi == NEG_INF ? 0.f : __fmul_rn(dt_ex2_approx(mi - M), inv);
+            }
+            asm volatile("bar.sync 2, 256;" ::: "memory");
+            const int np = min(P, segs - i0);
+            for (int r = tid / CPR; r < rows; r += RPI) {
+                float x[8] = {};
+                float4* acc = (float4*)(slot(0) + 2 * ROWS + (size_t)r * D + 8 * c);  // this thread's, read already
+                if (i0 > 0) {
+                    const float4 y = acc[0], z = acc[1];
+                    x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w, x[4] = z.x, x[5] = z.y, x[6] = z.z, x[7] = z.w;
+                }
+#pragma unroll 4
+                for (int i = 0; i < np; ++i) {
+                    const float4* o = (const float4*)(slot(i0 + i) + 2 * ROWS + (size_t)r * D + 8 * c);
+                    const float4 y = __ldcg(o), z = __ldcg(o + 1);
+                    const float f = wt[i * ROWS + r];
+                    x[0] = __fmaf_rn(y.x, f, x[0]), x[1] = __fmaf_rn(y.y, f, x[1]);
+                    x[2] = __fmaf_rn(y.z, f, x[2]), x[3] = __fmaf_rn(y.w, f, x[3]);
+                    x[4] = __fmaf_rn(z.x, f, x[4]), x[5] = __fmaf_rn(z.y, f, x[5]);
+                    x[6] = __fmaf_rn(z.z, f, x[6]), x[7] = __fmaf_rn(z.w, f, x[7]);
+                }
+                if (i0 + P < segs) {
+                    acc[0] = make_float4(x[0], x[1], x[2], x[3]);
+                    acc[1] = make_float4(x[4], x[5], x[6], x[7]);
+                } else {
+                    uint32_t o[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(__fmul_rn(x[2 * e], inv), __fmul_rn(x[2 * e + 1], inv));
-                o[e] = *(const uint32_t*)&b2;
+                    for (int e = 0; e < 4; ++e) o[e] = bf16x2(x[2 * e], x[2 * e + 1]);
+                    *(uint4*)(out_row(a, u, r) + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
             }
-            *(uint4*)out = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 };
@@ -692,7 +833,15 @@ __global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtA
             dt_mbar_init(&sh->pfull[i], TQ);
             dt_mbar_init(&sh->ofull[i], 1);
         }
-        for (int i = 0; i < RING; ++i) dt_mbar_init(&sh->scfull[i], NC);
+        for (int i = 0; i < RING; ++i) {
+            dt_mbar_init(&sh->scfull[i], 2);
+            dt_mbar_init(&sh->idfull[i], 1);
+            dt_mbar_init(&sh->ringfree[i], 1);
+        }
+        for (int i = 0; i < SEGS; ++i) {
+            dt_mbar_init(&sh->segfull[i], 1);
+            dt_mbar_init(&sh->segfree[i], NS + 2 * NC + 1 + 32);
+        }
         dt_mbar_init(&sh->qfull, NS);
         dt_fence_mbar_init();
         sh->fail = 0;
@@ -705,12 +854,20 @@ __global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtA
     dt_tc_fence_after();
     const uint32_t tmem = sh->tmem;
     if (tid < NS) {
+        set_regs<REG_SOFT>();
         at_zero_rest(a, cta, ctas, tid, NS);
-        Soft<D>::run(a, sm, sh, tmem, tid, cta, ctas, part, counters);
+        Soft<D>::run(a, sm, sh, tmem, tid, cta, part, counters);
     } else if (tid < NS + NC) {
-        Conv<D>::run(a, sm, sh, tid - NS, cta);
-    } else if (tid == NS + NC) {
-        issue_all<D>(a, sm, sh, tmem, cta);
+        set_regs<REG_CONV>();
+        Conv<D, true>::run(a, sm, sh, tid - NS);
+    } else if (tid < NS + 2 * NC) {
+        set_regs<REG_CONV>();
+        Conv<D, false>::run(a, sm, sh, tid - NS - NC);
+    } else {
+        set_regs<REG_MMA>();
+        if (tid == NS + 2 * NC) issue_all<D>(sm, sh, tmem);
+        if (tid == NS + 2 * NC + 32) walk_share(a, sh, cta);
+        if (wid == (NS + 2 * NC) / 32 + 2) look_up<D>(a, sh, tid & 31);
     }
     dt_tc_fence_before();
     __syncthreads();
