@@ -94,14 +94,18 @@ dt_status dt_tree_attention(const dt_kv_cache* c, const dt_rope* rope, int32_t b
     if ((s = check_rope(rope, c->D)) != DT_OK) return s;
     if (M < 1 || Hq < 1 || Hq % c->Hkv != 0) return DT_ERR_INVALID_ARG;
     if (Hq / c->Hkv > 128 || Hq > 65535 || M > (1 << 20)) return DT_ERR_UNSUPPORTED;
+    // the work division counts tiles in 32 bits
+    const long long rows = (long long)M * (Hq / c->Hkv);
+    const double tiles = (double)c->max_pages * c->page / 128 + M / 128 + 2;
+    if ((double)batch * c->Hkv * (rows / 256 + 1) * tiles * 5 > 4.2e9) return DT_ERR_UNSUPPORTED;
     if (!rows_ok(q, 2) || !rows_ok(k, 2) || !rows_ok(v, 2)) return DT_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !std::isfinite(scale)) return DT_ERR_INVALID_ARG;
     if (!out || !aligned16(out) || !status) return DT_ERR_INVALID_ARG;
     const size_t need = dt_tree_attention_workspace(c, batch, M, Hq);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return DT_ERR_INVALID_ARG;
     const dt_rope none = {nullptr, nullptr, 0, 0, 0};
-    const DtAttend a{*c, rope ? *rope : none, batch, M, Hq, *q, *k, *v, mask, pos, n_nodes, scale, out, status};
-    if ((long long)M * (Hq / c->Hkv) <= kStreamRows) return cuda_status(dt_kn11_launch(a, (cudaStream_t)stream));
+    const DtAttend a{*c, rope ? *rope : none, batch, M, Hq, Hq / c->Hkv, *q, *k, *v, mask, pos, n_nodes, scale, out, status};
+    if (rows <= kStreamRows) return cuda_status(dt_kn11_launch(a, (cudaStream_t)stream));
     return cuda_status(dt_kn12_launch(a, workspace, sm_count(), (cudaStream_t)stream));
 }
 

@@ -24,97 +24,91 @@ struct AtReq {  // one request
 
 template <int ROWS>
 struct AtPlan {
-    // Cost of a tile of a block: blocks of more than half the rows cost two.
-    static DT_DI int weight(int rows) { return 1; }
+    // Cost of a tile of a block: a block of at most half the rows costs less.
+    static constexpr uint32_t FULL = 5, PART = 3;
+    static DT_DI uint32_t weight(int rows) { return rows > ROWS / 2 ? FULL : PART; }
     static DT_DI AtReq req(const DtAttend& a, int b) {
         AtReq r;
         const int len = a.c.len[b], n = a.n_nodes ? a.n_nodes[b] : a.M;
-        r.bad = len < 0 || (long long)len > (long long)a.c.max_pages * a.c.page || n < 0 || n > a.M;
+        r.bad = len < 0 || len > a.c.max_pages * a.c.page || n < 0 || n > a.M;
         r.len = r.bad ? 0 : len;
         r.n = r.bad ? 0 : n;
         r.ctx = (r.len + AT_TILE - 1) / AT_TILE;
-        r.nqb = (int)(((long long)r.n * (a.Hq / a.c.Hkv) + ROWS - 1) / ROWS);
+        r.nqb = (r.n * a.G + ROWS - 1) / ROWS;
         return r;
     }
-    static DT_DI int block_rows(const DtAttend& a, const AtReq& r, int qb) {
-        const long long left = (long long)r.n * (a.Hq / a.c.Hkv) - (long long)qb * ROWS;
-        return left < ROWS ? (int)left : ROWS;
-    }
+    static DT_DI int block_rows(const DtAttend& a, const AtReq& r, int qb) { return min(r.n * a.G - qb * ROWS, ROWS); }
     // New rows that block qb can see: all of them, or up to its last node in a chain.
     static DT_DI int block_new(const DtAttend& a, const AtReq& r, int qb) {
-        if (a.mask) return r.n;
-        const int G = a.Hq / a.c.Hkv;
-        const long long last = ((long long)(qb + 1) * ROWS - 1) / G + 1;
-        return last < r.n ? (int)last : r.n;
+        return a.mask ? r.n : min(((qb + 1) * ROWS - 1) / a.G + 1, r.n);
     }
     static DT_DI int block_tiles(const DtAttend& a, const AtReq& r, int qb) {
         return r.ctx + (block_new(a, r, qb) + AT_TILE - 1) / AT_TILE;
     }
-    static DT_DI long long cost(const DtAttend& a, const AtReq& r) {
+    static DT_DI uint32_t cost(const DtAttend& a, const AtReq& r) {
         if (r.nqb == 0) return 0;
-        long long s = 0;
+        uint32_t s = block_tiles(a, r, r.nqb - 1) * weight(block_rows(a, r, r.nqb - 1));
         if (a.mask) {
-            const long long t = block_tiles(a, r, 0);
-            s = t * (weight(ROWS) * (r.nqb - 1) + weight(block_rows(a, r, r.nqb - 1)));
+            s += (r.nqb - 1) * block_tiles(a, r, 0) * FULL;
         } else {
-            for (int qb = 0; qb < r.nqb; ++qb) s += (long long)block_tiles(a, r, qb) * weight(block_rows(a, r, qb));
+#pragma unroll 1
+            for (int qb = 0; qb < r.nqb - 1; ++qb) s += block_tiles(a, r, qb) * FULL;
         }
         return s * a.c.Hkv;
     }
 };
 
-// The division's result in shared memory: the total cost, the CTAs that work,
-// and where this CTA's share begins (request, and that request's first cost).
+// The division's result in shared memory: `ctas` CTAs work; the first `rest` of
+// them take each + 1, the others `each`; this CTA's share is [beg, end) and
+// begins in request b0, whose own cost begins at b0_at.
 struct AtShare {
-    long long total, beg, end, b0_at;
+    uint32_t beg, end, b0_at, each, rest;
     int ctas, b0;
+    DT_DI uint32_t start_of(uint32_t c) const { return c * each + min(c, rest); }
+    DT_DI int owner(uint32_t x) const {  // of cost position x
+        const uint32_t wide = rest * (each + 1);
+        return (int)(x < wide ? x / (each + 1) : rest + (x - wide) / each);
+    }
 };
 
 // One warp: the share of CTA c of grid.  min_share: least cost worth a CTA.
 template <int ROWS>
-DT_DI void at_share(const DtAttend& a, int c, int grid, int min_share, AtShare* sh) {
+DT_DI void at_share(const DtAttend& a, uint32_t c, uint32_t grid, uint32_t min_share, AtShare* sh) {
     using P = AtPlan<ROWS>;
     const int lane = threadIdx.x & 31;
-    long long total = 0;
+    uint32_t total = 0;
+#pragma unroll 1
     for (int b = lane; b < a.batch; b += 32) {
         const AtReq r = P::req(a, b);
         if (r.bad && c == 0) atomicOr(&a.status[b], DT_DEV_BAD_CACHE);
         total += P::cost(a, r);
     }
-    total = (long long)dt_warp_sum_u64((unsigned long long)total);
-    long long g = total / min_share;
-    g = g < 1 ? 1 : g > grid ? grid : g;
-    const long long beg = c < g ? total * c / g : total, end = c < g ? total * (c + 1) / g : total;
+    total = __reduce_add_sync(0xffffffffu, total);
+    AtShare s;
+    s.ctas = (int)max(1u, min(total / min_share, grid));
+    s.each = total / s.ctas;
+    s.rest = total % s.ctas;
+    s.beg = c < s.ctas ? s.start_of(c) : total;
+    s.end = c < s.ctas ? s.start_of(c + 1) : total;
     // the request that holds position beg
-    long long at = 0;
-    int b0 = a.batch;
-    long long b0_at = total;
-    for (int base = 0; base < a.batch && beg < end; base += 32) {
+    s.b0 = a.batch;
+    s.b0_at = total;
+    uint32_t at = 0;
+#pragma unroll 1
+    for (int base = 0; base < a.batch && s.beg < s.end; base += 32) {
         const int b = base + lane;
-        const long long mine = b < a.batch ? P::cost(a, P::req(a, b)) : 0;
-        long long inc = mine;
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += t;
-        }
-        const bool hit = at + inc > beg;
-        const unsigned m = __ballot_sync(0xffffffffu, hit);
+        const uint32_t mine = b < a.batch ? P::cost(a, P::req(a, b)) : 0;
+        const uint32_t inc = (uint32_t)dt_warp_incl_scan((int)mine);
+        const unsigned m = __ballot_sync(0xffffffffu, at + inc > s.beg);
         if (m) {
             const int l = __ffs(m) - 1;
-            b0 = base + l;
-            b0_at = at + __shfl_sync(0xffffffffu, inc - mine, l);
+            s.b0 = base + l;
+            s.b0_at = at + __shfl_sync(0xffffffffu, inc - mine, l);
             break;
         }
         at += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (lane == 0) {
-        sh->total = total;
-        sh->beg = beg;
-        sh->end = end;
-        sh->ctas = (int)g;
-        sh->b0 = b0;
-        sh->b0_at = b0_at;
-    }
+    if (lane == 0) *sh = s;
 }
 
 // Walks a CTA's segments: the tiles [t0, t1) of one unit each.
@@ -123,8 +117,8 @@ struct AtWalk {
     using P = AtPlan<ROWS>;
     int b, qb, h;       // the unit
     AtReq r;
-    int rows, nt, w;    // its rows, tiles and tile cost
-    long long at;       // its first cost position
+    int rows, nt;       // its rows and tiles
+    uint32_t w, at;     // its tile cost and first cost position
     int t0, t1;         // this CTA's tiles of it
     int first, segs;    // the CTA that holds tile 0, and how many CTAs share it
 
@@ -137,34 +131,32 @@ struct AtWalk {
         b = s.b0;
         qb = h = 0;
         at = s.b0_at;
-        t1 = 0;
         if (b >= a.batch) return;
         r = P::req(a, b);
         unit(a);
-        // whole units before the share (blocks hold Hkv units of one cost)
-        while (at + (long long)a.c.Hkv * nt * w <= s.beg) {
-            at += (long long)a.c.Hkv * nt * w;
+        // whole blocks before the share (Hkv units of one cost each)
+#pragma unroll 1
+        while (at + a.c.Hkv * nt * w <= s.beg) {
+            at += a.c.Hkv * nt * w;
             ++qb;
             unit(a);
         }
-        h = (int)((s.beg - at) / ((long long)nt * w));
-        at += (long long)h * nt * w;
+        h = (int)((s.beg - at) / (nt * w));
+        at += h * nt * w;
     }
-    static DT_DI int owner(const AtShare& s, long long x) { return (int)(((x + 1) * s.ctas - 1) / s.total); }
     // The next segment, or false.  A unit of at most ATOM tiles is not split.
     DT_DI bool next(const DtAttend& a, const AtShare& s, int c) {
+#pragma unroll 1
         while (b < a.batch && at < s.end) {
+            first = s.owner(at);
             if (nt <= ATOM) {
-                first = owner(s, at);
                 segs = 1;
                 t0 = 0;
                 t1 = first == c ? nt : 0;
             } else {
-                const long long lo = s.beg - at, hi = s.end - at;
-                t0 = lo <= 0 ? 0 : (int)((lo + w - 1) / w);
-                t1 = (hi + w - 1) / w < nt ? (int)((hi + w - 1) / w) : nt;
-                first = owner(s, at);
-                segs = owner(s, at + (long long)w * (nt - 1)) - first + 1;
+                t0 = s.beg <= at ? 0 : (int)((s.beg - at + w - 1) / w);
+                t1 = (int)min((s.end - at + w - 1) / w, (uint32_t)nt);
+                segs = s.owner(at + w * (nt - 1)) - first + 1;
             }
             if (t1 > t0) return true;
             step(a);
@@ -172,10 +164,11 @@ struct AtWalk {
         return false;
     }
     DT_DI void step(const DtAttend& a) {  // to the next unit
-        at += (long long)nt * w;
+        at += nt * w;
         if (++h < a.c.Hkv) return;
         h = 0;
         ++qb;
+#pragma unroll 1
         while (qb >= r.nqb) {
             qb = 0;
             if (++b >= a.batch) return;
@@ -209,11 +202,14 @@ DT_DI int at_position(const DtAttend& a, int b, int len, int node) {
 // Zeros for the output rows past n_nodes (all rows of a request out of range),
 // spread over the grid.
 DT_DI void at_zero_rest(const DtAttend& a, int cta, int ctas, int tid, int nt) {
+    if (!a.n_nodes) return;  // a request out of range then has undefined rows
     const size_t chunks = (size_t)a.Hq * a.c.D / 8;
+#pragma unroll 1
     for (int b = 0; b < a.batch; ++b) {
         const int n = AtPlan<16>::req(a, b).n;
         uint4* o = (uint4*)a.out + ((size_t)b * a.M + n) * chunks;
         const size_t m = (size_t)(a.M - n) * chunks;
+#pragma unroll 1
         for (size_t i = (size_t)cta * nt + tid; i < m; i += (size_t)ctas * nt) o[i] = make_uint4(0u, 0u, 0u, 0u);
     }
 }

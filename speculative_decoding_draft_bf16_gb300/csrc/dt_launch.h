@@ -178,7 +178,7 @@ cudaError_t dt_kn10_launch(const dt_kv_cache& c, const dt_rope& rope, int batch,
 struct DtAttend {
     dt_kv_cache c;
     dt_rope rope;  // rot = 0: none
-    int batch, M, Hq;
+    int batch, M, Hq, G;  // G = Hq / Hkv
     dt_rows q, k, v;
     const uint32_t* mask;
     const int32_t* pos;

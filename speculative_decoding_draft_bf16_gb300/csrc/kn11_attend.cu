@@ -19,7 +19,7 @@ __global__ void __launch_bounds__(NW * 32) kn11_kernel(DtAttend a) {
     const int b = blockIdx.z, h = blockIdx.y, n = blockIdx.x * NW + w;
     if (n >= a.M) return;
     const dt_kv_cache& c = a.c;
-    const int kh = h / (a.Hq / c.Hkv);
+    const int kh = h / (a.G);
     uint16_t* out = (uint16_t*)a.out + (((size_t)b * a.M + n) * a.Hq + h) * D + lane * E;
     int len = c.len[b], rows = a.n_nodes ? a.n_nodes[b] : a.M;
     bool bad = len < 0 || (long long)len > (long long)c.max_pages * c.page || rows < 0 || rows > a.M;

@@ -30,8 +30,8 @@ constexpr int ROWS = 256;       // query rows of a block
 constexpr int TQ = 128;         // rows of a slot
 constexpr int NS = 256;         // softmax threads
 constexpr int NC = 128;         // converter threads for the keys, and as many for the values
-// Five warpgroups; in the last one a thread issues the MMAs, a thread of another
-// warp walks the CTA's share of the work and a third warp looks up pages.
+// Five warpgroups; in the last one two warps issue the MMAs of the slots, a thread
+// walks the CTA's share of the work and a warp looks up pages.
 constexpr int NT = NS + 2 * NC + 128;
 // Registers per thread of the warpgroups (softmax, converters, MMA): over the
 // CTA they sum to what it is launched with, LAUNCH_REGS each.  No loop of a role may
@@ -43,7 +43,7 @@ constexpr int STAGES = 2;       // K and V tiles in shared memory, each
 constexpr int RING = 8;         // tiles whose page ids and scales are kept
 constexpr int SEGS = 4;         // segments the walk may be ahead
 constexpr int ATOM = 4;         // tiles of the longest unit that is not split
-constexpr int MIN_SHARE = 2;    // least cost worth a CTA: two tiles of a full block
+constexpr uint32_t MIN_SHARE = 10;    // least cost worth a CTA: two tiles of a full block
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float HEADROOM = 5.f, LAZY = 8.f;
 
@@ -62,7 +62,7 @@ struct Seg {
 
 struct Shared {
     uint64_t kfull[STAGES], kfree[STAGES], vfull[STAGES], vfree[STAGES];
-    uint64_t sfull[2], pfull[2], ofull[2], qfull, scfull[RING], idfull[RING], ringfree[RING];
+    uint64_t sfull[2][2], pfull[2][2], qfull, scfull[RING], idfull[RING], ringfree[RING];
     uint32_t tmem;
     int fail, last;
     AtShare share;
@@ -84,26 +84,22 @@ struct Lay {
     static constexpr size_t SMEM = 1024 + SH + sizeof(Shared);
 };
 
-// Bounded wait; once one has run out, later ones return at once.
-DT_DI bool try_wait(uint64_t* bar, uint32_t phase) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(dt_smem_addr(bar)), "r"(phase)
-        : "memory");
-    return done;
-}
+// Bounded wait (some 10^8 to 10^9 clocks); once one has run out, `fail` is set and
+// later ones give up at their first look.  Short code: it stands in every role.
 DT_DI void wait(uint64_t* bar, uint32_t phase, int* fail) {
-    if (try_wait(bar, phase)) return;
-    const long long t0 = clock64();
-    while (!try_wait(bar, phase)) {
-        if (*(volatile int*)fail) return;
-        if (clock64() - t0 > DT_WAIT_BUDGET) {
-            *(volatile int*)fail = 1;
-            return;
-        }
-    }
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .u32 n, f;\n mov.u32 n, 4194304;\n"
+        "AGAIN:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1, 1000;\n @p bra DONE;\n"
+        " sub.u32 n, n, 1;\n setp.ne.u32 p, n, 0;\n @!p st.volatile.shared.u32 [%2], 1;\n"
+        " ld.volatile.shared.u32 f, [%2];\n setp.eq.u32 p, f, 0;\n @p bra AGAIN;\nDONE:\n}\n" ::"r"(dt_smem_addr(bar)),
+        "r"(phase), "r"(dt_smem_addr(fail))
+        : "memory");
+}
+
+DT_DI bool elect_one() {  // one lane of a converged warp
+    uint32_t p;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+    return p;
 }
 
 // This warpgroup's registers per thread, from the LAUNCH_REGS it started with
@@ -154,15 +150,13 @@ DT_DI float max3(float a, float b, float c) {
     return r;
 }
 
-// Streamed codes: read once by this CTA, not kept in L1; zeros unless `in`.
-DT_DI uint4 ldg16_if(const void* p, bool in) {
+// Streamed codes: read once by this CTA, not kept in L1.
+DT_DI uint4 ldg16(const void* p) {
     uint4 v;
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
-        " @p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}\n"
-        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-        : "l"(p), "r"((int)in)
-        : "memory");
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
     return v;
 }
 
@@ -192,8 +186,10 @@ DT_DI void scale_parts(float s, float& lg, float& inv) {
     inv = 1.0f / s;
 }
 
-// The converter warps of the keys (KEYS) or the values.
-template <int D, bool KEYS>
+// The converter warps: 128 threads for the keys, 128 for the values, one code (the
+// instruction caches nearest the SM's quarters hold little more than the loops of
+// the roles that run there).
+template <int D>
 struct Conv {
     // A thread reads 16-byte piece `piece` (of D / 16) of token i * TPI + `tok`
     // in iteration i.  Four lanes read half a row of 128 columns; eight lanes of
@@ -204,104 +200,114 @@ struct Conv {
     static DT_DI int piece_of(int ct) { return D == 128 ? (ct & 3) + ((ct >> 4) & 1) * 4 : ct & 3; }
     static DT_DI int tok_of(int ct) { return D == 128 ? ((ct >> 2) & 3) + (ct >> 5) * 4 : ct >> 2; }
     static constexpr int NI = AT_TILE / TPI;  // iterations per tile
-    static constexpr int BAR = KEYS ? 1 : 3, WHICH = KEYS ? 0 : 1;
     using L = Lay<D>;
 
-    static DT_DI void group_sync() { asm volatile("bar.sync %0, 128;" ::"n"(BAR) : "memory"); }
-
-    // Piece i of a tile: this thread's 16 bytes of token `tok`; zeros past len.
-    static DT_DI uint4 piece(const uint8_t* base, uint32_t page_bytes, int low, uint32_t id, int tok, int len) {
-        return ldg16_if(base + (size_t)id * page_bytes + (tok & low) * D, tok < len);
+    static DT_DI void group_sync(bool keys) {
+        if (keys) asm volatile("bar.sync 1, 128;" ::: "memory");
+        else asm volatile("bar.sync 3, 128;" ::: "memory");
     }
 
     // One tile of new rows, from row m0: keys rotated, scaled by a power of two
     // when the largest magnitude leaves fp16's comfortable range.
-    static DT_DI void fresh(const DtAttend& a, const Seg& u, int m0, int ct, Shared* sh, Ring* ring, uint32_t tile) {
-        const int b = u.b, n = u.n, len = u.len, left = min(AT_TILE, n - m0);
-        const dt_rows& src = KEYS ? a.k : a.v;
+    static DT_DI void fresh(const DtAttend& a, const Seg& u, bool keys, int m0, int ct, Shared* sh, Ring* ring,
+                            uint32_t tile) {
+        const int which = keys ? 0 : 1, b = u.b, n = u.n, len = u.len, left = min(AT_TILE, n - m0);
+        const dt_rows& src = keys ? a.k : a.v;
         const uint16_t* p = (const uint16_t*)src.ptr + b * src.stride_b + u.h * src.stride_h;
-        if (ct < 4) ring->bad[WHICH][ct] = 0u;
-        if (KEYS) sh->kpos[ct] = a.rope.rot && ct < left ? at_position(a, b, len, m0 + ct) : 0;
-        group_sync();
+        const long long stride = src.stride_n;
+        dt_rope rope = a.rope;
+        if (!keys) rope.rot = 0;
+        if (ct < 4) ring->bad[which][ct] = 0u;
+        if (keys) sh->kpos[ct] = rope.rot && ct < left ? at_position(a, b, len, m0 + ct) : 0;
+        group_sync(keys);
         const int pr = ct % PPT;  // this thread's chunk pair of rows ct / PPT + i * TPI
-        int c0 = 2 * pr, c1 = 2 * pr + 1;
-        if (KEYS) dt_pair_chunks(pr, a.rope, c0, c1);
-        uint32_t big = 0u;
-        auto convert = [&](float f) {
-#pragma unroll 2
-            for (int i = 0; i < NI; ++i) {
-                const int r = ct / PPT + i * TPI;
-                const uint16_t* row = p + (m0 + min(r, left - 1)) * src.stride_n;
-                float x[8], y[8];
-                if (KEYS) {
-                    dt_rotated_pair(row, pr, a.rope, sh->kpos[min(r, left - 1)], x, y);
-                } else {
-                    dt_load8(row + 16 * pr, x);
-                    dt_load8(row + 16 * pr + 8, y);
-                }
-                bool bad = false;
+        int c0, c1;
+        dt_pair_chunks(pr, rope, c0, c1);
+        constexpr int U = 2;  // rows in flight
+        int e = 0;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {  // the second one when the tile needs another scale
+            const float f = dt_pow2(-e);
+            uint32_t big = 0u;
+#pragma unroll 1
+            for (int i0 = 0; i0 < NI; i0 += U) {
+                float x[U][8], y[U][8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t v = __float_as_uint(x[e]) & 0x7FFFFFFFu, w = __float_as_uint(y[e]) & 0x7FFFFFFFu;
-                    const bool bx = v >= 0x7F800000u, by = w >= 0x7F800000u;
-                    bad |= bx | by;
-                    x[e] = bx || r >= left ? 0.f : x[e];
-                    y[e] = by || r >= left ? 0.f : y[e];
-                    big = max(big, max(__float_as_uint(x[e]) & 0x7FFFFFFFu, __float_as_uint(y[e]) & 0x7FFFFFFFu));
+                for (int k = 0; k < U; ++k) {
+                    const int r = min(ct / PPT + (i0 + k) * TPI, left - 1);
+                    dt_rotated_pair(p + (m0 + r) * stride, pr, rope, sh->kpos[r], x[k], y[k]);
                 }
-                if (bad && r < left) atomicOr(&ring->bad[WHICH][r >> 5], 1u << (r & 31));
-                uint32_t o[4], w[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    o[q] = f16x2(__fmul_rn(x[2 * q], f), __fmul_rn(x[2 * q + 1], f));
-                    w[q] = f16x2(__fmul_rn(y[2 * q], f), __fmul_rn(y[2 * q + 1], f));
+                for (int k = 0; k < U; ++k) {
+                    const int r = ct / PPT + (i0 + k) * TPI;
+                    bool bad = false;
+                    uint32_t o[4], w[4];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        float& u0 = x[k][q];
+                        float& u1 = y[k][q];
+                        const bool b0 = (__float_as_uint(u0) & 0x7FFFFFFFu) >= 0x7F800000u;
+                        const bool b1 = (__float_as_uint(u1) & 0x7FFFFFFFu) >= 0x7F800000u;
+                        bad |= b0 | b1;
+                        u0 = b0 || r >= left ? 0.f : __fmul_rn(u0, f);
+                        u1 = b1 || r >= left ? 0.f : __fmul_rn(u1, f);
+                        big = max(big, max(__float_as_uint(u0) & 0x7FFFFFFFu, __float_as_uint(u1) & 0x7FFFFFFFu));
+                    }
+                    if (bad && r < left) atomicOr(&ring->bad[which][r >> 5], 1u << (r & 31));
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        o[q] = f16x2(x[k][2 * q], x[k][2 * q + 1]);
+                        w[q] = f16x2(y[k][2 * q], y[k][2 * q + 1]);
+                    }
+                    sts16(tile + chunk_at(r, c0), o);
+                    sts16(tile + chunk_at(r, c1), w);
                 }
-                sts16(tile + chunk_at(r, c0), o);
-                sts16(tile + chunk_at(r, c1), w);
             }
-        };
-        convert(1.f);
-        big = dt_warp_max_u32(big);
-        if ((ct & 31) == 0) sh->amax[WHICH][ct >> 5] = big;
-        group_sync();
-        for (int i = 0; i < NC / 32; ++i) big = max(big, sh->amax[WHICH][i]);
-        // as they are in [2^-4, 2^15), else scaled to below 2^9; none or very small: 2^-57
-        int e = (int)(big >> 23) - 127;
-        e = e >= -4 && e < 15 ? 0 : max(e - 8, -57);
-        if (e != 0) convert(dt_pow2(-e));
+            if (pass) break;
+            big = dt_warp_max_u32(big);
+            if ((ct & 31) == 0) sh->amax[which][ct >> 5] = big;
+            group_sync(keys);
+            for (int i = 0; i < NC / 32; ++i) big = max(big, sh->amax[which][i]);
+            // as they are in [2^-4, 2^15), else scaled to below 2^9; none or very small: 2^-57
+            e = (int)(big >> 23) - 127;
+            e = e >= -4 && e < 15 ? 0 : max(e - 8, -57);
+            if (e == 0) break;
+        }
         if (ct < 8) {
-            if (KEYS) {
+            if (keys) {
                 ring->ks[ct] = dt_pow2(e);
             } else {
                 ring->lv[ct] = (float)e;
                 ring->iv[ct] = dt_pow2(-e);
             }
         }
+        group_sync(keys);
     }
 
-    static DT_DI void run(const DtAttend& a, unsigned char* sm, Shared* sh, int ct) {
-        const int lp = 31 - __clz(a.c.page);
-        const uint32_t base = dt_smem_addr(sm + (KEYS ? L::K : L::V));
+    static DT_DI void run(const DtAttend& a, unsigned char* sm, Shared* sh, int ct, bool keys) {
+        const int lp = 31 - __clz(a.c.page), low = a.c.page - 1;
+        const uint32_t base = dt_smem_addr(sm + (keys ? L::K : L::V));
         const uint32_t a0 = base + chunk_at(tok_of(ct), 2 * piece_of(ct)),
                        a1 = base + chunk_at(tok_of(ct), 2 * piece_of(ct) + 1);
-        uint64_t* full = KEYS ? sh->kfull : sh->vfull;
-        uint64_t* free_ = KEYS ? sh->kfree : sh->vfree;
+        const uint32_t page_bytes = ((uint32_t)a.c.Hkv << lp) * D;
+        uint64_t* full = keys ? sh->kfull : sh->vfull;
+        uint64_t* free_ = keys ? sh->kfree : sh->vfree;
         uint32_t g = 0, i = 0;  // tiles, segments done
         for (const Seg* sg; (sg = get_segment(sh, i)) != nullptr; release_segment(sh, i++)) {
             const Seg& u = *sg;
-            const int t1 = u.t1, cend = min(t1, u.ctx), len = u.len, low = a.c.page - 1;
-            const uint8_t* codes = (KEYS ? a.c.k : a.c.v) + (((size_t)u.h << lp) * D + piece_of(ct) * 16);
-            const uint32_t page_bytes = ((uint32_t)a.c.Hkv << lp) * D;
+            const int t1 = u.t1, cend = min(t1, u.ctx), last = u.len - 1;
+            const uint8_t* codes = (keys ? a.c.k : a.c.v) + (((size_t)u.h << lp) * D + piece_of(ct) * 16);
             // The next tile's codes are loaded in two batches, each when this
             // tile's have left its registers.  Page ids come from shared memory:
-            // loads that wait for loads would share their scoreboards.
+            // loads that wait for loads would share their scoreboards.  Past len,
+            // the last token's.
             uint4 q[NI];
             auto load = [&](int j, uint32_t g, int i0) {
                 const Ring* ring = &sh->ring[g % RING];
 #pragma unroll
                 for (int i = i0; i < i0 + NI / 2; ++i) {
-                    const int r = tok_of(ct) + i * TPI;
-                    q[i] = piece(codes, page_bytes, low, ring->id[r >> 4], j * AT_TILE + r, len);
+                    const int r = tok_of(ct) + i * TPI, tok = min(j * AT_TILE + r, last);
+                    q[i] = ldg16(codes + (size_t)ring->id[r >> 4] * page_bytes + (uint32_t)(tok & low) * D);
                 }
             };
             int j = u.t0;
@@ -310,10 +316,10 @@ struct Conv {
                 load(j, g, 0);
                 load(j, g, NI / 2);
             }
+#pragma unroll 1
             for (; j < t1; ++j, ++g) {
                 const int s = g % STAGES;
                 wait(&free_[s], (g / STAGES + 1) & 1, &sh->fail);
-                __syncwarp();
                 if (j < cend) {
                     if (ct == 0) dt_mbar_arrive(&sh->scfull[g % RING]);
                     const uint32_t o = s * L::TILE;
@@ -328,12 +334,12 @@ struct Conv {
                     }
                 } else {
                     wait(&sh->idfull[g % RING], (g / RING) & 1, &sh->fail);  // the ring's slot is free
-                    fresh(a, u, (j - u.ctx) * AT_TILE, ct, sh, &sh->ring[g % RING], base + s * L::TILE);
-                    group_sync();
+                    fresh(a, u, keys, (j - u.ctx) * AT_TILE, ct, sh, &sh->ring[g % RING], base + s * L::TILE);
                     if (ct == 0) dt_mbar_arrive(&sh->scfull[g % RING]);
                 }
                 dt_fence_proxy_async_smem();
-                dt_mbar_arrive(&full[s]);
+                __syncwarp();
+                if ((ct & 31) == 0) dt_mbar_arrive(&full[s]);
             }
         }
     }
@@ -352,20 +358,22 @@ DT_DI void look_up(const DtAttend& a, Shared* sh, int lane) {
         const int* table = a.c.table + (size_t)b * a.c.max_pages;
         for (int k = 0; k < nt; k += 4) {
             const int t = k + (lane >> 3), tok = (t0 + t) * AT_TILE + grp * 16;
-            const bool in = t < ctx && tok < len;
+            const bool in = t < ctx;
             uint32_t id = 0;
             float ks = 1.f, vs = 1.f;
             if (in) {
-                id = (uint32_t)table[tok >> lp];
+                id = (uint32_t)table[min(tok, len - 1) >> lp];
                 if (id >= (uint32_t)a.c.n_pages) {
                     atomicOr(&a.status[b], DT_DEV_BAD_CACHE);
                     id = 0;
                 }
+            }
+            if (in && tok < len) {
                 ks = a.c.k_scale[(size_t)id * a.c.Hkv + h];
                 vs = a.c.v_scale[(size_t)id * a.c.Hkv + h];
                 // the 16 tokens' codes: 16 D bytes of keys and of values
                 const size_t o = (size_t)id * page_bytes + ((size_t)h << lp) * D + (tok & (a.c.page - 1)) * D;
-#pragma unroll
+#pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.k + o + c * 128));
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.v + o + c * 128));
@@ -386,54 +394,81 @@ DT_DI void look_up(const DtAttend& a, Shared* sh, int lane) {
     }
 }
 
-// The MMA warp's one thread.
+// The MMA warp of slot s.  All its lanes walk along, so that operands stay in
+// uniform registers, and an elected one issues (39 clocks for an MMA at most,
+// against 52 from a branch of one thread); a warp for each slot, because one for
+// both cannot issue as fast as the tensor cores take them.  A tile's scores come
+// in two halves of 64 tokens with a buffer each, so that a slot's softmax works on
+// one half while the other half's probabilities meet V and its next scores are
+// formed.  sfull[s][h] counts, per segment: the first scores, then for each tile
+// of the slot its product P V of half h, with the next tile's scores when there
+// are any.  A tile's stages are free after two commits: one from each slot's
+// warp, or both from the one slot that uses it.
 template <int D>
-DT_DI void issue_all(unsigned char* sm, Shared* sh, uint32_t tmem) {
+DT_DI void issue_slot(unsigned char* sm, Shared* sh, uint32_t tmem, int s) {
     using L = Lay<D>;
-    constexpr uint32_t ID_S = dt_idesc_f16_f32(TQ, AT_TILE, false), ID_O = dt_idesc_f16_f32(TQ, D, true);
+    constexpr uint32_t ID_S = dt_idesc_f16_f32(TQ, 64, false), ID_O = dt_idesc_f16_f32(TQ, D, true);
     const uint32_t qd = dt_desc_lo(dt_smem_addr(sm + L::Q), 16), kd = dt_desc_lo(dt_smem_addr(sm + L::K), 16),
                    vd = dt_desc_lo(dt_smem_addr(sm + L::V), L::HALF);
-    uint32_t g0 = 0, seg = 0, pc[2] = {0u, 0u};
+    const bool el = elect_one();
+    const uint32_t ts = tmem + s * AT_TILE, to = tmem + 2 * AT_TILE + s * D;
+    uint32_t g0 = 0, seg = 0, pc = 0;  // pc: phase of pfull[s]
     for (const Seg* u; (u = get_segment(sh, seg)) != nullptr; ++seg) {
-        const bool dual = u->rows > TQ;  // two slots of rows; else two slots of tiles
-        const int nt = u->t1 - u->t0;
-        release_segment(sh, seg);
+        const bool dual = __shfl_sync(0xffffffffu, u->rows, 0) > TQ;  // two slots of rows; else two slots of tiles
+        const int nt = __shfl_sync(0xffffffffu, u->t1 - u->t0, 0), hop = dual ? 1 : 2;
+        if (el) release_segment(sh, seg);
         wait(&sh->qfull, seg & 1, &sh->fail);
-        auto qk = [&](int s, int lt) {
-            const uint32_t g = g0 + lt, st = g % STAGES;
-            wait(&sh->kfull[st], (g / STAGES) & 1, &sh->fail);
-            dt_tc_fence_after();
-            const uint32_t q = qd + (dual ? s : 0) * (L::TILE >> 4), k = kd + st * (L::TILE >> 4), d = tmem + s * AT_TILE;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t o = ((kk >> 2) * L::HALF + (kk & 3) * 32) >> 4;
-                dt_mma_ss_lo(d, q + o, k + o, ID_S, kk > 0);
-            }
-            dt_mma_commit(&sh->sfull[s]);
-            if (!dual || s == 1) dt_mma_commit(&sh->kfree[st]);
-        };
-        auto pv = [&](int s, int lt, bool first, bool last) {
-            const uint32_t g = g0 + lt, st = g % STAGES;
-            wait(&sh->pfull[s], pc[s]++ & 1, &sh->fail);
-            wait(&sh->vfull[st], (g / STAGES) & 1, &sh->fail);
-            dt_tc_fence_after();
-            const uint32_t v = vd + st * (L::TILE >> 4), p = tmem + s * AT_TILE, d = tmem + 2 * AT_TILE + s * D;
-#pragma unroll
-            for (int kk = 0; kk < AT_TILE / 16; ++kk)
-                dt_mma_ts_lo(d, p + kk * 8, v + kk * (2048 >> 4), ID_O, !first || kk > 0);
-            if (!dual || s == 1) {
-                dt_mma_commit(&sh->vfree[st]);
-                dt_mma_commit(&sh->ringfree[g % RING]);
-            }
-            if (last) dt_mma_commit(&sh->ofull[s]);
-        };
-        // slot s = i & 1 step by step: its product with V, then its next scores
-        const int hop = dual ? 1 : 2, steps = dual ? 2 * nt : nt + (nt & 1);
+        const uint32_t q = qd + (dual ? s : 0) * (L::TILE / 16);
 #pragma unroll 1
-        for (int i = -2; i < steps; ++i) {
-            const int s = i & 1, t = dual ? i >> 1 : i;  // i < 0: the tile before the slot's first
-            if (i >= 0 && t < nt) pv(s, t, i < 2, t + hop >= nt);
-            if (t + hop < nt) qk(s, t + hop);
+        for (int t = (dual ? 0 : s) - hop; t < nt; t += hop) {  // before the first tile: its scores only
+            const bool here = t >= 0, next = t + hop < nt;
+            if (!here && !next) break;
+            const uint32_t g = g0 + t, gn = g + hop, st = g % STAGES, sn = gn % STAGES;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                if (here) {
+                    wait(&sh->pfull[s][h], pc, &sh->fail);
+                    if (h == 0) wait(&sh->vfull[st], (g / STAGES) & 1, &sh->fail);
+                    __syncwarp();
+                    dt_tc_fence_after();
+                    const uint32_t v = vd + st * (L::TILE / 16) + h * (8192 / 16);
+                    if (el) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            dt_mma_ts_lo(to, ts + 64 * h + kk * 8, v + kk * (2048 / 16), ID_O, t >= hop || h > 0 || kk > 0);
+                        if (h == 1) {
+                            dt_mma_commit(&sh->vfree[st]);
+                            dt_mma_commit(&sh->ringfree[g % RING]);
+                            if (!dual) {
+                                dt_mma_commit(&sh->vfree[st]);
+                                dt_mma_commit(&sh->ringfree[g % RING]);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (next) {
+                    if (h == 0) wait(&sh->kfull[sn], (gn / STAGES) & 1, &sh->fail);
+                    __syncwarp();
+                    dt_tc_fence_after();
+                    const uint32_t kt = kd + sn * (L::TILE / 16) + h * (8192 / 16);
+                    if (el) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t o = ((kk >> 2) * L::HALF + (kk & 3) * 32) / 16;
+                            dt_mma_ss_lo(ts + 64 * h, q + o, kt + o, ID_S, kk > 0);
+                        }
+                        if (h == 1) {
+                            dt_mma_commit(&sh->kfree[sn]);
+                            if (!dual) dt_mma_commit(&sh->kfree[sn]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (el) dt_mma_commit(&sh->sfull[s][h]);
+                __syncwarp();
+            }
+            if (here) pc ^= 1;
         }
         g0 += nt;
     }
@@ -447,7 +482,7 @@ struct Soft {
     // The block's rows, rotated, scaled by a power of two and converted.
     static DT_DI void queries(const DtAttend& a, const Seg& u, unsigned char* sm, Shared* sh, int tid) {
         constexpr int PPR = D / 16, RPI = NS / PPR, U = 2;  // chunk pairs per row, rows per pass
-        const uint32_t G = a.Hq / a.c.Hkv;
+        const uint32_t G = a.G;
         const int tiles = u.rows > TQ ? 2 : 1;
         const uint32_t qb = dt_smem_addr(sm + L::Q);
         const int pr = tid % PPR;
@@ -495,56 +530,61 @@ struct Soft {
         dt_mbar_arrive(&sh->qfull);
     }
 
-    // The row's mask words of a tile that is not wholly visible.
-    static DT_DI void mask_words(const DtAttend& a, const Seg& u, int t, int row, uint32_t (&mk)[4]) {
-        const int G = a.Hq / a.c.Hkv;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (t < u.ctx) {
-                const int left = u.len - t * AT_TILE - 32 * i;
-                mk[i] = left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
-            } else {
-                const uint32_t node = ((uint32_t)u.qb * ROWS + row) / (uint32_t)G;
-                mk[i] = row < u.rows ? at_mask_word(a, u.b, (int)node, (t - u.ctx) * AT_TILE + 32 * i, u.n) : 0u;
-            }
+    // The row's mask of 64 tokens of a tile that is not wholly visible.
+    static DT_DI uint2 mask_words(const DtAttend& a, const Seg& u, int t, int h, int row) {
+        if (t < u.ctx) {
+            const int left = u.len - t * AT_TILE - 64 * h;
+            return make_uint2(left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u,
+                              left >= 64 ? ~0u : left <= 32 ? 0u : (1u << (left - 32)) - 1u);
         }
+        if (row >= u.rows) return make_uint2(0u, 0u);
+        const int node = (int)(((uint32_t)u.qb * ROWS + row) / (uint32_t)(a.G));
+        const int m0 = (t - u.ctx) * AT_TILE + 64 * h;
+        return make_uint2(at_mask_word(a, u.b, node, m0, u.n), at_mask_word(a, u.b, node, m0 + 32, u.n));
     }
+
     template <bool MASKED>
-    static DT_DI void blank(uint32_t (&x)[64], uint32_t lo, uint32_t hi) {
+    static DT_DI void blank(uint32_t (&x)[32], uint32_t bits) {
         if constexpr (MASKED) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-                if (!(((i < 32 ? lo : hi) >> (i & 31)) & 1)) x[i] = 0xFF800000u;  // -infinity
+            for (int i = 0; i < 32; ++i)
+                if (!((bits >> i) & 1)) x[i] = 0xFF800000u;  // -infinity
         }
     }
 
-    // One tile of a row: its scores at ts become probabilities in place, the
-    // running reference m and sum l move on, and O is rescaled when it has sums.
-    // The two halves of a tile share their code: five roles share the
-    // instruction cache.
+    // 64 tokens of a row: their scores at ts become probabilities in place, the
+    // running reference m and sum l move on, and O is rescaled when it has sums;
+    // before that every product of the slot must be done: `other` is the barrier
+    // of the other half's.  `ks`, `lv`, `iv`: the scales of the four groups.
     template <bool MASKED>
-    static DT_DI void tile(const Ring* ring, uint32_t ts, uint32_t to, bool has_o, float rowc, const uint32_t (&mk)[4],
-                           float& m, float& l) {
+    static DT_DI void half(const float* ks, const float* lv, const float* iv, uint32_t ts, uint32_t to, bool has_o,
+                           float rowc, uint2 mk, float& m, float& l, uint64_t* other, uint32_t other_ph, int* fail) {
         const float NEG_INF = -__int_as_float(0x7F800000);
-        uint32_t x[64];
-        // pass 1: the largest score + log2 of its value scale
-        float mx = NEG_INF;
+        if (MASKED && !__any_sync(0xffffffffu, mk.x | mk.y)) {  // none of the warp's rows sees any of them
+            const uint32_t z[16] = {};
+            dt_tmem_st16(ts, z);
+            dt_tmem_st16(ts + 16, z);
+            dt_tmem_st_wait();
+            return;
+        }
+        // The two passes read the scores again rather than keep them, 32 columns
+        // in a turn: short code and few registers.
+        float mx = NEG_INF;  // the largest score + log2 of its value scale
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
-            dt_tmem_ld64(ts + 64 * c, x);
-            blank<MASKED>(x, c ? mk[2] : mk[0], c ? mk[3] : mk[1]);
-            const float4 ks = *(const float4*)(ring->ks + 4 * c), lv = *(const float4*)(ring->lv + 4 * c);
-            const float k4[4] = {ks.x, ks.y, ks.z, ks.w}, l4[4] = {lv.x, lv.y, lv.z, lv.w};
+            uint32_t x[32];
+            dt_tmem_ld32(ts + 32 * c, x);
+            blank<MASKED>(x, c ? mk.y : mk.x);
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                float q0 = __uint_as_float(x[16 * h]), q1 = __uint_as_float(x[16 * h + 1]);
+            for (int g = 0; g < 2; ++g) {
+                float q0 = __uint_as_float(x[16 * g]), q1 = __uint_as_float(x[16 * g + 1]);
 #pragma unroll
                 for (int i = 2; i < 14; i += 4) {
-                    q0 = max3(q0, __uint_as_float(x[16 * h + i]), __uint_as_float(x[16 * h + i + 1]));
-                    q1 = max3(q1, __uint_as_float(x[16 * h + i + 2]), __uint_as_float(x[16 * h + i + 3]));
+                    q0 = max3(q0, __uint_as_float(x[16 * g + i]), __uint_as_float(x[16 * g + i + 1]));
+                    q1 = max3(q1, __uint_as_float(x[16 * g + i + 2]), __uint_as_float(x[16 * g + i + 3]));
                 }
-                q0 = max3(q0, __uint_as_float(x[16 * h + 14]), __uint_as_float(x[16 * h + 15]));
-                mx = fmaxf(mx, __fmaf_rn(fmaxf(q0, q1), __fmul_rn(rowc, k4[h]), l4[h]));
+                q0 = max3(q0, __uint_as_float(x[16 * g + 14]), __uint_as_float(x[16 * g + 15]));
+                mx = fmaxf(mx, __fmaf_rn(fmaxf(q0, q1), __fmul_rn(rowc, ks[2 * c + g]), lv[2 * c + g]));
             }
         }
         // a maximum that has grown moves the reference; rows of a warp do so together
@@ -555,6 +595,9 @@ struct Soft {
             m = to_m;
             l = __fmul_rn(l, f);
             if (has_o) {
+                wait(other, other_ph, fail);
+                __syncwarp();
+                dt_tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < D / 16; ++c) {
                     uint32_t o[16];
@@ -564,43 +607,33 @@ struct Soft {
                     for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__fmul_rn(__uint_as_float(o[i]), f));
                     dt_tmem_st16(to + 16 * c, o);
                 }
-                dt_tmem_st_wait();
             }
         }
         const float mu = m == NEG_INF ? 0.f : m;
-        // pass 2: probabilities, over the columns already read
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
-            dt_tmem_ld64(ts + 64 * c, x);
-            blank<MASKED>(x, c ? mk[2] : mk[0], c ? mk[3] : mk[1]);
-            const float4 ks = *(const float4*)(ring->ks + 4 * c), lv = *(const float4*)(ring->lv + 4 * c),
-                         iv = *(const float4*)(ring->iv + 4 * c);
-            const float k4[4] = {ks.x, ks.y, ks.z, ks.w}, l4[4] = {lv.x, lv.y, lv.z, lv.w},
-                        i4[4] = {iv.x, iv.y, iv.z, iv.w};
+            uint32_t x[32], p[16];
+            dt_tmem_ld32(ts + 32 * c, x);
+            blank<MASKED>(x, c ? mk.y : mk.x);
 #pragma unroll
-            for (int h = 0; h < 4; h += 2) {
-                uint32_t p[16];
+            for (int g = 0; g < 2; ++g) {
+                const float ka = __fmul_rn(rowc, ks[2 * c + g]), kb = __fsub_rn(lv[2 * c + g], mu);
+                const unsigned long long ka2 = dt_f2_pack(ka, ka), kb2 = dt_f2_pack(kb, kb);
+                unsigned long long sum = dt_f2_pack(0.f, 0.f);
 #pragma unroll
-                for (int g = h; g < h + 2; ++g) {
-                    const float ka = __fmul_rn(rowc, k4[g]), kb = __fsub_rn(l4[g], mu);
-                    const unsigned long long ka2 = dt_f2_pack(ka, ka), kb2 = dt_f2_pack(kb, kb);
-                    unsigned long long sum = dt_f2_pack(0.f, 0.f);
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        float e0, e1;
-                        dt_f2_unpack(dt_f2_fma(dt_f2_pack(__uint_as_float(x[16 * g + i]), __uint_as_float(x[16 * g + i + 1])),
-                                               ka2, kb2), e0, e1);
-                        e0 = dt_ex2_approx(e0);
-                        e1 = dt_ex2_approx(e1);
-                        sum = dt_f2_add(sum, dt_f2_pack(e0, e1));
-                        p[8 * (g - h) + i / 2] = f16x2(e0, e1);
-                    }
-                    float s0, s1;
-                    dt_f2_unpack(sum, s0, s1);
-                    l = __fmaf_rn(__fadd_rn(s0, s1), i4[g], l);
+                for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+                    float e0, e1;
+                    dt_f2_unpack(dt_f2_fma(dt_f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), ka2, kb2), e0, e1);
+                    e0 = dt_ex2_approx(e0);
+                    e1 = dt_ex2_approx(e1);
+                    sum = dt_f2_add(sum, dt_f2_pack(e0, e1));
+                    p[i / 2] = f16x2(e0, e1);
                 }
-                dt_tmem_st16(ts + 32 * c + 8 * h, p);
+                float s0, s1;
+                dt_f2_unpack(sum, s0, s1);
+                l = __fmaf_rn(__fadd_rn(s0, s1), iv[2 * c + g], l);
             }
+            dt_tmem_st16(ts + 16 * c, p);  // columns read already
         }
         dt_tmem_st_wait();
     }
@@ -611,7 +644,7 @@ struct Soft {
         const float NEG_INF = -__int_as_float(0x7F800000);
         const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
         const uint32_t ts = tmem + s * AT_TILE + lanes, to = tmem + 2 * AT_TILE + s * D + lanes;
-        uint32_t g0 = 0, sc = 0, oc = 0, seg = 0;
+        uint32_t g0 = 0, ph[2] = {0u, 0u}, seg = 0;  // ph: phases of sfull[s][h] waited for
         for (const Seg* sg; (sg = get_segment(sh, seg)) != nullptr; release_segment(sh, seg++)) {
             const Seg& u = *sg;
             // every product of the last segment has read its queries
@@ -627,30 +660,40 @@ struct Soft {
             for (int lt = dual ? 0 : s; lt < nt; lt += hop) {
                 const uint32_t g = g0 + lt;
                 const Ring* ring = &sh->ring[g % RING];
-                wait(&sh->sfull[s], sc++ & 1, &sh->fail);
-                wait(&sh->scfull[g % RING], (g / RING) & 1, &sh->fail);
-                __syncwarp();
-                dt_tc_fence_after();
                 const int t = u.t0 + lt;
-                uint32_t mk[4];
-                if ((t + 1) * AT_TILE > len) {
-                    mask_words(a, u, t, row, mk);
-                    if (t >= u.ctx) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) poison |= (mk[i] & (ring->bad[0][i] | ring->bad[1][i])) != 0u;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const bool masked = (t + 1) * AT_TILE > len;
+                    uint2 mk = make_uint2(~0u, ~0u);
+                    if (masked) mk = mask_words(a, u, t, h, row);
+                    if (h == 0) wait(&sh->scfull[g % RING], (g / RING) & 1, &sh->fail);
+                    wait(&sh->sfull[s][h], (h ? ph[1] : ph[0]) & 1, &sh->fail);
+                    __syncwarp();
+                    dt_tc_fence_after();
+                    uint64_t* other = &sh->sfull[s][h ^ 1];  // of half 0: waited for next; of half 1: of the next tile
+                    const uint32_t other_ph = (h ? ph[0] + 1 : ph[1]) & 1;
+                    const float *ks = ring->ks + 4 * h, *lv = ring->lv + 4 * h, *iv = ring->iv + 4 * h;
+                    if (masked) {
+                        if (t >= u.ctx)
+                            poison |= ((mk.x & (ring->bad[0][2 * h] | ring->bad[1][2 * h])) |
+                                       (mk.y & (ring->bad[0][2 * h + 1] | ring->bad[1][2 * h + 1]))) != 0u;
+                        half<true>(ks, lv, iv, ts + 64 * h, to, lt >= hop || h, rowc, mk, m, l, other, other_ph, &sh->fail);
+                    } else {
+                        half<false>(ks, lv, iv, ts + 64 * h, to, lt >= hop || h, rowc, mk, m, l, other, other_ph, &sh->fail);
                     }
-                    tile<true>(ring, ts, to, lt >= hop, rowc, mk, m, l);
-                } else {
-                    tile<false>(ring, ts, to, lt >= hop, rowc, mk, m, l);
+                    dt_tc_fence_before();
+                    __syncwarp();
+                    if ((tid & 31) == 0) dt_mbar_arrive(&sh->pfull[s][h]);
                 }
-                dt_tc_fence_before();
-                dt_mbar_arrive(&sh->pfull[s]);
+                ++ph[0];
+                ++ph[1];
             }
             if (poison) l = __int_as_float(0x7FC00000);
             // the segment's sums
             const bool any = dual || s < nt;  // the slot had a tile
             if (any) {
-                wait(&sh->ofull[s], oc++ & 1, &sh->fail);
+                wait(&sh->sfull[s][0], ph[0]++ & 1, &sh->fail);
+                wait(&sh->sfull[s][1], ph[1]++ & 1, &sh->fail);
                 __syncwarp();
                 dt_tc_fence_after();
             }
@@ -660,7 +703,9 @@ struct Soft {
             float f0 = 1.f, f1 = 0.f;  // weights of this slot's and the other slot's sums
             const uint32_t xb = dt_smem_addr(sm + L::Q) + (tid % TQ) * (D * 4);
             if (!dual) {
-                // slot 1 hands its rows to slot 0 by way of the query tiles
+                // slot 1 hands its rows to slot 0 by way of the query tiles, which the
+                // products of both slots have read
+                asm volatile("bar.sync 2, 256;" ::: "memory");
                 if (s == 1) {
                     sh->mrg_m[row] = m;
                     sh->mrg_l[row] = l;
@@ -724,7 +769,7 @@ struct Soft {
                         } else {
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                *(uint4*)(my + 2 * ROWS + (size_t)row * D + 16 * c + 4 * i) =
+                                *(uint4*)(my + 2 * ROWS + ((4 * c + i) * ROWS + row) * 4) =
                                     make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                         }
                     }
@@ -748,17 +793,18 @@ struct Soft {
     }
 
     static DT_DI uint16_t* out_row(const DtAttend& a, const Seg& u, int r) {
-        const uint32_t G = a.Hq / a.c.Hkv, rr = (uint32_t)u.qb * ROWS + r;
+        const uint32_t G = a.G, rr = (uint32_t)u.qb * ROWS + r;
         return (uint16_t*)a.out + (((size_t)u.b * a.M + rr / G) * a.Hq + u.h * G + rr % G) * D;
     }
 
-    // Joins the parts of a unit: O = sum O_i 2^(m_i - M), l likewise.  The
-    // weights go to shared memory (the query tiles) first, P parts at a time,
-    // so that the loads of a row's parts do not wait on each other.
+    // Joins the parts of a unit: O = sum O_i 2^(m_i - M), l likewise.  A part's O
+    // lies as [D / 4][ROWS][4], so that a warp of rows writes and reads whole
+    // lines.  The weights go to shared memory (the query tiles) first, P parts at a
+    // time, so that the loads of a row's parts do not wait on each other.
     static DT_DI void join(const DtAttend& a, unsigned char* sm, const Seg& u, float* part, int tid) {
-        constexpr int CPR = D / 8, RPI = NS / CPR, P = 16;  // 8 columns per thread
+        constexpr int P = 16;
         const float NEG_INF = -__int_as_float(0x7F800000);
-        const int c = tid % CPR, first = u.first, segs = u.segs, rows = u.rows;
+        const int first = u.first, segs = u.segs, rows = u.rows;
         float* wt = (float*)(sm + L::Q);  // [P][ROWS]
         auto slot = [&](int i) { return part + (size_t)(2 * (first + i) + (i == 0)) * ROWS * (D + 2); };
         float M = NEG_INF, l = 0.f;  // of row tid
@@ -772,6 +818,9 @@ struct Soft {
             }
         }
         const float inv = l == 0.f ? 0.f : 1.0f / l;
+        // a thread has two neighbouring chunks of 4 columns of 16 rows apart: lanes
+        // 0-15 and 16-31 of a warp take 16 rows each, 32 bytes of output together
+        const int r0 = tid & 15, c0 = ((tid >> 4) & 1) * 2, w = tid >> 5;
         for (int i0 = 0; i0 < segs; i0 += P) {
             // weight of part i for each row, 1 / l included; past the last part 0
             asm volatile("bar.sync 2, 256;" ::: "memory");
@@ -781,17 +830,18 @@ struct Soft {
             }
             asm volatile("bar.sync 2, 256;" ::: "memory");
             const int np = min(P, segs - i0);
-            for (int r = tid / CPR; r < rows; r += RPI) {
+            for (int k = w; k < (rows + 15) / 16 * (D / 16); k += NS / 32) {  // 16 rows, 16 columns
+                const int r = k / (D / 16) * 16 + r0, c = k % (D / 16) * 4 + c0;
                 float x[8] = {};
-                float4* acc = (float4*)(slot(0) + 2 * ROWS + (size_t)r * D + 8 * c);  // this thread's, read already
+                float4* acc = (float4*)(slot(0) + 2 * ROWS) + c * ROWS + r;  // this thread's, read already
                 if (i0 > 0) {
-                    const float4 y = acc[0], z = acc[1];
+                    const float4 y = acc[0], z = acc[ROWS];
                     x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w, x[4] = z.x, x[5] = z.y, x[6] = z.z, x[7] = z.w;
                 }
 #pragma unroll 4
                 for (int i = 0; i < np; ++i) {
-                    const float4* o = (const float4*)(slot(i0 + i) + 2 * ROWS + (size_t)r * D + 8 * c);
-                    const float4 y = __ldcg(o), z = __ldcg(o + 1);
+                    const float4* o = (const float4*)(slot(i0 + i) + 2 * ROWS) + c * ROWS + r;
+                    const float4 y = __ldcg(o), z = __ldcg(o + ROWS);
                     const float f = wt[i * ROWS + r];
                     x[0] = __fmaf_rn(y.x, f, x[0]), x[1] = __fmaf_rn(y.y, f, x[1]);
                     x[2] = __fmaf_rn(y.z, f, x[2]), x[3] = __fmaf_rn(y.w, f, x[3]);
@@ -800,12 +850,12 @@ struct Soft {
                 }
                 if (i0 + P < segs) {
                     acc[0] = make_float4(x[0], x[1], x[2], x[3]);
-                    acc[1] = make_float4(x[4], x[5], x[6], x[7]);
-                } else {
+                    acc[ROWS] = make_float4(x[4], x[5], x[6], x[7]);
+                } else if (r < rows) {
                     uint32_t o[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[e] = bf16x2(x[2 * e], x[2 * e + 1]);
-                    *(uint4*)(out_row(a, u, r) + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *(uint4*)(out_row(a, u, r) + 4 * c) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
         }
@@ -823,24 +873,23 @@ __global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtA
     if (wid == 0) dt_tmem_alloc(&sh->tmem, 512);
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) {
-            dt_mbar_init(&sh->kfull[i], NC);
-            dt_mbar_init(&sh->vfull[i], NC);
-            dt_mbar_init(&sh->kfree[i], 1);
-            dt_mbar_init(&sh->vfree[i], 1);
+            dt_mbar_init(&sh->kfull[i], NC / 32);
+            dt_mbar_init(&sh->vfull[i], NC / 32);
+            dt_mbar_init(&sh->kfree[i], 2);
+            dt_mbar_init(&sh->vfree[i], 2);
         }
-        for (int i = 0; i < 2; ++i) {
-            dt_mbar_init(&sh->sfull[i], 1);
-            dt_mbar_init(&sh->pfull[i], TQ);
-            dt_mbar_init(&sh->ofull[i], 1);
+        for (int i = 0; i < 4; ++i) {
+            dt_mbar_init(&sh->sfull[i >> 1][i & 1], 1);
+            dt_mbar_init(&sh->pfull[i >> 1][i & 1], TQ / 32);
         }
         for (int i = 0; i < RING; ++i) {
             dt_mbar_init(&sh->scfull[i], 2);
             dt_mbar_init(&sh->idfull[i], 1);
-            dt_mbar_init(&sh->ringfree[i], 1);
+            dt_mbar_init(&sh->ringfree[i], 2);
         }
         for (int i = 0; i < SEGS; ++i) {
             dt_mbar_init(&sh->segfull[i], 1);
-            dt_mbar_init(&sh->segfree[i], NS + 2 * NC + 1 + 32);
+            dt_mbar_init(&sh->segfree[i], NS + 2 * NC + 2 + 32);
         }
         dt_mbar_init(&sh->qfull, NS);
         dt_fence_mbar_init();
@@ -857,17 +906,16 @@ __global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtA
         set_regs<REG_SOFT>();
         at_zero_rest(a, cta, ctas, tid, NS);
         Soft<D>::run(a, sm, sh, tmem, tid, cta, part, counters);
-    } else if (tid < NS + NC) {
-        set_regs<REG_CONV>();
-        Conv<D, true>::run(a, sm, sh, tid - NS);
     } else if (tid < NS + 2 * NC) {
         set_regs<REG_CONV>();
-        Conv<D, false>::run(a, sm, sh, tid - NS - NC);
+        Conv<D>::run(a, sm, sh, (tid - NS) % NC, tid < NS + NC);
     } else {
         set_regs<REG_MMA>();
-        if (tid == NS + 2 * NC) issue_all<D>(sm, sh, tmem);
+        constexpr int W0 = (NS + 2 * NC) / 32;
+        if (wid == W0 || wid == W0 + 3)
+            issue_slot<D>(sm, sh, __shfl_sync(0xffffffffu, tmem, 0), __shfl_sync(0xffffffffu, wid != W0, 0));
         if (tid == NS + 2 * NC + 32) walk_share(a, sh, cta);
-        if (wid == (NS + 2 * NC) / 32 + 2) look_up<D>(a, sh, tid & 31);
+        if (wid == W0 + 2) look_up<D>(a, sh, tid & 31);
     }
     dt_tc_fence_before();
     __syncthreads();
