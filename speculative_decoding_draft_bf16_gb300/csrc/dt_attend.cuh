@@ -25,7 +25,7 @@ struct AtReq {  // one request
 template <int ROWS>
 struct AtPlan {
     // Cost of a tile of a block: a block of at most half the rows costs less.
-    static constexpr uint32_t FULL = 5, PART = 3;
+    static constexpr uint32_t FULL = 5, PART = 4;
     static DT_DI uint32_t weight(int rows) { return rows > ROWS / 2 ? FULL : PART; }
     static DT_DI AtReq req(const DtAttend& a, int b) {
         AtReq r;

@@ -37,7 +37,7 @@ constexpr int NT = NS + 2 * NC + 128;
 // CTA they sum to what it is launched with, LAUNCH_REGS each.  No loop of a role may
 // spill: the shared memory in use leaves the L1 less than the spills need.
 constexpr int LAUNCH_REGS = 65536 / NT / 8 * 8;
-constexpr int REG_SOFT = 112, REG_CONV = 104, REG_MMA = 48;
+constexpr int REG_SOFT = 120, REG_CONV = 96, REG_MMA = 48;
 static_assert(NS * REG_SOFT + 2 * NC * REG_CONV + 128 * REG_MMA == NT * LAUNCH_REGS, "register split");
 constexpr int STAGES = 2;       // K and V tiles in shared memory, each
 constexpr int RING = 8;         // tiles whose page ids and scales are kept
@@ -47,10 +47,16 @@ constexpr uint32_t MIN_SHARE = 10;    // least cost worth a CTA: two tiles of a 
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float HEADROOM = 5.f, LAZY = 8.f;
 
+struct Scales {  // of four groups of 16 tokens: key scale, log2 and inverse of the value scale
+    float4 ks, lv, iv;
+};
 struct __align__(16) Ring {
-    float ks[8], lv[8], iv[8];  // key scale, log2 and inverse of the value scale per 16 tokens
+    Scales half[2];
     uint32_t id[8];             // their pages
     uint32_t bad[2][4];         // new rows with a key, a value that is not finite
+    DT_DI float* ks(int g) { return &half[g >> 2].ks.x + (g & 3); }
+    DT_DI float* lv(int g) { return &half[g >> 2].lv.x + (g & 3); }
+    DT_DI float* iv(int g) { return &half[g >> 2].iv.x + (g & 3); }
 };
 
 // The tiles [t0, t1) of a unit (b, h, qb), from the walk to the roles.
@@ -275,10 +281,10 @@ struct Conv {
         }
         if (ct < 8) {
             if (keys) {
-                ring->ks[ct] = dt_pow2(e);
+                *ring->ks(ct) = dt_pow2(e);
             } else {
-                ring->lv[ct] = (float)e;
-                ring->iv[ct] = dt_pow2(-e);
+                *ring->lv(ct) = (float)e;
+                *ring->iv(ct) = dt_pow2(-e);
             }
         }
         group_sync(keys);
@@ -316,30 +322,36 @@ struct Conv {
                 load(j, g, 0);
                 load(j, g, NI / 2);
             }
+            auto stored = [&](int s) {
+                dt_fence_proxy_async_smem();
+                __syncwarp();
+                if ((ct & 31) == 0) dt_mbar_arrive(&full[s]);
+            };
+#pragma unroll 1
+            for (; j < cend; ++j, ++g) {
+                const int s = g % STAGES;
+                wait(&free_[s], (g / STAGES + 1) & 1, &sh->fail);
+                if (ct == 0) dt_mbar_arrive(&sh->scfull[g % RING]);
+                const uint32_t o = s * L::TILE;
+                const bool more = j + 1 < cend;
+                if (more) wait(&sh->idfull[(g + 1) % RING], ((g + 1) / RING) & 1, &sh->fail);
+#pragma unroll
+                for (int i0 = 0; i0 < NI; i0 += NI / 2) {
+#pragma unroll
+                    for (int i = i0; i < i0 + NI / 2; ++i)  // rows TPI apart, a multiple of 8, swizzle alike
+                        store_codes(a0 + o + i * (TPI * 128), a1 + o + i * (TPI * 128), q[i]);
+                    if (more) load(j + 1, g + 1, i0);
+                }
+                stored(s);
+            }
 #pragma unroll 1
             for (; j < t1; ++j, ++g) {
                 const int s = g % STAGES;
                 wait(&free_[s], (g / STAGES + 1) & 1, &sh->fail);
-                if (j < cend) {
-                    if (ct == 0) dt_mbar_arrive(&sh->scfull[g % RING]);
-                    const uint32_t o = s * L::TILE;
-                    const bool more = j + 1 < cend;
-                    if (more) wait(&sh->idfull[(g + 1) % RING], ((g + 1) / RING) & 1, &sh->fail);
-#pragma unroll
-                    for (int i0 = 0; i0 < NI; i0 += NI / 2) {
-#pragma unroll
-                        for (int i = i0; i < i0 + NI / 2; ++i)  // rows TPI apart, a multiple of 8, swizzle alike
-                            store_codes(a0 + o + i * (TPI * 128), a1 + o + i * (TPI * 128), q[i]);
-                        if (more) load(j + 1, g + 1, i0);
-                    }
-                } else {
-                    wait(&sh->idfull[g % RING], (g / RING) & 1, &sh->fail);  // the ring's slot is free
-                    fresh(a, u, keys, (j - u.ctx) * AT_TILE, ct, sh, &sh->ring[g % RING], base + s * L::TILE);
-                    if (ct == 0) dt_mbar_arrive(&sh->scfull[g % RING]);
-                }
-                dt_fence_proxy_async_smem();
-                __syncwarp();
-                if ((ct & 31) == 0) dt_mbar_arrive(&full[s]);
+                wait(&sh->idfull[g % RING], (g / RING) & 1, &sh->fail);  // the ring's slot is free
+                fresh(a, u, keys, (j - u.ctx) * AT_TILE, ct, sh, &sh->ring[g % RING], base + s * L::TILE);
+                if (ct == 0) dt_mbar_arrive(&sh->scfull[g % RING]);
+                stored(s);
             }
         }
     }
@@ -384,8 +396,8 @@ DT_DI void look_up(const DtAttend& a, Shared* sh, int lane) {
                 if ((lane >> 3) == d && k + d < ctx) {
                     Ring* ring = &sh->ring[g % RING];
                     ring->id[grp] = id;
-                    ring->ks[grp] = ks;
-                    scale_parts(vs, ring->lv[grp], ring->iv[grp]);
+                    *ring->ks(grp) = ks;
+                    scale_parts(vs, *ring->lv(grp), *ring->iv(grp));
                 }
                 __syncwarp();
                 if (lane == 0) dt_mbar_arrive(&sh->idfull[g % RING]);
@@ -543,50 +555,44 @@ struct Soft {
         return make_uint2(at_mask_word(a, u.b, node, m0, u.n), at_mask_word(a, u.b, node, m0 + 32, u.n));
     }
 
-    template <bool MASKED>
-    static DT_DI void blank(uint32_t (&x)[32], uint32_t bits) {
-        if constexpr (MASKED) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (!((bits >> i) & 1)) x[i] = 0xFF800000u;  // -infinity
-        }
-    }
-
     // 64 tokens of a row: their scores at ts become probabilities in place, the
     // running reference m and sum l move on, and O is rescaled when it has sums;
     // before that every product of the slot must be done: `other` is the barrier
-    // of the other half's.  `ks`, `lv`, `iv`: the scales of the four groups.
-    template <bool MASKED>
-    static DT_DI void half(const float* ks, const float* lv, const float* iv, uint32_t ts, uint32_t to, bool has_o,
-                           float rowc, uint2 mk, float& m, float& l, uint64_t* other, uint32_t other_ph, int* fail) {
+    // of the other half's.  sc: the scales of the four groups.
+    static DT_DI void half(const Scales* sc, uint32_t ts, uint32_t to, bool has_o, float rowc, bool masked, uint2 mk,
+                           float& m, float& l, uint64_t* other, uint32_t other_ph, int* fail) {
         const float NEG_INF = -__int_as_float(0x7F800000);
-        if (MASKED && !__any_sync(0xffffffffu, mk.x | mk.y)) {  // none of the warp's rows sees any of them
+        if (masked && !__any_sync(0xffffffffu, mk.x | mk.y)) {  // none of the warp's rows sees any of them
             const uint32_t z[16] = {};
             dt_tmem_st16(ts, z);
             dt_tmem_st16(ts + 16, z);
             dt_tmem_st_wait();
             return;
         }
-        // The two passes read the scores again rather than keep them, 32 columns
-        // in a turn: short code and few registers.
-        float mx = NEG_INF;  // the largest score + log2 of its value scale
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-            uint32_t x[32];
-            dt_tmem_ld32(ts + 32 * c, x);
-            blank<MASKED>(x, c ? mk.y : mk.x);
+        uint32_t x[64];
+        const float4 ks = sc->ks, lv = sc->lv, iv = sc->iv;
+        dt_tmem_ld64(ts, x);
+        const float ka[4] = {__fmul_rn(rowc, ks.x), __fmul_rn(rowc, ks.y), __fmul_rn(rowc, ks.z), __fmul_rn(rowc, ks.w)};
+        const float l4[4] = {lv.x, lv.y, lv.z, lv.w}, i4[4] = {iv.x, iv.y, iv.z, iv.w};
+        if (masked) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                float q0 = __uint_as_float(x[16 * g]), q1 = __uint_as_float(x[16 * g + 1]);
-#pragma unroll
-                for (int i = 2; i < 14; i += 4) {
-                    q0 = max3(q0, __uint_as_float(x[16 * g + i]), __uint_as_float(x[16 * g + i + 1]));
-                    q1 = max3(q1, __uint_as_float(x[16 * g + i + 2]), __uint_as_float(x[16 * g + i + 3]));
-                }
-                q0 = max3(q0, __uint_as_float(x[16 * g + 14]), __uint_as_float(x[16 * g + 15]));
-                mx = fmaxf(mx, __fmaf_rn(fmaxf(q0, q1), __fmul_rn(rowc, ks[2 * c + g]), lv[2 * c + g]));
-            }
+            for (int i = 0; i < 64; ++i)
+                if (!(((i < 32 ? mk.x : mk.y) >> (i & 31)) & 1)) x[i] = 0xFF800000u;  // -infinity
         }
+        // the largest score + log2 of its value scale
+        float tg[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            float q0 = __uint_as_float(x[16 * g]), q1 = __uint_as_float(x[16 * g + 1]);
+#pragma unroll
+            for (int i = 2; i < 14; i += 4) {
+                q0 = max3(q0, __uint_as_float(x[16 * g + i]), __uint_as_float(x[16 * g + i + 1]));
+                q1 = max3(q1, __uint_as_float(x[16 * g + i + 2]), __uint_as_float(x[16 * g + i + 3]));
+            }
+            q0 = max3(q0, __uint_as_float(x[16 * g + 14]), __uint_as_float(x[16 * g + 15]));
+            tg[g] = __fmaf_rn(fmaxf(q0, q1), ka[g], l4[g]);
+        }
+        const float mx = fmaxf(max3(tg[0], tg[1], tg[2]), tg[3]);
         // a maximum that has grown moves the reference; rows of a warp do so together
         const bool grown = mx > m + (HEADROOM + LAZY);
         if (__any_sync(0xffffffffu, grown)) {
@@ -610,30 +616,29 @@ struct Soft {
             }
         }
         const float mu = m == NEG_INF ? 0.f : m;
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-            uint32_t x[32], p[16];
-            dt_tmem_ld32(ts + 32 * c, x);
-            blank<MASKED>(x, c ? mk.y : mk.x);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const float ka = __fmul_rn(rowc, ks[2 * c + g]), kb = __fsub_rn(lv[2 * c + g], mu);
-                const unsigned long long ka2 = dt_f2_pack(ka, ka), kb2 = dt_f2_pack(kb, kb);
+        for (int g2 = 0; g2 < 4; g2 += 2) {
+            uint32_t p[16];
+#pragma unroll
+            for (int g = g2; g < g2 + 2; ++g) {
+                const float kb = __fsub_rn(l4[g], mu);
+                const unsigned long long ka2 = dt_f2_pack(ka[g], ka[g]), kb2 = dt_f2_pack(kb, kb);
                 unsigned long long sum = dt_f2_pack(0.f, 0.f);
 #pragma unroll
-                for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+                for (int i = 0; i < 16; i += 2) {
                     float e0, e1;
-                    dt_f2_unpack(dt_f2_fma(dt_f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), ka2, kb2), e0, e1);
+                    dt_f2_unpack(dt_f2_fma(dt_f2_pack(__uint_as_float(x[16 * g + i]), __uint_as_float(x[16 * g + i + 1])),
+                                           ka2, kb2), e0, e1);
                     e0 = dt_ex2_approx(e0);
                     e1 = dt_ex2_approx(e1);
                     sum = dt_f2_add(sum, dt_f2_pack(e0, e1));
-                    p[i / 2] = f16x2(e0, e1);
+                    p[8 * (g - g2) + i / 2] = f16x2(e0, e1);
                 }
                 float s0, s1;
                 dt_f2_unpack(sum, s0, s1);
-                l = __fmaf_rn(__fadd_rn(s0, s1), iv[2 * c + g], l);
+                l = __fmaf_rn(__fadd_rn(s0, s1), i4[g], l);
             }
-            dt_tmem_st16(ts + 16 * c, p);  // columns read already
+            dt_tmem_st16(ts + 8 * g2, p);  // over columns that are in registers
         }
         dt_tmem_st_wait();
     }
@@ -644,7 +649,7 @@ struct Soft {
         const float NEG_INF = -__int_as_float(0x7F800000);
         const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
         const uint32_t ts = tmem + s * AT_TILE + lanes, to = tmem + 2 * AT_TILE + s * D + lanes;
-        uint32_t g0 = 0, ph[2] = {0u, 0u}, seg = 0;  // ph: phases of sfull[s][h] waited for
+        uint32_t g0 = 0, ph = 0, seg = 0;  // ph: next phase of sfull[s][0] and [1]
         for (const Seg* sg; (sg = get_segment(sh, seg)) != nullptr; release_segment(sh, seg++)) {
             const Seg& u = *sg;
             // every product of the last segment has read its queries
@@ -657,43 +662,42 @@ struct Soft {
             const float rowc = sh->qscale[row];
             float m = NEG_INF, l = 0.f;
             bool poison = false;
-            for (int lt = dual ? 0 : s; lt < nt; lt += hop) {
+            const int clear = len / AT_TILE - u.t0;  // tiles before this one are wholly visible
+            uint32_t pa = ph & 1;                    // phase of both halves' scores
+#pragma unroll 1
+            for (int lt = dual ? 0 : s; lt < nt; lt += hop, pa ^= 1) {
                 const uint32_t g = g0 + lt;
                 const Ring* ring = &sh->ring[g % RING];
-                const int t = u.t0 + lt;
+                wait(&sh->scfull[g % RING], (g / RING) & 1, &sh->fail);
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
-                    const bool masked = (t + 1) * AT_TILE > len;
-                    uint2 mk = make_uint2(~0u, ~0u);
-                    if (masked) mk = mask_words(a, u, t, h, row);
-                    if (h == 0) wait(&sh->scfull[g % RING], (g / RING) & 1, &sh->fail);
-                    wait(&sh->sfull[s][h], (h ? ph[1] : ph[0]) & 1, &sh->fail);
-                    __syncwarp();
-                    dt_tc_fence_after();
                     uint64_t* other = &sh->sfull[s][h ^ 1];  // of half 0: waited for next; of half 1: of the next tile
-                    const uint32_t other_ph = (h ? ph[0] + 1 : ph[1]) & 1;
-                    const float *ks = ring->ks + 4 * h, *lv = ring->lv + 4 * h, *iv = ring->iv + 4 * h;
+                    const uint32_t other_ph = pa ^ h, st = ts + 64 * h;
+                    const bool has_o = lt >= hop || h;
+                    const bool masked = lt >= clear;
+                    uint2 mk = make_uint2(0u, 0u);
                     if (masked) {
-                        if (t >= u.ctx)
+                        mk = mask_words(a, u, u.t0 + lt, h, row);
+                        if (u.t0 + lt >= u.ctx)
                             poison |= ((mk.x & (ring->bad[0][2 * h] | ring->bad[1][2 * h])) |
                                        (mk.y & (ring->bad[0][2 * h + 1] | ring->bad[1][2 * h + 1]))) != 0u;
-                        half<true>(ks, lv, iv, ts + 64 * h, to, lt >= hop || h, rowc, mk, m, l, other, other_ph, &sh->fail);
-                    } else {
-                        half<false>(ks, lv, iv, ts + 64 * h, to, lt >= hop || h, rowc, mk, m, l, other, other_ph, &sh->fail);
                     }
+                    wait(&sh->sfull[s][h], pa, &sh->fail);
+                    __syncwarp();
+                    dt_tc_fence_after();
+                    half(&ring->half[h], st, to, has_o, rowc, masked, mk, m, l, other, other_ph, &sh->fail);
                     dt_tc_fence_before();
                     __syncwarp();
                     if ((tid & 31) == 0) dt_mbar_arrive(&sh->pfull[s][h]);
                 }
-                ++ph[0];
-                ++ph[1];
             }
             if (poison) l = __int_as_float(0x7FC00000);
             // the segment's sums
             const bool any = dual || s < nt;  // the slot had a tile
             if (any) {
-                wait(&sh->sfull[s][0], ph[0]++ & 1, &sh->fail);
-                wait(&sh->sfull[s][1], ph[1]++ & 1, &sh->fail);
+                wait(&sh->sfull[s][0], pa, &sh->fail);
+                wait(&sh->sfull[s][1], pa, &sh->fail);
+                ph = pa ^ 1;
                 __syncwarp();
                 dt_tc_fence_after();
             }
