@@ -187,7 +187,7 @@ struct DtAttend {
     void* out;
     int32_t* status;
 };
-cudaError_t dt_kn11_launch(const DtAttend& a, cudaStream_t st);
+cudaError_t dt_kn11_launch(const DtAttend& a, void* workspace, int ctas, cudaStream_t st);
 // The same for many rows per key head, on the tensor cores (kn12_attend_tc.cu),
 // with ctas CTAs and dt_kn12_workspace bytes.
 size_t dt_kn12_workspace(int D, int ctas);

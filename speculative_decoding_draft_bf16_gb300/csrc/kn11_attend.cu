@@ -1,99 +1,527 @@
-// kn11_attend.cu -- tree attention over the paged e4m3 cache (dt_tree_attention).
+// kn11_attend.cu -- tree attention for up to 16 query rows per key head (single
+// tokens and small trees), bound by the reading of the cache (dt_tree_attention).
 //
-// One warp per query row: the lanes share the head's elements, keys come one
-// at a time, with a running maximum and sum.  fp32 throughout.
-#include "dt_cache.cuh"
-#include "dt_launch.h"
+// A CTA streams runs of 128-token tiles, 16 tokens to each of its 8 warps.  A
+// lane copies the bytes that it will need itself to its own places in shared
+// memory (cp.async, STAGES tiles ahead: up to 160 KB of a CTA's loads are in
+// flight, and nothing is waited for but the lane's own copies), turns the e4m3
+// codes into fp16 in registers and feeds 16 x 8 x 16 MMAs:
+//   S = Q K^T   a lane's 32 bytes of a token serve as the K-fragment of all
+//               steps: which elements of the head a step takes is free, as long
+//               as Q's fragments are cut alike;
+//   O += P V    P's fragments are S's; a lane reads 16 columns of four tokens and
+//               pairs the tokens' bytes before it converts them.
+// (These narrow products cannot fill a tcgen05 tile: 16 rows of 128, and the
+// cache's bytes, not the products, bound the time.)  Scales as on the tensor
+// cores: P holds 2^(t + log2 vs - m), the row sum adds p / vs, and m moves only
+// when the maximum has grown by more than 8.  The warps' sums are joined in
+// shared memory, the CTAs' in the workspace.
+#include "dt_attend.cuh"
 
 namespace {
 
-constexpr int NW = 4;  // warps (query rows) per CTA
+constexpr int ROWS = 16, NW = 8, NT = NW * 32;
+constexpr int ATOM = 2;              // tiles of the longest unit that is not split
+constexpr uint32_t MIN_SHARE = 2;    // tiles worth a CTA
+constexpr float LOG2E = 1.44269504088896340736f;
+constexpr float HEADROOM = 5.f, LAZY = 8.f;
 
 template <int D>
-__global__ void __launch_bounds__(NW * 32) kn11_kernel(DtAttend a) {
-    constexpr int E = D / 32;  // elements per lane
-    __shared__ float vec[NW][2][D];
+struct Lay {
+    static constexpr int KC = D / 64;             // 16-byte pieces of a token's keys per lane
+    static constexpr int VB = D / 8;              // bytes of a token's values per lane
+    static constexpr int STAGES = D == 128 ? 5 : 8;
+    static constexpr int KBYTES = 2 * KC * 512, BYTES = KBYTES + 4 * VB * 32;  // per warp and stage
+    static constexpr size_t FIFO = (size_t)NW * STAGES * BYTES;
+    static constexpr size_t JOIN = (size_t)NW * ROWS * D * 4;
+    static constexpr size_t SMEM = FIFO > JOIN ? FIFO : JOIN;
+};
+
+struct Shared {
+    AtShare share;
+    float m[NW][ROWS], l[NW][ROWS], w[NW][ROWS];
+    int last;
+};
+
+DT_DI uint32_t f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+DT_DI uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *(const uint32_t*)&v;
+}
+DT_DI void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <int BYTES>
+DT_DI void copy_async(uint32_t dst, const void* src) {
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+template <int WORDS>
+DT_DI void lds(uint32_t addr, uint32_t (&w)[WORDS]) {
+    if constexpr (WORDS == 4)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+    else
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+}
+
+template <int D>
+struct Stream {
+    using L = Lay<D>;
+    using Walk = AtWalk<ROWS, ATOM>;
+    static constexpr int KS = D / 16;  // steps of Q K^T
+    static constexpr int NV = D / 8;   // column tiles of P V; tile j has columns NV * g + j
+
+    uint32_t q[KS][4];                 // Q's fragments (rows g and g + 8)
+    float rowc[2], m[2], l[2];
+    float o[NV][4];
+
+    // Two 8-element chunks (16 elements from 16 * c) of a head vector, rotated.
+    static DT_DI void pick16(const uint16_t* row, int c, const dt_rope& r, int at, float (&x)[16]) {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            dt_rotated8(row, 2 * c + i, r, at, y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[8 * i + e] = y[e];
+        }
+    }
+
+    DT_DI void queries(const DtAttend& a, const Walk& u, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = g + 8 * i;
+            float x[L::KC][16];
+            uint32_t big = 0;
+#pragma unroll
+            for (int j = 0; j < L::KC; ++j) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[j][e] = 0.f;
+            }
+            if (r < u.rows) {
+                const int n = r / a.G;
+                const uint16_t* p = (const uint16_t*)a.q.ptr + u.b * a.q.stride_b + n * a.q.stride_n +
+                                    (u.h * a.G + r % a.G) * a.q.stride_h;
+                const int at = a.rope.rot ? at_position(a, u.b, u.r.len, n) : 0;
+#pragma unroll
+                for (int j = 0; j < L::KC; ++j) {
+                    pick16(p, t + 4 * j, a.rope, at, x[j]);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) big = max(big, __float_as_uint(x[j][e]) & 0x7FFFFFFFu);
+                }
+            }
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            int ex = (int)(big >> 23) - 127;  // largest magnitude in [2^ex, 2^(ex+1))
+            ex = big >= 0x7F800000u ? 0 : max(ex, -100);
+            const float f = dt_pow2(-ex);
+            rowc[i] = __fmul_rn(__fmul_rn(a.scale, LOG2E), dt_pow2(ex));
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const float* y = x[s >> 2] + 4 * (s & 3);
+                q[s][i] = f16x2(__fmul_rn(y[0], f), __fmul_rn(y[1], f));
+                q[s][2 + i] = f16x2(__fmul_rn(y[2], f), __fmul_rn(y[3], f));
+            }
+        }
+    }
+
+    // Scores of two groups of 8 tokens (columns 2t, 2t + 1 of each; rows g, g + 8),
+    // masked, to probabilities as the fragments of P; ks, lv, iv: the 16 tokens'.
+    DT_DI void weigh(float (&c)[2][4], float ks, float lv, float iv, uint32_t (&p)[4]) {
+        const float NEG_INF = -__int_as_float(0x7F800000);
+        const float k0 = __fmul_rn(rowc[0], ks), k1 = __fmul_rn(rowc[1], ks);
+        float t0 = fmaxf(fmaxf(c[0][0], c[0][1]), fmaxf(c[1][0], c[1][1]));
+        float t1 = fmaxf(fmaxf(c[0][2], c[0][3]), fmaxf(c[1][2], c[1][3]));
+        t0 = __fmaf_rn(t0, k0, lv);
+        t1 = __fmaf_rn(t1, k1, lv);
+        if (__any_sync(0xffffffffu, t0 > m[0] + (HEADROOM + LAZY) || t1 > m[1] + (HEADROOM + LAZY))) {
+#pragma unroll
+            for (int x = 1; x < 4; x <<= 1) {
+                t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
+                t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
+            }
+            const float n0 = t0 > m[0] + (HEADROOM + LAZY) ? t0 - HEADROOM : m[0];
+            const float n1 = t1 > m[1] + (HEADROOM + LAZY) ? t1 - HEADROOM : m[1];
+            const float f0 = n0 == m[0] ? 1.f : dt_ex2_approx(m[0] - n0);  // m = -inf: 0
+            const float f1 = n1 == m[1] ? 1.f : dt_ex2_approx(m[1] - n1);
+            m[0] = n0, m[1] = n1;
+            l[0] = __fmul_rn(l[0], f0), l[1] = __fmul_rn(l[1], f1);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                o[j][0] = __fmul_rn(o[j][0], f0), o[j][1] = __fmul_rn(o[j][1], f0);
+                o[j][2] = __fmul_rn(o[j][2], f1), o[j][3] = __fmul_rn(o[j][3], f1);
+            }
+        }
+        const float b0 = __fsub_rn(lv, m[0] == NEG_INF ? 0.f : m[0]), b1 = __fsub_rn(lv, m[1] == NEG_INF ? 0.f : m[1]);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[n][e] = dt_ex2_approx(__fmaf_rn(c[n][e], e < 2 ? k0 : k1, e < 2 ? b0 : b1));
+        }
+        l[0] = __fmaf_rn(__fadd_rn(__fadd_rn(c[0][0], c[0][1]), __fadd_rn(c[1][0], c[1][1])), iv, l[0]);
+        l[1] = __fmaf_rn(__fadd_rn(__fadd_rn(c[0][2], c[0][3]), __fadd_rn(c[1][2], c[1][3])), iv, l[1]);
+        p[0] = f16x2(c[0][0], c[0][1]);
+        p[1] = f16x2(c[0][2], c[0][3]);
+        p[2] = f16x2(c[1][0], c[1][1]);
+        p[3] = f16x2(c[1][2], c[1][3]);
+    }
+
+    // The staged 16 tokens at `st`, of which the first `left` exist.
+    DT_DI void tile(uint32_t st, int lane, int left, float ks, float vs) {
+        const int t = lane & 3;
+        const uint32_t my = st + lane * 16;
+        float c[2][4] = {};
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+#pragma unroll
+            for (int j = 0; j < L::KC; ++j) {
+                uint32_t w[4];
+                lds<4>(my + (n * L::KC + j) * 512, w);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) mma(c[n], q[4 * j + s], dt_e4m3x2_to_f16x2(w[s]), dt_e4m3x2_to_f16x2(w[s] >> 16));
+            }
+        }
+        if (left < 16) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (8 * n + 2 * t + (e & 1) >= left) c[n][e] = -__int_as_float(0x7F800000);
+            }
+        }
+        uint32_t p[4];
+        weigh(c, ks, log2f(vs), 1.0f / vs, p);
+        // values of tokens 2t, 2t + 1, 2t + 8, 2t + 9
+        constexpr int VW = L::VB / 4;
+        uint32_t w[4][VW];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) lds<VW>(st + L::KBYTES + k * (L::VB * 32) + lane * L::VB, w[k]);
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+            const uint32_t a0 = __byte_perm(w[0][j], w[1][j], 0x5140), a1 = __byte_perm(w[0][j], w[1][j], 0x7362);
+            const uint32_t b0 = __byte_perm(w[2][j], w[3][j], 0x5140), b1 = __byte_perm(w[2][j], w[3][j], 0x7362);
+            mma(o[4 * j], p, dt_e4m3x2_to_f16x2(a0), dt_e4m3x2_to_f16x2(b0));
+            mma(o[4 * j + 1], p, dt_e4m3x2_to_f16x2(a0 >> 16), dt_e4m3x2_to_f16x2(b0 >> 16));
+            mma(o[4 * j + 2], p, dt_e4m3x2_to_f16x2(a1), dt_e4m3x2_to_f16x2(b1));
+            mma(o[4 * j + 3], p, dt_e4m3x2_to_f16x2(a1 >> 16), dt_e4m3x2_to_f16x2(b1 >> 16));
+        }
+    }
+
+    // Up to 16 new rows (one warp): rotated, scaled by powers of two to a largest
+    // magnitude below 2, a row that is not finite replaced by zeros and reported
+    // to those that see it.
+    DT_DI void fresh(const DtAttend& a, const Walk& u, int lane) {
+        const int g = lane >> 2, t = lane & 3, n = u.r.n;
+        const uint16_t* kp = (const uint16_t*)a.k.ptr + u.b * a.k.stride_b + u.h * a.k.stride_h;
+        const uint16_t* vp = (const uint16_t*)a.v.ptr + u.b * a.v.stride_b + u.h * a.v.stride_h;
+        uint32_t bad = 0;  // bit per row
+        auto clean = [&](float (&x)[16], int row, uint32_t& big) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const uint32_t v = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+                if (v >= 0x7F800000u) x[e] = 0.f, bad |= 1u << row;
+                else big = max(big, v);
+            }
+        };
+        auto exponent = [](uint32_t big) {
+            big = __reduce_max_sync(0xffffffffu, big);
+            return max((int)(big >> 23) - 127, -57);
+        };
+        float c[2][4] = {};
+        float k[2][L::KC][16];
+        uint32_t big = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = g + 8 * i;
+#pragma unroll
+            for (int j = 0; j < L::KC; ++j) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) k[i][j][e] = 0.f;
+                if (row < n) {
+                    pick16(kp + row * a.k.stride_n, t + 4 * j, a.rope, at_position(a, u.b, u.r.len, row), k[i][j]);
+                    clean(k[i][j], row, big);
+                }
+            }
+        }
+        const int ek = exponent(big);
+        const float fk = dt_pow2(-ek);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const float* y = k[i][s >> 2] + 4 * (s & 3);
+                mma(c[i], q[s], f16x2(__fmul_rn(y[0], fk), __fmul_rn(y[1], fk)), f16x2(__fmul_rn(y[2], fk), __fmul_rn(y[3], fk)));
+            }
+        }
+        float v[4][L::VB];
+        big = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 2 * t + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+            for (int e = 0; e < L::VB; e += 8) {
+                float y[8] = {};
+                if (row < n) dt_load8(vp + row * a.v.stride_n + L::VB * g + e, y);
+#pragma unroll
+                for (int k8 = 0; k8 < 8; ++k8) {
+                    const uint32_t w = __float_as_uint(y[k8]) & 0x7FFFFFFFu;
+                    if (w >= 0x7F800000u) y[k8] = 0.f, bad |= 1u << row;
+                    else big = max(big, w);
+                    v[i][e + k8] = y[k8];
+                }
+            }
+        }
+        const int ev = exponent(big);
+        const float fv = dt_pow2(-ev);
+        bad = __reduce_or_sync(0xffffffffu, bad);
+        // what rows g and g + 8 see
+        bool poison[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = g + 8 * i;
+            const uint32_t sees = r < u.rows ? at_mask_word(a, u.b, r / a.G, 0, n) : 0u;
+            poison[i] = (sees & bad) != 0u;
+#pragma unroll
+            for (int k8 = 0; k8 < 2; ++k8) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (!((sees >> (8 * k8 + 2 * t + e)) & 1)) c[k8][2 * i + e] = -__int_as_float(0x7F800000);
+            }
+        }
+        uint32_t p[4];
+        weigh(c, dt_pow2(ek), (float)ev, dt_pow2(-ev), p);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (poison[i]) l[i] = __int_as_float(0x7FC00000);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            mma(o[j], p, f16x2(__fmul_rn(v[0][j], fv), __fmul_rn(v[1][j], fv)),
+                f16x2(__fmul_rn(v[2][j], fv), __fmul_rn(v[3][j], fv)));
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(NT, 1) kn11_kernel(const __grid_constant__ DtAttend a, float* part, int* counters) {
+    using L = Lay<D>;
+    using S = Stream<D>;
+    constexpr int NV = S::NV;
+    extern __shared__ __align__(128) unsigned char fifo[];
+    __shared__ Shared sh;
+    const float NEG_INF = -__int_as_float(0x7F800000);
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int cta = blockIdx.x, ctas = gridDim.x;
     dt_pdl_trigger();
     dt_pdl_wait();
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.z, h = blockIdx.y, n = blockIdx.x * NW + w;
-    if (n >= a.M) return;
-    const dt_kv_cache& c = a.c;
-    const int kh = h / (a.G);
-    uint16_t* out = (uint16_t*)a.out + (((size_t)b * a.M + n) * a.Hq + h) * D + lane * E;
-    int len = c.len[b], rows = a.n_nodes ? a.n_nodes[b] : a.M;
-    bool bad = len < 0 || (long long)len > (long long)c.max_pages * c.page || rows < 0 || rows > a.M;
-    if (bad) len = rows = 0;
-    float acc[E] = {}, m_run = -__int_as_float(0x7F800000), l_run = 0.f;
-    float q[E], x[8];
+    if (w == 0) at_share<ROWS>(a, cta, ctas, MIN_SHARE, &sh.share);
+    at_zero_rest(a, cta, ctas, tid, NT);
+    __syncthreads();
+    const AtShare share = sh.share;
+    const int lp = 31 - __clz(a.c.page), low = a.c.page - 1;
+    const uint32_t page_bytes = ((uint32_t)a.c.Hkv << lp) * D;
+    const uint32_t my_fifo = dt_smem_addr(fifo) + w * L::STAGES * L::BYTES;
+    AtWalk<ROWS, ATOM> u;
+    u.start(a, share);
+    S x;
+    for (; u.next(a, share, cta); u.step(a)) {
+        const int len = u.r.len, cend = min(u.t1, u.r.ctx), n = max(0, cend - u.t0);
+        const int* table = a.c.table + (size_t)u.b * a.c.max_pages;
+        const uint8_t* kbase = a.c.k + ((size_t)u.h << lp) * D + t * 16;
+        const uint8_t* vbase = a.c.v + ((size_t)u.h << lp) * D + g * L::VB;
+        // Pages and scales of this warp's 16 tokens of 32 tiles at a time, one
+        // tile to a lane; the next batch's pages are loaded a batch ahead.
+        auto page_at = [&](int i) {  // of tile t0 + i (past the end: of the last token)
+            const int tok = min((u.t0 + i) * AT_TILE + w * 16, len - 1);
+            uint32_t id = (uint32_t)table[tok >> lp];
+            if (id >= (uint32_t)a.c.n_pages) {
+                atomicOr(&a.status[u.b], DT_DEV_BAD_CACHE);
+                id = 0;
+            }
+            return id;
+        };
+        uint32_t id = 0, id_next = 0;
+        float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};  // of batches, by parity
+        auto scales_of = [&](uint32_t page, float& k, float& v) {
+            k = a.c.k_scale[(size_t)page * a.c.Hkv + u.h];
+            v = a.c.v_scale[(size_t)page * a.c.Hkv + u.h];
+        };
+        int issued = 0;
+        auto issue = [&]() {  // the next tile's copies (past the last one: none)
+            if (issued < n) {
+                if ((issued & 31) == 0 && issued > 0) {
+                    id = id_next;
+                    if ((issued >> 5) & 1) scales_of(id, ks[1], vs[1]);
+                    else scales_of(id, ks[0], vs[0]);
+                    id_next = page_at(issued + 32 + lane);
+                }
+                const uint32_t p = __shfl_sync(0xffffffffu, id, issued & 31);
+                const int tok0 = (u.t0 + issued) * AT_TILE + w * 16;
+                const size_t o = (size_t)p * page_bytes;
+                const uint32_t st = my_fifo + (issued % L::STAGES) * L::BYTES;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint8_t* src = kbase + o + (uint32_t)(min(tok0 + g + 8 * i, max(len - 1, tok0)) & low) * D;
+#pragma unroll
+                    for (int j = 0; j < L::KC; ++j) copy_async<16>(st + (i * L::KC + j) * 512 + lane * 16, src + 64 * j);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = min(tok0 + 2 * t + (i & 1) + 8 * (i >> 1), max(len - 1, tok0));
+                    copy_async<L::VB>(st + L::KBYTES + i * (L::VB * 32) + lane * L::VB, vbase + o + (uint32_t)(tok & low) * D);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            ++issued;
+        };
+        if (n > 0) {
+            id = page_at(lane);
+            id_next = page_at(32 + lane);
+            scales_of(id, ks[0], vs[0]);
+        }
+        for (int i = 0; i < L::STAGES - 1; ++i) issue();
+        x.queries(a, u, lane);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) x.o[j][0] = x.o[j][1] = x.o[j][2] = x.o[j][3] = 0.f;
+        x.m[0] = x.m[1] = NEG_INF;
+        x.l[0] = x.l[1] = 0.f;
+        for (int i = 0; i < n; ++i) {
+            issue();
+            asm volatile("cp.async.wait_group %0;" ::"n"(L::STAGES - 1) : "memory");
+            const bool odd = (i >> 5) & 1;
+            const float k = __shfl_sync(0xffffffffu, odd ? ks[1] : ks[0], i & 31);
+            const float v = __shfl_sync(0xffffffffu, odd ? vs[1] : vs[0], i & 31);
+            const int left = len - (u.t0 + i) * AT_TILE - w * 16;
+            if (left > 0) x.tile(my_fifo + (i % L::STAGES) * L::BYTES, lane, left, k, v);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (w == 0 && u.t1 > u.r.ctx) x.fresh(a, u, lane);
 
-    // a new row's vector (rotated when it is a query or key) by way of shared memory
-    auto fetch = [&](const dt_rows& r, int row, int head, bool turn, float (&o)[E]) {
-        const uint16_t* p = (const uint16_t*)r.ptr + b * r.stride_b + row * r.stride_n + head * r.stride_h;
-        if (lane < D / 8) {
-            int at = 0;
-            dt_rope rope = a.rope;
-            if (!turn) rope.rot = 0;
-            if (rope.rot) {
-                at = len + (a.pos ? a.pos[(size_t)b * a.M + row] : row);
-                if (at < 0 || at >= rope.max_pos) bad = true, at = 0;
+        // join the warps
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+            x.l[0] = __fadd_rn(x.l[0], __shfl_xor_sync(0xffffffffu, x.l[0], d));
+            x.l[1] = __fadd_rn(x.l[1], __shfl_xor_sync(0xffffffffu, x.l[1], d));
+        }
+        if (t == 0) {
+            sh.m[w][g] = x.m[0], sh.m[w][g + 8] = x.m[1];
+            sh.l[w][g] = x.l[0], sh.l[w][g + 8] = x.l[1];
+        }
+        __syncthreads();  // all copies have been read
+        // O as [warp][row][D]; a lane's columns NV * (2t + e) + j, j = 0 .. NV - 1
+        float* all = (float*)fifo;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = g + 8 * i;
+            if (r < u.rows) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float* dst = all + ((size_t)w * ROWS + r) * D + NV * (2 * t + e);
+#pragma unroll
+                    for (int j = 0; j < NV; j += 4)
+                        *(float4*)(dst + j) = make_float4(x.o[j][2 * i + e], x.o[j + 1][2 * i + e], x.o[j + 2][2 * i + e],
+                                                          x.o[j + 3][2 * i + e]);
+                }
             }
-            dt_rotated8(p, lane, rope, at, x);
-            for (int i = 0; i < 8; ++i) vec[w][turn][lane * 8 + i] = isfinite(x[i]) ? x[i] : __int_as_float(0x7FC00000);
         }
-        __syncwarp();
-        for (int i = 0; i < E; ++i) o[i] = vec[w][turn][lane * E + i];
-        __syncwarp();
-    };
-    auto add = [&](const float (&k)[E], const float (&v)[E], float ks, float vs) {
-        float s = 0.f;
-        for (int i = 0; i < E; ++i) s = fmaf(q[i], k[i], s);
-        s = dt_warp_sum(s) * ks * a.scale;
-        const float m = fmaxf(m_run, s);
-        const float f = m_run == m ? 1.f : expf(m_run - m), p = expf(s - m);
-        for (int i = 0; i < E; ++i) acc[i] = fmaf(acc[i], f, p * (v[i] * vs));
-        l_run = fmaf(l_run, f, p);
-        m_run = m;
-    };
-    if (n < rows) {
-        fetch(a.q, n, h, true, q);
-        for (int j = 0; j < len; ++j) {
-            int page = c.table[(size_t)b * c.max_pages + j / c.page];
-            if ((unsigned)page >= (unsigned)c.n_pages) bad = true, page = 0;
-            const size_t blk = (size_t)page * c.Hkv + kh;
-            const size_t off = (blk * c.page + j % c.page) * D + lane * E;
-            float k[E], v[E];
-            for (int i = 0; i < E; i += 2) {
-                const float2 kf = dt_e4m3x2_to_f32x2(*(const uint16_t*)(c.k + off + i));
-                const float2 vf = dt_e4m3x2_to_f32x2(*(const uint16_t*)(c.v + off + i));
-                k[i] = kf.x, k[i + 1] = kf.y, v[i] = vf.x, v[i + 1] = vf.y;
+        const bool whole = u.t0 == 0 && u.t1 == u.nt;
+        if (tid < ROWS) {
+            float M = NEG_INF, sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < NW; ++i) M = fmaxf(M, sh.m[i][tid]);
+#pragma unroll
+            for (int i = 0; i < NW; ++i) {
+                const float mi = sh.m[i][tid], f = mi == NEG_INF ? 0.f : dt_ex2_approx(mi - M);
+                sh.w[i][tid] = f;
+                sum = __fmaf_rn(sh.l[i][tid], f, sum);
             }
-            add(k, v, c.k_scale[blk], c.v_scale[blk]);
+            // NaN of a row that saw something not finite passes even with weight 0
+            sh.m[0][tid] = M;
+            sh.l[0][tid] = sum;
         }
-        const int words = (a.M + 31) / 32;
-        for (int m = 0; m < rows; ++m) {
-            const bool sees = a.mask ? (a.mask[((size_t)b * a.M + n) * words + m / 32] >> (m % 32)) & 1 : m <= n;
-            if (!sees) continue;
-            float k[E], v[E];
-            fetch(a.k, m, kh, true, k);
-            fetch(a.v, m, kh, false, v);
-            // a value that is not finite makes the whole row NaN
-            bool odd = false;
-            for (int i = 0; i < E; ++i) odd |= k[i] != k[i] || v[i] != v[i];
-            if (__any_sync(0xffffffffu, odd)) k[0] = __int_as_float(0x7FC00000);
-            add(k, v, 1.f, 1.f);
+        __syncthreads();
+        constexpr int C4 = D / 4;
+        float* my = part + (size_t)(2 * cta + (u.t0 == 0)) * ROWS * (D + 2);
+        auto out_row = [&](int r) {
+            return (uint16_t*)a.out + (((size_t)u.b * a.M + r / a.G) * a.Hq + u.h * a.G + r % a.G) * D;
+        };
+        for (int i = tid; i < u.rows * C4; i += NT) {
+            const int r = i / C4, c = i % C4 * 4;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < NW; ++k) {
+                const float4 z = *(const float4*)(all + ((size_t)k * ROWS + r) * D + c);
+                const float f = sh.w[k][r];
+                y.x = __fmaf_rn(z.x, f, y.x), y.y = __fmaf_rn(z.y, f, y.y);
+                y.z = __fmaf_rn(z.z, f, y.z), y.w = __fmaf_rn(z.w, f, y.w);
+            }
+            if (whole) {
+                const float sum = sh.l[0][r], inv = sum == 0.f ? 0.f : 1.0f / sum;
+                *(uint2*)(out_row(r) + c) = make_uint2(bf16x2(__fmul_rn(y.x, inv), __fmul_rn(y.y, inv)),
+                                                       bf16x2(__fmul_rn(y.z, inv), __fmul_rn(y.w, inv)));
+            } else {
+                *(float4*)(my + 2 * ROWS + (size_t)r * D + c) = y;
+            }
         }
+        if (!whole) {
+            if (tid < u.rows) my[tid] = sh.m[0][tid], my[ROWS + tid] = sh.l[0][tid];
+            // the CTA that finishes a unit's last part joins all of them, in their order
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const int done = atomicAdd(&counters[u.first], 1) + 1;
+                sh.last = done == u.segs;
+                if (done == u.segs) counters[u.first] = 0;
+                __threadfence();
+            }
+            __syncthreads();
+            if (sh.last) {
+                auto slot = [&](int i) { return part + (size_t)(2 * (u.first + i) + (i == 0)) * ROWS * (D + 2); };
+                for (int i = tid; i < u.rows * C4; i += NT) {
+                    const int r = i / C4, c = i % C4 * 4;
+                    float M = NEG_INF, sum = 0.f;
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                    for (int k = 0; k < u.segs; ++k) M = fmaxf(M, __ldcg(slot(k) + r));
+#pragma unroll 4
+                    for (int k = 0; k < u.segs; ++k) {
+                        const float mk = __ldcg(slot(k) + r), f = mk == NEG_INF ? 0.f : dt_ex2_approx(mk - M);
+                        const float4 z = __ldcg((const float4*)(slot(k) + 2 * ROWS + (size_t)r * D + c));
+                        sum = __fmaf_rn(__ldcg(slot(k) + ROWS + r), f, sum);
+                        y.x = __fmaf_rn(z.x, f, y.x), y.y = __fmaf_rn(z.y, f, y.y);
+                        y.z = __fmaf_rn(z.z, f, y.z), y.w = __fmaf_rn(z.w, f, y.w);
+                    }
+                    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+                    *(uint2*)(out_row(r) + c) = make_uint2(bf16x2(__fmul_rn(y.x, inv), __fmul_rn(y.y, inv)),
+                                                           bf16x2(__fmul_rn(y.z, inv), __fmul_rn(y.w, inv)));
+                }
+            }
+        }
+        __syncthreads();  // before the next segment's copies
     }
-    for (int i = 0; i < E; ++i) {
-        const __nv_bfloat16 o = __float2bfloat16_rn(l_run == 0.f ? 0.f : acc[i] / l_run);
-        out[i] = *(const uint16_t*)&o;
-    }
-    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&a.status[b], DT_DEV_BAD_CACHE);
+}
+
+template <int D>
+cudaError_t launch(const DtAttend& a, void* workspace, int ctas, cudaStream_t st) {
+    constexpr size_t smem = Lay<D>::SMEM;
+    static_assert(smem + sizeof(Shared) <= 227 * 1024, "shared memory of a CTA");
+    cudaError_t e = cudaFuncSetAttribute(kn11_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    DtLaunch lc(dim3(ctas), dim3(NT), smem, st);
+    return cudaLaunchKernelEx(&lc.cfg, kn11_kernel<D>, a, (float*)((char*)workspace + AT_MAX_CTAS * sizeof(int)),
+                              (int*)workspace);
 }
 
 }  // namespace
 
-cudaError_t dt_kn11_launch(const DtAttend& a, cudaStream_t st) {
-    DtLaunch lc(dim3((a.M + NW - 1) / NW, a.Hq, a.batch), dim3(NW * 32), 0, st);
-    return a.c.D == 64 ? cudaLaunchKernelEx(&lc.cfg, kn11_kernel<64>, a) : cudaLaunchKernelEx(&lc.cfg, kn11_kernel<128>, a);
+cudaError_t dt_kn11_launch(const DtAttend& a, void* workspace, int ctas, cudaStream_t st) {
+    return a.c.D == 64 ? launch<64>(a, workspace, ctas, st) : launch<128>(a, workspace, ctas, st);
 }
