@@ -25,7 +25,7 @@ int sm_count() {
         (void)cudaGetLastError();
         return 152;
     }
-    return n < 1024 ? n : 1024;
+    return n < 512 ? n : 512;
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -105,7 +105,7 @@ dt_status dt_tree_attention(const dt_kv_cache* c, const dt_rope* rope, int32_t b
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return DT_ERR_INVALID_ARG;
     const dt_rope none = {nullptr, nullptr, 0, 0, 0};
     const DtAttend a{*c, rope ? *rope : none, batch, M, Hq, Hq / c->Hkv, *q, *k, *v, mask, pos, n_nodes, scale, out, status};
-    if (rows <= kStreamRows) return cuda_status(dt_kn11_launch(a, workspace, sm_count(), (cudaStream_t)stream));
+    if (rows <= kStreamRows) return cuda_status(dt_kn11_launch(a, workspace, 2 * sm_count(), (cudaStream_t)stream));
     return cuda_status(dt_kn12_launch(a, workspace, sm_count(), (cudaStream_t)stream));
 }
 

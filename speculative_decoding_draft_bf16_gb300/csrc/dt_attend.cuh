@@ -27,6 +27,8 @@ struct AtPlan {
     // Cost of a tile of a block; one of at most half of 256 rows costs less (3.5
     // against 4.2 thousand clocks measured).
     static constexpr uint32_t FULL = ROWS == 256 ? 5 : 1, PART = ROWS == 256 ? 4 : 1;
+    // What starting on a unit costs: its queries, its sums' way out.
+    static constexpr uint32_t HEAD = ROWS == 256 ? 20 : 2;
     static DT_DI uint32_t weight(int rows) { return rows > ROWS / 2 ? FULL : PART; }
     static DT_DI AtReq req(const DtAttend& a, int b) {
         AtReq r;
@@ -48,7 +50,7 @@ struct AtPlan {
     }
     static DT_DI uint32_t cost(const DtAttend& a, const AtReq& r) {
         if (r.nqb == 0) return 0;
-        uint32_t s = block_tiles(a, r, r.nqb - 1) * weight(block_rows(a, r, r.nqb - 1));
+        uint32_t s = block_tiles(a, r, r.nqb - 1) * weight(block_rows(a, r, r.nqb - 1)) + r.nqb * HEAD;
         if (a.mask) {
             s += (r.nqb - 1) * block_tiles(a, r, 0) * FULL;
         } else {
@@ -119,7 +121,7 @@ struct AtWalk {
     int b, qb, h;       // the unit
     AtReq r;
     int rows, nt;       // its rows and tiles
-    uint32_t w, at;     // its tile cost and first cost position
+    uint32_t w, at;     // its tile cost and first cost position; tile 0 costs P::HEAD more
     int t0, t1;         // this CTA's tiles of it
     int first, segs;    // the CTA that holds tile 0, and how many CTAs share it
 
@@ -137,13 +139,19 @@ struct AtWalk {
         unit(a);
         // whole blocks before the share (Hkv units of one cost each)
 #pragma unroll 1
-        while (at + a.c.Hkv * nt * w <= s.beg) {
-            at += a.c.Hkv * nt * w;
+        while (at + a.c.Hkv * (nt * w + P::HEAD) <= s.beg) {
+            at += a.c.Hkv * (nt * w + P::HEAD);
             ++qb;
             unit(a);
         }
-        h = (int)((s.beg - at) / (nt * w));
-        at += h * nt * w;
+        h = (int)((s.beg - at) / (nt * w + P::HEAD));
+        at += h * (nt * w + P::HEAD);
+    }
+    // The first tile that starts at cost position x or later.
+    DT_DI int tile_from(uint32_t x) const {
+        if (x <= at) return 0;
+        const uint32_t one = at + P::HEAD + w;  // where tile 1 starts
+        return x <= one ? 1 : min((int)((x - one + w - 1) / w) + 1, nt);
     }
     // The next segment, or false.  A unit of at most ATOM tiles is not split.
     DT_DI bool next(const DtAttend& a, const AtShare& s, int c) {
@@ -155,9 +163,9 @@ struct AtWalk {
                 t0 = 0;
                 t1 = first == c ? nt : 0;
             } else {
-                t0 = s.beg <= at ? 0 : (int)((s.beg - at + w - 1) / w);
-                t1 = (int)min((s.end - at + w - 1) / w, (uint32_t)nt);
-                segs = s.owner(at + w * (nt - 1)) - first + 1;
+                t0 = tile_from(s.beg);
+                t1 = tile_from(s.end);
+                segs = s.owner(at + P::HEAD + w * (nt - 1)) - first + 1;
             }
             if (t1 > t0) return true;
             step(a);
@@ -165,7 +173,7 @@ struct AtWalk {
         return false;
     }
     DT_DI void step(const DtAttend& a) {  // to the next unit
-        at += nt * w;
+        at += nt * w + P::HEAD;
         if (++h < a.c.Hkv) return;
         h = 0;
         ++qb;

@@ -93,6 +93,12 @@ DT_DI uint32_t dt_e4m3x2_to_f16x2(uint32_t codes) {
     asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(d) : "r"(codes));
     return d;
 }
+// Four codes as two pairs.
+DT_DI void dt_e4m3x4_to_f16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
+}
 DT_DI float2 dt_e4m3x2_to_f32x2(uint32_t codes) {
     const uint32_t h = dt_e4m3x2_to_f16x2(codes);
     return __half22float2(*(const __half2*)&h);

@@ -3,7 +3,7 @@
 //
 // A CTA streams runs of 128-token tiles, 16 tokens to each of its 8 warps.  A
 // lane copies the bytes that it will need itself to its own places in shared
-// memory (cp.async, STAGES tiles ahead: up to 160 KB of a CTA's loads are in
+// memory (cp.async, STAGES tiles ahead: up to 192 KB of an SM's loads are in
 // flight, and nothing is waited for but the lane's own copies), turns the e4m3
 // codes into fp16 in registers and feeds 16 x 8 x 16 MMAs:
 //   S = Q K^T   a lane's 32 bytes of a token serve as the K-fragment of all
@@ -22,7 +22,8 @@ namespace {
 
 constexpr int ROWS = 16, NW = 8, NT = NW * 32;
 constexpr int ATOM = 2;              // tiles of the longest unit that is not split
-constexpr uint32_t MIN_SHARE = 2;    // tiles worth a CTA
+constexpr uint32_t MIN_SHARE = 4;    // least cost worth a CTA: the start and two tiles
+static_assert(MIN_SHARE >= AtPlan<ROWS>::HEAD + AtPlan<ROWS>::FULL, "every CTA between a unit's ends has a tile of it");
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float HEADROOM = 5.f, LAZY = 8.f;
 
@@ -30,7 +31,7 @@ template <int D>
 struct Lay {
     static constexpr int KC = D / 64;             // 16-byte pieces of a token's keys per lane
     static constexpr int VB = D / 8;              // bytes of a token's values per lane
-    static constexpr int STAGES = D == 128 ? 5 : 8;
+    static constexpr int STAGES = D == 128 ? 3 : 6;
     static constexpr int KBYTES = 2 * KC * 512, BYTES = KBYTES + 4 * VB * 32;  // per warp and stage
     static constexpr size_t FIFO = (size_t)NW * STAGES * BYTES;
     static constexpr size_t JOIN = (size_t)NW * ROWS * D * 4;
@@ -81,7 +82,7 @@ struct Stream {
     static constexpr int KS = D / 16;  // steps of Q K^T
     static constexpr int NV = D / 8;   // column tiles of P V; tile j has columns NV * g + j
 
-    uint32_t q[KS][4];                 // Q's fragments (rows g and g + 8)
+    uint32_t qs;                       // Q's fragments in shared memory, [KS][32 lanes][4 words]
     float rowc[2], m[2], l[2];
     float o[NV][4];
 
@@ -126,13 +127,22 @@ struct Stream {
             ex = big >= 0x7F800000u ? 0 : max(ex, -100);
             const float f = dt_pow2(-ex);
             rowc[i] = __fmul_rn(__fmul_rn(a.scale, LOG2E), dt_pow2(ex));
+            // every warp writes the same words
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 const float* y = x[s >> 2] + 4 * (s & 3);
-                q[s][i] = f16x2(__fmul_rn(y[0], f), __fmul_rn(y[1], f));
-                q[s][2 + i] = f16x2(__fmul_rn(y[2], f), __fmul_rn(y[3], f));
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qs + s * 512 + lane * 16 + i * 8),
+                             "r"(f16x2(__fmul_rn(y[0], f), __fmul_rn(y[1], f))),
+                             "r"(f16x2(__fmul_rn(y[2], f), __fmul_rn(y[3], f)))
+                             : "memory");
             }
         }
+    }
+    // The fragments of step s: rows g, g + 8 of the first two elements, then of the others.
+    DT_DI void frag(int s, int lane, uint32_t (&f)[4]) const {
+        uint32_t w[4];
+        lds<4>(qs + s * 512 + lane * 16, w);
+        f[0] = w[0], f[2] = w[1], f[1] = w[2], f[3] = w[3];
     }
 
     // Scores of two groups of 8 tokens (columns 2t, 2t + 1 of each; rows g, g + 8),
@@ -177,18 +187,24 @@ struct Stream {
     }
 
     // The staged 16 tokens at `st`, of which the first `left` exist.
-    DT_DI void tile(uint32_t st, int lane, int left, float ks, float vs) {
+    DT_DI void tile(uint32_t st, int lane, int left, float ks, float lv, float iv) {
         const int t = lane & 3;
         const uint32_t my = st + lane * 16;
         float c[2][4] = {};
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int j = 0; j < L::KC; ++j) {
+            uint32_t w[2][4];
+            lds<4>(my + j * 512, w[0]);
+            lds<4>(my + (L::KC + j) * 512, w[1]);
 #pragma unroll
-            for (int j = 0; j < L::KC; ++j) {
-                uint32_t w[4];
-                lds<4>(my + (n * L::KC + j) * 512, w);
+            for (int s = 0; s < 4; ++s) {
+                uint32_t f[4], b0, b1;
+                frag(4 * j + s, lane, f);
 #pragma unroll
-                for (int s = 0; s < 4; ++s) mma(c[n], q[4 * j + s], dt_e4m3x2_to_f16x2(w[s]), dt_e4m3x2_to_f16x2(w[s] >> 16));
+                for (int n = 0; n < 2; ++n) {
+                    dt_e4m3x4_to_f16x4(w[n][s], b0, b1);
+                    mma(c[n], f, b0, b1);
+                }
             }
         }
         if (left < 16) {
@@ -200,7 +216,7 @@ struct Stream {
             }
         }
         uint32_t p[4];
-        weigh(c, ks, log2f(vs), 1.0f / vs, p);
+        weigh(c, ks, lv, iv, p);
         // values of tokens 2t, 2t + 1, 2t + 8, 2t + 9
         constexpr int VW = L::VB / 4;
         uint32_t w[4][VW];
@@ -210,10 +226,13 @@ struct Stream {
         for (int j = 0; j < VW; ++j) {
             const uint32_t a0 = __byte_perm(w[0][j], w[1][j], 0x5140), a1 = __byte_perm(w[0][j], w[1][j], 0x7362);
             const uint32_t b0 = __byte_perm(w[2][j], w[3][j], 0x5140), b1 = __byte_perm(w[2][j], w[3][j], 0x7362);
-            mma(o[4 * j], p, dt_e4m3x2_to_f16x2(a0), dt_e4m3x2_to_f16x2(b0));
-            mma(o[4 * j + 1], p, dt_e4m3x2_to_f16x2(a0 >> 16), dt_e4m3x2_to_f16x2(b0 >> 16));
-            mma(o[4 * j + 2], p, dt_e4m3x2_to_f16x2(a1), dt_e4m3x2_to_f16x2(b1));
-            mma(o[4 * j + 3], p, dt_e4m3x2_to_f16x2(a1 >> 16), dt_e4m3x2_to_f16x2(b1 >> 16));
+            uint32_t a[4], b[4];
+            dt_e4m3x4_to_f16x4(a0, a[0], a[1]);
+            dt_e4m3x4_to_f16x4(a1, a[2], a[3]);
+            dt_e4m3x4_to_f16x4(b0, b[0], b[1]);
+            dt_e4m3x4_to_f16x4(b1, b[2], b[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mma(o[4 * j + e], p, a[e], b[e]);
         }
     }
 
@@ -260,7 +279,9 @@ struct Stream {
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 const float* y = k[i][s >> 2] + 4 * (s & 3);
-                mma(c[i], q[s], f16x2(__fmul_rn(y[0], fk), __fmul_rn(y[1], fk)), f16x2(__fmul_rn(y[2], fk), __fmul_rn(y[3], fk)));
+                uint32_t f[4];
+                frag(s, lane, f);
+                mma(c[i], f, f16x2(__fmul_rn(y[0], fk), __fmul_rn(y[1], fk)), f16x2(__fmul_rn(y[2], fk), __fmul_rn(y[3], fk)));
             }
         }
         float v[4][L::VB];
@@ -311,12 +332,13 @@ struct Stream {
 };
 
 template <int D>
-__global__ void __launch_bounds__(NT, 1) kn11_kernel(const __grid_constant__ DtAttend a, float* part, int* counters) {
+__global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtAttend a, float* part, int* counters) {
     using L = Lay<D>;
     using S = Stream<D>;
     constexpr int NV = S::NV;
     extern __shared__ __align__(128) unsigned char fifo[];
     __shared__ Shared sh;
+    __shared__ __align__(16) uint32_t qfrag[S::KS * 128];
     const float NEG_INF = -__int_as_float(0x7F800000);
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int cta = blockIdx.x, ctas = gridDim.x;
@@ -332,6 +354,7 @@ __global__ void __launch_bounds__(NT, 1) kn11_kernel(const __grid_constant__ DtA
     AtWalk<ROWS, ATOM> u;
     u.start(a, share);
     S x;
+    x.qs = dt_smem_addr(qfrag);
     for (; u.next(a, share, cta); u.step(a)) {
         const int len = u.r.len, cend = min(u.t1, u.r.ctx), n = max(0, cend - u.t0);
         const int* table = a.c.table + (size_t)u.b * a.c.max_pages;
@@ -354,7 +377,8 @@ __global__ void __launch_bounds__(NT, 1) kn11_kernel(const __grid_constant__ DtA
             k = a.c.k_scale[(size_t)page * a.c.Hkv + u.h];
             v = a.c.v_scale[(size_t)page * a.c.Hkv + u.h];
         };
-        int issued = 0;
+        float lv = 0.f, iv = 1.f;  // log2 and inverse of the value scale, of the batch being computed
+        int issued = 0, put = 0;
         auto issue = [&]() {  // the next tile's copies (past the last one: none)
             if (issued < n) {
                 if ((issued & 31) == 0 && issued > 0) {
@@ -365,22 +389,34 @@ __global__ void __launch_bounds__(NT, 1) kn11_kernel(const __grid_constant__ DtA
                 }
                 const uint32_t p = __shfl_sync(0xffffffffu, id, issued & 31);
                 const int tok0 = (u.t0 + issued) * AT_TILE + w * 16;
-                const size_t o = (size_t)p * page_bytes;
-                const uint32_t st = my_fifo + (issued % L::STAGES) * L::BYTES;
+                const uint32_t st = my_fifo + put * L::BYTES + lane * 16, sv = my_fifo + put * L::BYTES + L::KBYTES + lane * L::VB;
+                const size_t o = (size_t)p * page_bytes + (uint32_t)(tok0 & low) * D;
+                if (tok0 + 16 <= len) {  // 16 tokens lie in one page
+                    const uint8_t* k = kbase + o + g * D;
+                    const uint8_t* v = vbase + o + 2 * t * D;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint8_t* src = kbase + o + (uint32_t)(min(tok0 + g + 8 * i, max(len - 1, tok0)) & low) * D;
+                    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                    for (int j = 0; j < L::KC; ++j) copy_async<16>(st + (i * L::KC + j) * 512 + lane * 16, src + 64 * j);
-                }
+                        for (int j = 0; j < L::KC; ++j) copy_async<16>(st + (i * L::KC + j) * 512, k + 8 * i * D + 64 * j);
+                    }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = min(tok0 + 2 * t + (i & 1) + 8 * (i >> 1), max(len - 1, tok0));
-                    copy_async<L::VB>(st + L::KBYTES + i * (L::VB * 32) + lane * L::VB, vbase + o + (uint32_t)(tok & low) * D);
+                    for (int i = 0; i < 4; ++i) copy_async<L::VB>(sv + i * (L::VB * 32), v + ((i & 1) + 8 * (i >> 1)) * D);
+                } else {  // past len: the last token again
+                    const int last = max(len - 1 - tok0, 0);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint8_t* k = kbase + o + min(g + 8 * i, last) * D;
+#pragma unroll
+                        for (int j = 0; j < L::KC; ++j) copy_async<16>(st + (i * L::KC + j) * 512, k + 64 * j);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        copy_async<L::VB>(sv + i * (L::VB * 32), vbase + o + min(2 * t + (i & 1) + 8 * (i >> 1), last) * D);
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
             ++issued;
+            put = put + 1 == L::STAGES ? 0 : put + 1;
         };
         if (n > 0) {
             id = page_at(lane);
@@ -389,18 +425,26 @@ __global__ void __launch_bounds__(NT, 1) kn11_kernel(const __grid_constant__ DtA
         }
         for (int i = 0; i < L::STAGES - 1; ++i) issue();
         x.queries(a, u, lane);
+        __syncwarp();
 #pragma unroll
         for (int j = 0; j < NV; ++j) x.o[j][0] = x.o[j][1] = x.o[j][2] = x.o[j][3] = 0.f;
         x.m[0] = x.m[1] = NEG_INF;
         x.l[0] = x.l[1] = 0.f;
+        int slot = 0;  // of tile i
         for (int i = 0; i < n; ++i) {
             issue();
             asm volatile("cp.async.wait_group %0;" ::"n"(L::STAGES - 1) : "memory");
             const bool odd = (i >> 5) & 1;
+            if ((i & 31) == 0) {
+                const float v = odd ? vs[1] : vs[0];
+                lv = log2f(v);
+                iv = 1.0f / v;
+            }
             const float k = __shfl_sync(0xffffffffu, odd ? ks[1] : ks[0], i & 31);
-            const float v = __shfl_sync(0xffffffffu, odd ? vs[1] : vs[0], i & 31);
+            const float v = __shfl_sync(0xffffffffu, lv, i & 31), r = __shfl_sync(0xffffffffu, iv, i & 31);
             const int left = len - (u.t0 + i) * AT_TILE - w * 16;
-            if (left > 0) x.tile(my_fifo + (i % L::STAGES) * L::BYTES, lane, left, k, v);
+            if (left > 0) x.tile(my_fifo + slot * L::BYTES, lane, left, k, v, r);
+            slot = slot + 1 == L::STAGES ? 0 : slot + 1;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         if (w == 0 && u.t1 > u.r.ctx) x.fresh(a, u, lane);
@@ -512,7 +556,7 @@ __global__ void __launch_bounds__(NT, 1) kn11_kernel(const __grid_constant__ DtA
 template <int D>
 cudaError_t launch(const DtAttend& a, void* workspace, int ctas, cudaStream_t st) {
     constexpr size_t smem = Lay<D>::SMEM;
-    static_assert(smem + sizeof(Shared) <= 227 * 1024, "shared memory of a CTA");
+    static_assert(2 * (smem + sizeof(Shared) + 4096 + 1024) <= 228 * 1024, "two CTAs per SM");
     cudaError_t e = cudaFuncSetAttribute(kn11_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     DtLaunch lc(dim3(ctas), dim3(NT), smem, st);

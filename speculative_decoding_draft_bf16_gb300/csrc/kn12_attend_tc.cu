@@ -43,7 +43,8 @@ constexpr int STAGES = 2;       // K and V tiles in shared memory, each
 constexpr int RING = 8;         // tiles whose page ids and scales are kept
 constexpr int SEGS = 4;         // segments the walk may be ahead
 constexpr int ATOM = 4;         // tiles of the longest unit that is not split
-constexpr uint32_t MIN_SHARE = 10;    // least cost worth a CTA: two tiles of a full block
+constexpr uint32_t MIN_SHARE = 30;    // least cost worth a CTA: the start and two tiles of a full block
+static_assert(MIN_SHARE >= AtPlan<ROWS>::HEAD + AtPlan<ROWS>::FULL, "every CTA between a unit's ends has a tile of it");
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float HEADROOM = 5.f, LAZY = 8.f;
 
@@ -178,11 +179,11 @@ DT_DI void sts16(uint32_t addr, const uint32_t (&w)[4]) {
 // Sixteen e4m3 codes to two fp16 chunks at a0 and a1.
 DT_DI void store_codes(uint32_t a0, uint32_t a1, const uint4& q) {
     uint32_t w[4];
-    w[0] = dt_e4m3x2_to_f16x2(q.x), w[1] = dt_e4m3x2_to_f16x2(q.x >> 16);
-    w[2] = dt_e4m3x2_to_f16x2(q.y), w[3] = dt_e4m3x2_to_f16x2(q.y >> 16);
+    dt_e4m3x4_to_f16x4(q.x, w[0], w[1]);
+    dt_e4m3x4_to_f16x4(q.y, w[2], w[3]);
     sts16(a0, w);
-    w[0] = dt_e4m3x2_to_f16x2(q.z), w[1] = dt_e4m3x2_to_f16x2(q.z >> 16);
-    w[2] = dt_e4m3x2_to_f16x2(q.w), w[3] = dt_e4m3x2_to_f16x2(q.w >> 16);
+    dt_e4m3x4_to_f16x4(q.z, w[0], w[1]);
+    dt_e4m3x4_to_f16x4(q.w, w[2], w[3]);
     sts16(a1, w);
 }
 
