@@ -116,7 +116,7 @@ dt_status dt_token_logprobs(const void* logits, int32_t dtype, int32_t batch, in
     if (!logits || !tokens || batch < 1 || M < 1 || V < 1 || stride < V || stride_b < 0 || N < 1) return DT_ERR_INVALID_ARG;
     if (dtype != DT_BF16 && dtype != DT_F32) return DT_ERR_INVALID_ARG;
     if ((uintptr_t)logits % (dtype == DT_BF16 ? 2 : 4)) return DT_ERR_INVALID_ARG;
-    if (V > DT_MAX_V || (long long)batch * N > 0x7fffffffll) return DT_ERR_UNSUPPORTED;
+    if (V > DT_MAX_V || (long long)batch * N > 0x0fffffffll) return DT_ERR_UNSUPPORTED;
     if (!rows && N > M) return DT_ERR_INVALID_ARG;
     if (top < 0 || top > DT_MAX_TOP || top > V) return DT_ERR_INVALID_ARG;
     if (top > 0 && (!top_id || !top_logprob)) return DT_ERR_INVALID_ARG;

@@ -1,102 +1,467 @@
 // kn13_logprobs.cu -- log-probability, rank, entropy and best alternatives of
 // given tokens (dt_token_logprobs).
 //
-// One CTA per row, one pass per quantity.
-#include "dt_launch.h"
+// One pass over a row, by a cluster of S CTAs (S > 1 when there are few rows).
+// A thread keeps, for the elements x that it has read, sums relative to a
+// reference m of its own: s = sum e^(x-m) and u = sum (x-m) e^(x-m).  m is
+// its first vector's maximum and moves only when an element lies more than 20
+// above it.  Then lse = m + ln s and the entropy is ln s - u / s, without
+// cancellation between large numbers.
+//
+// What concerns few elements is looked at once per 16-byte vector, by its
+// maximum: elements at least as large as the token (its rank), and elements at
+// least as large as a lower bound of the row's top-th best, which go to a list in
+// shared memory.  The bound starts as the least of `top` groups' maxima and rises
+// when the list is cut back to its best; a round that overflows the list is read
+// again with a higher bound.
+//
+// Bound by the row's bytes: HBM for many rows, latency for few.
+#include <type_traits>
+
 #include "dt_device.cuh"
+#include "dt_launch.h"
 
 namespace {
 
-constexpr int NT = 512;
+constexpr int U = 4;                // vectors in flight per thread
+constexpr int ROUND = 4;            // batches between two looks at the list
+constexpr int CAP = 1024;           // list entries
+#ifndef DT_KN13_MANY
+#define DT_KN13_MANY 608
+#endif
+constexpr float FAR = 20.f;         // how far above its reference a thread lets an element lie
+constexpr float LOG2E = 1.44269504088896340736f;
 
-// Order of tokens: larger logit first, then the smaller id; as one key.
+typedef unsigned long long u64;
+
+// Order of tokens: larger logit first, then the smaller id; as one key (never 0).
 template <typename T>
-DT_DI unsigned long long order_key(T x, int id) {
-    return (unsigned long long)DtElem<T>::key(x) << 32 | (uint32_t)~id;
+DT_DI u64 order_key(T x, int id) {
+    return (u64)DtElem<T>::key(x) << 32 | (uint32_t)~id;
+}
+template <typename T>
+DT_DI float key_value(u64 k) {
+    return DtElem<T>::key_val((uint32_t)(k >> 32));
 }
 
-template <typename T>
-__global__ void __launch_bounds__(NT) kn13_kernel(DtLogprobs a) {
+// The vector with -infinity replaced by a number so low that its exponential is
+// zero (0 times -infinity would be NaN); NaN stays.
+DT_DI uint32_t floor2(uint32_t w) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0xFF7FFF7Fu));
+    return r;
+}
+DT_DI void finite_vals(const uint4& q, float (&x)[8]) {
+    const uint4 f = make_uint4(floor2(q.x), floor2(q.y), floor2(q.z), floor2(q.w));
+    dt_vec_vals<uint16_t>(f, x);
+}
+DT_DI void finite_vals(const uint4& q, float (&x)[4]) {
+    dt_vec_vals<float>(q, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(x[i]) : "f"(-3.0e38f));
+}
+
+struct Part {  // of a CTA, in rank 0's shared memory
+    float m, s, u;
+    int before, any;
+    u64 top[32];
+};
+
+template <int NT>
+struct Shared {
+    u64 list[CAP];
+    u64 scratch[NT];
+    uint32_t group[32];
+    u64 bound;
+    int count, kept;
+    float rm[NT / 32], rs[NT / 32], ru[NT / 32];
+    int rb[NT / 32];
+    Part part[8];
+};
+
+template <typename T, bool TOP>
+struct Row {
     using E = DtElem<T>;
-    __shared__ float fred[NT / 32];
-    __shared__ unsigned long long kred[NT / 32];
+    static constexpr int EV = 16 / sizeof(T);  // elements of a vector
+    float m;         // reference
+    u64 s2, u2;      // s and u, two fp32 parts each
+    int before;
+    bool any;        // a value above -infinity
+    float token;     // the token's logit
+    typename std::conditional<sizeof(T) == 2, uint32_t, float>::type
+        least_pre, least_post;  // what an element must reach to come before it, ahead of the token and
+                                // after it (bf16: in both halves)
+    __nv_bfloat162 count2;      // bf16: counts of even and odd elements since the last flush (whole to 256)
+
+    DT_DI void move(float to) {  // the reference
+        const float d = __fsub_rn(m, to), f = dt_ex2_approx(__fmul_rn(d, LOG2E));
+        u2 = dt_f2_mul(dt_f2_fma(s2, dt_f2_pack(d, d), u2), dt_f2_pack(f, f));
+        s2 = dt_f2_mul(s2, dt_f2_pack(f, f));
+        m = to;
+    }
+    DT_DI void add(float x0, float x1) {
+        const u64 d = dt_f2_add(dt_f2_pack(x0, x1), dt_f2_pack(-m, -m));
+        float y0, y1;
+        dt_f2_unpack(dt_f2_mul(d, dt_f2_pack(LOG2E, LOG2E)), y0, y1);
+        const u64 e = dt_f2_pack(dt_ex2_approx(y0), dt_ex2_approx(y1));
+        s2 = dt_f2_add(s2, e);
+        u2 = dt_f2_fma(d, e, u2);
+    }
+    // A vector's sums, and how many of its elements come before the token: those
+    // not smaller when they precede it, the larger ones when they follow.
+    DT_DI void sums(const uint4& q, int id, int tok) {
+        float x[EV];
+        finite_vals(q, x);
+#pragma unroll
+        for (int i = 0; i < EV; i += 2) add(x[i], x[i + 1]);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        if ((uint32_t)(tok - id) < (uint32_t)EV) {
+#pragma unroll
+            for (int i = 0; i < EV; ++i) {
+                const float v = sizeof(T) == 2 ? __uint_as_float((w[i >> 1] >> (16 * (i & 1))) << 16) : __uint_as_float(w[i]);
+                before += i < tok - id ? v >= token : v > token;
+            }
+        } else if constexpr (sizeof(T) == 2) {
+            const uint32_t t2 = id < tok ? least_pre : least_post;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // 1 or 0 each
+                count2 = __hadd2(count2, __hge2(*(const __nv_bfloat162*)&w[i], *(const __nv_bfloat162*)&t2));
+        } else {
+            const float t = id < tok ? least_pre : least_post;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) before += __uint_as_float(w[i]) >= t;
+        }
+    }
+    DT_DI void flush() {
+        if (sizeof(T) == 2) {
+            before += (int)(__low2float(count2) + __high2float(count2));
+            count2 = __nv_bfloat162(0.f, 0.f);
+        }
+    }
+};
+
+// Lists the elements that may be among the best of the warp's vectors that hold
+// such (hit): each of these in turn, an element to a lane.  id: of the vector's
+// first element.  All lanes.
+template <typename T, int NT>
+DT_DI void list_hits(bool hit, const uint4& q, int id, Shared<NT>* sh) {
+    constexpr int EV = 16 / sizeof(T);
+    const int lane = threadIdx.x & 31;
+    const u64 bound = sh->bound;
+    for (unsigned m = __ballot_sync(0xffffffffu, hit); m; m &= m - 1) {
+        const int src = __ffs(m) - 1;
+        const uint32_t x = __shfl_sync(0xffffffffu, q.x, src), y = __shfl_sync(0xffffffffu, q.y, src);
+        const uint32_t z = __shfl_sync(0xffffffffu, q.z, src), w = __shfl_sync(0xffffffffu, q.w, src);
+        const int i = __shfl_sync(0xffffffffu, id, src) + lane, word = sizeof(T) == 2 ? lane >> 1 : lane;
+        const uint32_t v = word < 2 ? (word ? y : x) : (word == 2 ? z : w);
+        T t;
+        if constexpr (sizeof(T) == 2) t = (T)(v >> (16 * (lane & 1)));
+        else t = __uint_as_float(v);
+        const u64 k = order_key<T>(t, i);
+        if (lane < EV && k >= bound) {
+            const int at = atomicAdd(&sh->count, 1);
+            if (at < CAP) sh->list[at] = k;
+        }
+    }
+}
+
+// The next larger number (finite or infinite input).
+DT_DI uint16_t next_up(uint16_t h) {
+    if ((h & 0x7FFFu) == 0) return 1;
+    return (h & 0x8000u) ? h - 1 : h + 1;
+}
+DT_DI float next_up(float x) {
+    const uint32_t b = __float_as_uint(x);
+    if ((b & 0x7FFFFFFFu) == 0) return __uint_as_float(1);
+    return __uint_as_float((b & 0x80000000u) ? b - 1 : b + 1);
+}
+
+// The k best keys of the list (k <= 32) to its front, in order; the k-th becomes
+// the bound when there are as many.  All threads.
+template <int NT>
+DT_DI void cut_list(Shared<NT>* sh, int n, int k) {
+    u64 best = 0ull;
+    if (n <= 128) {
+        if (threadIdx.x < 32) {
+            for (int i = threadIdx.x; i < n + (int)threadIdx.x; i += 32) {
+                const u64 x = dt_warp_sort_reg(i < n ? sh->list[i] : 0ull, true);
+                best = i < 32 ? x : dt_warp_top32_merge(best, x);
+            }
+        }
+    } else {
+        best = dt_block_top32<NT>(n, [&](int i) { return sh->list[i]; }, sh->scratch);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        if (threadIdx.x < k && threadIdx.x < n) sh->list[threadIdx.x] = best;
+        if (threadIdx.x == k - 1 && n >= k) sh->bound = best;
+        if (threadIdx.x == 0) sh->count = min(n, k);
+    }
+    __syncthreads();
+}
+
+template <typename T, bool TOP, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) kn13_kernel(const __grid_constant__ DtLogprobs a, int S) {
+    using E = DtElem<T>;
+    using R = Row<T, TOP>;
+    constexpr int EV = R::EV;
+    __shared__ Shared<NT> sh;
+    const float NEG_INF = -__int_as_float(0x7F800000), NaN = __int_as_float(0x7FC00000);
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     dt_pdl_trigger();
     dt_pdl_wait();
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const size_t e = blockIdx.x;
-    const int b = (int)(e / a.N), j = (int)(e % a.N);
+    const uint32_t c = blockIdx.x % (uint32_t)S;  // rank in the row's cluster
+    const uint32_t e = blockIdx.x / (uint32_t)S;
+    const int b = (int)(e / (uint32_t)a.N), j = (int)(e % (uint32_t)a.N);
     const int row = a.rows ? a.rows[e] : j, tok = a.tokens[e];
-    const float nan = __int_as_float(0x7FC00000);
-    if (row < 0 || row >= a.M) {
-        const float v = row < 0 ? 0.f : nan;
-        if (tid == 0) {
-            if (a.logprob) a.logprob[e] = v;
-            if (a.entropy) a.entropy[e] = v;
-            if (a.rank) a.rank[e] = -1;
+    if (row < 0 || row >= a.M) {  // the whole cluster
+        const float v = row < 0 ? 0.f : NaN;
+        if (c == 0) {
+            if (tid == 0) {
+                if (a.logprob) a.logprob[e] = v;
+                if (a.entropy) a.entropy[e] = v;
+                if (a.rank) a.rank[e] = -1;
+            }
+            if (tid < a.top) a.top_id[(size_t)e * a.top + tid] = -1, a.top_logprob[(size_t)e * a.top + tid] = v;
         }
-        if (tid < a.top) a.top_id[e * a.top + tid] = -1, a.top_logprob[e * a.top + tid] = v;
         return;
     }
     const T* x = (const T*)a.logits + b * a.stride_b + row * a.stride;
-    auto total = [&](float v) {
-        v = dt_warp_sum(v);
-        __syncthreads();
-        if (lane == 0) fred[w] = v;
-        __syncthreads();
-        float t = 0.f;
-        for (int i = 0; i < NT / 32; ++i) t += fred[i];
-        return t;
-    };
-    float m = -__int_as_float(0x7F800000);
-    for (int i = tid; i < a.V; i += NT) m = fmaxf(m, E::val(x[i]));
-    m = dt_warp_max(m);
-    if (lane == 0) fred[w] = m;
-    __syncthreads();
-    for (int i = 0; i < NT / 32; ++i) m = fmaxf(m, fred[i]);
+    // elements before the first 16-byte boundary and after the last vector go one by one
+    const int lead = min((int)((16 - ((uintptr_t)x & 15)) & 15) / (int)sizeof(T), a.V);
+    const int nvec = (a.V - lead) / EV, tail = lead + nvec * EV;
+    const uint4* vec = (const uint4*)(x + lead);
+    const int per = (nvec + S - 1) / S, v0 = min((int)c * per, nvec), v1 = min(v0 + per, nvec);
     const bool named = tok >= 0 && tok < a.V;
-    const unsigned long long mine = named ? order_key<T>(x[tok], tok) : ~0ull;
-    float s = 0.f, t = 0.f;
-    int before = 0;
-    for (int i = tid; i < a.V; i += NT) {
-        const float d = E::val(x[i]) - m, p = expf(d);
-        s += p;
-        if (p > 0.f) t += d * p;
-        before += order_key<T>(x[i], i) > mine;
+
+    R r;
+    r.s2 = r.u2 = dt_f2_pack(0.f, 0.f);
+    r.before = 0;
+    r.count2 = __nv_bfloat162(0.f, 0.f);
+    uint4 q[U];
+    const uint4 none = sizeof(T) == 2 ? make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u)
+                                      : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+    // a batch: vectors base + tid + i * NT
+    auto fetch = [&](int base, int i) {
+        const int v = base + i * NT + tid;
+        q[i] = none;
+        if (v < v1) q[i] = vec[v];
+    };
+#pragma unroll
+    for (int i = 0; i < U; ++i) fetch(v0, i);
+    T raw_token = (T)0;
+    if (named) raw_token = x[tok];
+    r.token = named ? E::val(raw_token) : __int_as_float(0x7F800000);
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t pre = named ? raw_token : 0x7FC0u, post = named ? next_up(raw_token) : 0x7FC0u;
+        r.least_pre = pre | pre << 16;  // no number reaches NaN
+        r.least_post = post | post << 16;
+    } else {
+        r.least_pre = named ? raw_token : NaN;
+        r.least_post = named ? next_up(raw_token) : NaN;
     }
-    s = total(s);
-    t = total(t);
-    before = (int)total((float)before);
-    const float ln = logf(s);
-    const float lse = m + ln;
+    float first = NEG_INF;
+#pragma unroll
+    for (int i = 0; i < U; ++i) first = fmaxf(first, dt_vec_max<T>(q[i]));
+    r.any = first > NEG_INF;
+    r.m = r.any ? first : 0.f;
+    float bound_val = __int_as_float(0x7F800000);
+    if (TOP) {
+        if (tid == 0) sh.count = 0;
+        // the bound: the least of G groups' maxima, G >= top a power of two, with the
+        // last id (NaN: no number, a lower bound all the same)
+        uint32_t best = r.any ? (uint32_t)(order_key<float>(first, 0) >> 32) : 0u;
+        constexpr int PER = NT / 32;  // threads of the smallest group
+#pragma unroll
+        for (int o = PER / 2; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+        if (lane % PER == 0) sh.group[tid / PER] = best;
+        __syncthreads();
+        if (w == 0) {
+            uint32_t k = sh.group[lane];
+            for (int g = 32; g > 1 && g >= 2 * a.top; g >>= 1) k = max(k, __shfl_xor_sync(0xffffffffu, k, g >> 1));
+            k = __reduce_min_sync(0xffffffffu, k);
+            if (lane == 0) sh.bound = k ? order_key<T>(dt_to_elem<T>(dt_fkey_val(k)), -1) : 0ull;
+        }
+        __syncthreads();
+        bound_val = sh.bound ? key_value<T>(sh.bound) : NEG_INF;
+    }
+    for (int round = v0; round < v1; round += ROUND * U * NT) {
+        const int rend = min(round + ROUND * U * NT, v1);
+#pragma unroll 1
+        for (int base = round; base < rend; base += U * NT) {
+#pragma unroll
+            for (int h = 0; h < U; h += U / 2) {  // half a batch read, the next one's half on its way
+#pragma unroll
+                for (int i = h; i < h + U / 2; ++i) {
+                    // a vector past the end is all -infinity and behind every token; the
+                    // warp stays together, or it would do its sums twice
+                    const int v = base + i * NT + tid;
+                    const int id = v < v1 ? lead + v * EV : 0x7FFFFFFF;
+                    const float vm = dt_vec_max<T>(q[i]);
+                    r.any |= vm > NEG_INF;
+                    const bool far = vm > r.m + FAR, hit = TOP && vm >= bound_val && v < v1;
+                    if (__any_sync(0xffffffffu, far || hit)) {
+                        if (far) r.move(vm);
+                        __syncwarp();
+                        if (TOP) list_hits<T, NT>(hit, q[i], id, &sh);
+                    }
+                    r.sums(q[i], id, tok);
+                }
+#pragma unroll
+                for (int i = h; i < h + U / 2; ++i) fetch(base + U * NT, i);
+            }
+            r.flush();
+        }
+        if (TOP) {
+            const int kept = round == v0 ? 0 : sh.kept;
+            __syncthreads();
+            int n = sh.count;
+            while (n > CAP) {  // this round again, with a higher bound
+                const u64 was = sh.bound;
+                __syncthreads();
+                // the best of what the list holds bound the rest; entries from earlier rounds stay
+                const u64 top = dt_block_top32<NT>(CAP, [&](int i) { return sh.list[i]; }, sh.scratch);
+                __syncthreads();
+                if (tid == a.top - 1) sh.bound = max(top, was);
+                if (tid == 0) sh.count = kept;
+                __syncthreads();
+#pragma unroll 1
+                for (int first_v = round; first_v < rend; first_v += NT) {
+                    const int v = first_v + tid;
+                    uint4 y = none;
+                    if (v < rend) y = vec[v];
+                    list_hits<T, NT>(v < rend && dt_vec_max<T>(y) >= key_value<T>(sh.bound), y, lead + v * EV, &sh);
+                }
+                __syncthreads();
+                n = sh.count;
+            }
+            if (n > CAP / 2) cut_list(&sh, n, a.top);
+            if (tid == 0) sh.kept = sh.count;
+            __syncthreads();
+            bound_val = sh.bound ? key_value<T>(sh.bound) : NEG_INF;
+        }
+    }
+    if (TOP && v0 >= v1) {
+        if (tid == 0) sh.kept = 0;
+        __syncthreads();
+    }
+    // the elements outside the vectors (fewer than 2 * EV, rank 0)
+    if (c == 0) {
+        const int n = lead + a.V - tail;
+        if (tid < n) {
+            const int id = tid < lead ? tid : tail + tid - lead;
+            const T raw = x[id];
+            float y = E::val(raw);
+            r.before += named && (id < tok ? y >= r.token : y > r.token);
+            if (y > NEG_INF) {
+                if (!r.any) r.m = y;
+                r.any = true;
+            }
+            if (y > r.m + FAR) r.move(y);
+            if (y == NEG_INF) y = -3.0e38f;
+            const float d = y - r.m, ex = dt_ex2_approx(__fmul_rn(d, LOG2E));
+            r.s2 = dt_f2_add(r.s2, dt_f2_pack(ex, 0.f));
+            r.u2 = dt_f2_add(r.u2, dt_f2_pack(__fmul_rn(d, ex), 0.f));
+            if (TOP) sh.list[sh.kept + tid] = order_key<T>(raw, id);  // kept <= CAP / 2
+        }
+        if (TOP) {
+            __syncthreads();
+            if (tid == 0) sh.count = sh.kept + n;
+        }
+    }
+    __syncthreads();
+    if (TOP) {
+        const int n = sh.count;
+        cut_list(&sh, n, a.top);
+    }
+    // the CTA's sums, relative to the largest reference among those with a value
+    float M = r.any ? r.m : NEG_INF;
+    M = dt_warp_max(M);
+    if (lane == 0) sh.rm[w] = M;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) M = fmaxf(M, sh.rm[i]);
+    const float ref = M > NEG_INF ? M : 0.f;
+    // a thread without a value has sums of zeros, or NaN
+    float sa, sb, ua, ub;
+    dt_f2_unpack(r.s2, sa, sb);
+    r.move(r.any || sa != sa || sb != sb ? ref : r.m);
+    dt_f2_unpack(r.s2, sa, sb);
+    dt_f2_unpack(r.u2, ua, ub);
+    const float s = dt_warp_sum(__fadd_rn(sa, sb)), u = dt_warp_sum(__fadd_rn(ua, ub));
+    const int before = dt_warp_sum_i(r.before);
+    if (lane == 0) sh.rs[w] = s, sh.ru[w] = u, sh.rb[w] = before;
+    __syncthreads();
+    cg::cluster_group cluster = cg::this_cluster();
+    Part* to = S > 1 ? cluster.map_shared_rank(&sh.part[c], 0) : &sh.part[0];
+    if (S > 1) cluster.sync();  // rank 0 runs before others write to it
     if (tid == 0) {
-        if (a.logprob) a.logprob[e] = named ? E::val(x[tok]) - lse : tok < 0 ? 0.f : nan;
-        if (a.entropy) a.entropy[e] = ln - t / s;
-        if (a.rank) a.rank[e] = named ? before : -1;
+        float ss = 0.f, uu = 0.f;
+        int bb = 0;
+        for (int i = 0; i < NT / 32; ++i) ss += sh.rs[i], uu += sh.ru[i], bb += sh.rb[i];
+        to->m = ref;
+        to->s = ss;
+        to->u = uu;
+        to->before = bb;
+        to->any = M > NEG_INF;
     }
-    unsigned long long last = ~0ull;
-    for (int k = 0; k < a.top; ++k) {
-        unsigned long long best = 0ull;
-        for (int i = tid; i < a.V; i += NT) {
-            const unsigned long long key = order_key<T>(x[i], i);
-            if (key < last && key > best) best = key;
-        }
-        for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-        __syncthreads();
-        if (lane == 0) kred[w] = best;
-        __syncthreads();
-        for (int i = 0; i < NT / 32; ++i) best = max(best, kred[i]);
-        last = best;
-        if (tid == 0) {
-            a.top_id[e * a.top + k] = (int)~(uint32_t)best;
-            a.top_logprob[e * a.top + k] = E::key_val((uint32_t)(best >> 32)) - lse;
+    if (TOP && tid < 32) to->top[tid] = tid < sh.count ? sh.list[tid] : 0ull;
+    if (S > 1) cluster.sync();
+    else __syncthreads();
+    if (c != 0 || w != 0) return;
+    // rank 0's first warp: the CTAs' parts in their order
+    float m = NEG_INF;
+    bool any = false;
+    for (int i = 0; i < S; ++i) {
+        if (sh.part[i].any) m = fmaxf(m, sh.part[i].m);
+        any |= sh.part[i].any != 0;
+    }
+    float ts = 0.f, tu = 0.f;
+    int tb = 0;
+    for (int i = 0; i < S; ++i) {
+        const Part& p = sh.part[i];
+        tb += p.before;
+        const float d = p.any && any ? p.m - m : 0.f, f = dt_ex2_approx(__fmul_rn(d, LOG2E));
+        tu = __fmaf_rn(__fmaf_rn(p.s, d, p.u), f, tu);
+        ts = __fmaf_rn(p.s, f, ts);
+    }
+    const float ln = logf(ts);
+    const float lse = any ? m + ln : NaN;
+    if (lane == 0) {
+        if (a.logprob) a.logprob[e] = named ? r.token - lse : tok < 0 ? 0.f : NaN;
+        if (a.entropy) a.entropy[e] = any ? ln - tu / ts : NaN;
+        if (a.rank) a.rank[e] = named ? tb : -1;
+    }
+    if (TOP) {
+        u64 best = sh.part[0].top[lane];
+        for (int i = 1; i < S; ++i) best = dt_warp_top32_merge(best, sh.part[i].top[lane]);
+        if (lane < a.top) {
+            a.top_id[(size_t)e * a.top + lane] = (int)~(uint32_t)best;
+            a.top_logprob[(size_t)e * a.top + lane] = key_value<T>(best) - lse;
         }
     }
+}
+
+template <typename T, int NT>
+cudaError_t launch(const DtLogprobs& a, int S, cudaStream_t st) {
+    const unsigned rows = (unsigned)((size_t)a.batch * a.N);
+    DtLaunch lc(dim3(rows * S), dim3(NT), 0, st, S > 1 ? S : 0);
+    return a.top > 0 ? cudaLaunchKernelEx(&lc.cfg, kn13_kernel<T, true, NT>, a, S)
+                     : cudaLaunchKernelEx(&lc.cfg, kn13_kernel<T, false, NT>, a, S);
 }
 
 }  // namespace
 
 cudaError_t dt_kn13_launch(const DtLogprobs& a, cudaStream_t st) {
-    DtLaunch lc(dim3((unsigned)((size_t)a.batch * a.N)), dim3(NT), 0, st);
-    return a.dtype == DT_BF16 ? cudaLaunchKernelEx(&lc.cfg, kn13_kernel<uint16_t>, a)
-                              : cudaLaunchKernelEx(&lc.cfg, kn13_kernel<float>, a);
+    // A cluster per row while rows alone leave SMs idle (two CTAs fit an SM), with
+    // a batch of vectors at least for every thread.
+    const long long rows = (long long)a.batch * a.N;
+    const long long bytes = (long long)a.V * (a.dtype == DT_BF16 ? 2 : 4);
+    int S = 1;
+    while (S < 8 && rows * S * 2 <= 2 * 152 && bytes >= (long long)S * 2 * 512 * 16 * 2) S *= 2;
+    // Many rows: few threads to a row, so that what a row costs once is spread over
+    // more of its vectors.
+    if (rows >= DT_KN13_MANY)
+        return a.dtype == DT_BF16 ? launch<uint16_t, 128>(a, S, st) : launch<float, 128>(a, S, st);
+    return a.dtype == DT_BF16 ? launch<uint16_t, 512>(a, S, st) : launch<float, 512>(a, S, st);
 }
