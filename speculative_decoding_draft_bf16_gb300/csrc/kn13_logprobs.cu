@@ -11,7 +11,7 @@
 // What concerns few elements is looked at once per 16-byte vector, by its
 // maximum: elements at least as large as the token (its rank), and elements at
 // least as large as a lower bound of the row's top-th best, which go to a list in
-// shared memory.  The bound starts as the least of `top` groups' maxima and rises
+// shared memory.  The bound starts as the top-th best of the threads' maxima and rises
 // when the list is cut back to its best; a round that overflows the list is read
 // again with a higher bound.
 //
@@ -71,7 +71,7 @@ template <int NT>
 struct Shared {
     u64 list[CAP];
     u64 scratch[NT];
-    uint32_t group[32];
+
     u64 bound;
     int count, kept;
     float rm[NT / 32], rs[NT / 32], ru[NT / 32];
@@ -268,19 +268,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) kn13_kernel(const __grid_consta
     float bound_val = __int_as_float(0x7F800000);
     if (TOP) {
         if (tid == 0) sh.count = 0;
-        // the bound: the least of G groups' maxima, G >= top a power of two, with the
-        // last id (NaN: no number, a lower bound all the same)
-        uint32_t best = r.any ? (uint32_t)(order_key<float>(first, 0) >> 32) : 0u;
-        constexpr int PER = NT / 32;  // threads of the smallest group
-#pragma unroll
-        for (int o = PER / 2; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-        if (lane % PER == 0) sh.group[tid / PER] = best;
+        // the bound: the top-th best of the threads' maxima, with the last id (NaN: no
+        // number, a lower bound all the same)
+        const u64 mine = (r.any ? (u64)dt_fkey(first) : 0ull) << 32 | (uint32_t)tid;
         __syncthreads();
-        if (w == 0) {
-            uint32_t k = sh.group[lane];
-            for (int g = 32; g > 1 && g >= 2 * a.top; g >>= 1) k = max(k, __shfl_xor_sync(0xffffffffu, k, g >> 1));
-            k = __reduce_min_sync(0xffffffffu, k);
-            if (lane == 0) sh.bound = k ? order_key<T>(dt_to_elem<T>(dt_fkey_val(k)), -1) : 0ull;
+        const u64 best = dt_block_top32<NT>(NT, [&](int) { return mine; }, sh.scratch);  // asked for tid only
+        if (tid == a.top - 1) {
+            const uint32_t k = (uint32_t)(best >> 32);
+            sh.bound = k ? order_key<T>(dt_to_elem<T>(dt_fkey_val(k)), -1) : 0ull;
         }
         __syncthreads();
         bound_val = sh.bound ? key_value<T>(sh.bound) : NEG_INF;
@@ -335,7 +330,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) kn13_kernel(const __grid_consta
                 __syncthreads();
                 n = sh.count;
             }
-            if (n > CAP / 2) cut_list(&sh, n, a.top);
+            // after the first round the list's own best are a much better bound
+            if (n > CAP / 2 || (round == v0 && n > a.top)) cut_list(&sh, n, a.top);
             if (tid == 0) sh.kept = sh.count;
             __syncthreads();
             bound_val = sh.bound ? key_value<T>(sh.bound) : NEG_INF;
@@ -458,7 +454,7 @@ cudaError_t dt_kn13_launch(const DtLogprobs& a, cudaStream_t st) {
     const long long rows = (long long)a.batch * a.N;
     const long long bytes = (long long)a.V * (a.dtype == DT_BF16 ? 2 : 4);
     int S = 1;
-    while (S < 8 && rows * S * 2 <= 2 * 152 && bytes >= (long long)S * 2 * 512 * 16 * 2) S *= 2;
+    while (S < 8 && rows * S < 2 * 152 && bytes >= (long long)S * 2 * 512 * 16 * 2) S *= 2;
     // Many rows: few threads to a row, so that what a row costs once is spread over
     // more of its vectors.
     if (rows >= DT_KN13_MANY)
