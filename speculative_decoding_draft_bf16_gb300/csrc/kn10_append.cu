@@ -27,11 +27,21 @@ DT_DI int scale_exponent(float scale) {
     return (int)(b >> 23) - 127 + ((b & 0x7FFFFFu) ? 1 : 0);
 }
 
-template <typename T, int CH>  // CH: chunks of 8 elements a thread may own
-__global__ void __launch_bounds__(NT) kn10_kernel(dt_kv_cache c, dt_rope rope, int M, dt_rows kr, dt_rows vr,
-                                                  const int32_t* __restrict__ rows, int N,
-                                                  const int32_t* __restrict__ count, int count_add,
-                                                  int32_t* __restrict__ len_out, int32_t* __restrict__ status) {
+// Two codes' bytes of eight scaled values.
+DT_DI uint2 codes8(const float (&x)[8], float inv) {
+    uint2 w;
+    w.x = dt_f32x2_to_e4m3x2(__fmul_rn(x[0], inv), __fmul_rn(x[1], inv)) |
+          dt_f32x2_to_e4m3x2(__fmul_rn(x[2], inv), __fmul_rn(x[3], inv)) << 16;
+    w.y = dt_f32x2_to_e4m3x2(__fmul_rn(x[4], inv), __fmul_rn(x[5], inv)) |
+          dt_f32x2_to_e4m3x2(__fmul_rn(x[6], inv), __fmul_rn(x[7], inv)) << 16;
+    return w;
+}
+
+template <typename T, int CP>  // CP: pairs of 8-element chunks a thread may own
+__global__ void __launch_bounds__(NT) kn10_kernel(const __grid_constant__ dt_kv_cache c, const __grid_constant__ dt_rope kv_rope,
+                                                  int M, const __grid_constant__ dt_rows kr, const __grid_constant__ dt_rows vr,
+                                                  const int32_t* rows, int N, const int32_t* count, int count_add,
+                                                  int32_t* len_out, int32_t* status) {
     __shared__ uint32_t red[NT / 32];
     dt_pdl_trigger();
     dt_pdl_wait();
@@ -41,81 +51,92 @@ __global__ void __launch_bounds__(NT) kn10_kernel(dt_kv_cache c, dt_rope rope, i
     const int len = c.len[b], n = count ? count[b] + count_add : N;
     const int* table = c.table + (size_t)b * c.max_pages;
     const long long cap = (long long)c.max_pages * c.page;
+    bool bad = len < 0 || n < 0 || n > N || (long long)len + n > cap ||
+               (kv_rope.rot && n > 0 && (long long)len + n > kv_rope.max_pos);
+    const int lp = 31 - __clz(c.page), p = bad ? 0 : (len >> lp) + at;
+    const int lo = bad ? 0 : max(len, p << lp), hi = bad ? 0 : min(len + n, (p + 1) << lp);  // slots of new rows
+    const bool mine = lo < hi;
+    const dt_rows& src = keys ? kr : vr;
+    dt_rope rope = kv_rope;
+    if (!keys) rope.rot = 0;
+    // The rows are read before the verdict on the request is known (row numbers
+    // clamped), so that their latency and the checks' overlap.
+    const int ppr = c.D >> 4, sh = c.D == 128 ? 3 : 2;  // chunk pairs per row
+    const int m = mine ? (hi - lo) << sh : 0;
+    float x[CP][8], y[CP][8];
+#pragma unroll
+    for (int i = 0; i < CP; ++i) {
+        const int q = tid + i * NT;
+        if (q < m) {
+            const int j = lo - len + (q >> sh);
+            const int row = rows ? min(max(rows[(size_t)b * N + j], 0), M - 1) : j;
+            dt_rotated_pair((const T*)src.ptr + b * src.stride_b + row * src.stride_n + h * src.stride_h, q & (ppr - 1), rope,
+                            len + j, x[i], y[i]);
+        }
+    }
     // every CTA of a request comes to the same verdict on it
-    bool bad = len < 0 || n < 0 || n > N || (long long)len + n > cap || (rope.rot && n > 0 && (long long)len + n > rope.max_pos);
+    int id = 0;
     if (!bad && n > 0) {
         if (rows)
             for (int j = tid; j < n; j += NT) bad |= (unsigned)rows[(size_t)b * N + j] >= (unsigned)M;
-        const int last = (len + n - 1) / c.page;
-        for (int p = len / c.page + tid; p <= last; p += NT) bad |= (unsigned)table[p] >= (unsigned)c.n_pages;
+        const int last = (len + n - 1) >> lp;
+        for (int k = (len >> lp) + tid; k <= last; k += NT) bad |= (unsigned)table[k] >= (unsigned)c.n_pages;
+        if (mine) id = table[p];
     }
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < CP; ++i) {
+        if (tid + i * NT < m) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                amax = max(amax, max(__float_as_uint(x[i][e]) & 0x7FFFFFFFu, __float_as_uint(y[i][e]) & 0x7FFFFFFFu));
+        }
+    }
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    if ((tid & 31) == 0) red[tid >> 5] = amax;
     bad = __syncthreads_or(bad);
     if (blockIdx.x == 0 && h == 0 && tid == 0) {
         if (len_out) len_out[b] = bad ? len : len + n;
         if (bad) atomicOr(&status[b], DT_DEV_BAD_CACHE);
     }
-    if (bad || n == 0) return;
-    const int p = len / c.page + at;
-    const int lo = max(len, p * c.page), hi = min(len + n, (p + 1) * c.page);  // slots of new rows
-    if (lo >= hi) return;
-
-    const dt_rows& src = keys ? kr : vr;
-    const int cpr = c.D >> 3;  // chunks per row
-    const int m = (hi - lo) * cpr;
-    float x[CH][8];
-    uint32_t amax = 0;
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const int q = tid + i * NT;
-        if (q < m) {
-            const int j = lo - len + q / cpr, ch = q % cpr;
-            const int row = rows ? rows[(size_t)b * N + j] : j;
-            const T* ptr = (const T*)src.ptr + b * src.stride_b + row * src.stride_n + h * src.stride_h;
-            if (keys)
-                dt_rotated8(ptr, ch, rope, len + j, x[i]);
-            else
-                dt_load8(ptr + 8 * ch, x[i]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(x[i][e]) & 0x7FFFFFFFu);
-        }
-    }
-    amax = dt_warp_max_u32(amax);
-    if ((tid & 31) == 0) red[tid >> 5] = amax;
-    __syncthreads();
+    if (bad || !mine) return;
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) amax = max(amax, red[w]);
 
-    const size_t blk = (size_t)table[p] * c.Hkv + h;
+    const size_t blk = (size_t)id * c.Hkv + h;
     float* scale = (keys ? c.k_scale : c.v_scale) + blk;
-    uint8_t* codes = (keys ? c.k : c.v) + blk * c.page * c.D;
-    const bool held = lo > p * c.page;  // the block holds older tokens
+    uint8_t* codes = (keys ? c.k : c.v) + ((blk << lp) * c.D);
+    const int first = lo - (p << lp);  // slot of the first new row
     int e = amax < 0x7F800000u ? block_exponent(amax) : 0;
     bool nan = amax >= 0x7F800000u;
     float old = 1.f;
-    if (held) {
+    if (first > 0) {  // the block holds older tokens
         old = *scale;
         if (old > 0.f && old <= dt_pow2(120)) e = max(e, scale_exponent(old));
         else nan = true;  // also a scale above any that a finite value gives
+        __syncthreads();  // every thread has read the scale
     }
-    __syncthreads();  // every thread has read the scale
     if (tid == 0) *scale = nan ? __int_as_float(0x7FC00000) : dt_pow2(e);
     const float inv = dt_pow2(-e);  // -e in [-120, 48]
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
+    for (int i = 0; i < CP; ++i) {
         const int q = tid + i * NT;
         if (q < m) {
-            uint2 w;
-            w.x = dt_f32x2_to_e4m3x2(__fmul_rn(x[i][0], inv), __fmul_rn(x[i][1], inv)) |
-                  dt_f32x2_to_e4m3x2(__fmul_rn(x[i][2], inv), __fmul_rn(x[i][3], inv)) << 16;
-            w.y = dt_f32x2_to_e4m3x2(__fmul_rn(x[i][4], inv), __fmul_rn(x[i][5], inv)) |
-                  dt_f32x2_to_e4m3x2(__fmul_rn(x[i][6], inv), __fmul_rn(x[i][7], inv)) << 16;
-            *(uint2*)(codes + (size_t)(lo - p * c.page) * c.D + 8 * q) = w;
+            int c0, c1;
+            dt_pair_chunks(q & (ppr - 1), rope, c0, c1);
+            uint8_t* dst = codes + (first + (q >> sh)) * c.D;
+            const uint2 u = codes8(x[i], inv), v = codes8(y[i], inv);
+            if (c1 == c0 + 1) {
+                *(uint4*)(dst + 8 * c0) = make_uint4(u.x, u.y, v.x, v.y);
+            } else {
+                *(uint2*)(dst + 8 * c0) = u;
+                *(uint2*)(dst + 8 * c1) = v;
+            }
         }
     }
-    if (held && !nan && dt_pow2(e) != old) {  // older codes to the larger scale
+    if (first > 0 && !nan && dt_pow2(e) != old) {  // older codes to the larger scale
         const float f = __fmul_rn(old, inv);
-        const int words = (lo - p * c.page) * c.D / 4;
-        for (int q = tid; q < words; q += NT) {
+        for (int q = tid; q < first * c.D / 4; q += NT) {
             const uint32_t w = ((const uint32_t*)codes)[q];
             const float2 a = dt_e4m3x2_to_f32x2(w & 0xFFFFu), d = dt_e4m3x2_to_f32x2(w >> 16);
             ((uint32_t*)codes)[q] = dt_f32x2_to_e4m3x2(__fmul_rn(a.x, f), __fmul_rn(a.y, f)) |
@@ -124,13 +145,13 @@ __global__ void __launch_bounds__(NT) kn10_kernel(dt_kv_cache c, dt_rope rope, i
     }
 }
 
-template <typename T, int CH>
+template <typename T, int CP>
 cudaError_t launch(const dt_kv_cache& c, const dt_rope& rope, int batch, int M, const dt_rows& k, const dt_rows& v,
                    const int32_t* rows, int N, const int32_t* count, int count_add, int32_t* len_out, int32_t* status,
                    cudaStream_t st) {
     const int touched = (N + c.page - 2) / c.page + 1;  // pages that N rows may touch
     DtLaunch lc(dim3(2 * touched, c.Hkv, batch), dim3(NT), 0, st);
-    return cudaLaunchKernelEx(&lc.cfg, kn10_kernel<T, CH>, c, rope, M, k, v, rows, N, count, count_add, len_out,
+    return cudaLaunchKernelEx(&lc.cfg, kn10_kernel<T, CP>, c, rope, M, k, v, rows, N, count, count_add, len_out,
                               status);
 }
 
@@ -138,9 +159,9 @@ template <typename T>
 cudaError_t launch_ch(const dt_kv_cache& c, const dt_rope& rope, int batch, int M, const dt_rows& k, const dt_rows& v,
                       const int32_t* rows, int N, const int32_t* count, int count_add, int32_t* len_out,
                       int32_t* status, cudaStream_t st) {
-    // chunks of a block that new rows can fill, per thread
-    const int most = ((N < c.page ? N : c.page) * (c.D / 8) + NT - 1) / NT;
-    auto f = most <= 1 ? launch<T, 1> : most <= 2 ? launch<T, 2> : most <= 4 ? launch<T, 4> : launch<T, 8>;
+    // chunk pairs of a block that new rows can fill, per thread
+    const int most = ((N < c.page ? N : c.page) * (c.D / 16) + NT - 1) / NT;
+    auto f = most <= 1 ? launch<T, 1> : most <= 2 ? launch<T, 2> : launch<T, 4>;
     return f(c, rope, batch, M, k, v, rows, N, count, count_add, len_out, status, st);
 }
 
