@@ -48,10 +48,12 @@ __global__ void __launch_bounds__(NT) kn10_kernel(const __grid_constant__ dt_kv_
     const int tid = threadIdx.x, b = blockIdx.z, h = blockIdx.y;
     const bool keys = (blockIdx.x & 1) == 0;
     const int at = blockIdx.x >> 1;  // page touched, counted from the first one
-    const int len = c.len[b], n = count ? count[b] + count_add : N;
+    const int len = c.len[b];
+    const long long want = count ? (long long)count[b] + count_add : N;
+    const int n = want < 0 || want > N ? -1 : (int)want;
     const int* table = c.table + (size_t)b * c.max_pages;
     const long long cap = (long long)c.max_pages * c.page;
-    bool bad = len < 0 || n < 0 || n > N || (long long)len + n > cap ||
+    bool bad = len < 0 || n < 0 || (long long)len + n > cap ||
                (kv_rope.rot && n > 0 && (long long)len + n > kv_rope.max_pos);
     const int lp = 31 - __clz(c.page), p = bad ? 0 : (len >> lp) + at;
     const int lo = bad ? 0 : max(len, p << lp), hi = bad ? 0 : min(len + n, (p + 1) << lp);  // slots of new rows

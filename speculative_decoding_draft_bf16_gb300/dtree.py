@@ -156,8 +156,10 @@ def _ptr(t):
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    # the current stream's handle, without a Stream object (4 us of host time per call)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _dtype_code(t):
@@ -624,6 +626,10 @@ def _head_rows(t, batch, M, H, D, name):
     return RowsStruct(t.data_ptr(), sb, sn, sh)
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _need_status(status, batch):
     return _need(status, torch.int32, "status", numel=batch)
 
@@ -650,8 +656,8 @@ def kv_append(cache, k, v, rope=None, rows=None, count=None, count_add=0, len_ou
         _need(len_out, torch.int32, "len_out", numel=batch)
     status = torch.zeros((batch,), dtype=torch.int32, device=k.device) if status is None else _need_status(status, batch)
     _check(lib().dt_kv_append(cache._ref, rope._ref if rope is not None else None, batch, M, _dtype_code(k),
-                              ctypes.byref(kr), ctypes.byref(vr), _ptr(rows), N, _ptr(count), int(count_add),
-                              _ptr(len_out), _ptr(status), _stream(stream)), "dt_kv_append")
+                              ctypes.byref(kr), ctypes.byref(vr), _addr(rows), N, _addr(count), int(count_add),
+                              _addr(len_out), _addr(status), _stream(stream)), "dt_kv_append")
     return status
 
 
@@ -694,8 +700,8 @@ def tree_attention(cache, q, k, v, mask=None, pos=None, n_nodes=None, rope=None,
     if scale is None:
         scale = 1.0 / math.sqrt(cache.D)
     _check(lib().dt_tree_attention(cache._ref, rope._ref if rope is not None else None, batch, M, Hq,
-                                   ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), _ptr(mask), _ptr(pos),
-                                   _ptr(n_nodes), scale, _ptr(out), _ptr(ws), n, _ptr(status), _stream(stream)),
+                                   ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), _addr(mask), _addr(pos),
+                                   _addr(n_nodes), scale, _addr(out), _addr(ws), n, _addr(status), _stream(stream)),
            "dt_tree_attention")
     return out
 
@@ -749,8 +755,8 @@ def token_logprobs(logits, tokens, top=0, rows=None, out=None, stream=None):
                 raise ValueError("out has no room for alternatives (alloc_logprobs(batch, N, top))")
             _need(out.top_id, torch.int32, "top_id", numel=batch * N * top)
             _need(out.top_logprob, torch.float32, "top_logprob", numel=batch * N * top)
-    _check(lib().dt_token_logprobs(_ptr(logits), _dtype_code(logits), batch, M, V, sb, max(sm, V), _ptr(rows),
-                                   _ptr(tokens), N, int(top), _ptr(out.logprob), _ptr(out.entropy), _ptr(out.rank),
-                                   _ptr(out.top_id) if top > 0 else None, _ptr(out.top_logprob) if top > 0 else None,
+    _check(lib().dt_token_logprobs(_addr(logits), _dtype_code(logits), batch, M, V, sb, max(sm, V), _addr(rows),
+                                   _addr(tokens), N, int(top), _addr(out.logprob), _addr(out.entropy), _addr(out.rank),
+                                   _addr(out.top_id) if top > 0 else None, _addr(out.top_logprob) if top > 0 else None,
                                    _stream(stream)), "dt_token_logprobs")
     return out
