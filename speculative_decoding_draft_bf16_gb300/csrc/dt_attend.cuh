@@ -29,6 +29,8 @@ struct AtPlan {
     static constexpr uint32_t FULL = ROWS == 256 ? 5 : 1, PART = ROWS == 256 ? 4 : 1;
     // What starting on a unit costs: its queries, its sums' way out.
     static constexpr uint32_t HEAD = ROWS == 256 ? 20 : 2;
+    // Pieces of so few tiles at a unit's end are not worth starting on.
+    static constexpr int SNAP = ROWS == 256 ? 2 : 1;
     static DT_DI uint32_t weight(int rows) { return rows > ROWS / 2 ? FULL : PART; }
     static DT_DI AtReq req(const DtAttend& a, int b) {
         AtReq r;
@@ -147,14 +149,16 @@ struct AtWalk {
         h = (int)((s.beg - at) / (nt * w + P::HEAD));
         at += h * (nt * w + P::HEAD);
     }
-    // The first tile that starts at cost position x or later.
+    // The first tile that starts at cost position x or later; no cut leaves a piece
+    // of SNAP tiles or fewer at either end of the unit.
     DT_DI int tile_from(uint32_t x) const {
-        if (x <= at) return 0;
-        const uint32_t one = at + P::HEAD + w;  // where tile 1 starts
-        return x <= one ? 1 : min((int)((x - one + w - 1) / w) + 1, nt);
+        if (x <= at + P::HEAD + P::SNAP * w) return 0;
+        const int t = (int)((x - at - P::HEAD + w - 1) / w);
+        return t >= nt - P::SNAP ? nt : t;
     }
     // The next segment, or false.  A unit of at most ATOM tiles is not split.
     DT_DI bool next(const DtAttend& a, const AtShare& s, int c) {
+        static_assert(ATOM >= 2 * P::SNAP, "a cut is near one end of a unit only");
 #pragma unroll 1
         while (b < a.batch && at < s.end) {
             first = s.owner(at);
@@ -165,7 +169,10 @@ struct AtWalk {
             } else {
                 t0 = tile_from(s.beg);
                 t1 = tile_from(s.end);
-                segs = s.owner(at + P::HEAD + w * (nt - 1)) - first + 1;
+                int last = s.owner(at + P::HEAD + w * (nt - 1));
+                if (tile_from(s.start_of(first + 1)) == 0) ++first;
+                if (tile_from(s.start_of(last)) == nt) --last;
+                segs = last - first + 1;
             }
             if (t1 > t0) return true;
             step(a);
@@ -208,17 +215,23 @@ DT_DI int at_position(const DtAttend& a, int b, int len, int node) {
     return (int)at;
 }
 
-// Zeros for the output rows past n_nodes (all rows of a request out of range),
-// spread over the grid.
+// Zeros for the output rows past n_nodes, spread over the grid: a warp reads 32
+// requests' counts at a time and takes every (nt / 32)th of those.
 DT_DI void at_zero_rest(const DtAttend& a, int cta, int ctas, int tid, int nt) {
     if (!a.n_nodes) return;  // a request out of range then has undefined rows
+    const int lane = tid & 31, w = tid >> 5;
     const size_t chunks = (size_t)a.Hq * a.c.D / 8;
 #pragma unroll 1
-    for (int b = 0; b < a.batch; ++b) {
-        const int n = AtPlan<16>::req(a, b).n;
-        uint4* o = (uint4*)a.out + ((size_t)b * a.M + n) * chunks;
-        const size_t m = (size_t)(a.M - n) * chunks;
+    for (int base = 0; base < a.batch; base += 32) {
+        const int mine = base + lane < a.batch ? AtPlan<16>::req(a, base + lane).n : a.M;
 #pragma unroll 1
-        for (size_t i = (size_t)cta * nt + tid; i < m; i += (size_t)ctas * nt) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int k = w; k < 32; k += nt / 32) {
+            const int n = __shfl_sync(0xffffffffu, mine, k);
+            uint4* o = (uint4*)a.out + ((size_t)(base + k) * a.M + n) * chunks;
+            const size_t m = (size_t)(a.M - n) * chunks;
+#pragma unroll 1
+            for (size_t i = (size_t)cta * 32 + lane; i < m; i += (size_t)ctas * 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+            __syncwarp();
+        }
     }
 }

@@ -56,36 +56,67 @@ DT_DI void dt_pair_chunks(int p, const dt_rope& r, int& c0, int& c1) {
     c0 = halves ? p : 2 * p;
     c1 = halves ? p + (r.rot >> 4) : 2 * p + 1;
 }
-// Both chunks as fp32, rotated to position `at` (which must lie in the tables).
+// Eight elements as they are stored.
 template <typename T>
-DT_DI void dt_rotated_pair(const T* row, int p, const dt_rope& r, int at, float (&x)[8], float (&y)[8]) {
-    int c0, c1;
-    dt_pair_chunks(p, r, c0, c1);
-    dt_load8(row + 8 * c0, x);
-    dt_load8(row + 8 * c1, y);
-    if (16 * p >= r.rot) return;
-    float cv[8], sv[8];
-    const size_t o = (size_t)at * (r.rot >> 1) + 8 * p;
-    dt_load8(r.cos + o, cv);
-    dt_load8(r.sin + o, sv);
-    if (r.interleaved) {
+struct DtRaw8;
+template <>
+struct DtRaw8<uint16_t> {
+    uint4 v;
+    DT_DI void load(const uint16_t* p) { v = *(const uint4*)p; }
+    DT_DI void values(float (&x)[8]) const { dt_vec_vals<uint16_t>(v, x); }
+};
+template <>
+struct DtRaw8<float> {
+    float4 v, w;
+    DT_DI void load(const float* p) { v = ((const float4*)p)[0], w = ((const float4*)p)[1]; }
+    DT_DI void values(float (&x)[8]) const {
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w, x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
+    }
+};
+// Both chunks and their angles, loads (no branch among them, so that those of
+// several rows are in flight together) and arithmetic apart.
+template <typename T>
+struct DtPair {
+    DtRaw8<T> a, b;
+    DtRaw8<float> c, s;
+    // `at` must lie in the tables.
+    DT_DI void load(const T* row, int p, const dt_rope& r, int at) {
+        int c0, c1;
+        dt_pair_chunks(p, r, c0, c1);
+        a.load(row + 8 * c0);
+        b.load(row + 8 * c1);
+        const bool turn = 16 * p < r.rot;  // else any 32 bytes
+        const size_t o = (size_t)at * (r.rot >> 1) + 8 * p;
+        c.load(turn ? r.cos + o : (const float*)row);
+        s.load(turn ? r.sin + o : (const float*)row);
+    }
+    // The chunks as fp32, rotated.
+    DT_DI void rotated(int p, const dt_rope& r, float (&x)[8], float (&y)[8]) const {
+        a.values(x);
+        b.values(y);
+        if (16 * p >= r.rot) return;
+        float cv[8], sv[8];
+        c.values(cv);
+        s.values(sv);
+        if (r.interleaved) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1], c = y[2 * i], d = y[2 * i + 1];
-            x[2 * i] = __fsub_rn(__fmul_rn(a, cv[i]), __fmul_rn(b, sv[i]));
-            x[2 * i + 1] = __fadd_rn(__fmul_rn(b, cv[i]), __fmul_rn(a, sv[i]));
-            y[2 * i] = __fsub_rn(__fmul_rn(c, cv[4 + i]), __fmul_rn(d, sv[4 + i]));
-            y[2 * i + 1] = __fadd_rn(__fmul_rn(d, cv[4 + i]), __fmul_rn(c, sv[4 + i]));
-        }
-    } else {
+            for (int i = 0; i < 4; ++i) {
+                const float u0 = x[2 * i], u1 = x[2 * i + 1], v0 = y[2 * i], v1 = y[2 * i + 1];
+                x[2 * i] = __fsub_rn(__fmul_rn(u0, cv[i]), __fmul_rn(u1, sv[i]));
+                x[2 * i + 1] = __fadd_rn(__fmul_rn(u1, cv[i]), __fmul_rn(u0, sv[i]));
+                y[2 * i] = __fsub_rn(__fmul_rn(v0, cv[4 + i]), __fmul_rn(v1, sv[4 + i]));
+                y[2 * i + 1] = __fadd_rn(__fmul_rn(v1, cv[4 + i]), __fmul_rn(v0, sv[4 + i]));
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float a = x[i], b = y[i];
-            x[i] = __fsub_rn(__fmul_rn(a, cv[i]), __fmul_rn(b, sv[i]));
-            y[i] = __fadd_rn(__fmul_rn(b, cv[i]), __fmul_rn(a, sv[i]));
+            for (int i = 0; i < 8; ++i) {
+                const float u = x[i], v = y[i];
+                x[i] = __fsub_rn(__fmul_rn(u, cv[i]), __fmul_rn(v, sv[i]));
+                y[i] = __fadd_rn(__fmul_rn(v, cv[i]), __fmul_rn(u, sv[i]));
+            }
         }
     }
-}
+};
 
 // Two e4m3 codes (the low 16 bits) as an exact fp16 pair.
 DT_DI uint32_t dt_e4m3x2_to_f16x2(uint32_t codes) {

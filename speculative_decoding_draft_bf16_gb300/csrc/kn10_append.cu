@@ -66,14 +66,23 @@ __global__ void __launch_bounds__(NT) kn10_kernel(const __grid_constant__ dt_kv_
     const int ppr = c.D >> 4, sh = c.D == 128 ? 3 : 2;  // chunk pairs per row
     const int m = mine ? (hi - lo) << sh : 0;
     float x[CP][8], y[CP][8];
+    constexpr int U = CP < 2 ? 1 : 2;  // rows in flight
 #pragma unroll
-    for (int i = 0; i < CP; ++i) {
-        const int q = tid + i * NT;
-        if (q < m) {
-            const int j = lo - len + (q >> sh);
-            const int row = rows ? min(max(rows[(size_t)b * N + j], 0), M - 1) : j;
-            dt_rotated_pair((const T*)src.ptr + b * src.stride_b + row * src.stride_n + h * src.stride_h, q & (ppr - 1), rope,
-                            len + j, x[i], y[i]);
+    for (int i0 = 0; i0 < CP; i0 += U) {
+        DtPair<T> raw[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int q = tid + (i0 + k) * NT, j = lo - len + (q >> sh);
+            if (q < m) {
+                const int row = rows ? min(max(rows[(size_t)b * N + j], 0), M - 1) : j;
+                raw[k].load((const T*)src.ptr + b * src.stride_b + row * src.stride_n + h * src.stride_h, q & (ppr - 1),
+                            rope, len + j);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int q = tid + (i0 + k) * NT;
+            if (q < m) raw[k].rotated(q & (ppr - 1), rope, x[i0 + k], y[i0 + k]);
         }
     }
     // every CTA of a request comes to the same verdict on it

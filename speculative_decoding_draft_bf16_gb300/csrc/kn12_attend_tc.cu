@@ -43,8 +43,9 @@ constexpr int STAGES = 2;       // K and V tiles in shared memory, each
 constexpr int RING = 8;         // tiles whose page ids and scales are kept
 constexpr int SEGS = 4;         // segments the walk may be ahead
 constexpr int ATOM = 4;         // tiles of the longest unit that is not split
-constexpr uint32_t MIN_SHARE = 30;    // least cost worth a CTA: the start and two tiles of a full block
-static_assert(MIN_SHARE >= AtPlan<ROWS>::HEAD + AtPlan<ROWS>::FULL, "every CTA between a unit's ends has a tile of it");
+constexpr uint32_t MIN_SHARE = 36;    // least cost worth a CTA: the start and three tiles of a full block
+static_assert(MIN_SHARE >= AtPlan<ROWS>::HEAD + (AtPlan<ROWS>::SNAP + 1) * AtPlan<ROWS>::FULL,
+              "every CTA between a unit's ends has a tile of it");
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float HEADROOM = 5.f, LAZY = 8.f;
 
@@ -230,7 +231,7 @@ struct Conv {
         const int pr = ct % PPT;  // this thread's chunk pair of rows ct / PPT + i * TPI
         int c0, c1;
         dt_pair_chunks(pr, rope, c0, c1);
-        constexpr int U = 2;  // rows in flight
+        constexpr int U = 1;  // rows in flight
         int e = 0;
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {  // the second one when the tile needs another scale
@@ -238,21 +239,23 @@ struct Conv {
             uint32_t big = 0u;
 #pragma unroll 1
             for (int i0 = 0; i0 < NI; i0 += U) {
-                float x[U][8], y[U][8];
+                DtPair<uint16_t> raw[U];
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
                     const int r = min(ct / PPT + (i0 + k) * TPI, left - 1);
-                    dt_rotated_pair(p + (m0 + r) * stride, pr, rope, sh->kpos[r], x[k], y[k]);
+                    raw[k].load(p + (m0 + r) * stride, pr, rope, sh->kpos[r]);
                 }
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
                     const int r = ct / PPT + (i0 + k) * TPI;
                     bool bad = false;
                     uint32_t o[4], w[4];
+                    float x[8], y[8];
+                    raw[k].rotated(pr, rope, x, y);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
-                        float& u0 = x[k][q];
-                        float& u1 = y[k][q];
+                        float& u0 = x[q];
+                        float& u1 = y[q];
                         const bool b0 = (__float_as_uint(u0) & 0x7FFFFFFFu) >= 0x7F800000u;
                         const bool b1 = (__float_as_uint(u1) & 0x7FFFFFFFu) >= 0x7F800000u;
                         bad |= b0 | b1;
@@ -263,8 +266,8 @@ struct Conv {
                     if (bad && r < left) atomicOr(&ring->bad[which][r >> 5], 1u << (r & 31));
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        o[q] = f16x2(x[k][2 * q], x[k][2 * q + 1]);
-                        w[q] = f16x2(y[k][2 * q], y[k][2 * q + 1]);
+                        o[q] = f16x2(x[2 * q], x[2 * q + 1]);
+                        w[q] = f16x2(y[2 * q], y[2 * q + 1]);
                     }
                     sts16(tile + chunk_at(r, c0), o);
                     sts16(tile + chunk_at(r, c1), w);
@@ -358,6 +361,8 @@ struct Conv {
     }
 };
 
+DT_DI void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // The warp that looks up pages and scales, four tiles at a time (eight lanes,
 // of 16 tokens each, to a tile), up to RING tiles ahead of their use, and asks
 // L2 for the codes.  A page id out of range is reported and reads another page.
@@ -388,9 +393,25 @@ DT_DI void look_up(const DtAttend& a, Shared* sh, int lane) {
                 const size_t o = (size_t)id * page_bytes + ((size_t)h << lp) * D + (tok & (a.c.page - 1)) * D;
 #pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.k + o + c * 128));
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.v + o + c * 128));
+                    prefetch_l2(a.c.k + o + c * 128);
+                    prefetch_l2(a.c.v + o + c * 128);
                 }
+            }
+            if (t >= ctx && t < nt) {  // 16 new rows
+                const int m0 = (t0 + t - sg->ctx) * AT_TILE + grp * 16;
+                for (int m = m0; m < min(m0 + 16, sg->n); ++m) {
+                    for (int c = 0; c < D; c += 64) {
+                        prefetch_l2((const uint16_t*)a.k.ptr + b * a.k.stride_b + m * a.k.stride_n + h * a.k.stride_h + c);
+                        prefetch_l2((const uint16_t*)a.v.ptr + b * a.v.stride_b + m * a.v.stride_n + h * a.v.stride_h + c);
+                    }
+                }
+            }
+            if (k == 0) {  // the block's query rows
+                const uint32_t G = a.G, r0 = (uint32_t)sg->qb * ROWS;
+                const uint16_t* q = (const uint16_t*)a.q.ptr + b * a.q.stride_b + (size_t)h * G * a.q.stride_h;
+#pragma unroll 1
+                for (uint32_t r = r0 + lane; r < r0 + sg->rows; r += 32)
+                    for (int c = 0; c < D; c += 64) prefetch_l2(q + r / G * a.q.stride_n + r % G * a.q.stride_h + c);
             }
             for (int d = 0; d < 4 && k + d < nt; ++d, ++g) {
                 wait(&sh->ringfree[g % RING], (g / RING + 1) & 1, &sh->fail);
@@ -510,18 +531,20 @@ struct Soft {
         const uint16_t* base = (const uint16_t*)a.q.ptr + u.b * a.q.stride_b + (size_t)u.h * G * a.q.stride_h;
 #pragma unroll 1
         for (int r0 = tid / PPR; r0 < tiles * TQ; r0 += U * RPI) {
-            float x[U][8], y[U][8];
+            DtPair<uint16_t> raw[U];
 #pragma unroll
             for (int k = 0; k < U; ++k)  // U rows in flight
-                dt_rotated_pair(base + sh->qoff[r0 + k * RPI], pr, a.rope, sh->qpos[r0 + k * RPI], x[k], y[k]);
+                raw[k].load(base + sh->qoff[r0 + k * RPI], pr, a.rope, sh->qpos[r0 + k * RPI]);
 #pragma unroll
             for (int k = 0; k < U; ++k) {
                 const int r = r0 + k * RPI;
                 uint32_t big = 0;
+                float x[8], y[8];
+                raw[k].rotated(pr, a.rope, x, y);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    if (r >= u.rows) x[k][e] = y[k][e] = 0.f;
-                    big = max(big, max(__float_as_uint(x[k][e]) & 0x7FFFFFFFu, __float_as_uint(y[k][e]) & 0x7FFFFFFFu));
+                    if (r >= u.rows) x[e] = y[e] = 0.f;
+                    big = max(big, max(__float_as_uint(x[e]) & 0x7FFFFFFFu, __float_as_uint(y[e]) & 0x7FFFFFFFu));
                 }
 #pragma unroll
                 for (int o = PPR / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
@@ -531,8 +554,8 @@ struct Soft {
                 uint32_t w[4], z[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    w[e] = f16x2(__fmul_rn(x[k][2 * e], f), __fmul_rn(x[k][2 * e + 1], f));
-                    z[e] = f16x2(__fmul_rn(y[k][2 * e], f), __fmul_rn(y[k][2 * e + 1], f));
+                    w[e] = f16x2(__fmul_rn(x[2 * e], f), __fmul_rn(x[2 * e + 1], f));
+                    z[e] = f16x2(__fmul_rn(y[2 * e], f), __fmul_rn(y[2 * e + 1], f));
                 }
                 sts16(qb + (r / TQ) * L::TILE + chunk_at(r % TQ, c0), w);
                 sts16(qb + (r / TQ) * L::TILE + chunk_at(r % TQ, c1), z);
@@ -815,52 +838,76 @@ struct Soft {
         float M = NEG_INF, l = 0.f;  // of row tid
         if (tid < rows) {
 #pragma unroll 4
-            for (int i = 0; i < segs; ++i) M = fmaxf(M, __ldcg(slot(i) + tid));
-#pragma unroll 4
             for (int i = 0; i < segs; ++i) {
-                const float mi = __ldcg(slot(i) + tid);
-                l = __fmaf_rn(__ldcg(slot(i) + ROWS + tid), mi == NEG_INF ? 0.f : dt_ex2_approx(mi - M), l);
+                const float mi = __ldcg(slot(i) + tid), li = __ldcg(slot(i) + ROWS + tid), up = fmaxf(M, mi);
+                if (up != NEG_INF) l = __fmaf_rn(li, dt_ex2_approx(mi - up), __fmul_rn(l, dt_ex2_approx(M - up)));
+                else l = __fadd_rn(l, li);  // 0, or NaN
+                M = up;
             }
         }
         const float inv = l == 0.f ? 0.f : 1.0f / l;
         // a thread has two neighbouring chunks of 4 columns of 16 rows apart: lanes
-        // 0-15 and 16-31 of a warp take 16 rows each, 32 bytes of output together
-        const int r0 = tid & 15, c0 = ((tid >> 4) & 1) * 2, w = tid >> 5;
+        // 0-15 and 16-31 of a warp take 16 rows each, 32 bytes of output together;
+        // U such pieces at a time, so that their loads are in flight together
+        constexpr int U = 4;
+        const int r0 = tid & 15, c0 = ((tid >> 4) & 1) * 2, w = tid >> 5, pieces = (rows + 15) / 16 * (D / 16);
         for (int i0 = 0; i0 < segs; i0 += P) {
-            // weight of part i for each row, 1 / l included; past the last part 0
+            // weight of part i for each row, 1 / l included
+            const int np = min(P, segs - i0);
             asm volatile("bar.sync 2, 256;" ::: "memory");
-            for (int i = 0; i < P; ++i) {
-                const float mi = tid < rows && i0 + i < segs ? __ldcg(slot(i0 + i) + tid) : NEG_INF;
+#pragma unroll 4
+            for (int i = 0; i < np; ++i) {
+                const float mi = tid < rows ? __ldcg(slot(i0 + i) + tid) : NEG_INF;
                 wt[i * ROWS + tid] = mi == NEG_INF ? 0.f : __fmul_rn(dt_ex2_approx(mi - M), inv);
             }
             asm volatile("bar.sync 2, 256;" ::: "memory");
-            const int np = min(P, segs - i0);
-            for (int k = w; k < (rows + 15) / 16 * (D / 16); k += NS / 32) {  // 16 rows, 16 columns
-                const int r = k / (D / 16) * 16 + r0, c = k % (D / 16) * 4 + c0;
-                float x[8] = {};
-                float4* acc = (float4*)(slot(0) + 2 * ROWS) + c * ROWS + r;  // this thread's, read already
-                if (i0 > 0) {
-                    const float4 y = acc[0], z = acc[ROWS];
-                    x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w, x[4] = z.x, x[5] = z.y, x[6] = z.z, x[7] = z.w;
-                }
-#pragma unroll 4
-                for (int i = 0; i < np; ++i) {
-                    const float4* o = (const float4*)(slot(i0 + i) + 2 * ROWS) + c * ROWS + r;
-                    const float4 y = __ldcg(o), z = __ldcg(o + ROWS);
-                    const float f = wt[i * ROWS + r];
-                    x[0] = __fmaf_rn(y.x, f, x[0]), x[1] = __fmaf_rn(y.y, f, x[1]);
-                    x[2] = __fmaf_rn(y.z, f, x[2]), x[3] = __fmaf_rn(y.w, f, x[3]);
-                    x[4] = __fmaf_rn(z.x, f, x[4]), x[5] = __fmaf_rn(z.y, f, x[5]);
-                    x[6] = __fmaf_rn(z.z, f, x[6]), x[7] = __fmaf_rn(z.w, f, x[7]);
-                }
-                if (i0 + P < segs) {
-                    acc[0] = make_float4(x[0], x[1], x[2], x[3]);
-                    acc[ROWS] = make_float4(x[4], x[5], x[6], x[7]);
-                } else if (r < rows) {
-                    uint32_t o[4];
+#pragma unroll 1
+            for (int k0 = w; k0 < pieces; k0 += U * (NS / 32)) {
+                float x[U][8] = {};
+                int at[U];  // row + ROWS * chunk of a piece; past the end the first one again
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] = bf16x2(x[2 * e], x[2 * e + 1]);
-                    *(uint4*)(out_row(a, u, r) + 4 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+                for (int v = 0; v < U; ++v) {
+                    const int k = k0 + v * (NS / 32) < pieces ? k0 + v * (NS / 32) : k0;
+                    at[v] = k / (D / 16) * 16 + r0 + (k % (D / 16) * 4 + c0) * ROWS;
+                }
+                if (i0 > 0) {
+#pragma unroll
+                    for (int v = 0; v < U; ++v) {
+                        const float4* acc = (const float4*)(slot(0) + 2 * ROWS) + at[v];  // this thread's, read already
+                        const float4 y = acc[0], z = acc[ROWS];
+                        x[v][0] = y.x, x[v][1] = y.y, x[v][2] = y.z, x[v][3] = y.w;
+                        x[v][4] = z.x, x[v][5] = z.y, x[v][6] = z.z, x[v][7] = z.w;
+                    }
+                }
+#pragma unroll 1
+                for (int i = 0; i < np; ++i) {
+                    const float4* o = (const float4*)(slot(i0 + i) + 2 * ROWS);
+                    float4 y[U], z[U];
+#pragma unroll
+                    for (int v = 0; v < U; ++v) y[v] = __ldcg(o + at[v]), z[v] = __ldcg(o + at[v] + ROWS);
+#pragma unroll
+                    for (int v = 0; v < U; ++v) {
+                        const float f = wt[i * ROWS + at[v] % ROWS];
+                        x[v][0] = __fmaf_rn(y[v].x, f, x[v][0]), x[v][1] = __fmaf_rn(y[v].y, f, x[v][1]);
+                        x[v][2] = __fmaf_rn(y[v].z, f, x[v][2]), x[v][3] = __fmaf_rn(y[v].w, f, x[v][3]);
+                        x[v][4] = __fmaf_rn(z[v].x, f, x[v][4]), x[v][5] = __fmaf_rn(z[v].y, f, x[v][5]);
+                        x[v][6] = __fmaf_rn(z[v].z, f, x[v][6]), x[v][7] = __fmaf_rn(z[v].w, f, x[v][7]);
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < U; ++v) {
+                    if (k0 + v * (NS / 32) >= pieces) continue;
+                    const int r = at[v] % ROWS;
+                    if (i0 + P < segs) {
+                        float4* acc = (float4*)(slot(0) + 2 * ROWS) + at[v];
+                        acc[0] = make_float4(x[v][0], x[v][1], x[v][2], x[v][3]);
+                        acc[ROWS] = make_float4(x[v][4], x[v][5], x[v][6], x[v][7]);
+                    } else if (r < rows) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[e] = bf16x2(x[v][2 * e], x[v][2 * e + 1]);
+                        *(uint4*)(out_row(a, u, r) + 4 * (at[v] / ROWS)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
                 }
             }
         }
@@ -909,11 +956,11 @@ __global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtA
     const uint32_t tmem = sh->tmem;
     if (tid < NS) {
         set_regs<REG_SOFT>();
-        at_zero_rest(a, cta, ctas, tid, NS);
         Soft<D>::run(a, sm, sh, tmem, tid, cta, part, counters);
     } else if (tid < NS + 2 * NC) {
         set_regs<REG_CONV>();
         Conv<D>::run(a, sm, sh, (tid - NS) % NC, tid < NS + NC);
+        at_zero_rest(a, cta, ctas, tid - NS, 2 * NC);
     } else {
         set_regs<REG_MMA>();
         constexpr int W0 = (NS + 2 * NC) / 32;
