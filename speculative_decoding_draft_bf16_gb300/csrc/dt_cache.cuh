@@ -14,48 +14,6 @@ DT_DI void dt_load8(const float* p, float (&x)[8]) {
     x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
-// Elements 8c .. 8c+7 of a head vector, rotated to position `at` (which must
-// lie in the tables).  The partner chunk of the split-halves form is read
-// again by the thread that owns it: both reads hit the same cache lines.
-template <typename T>
-DT_DI void dt_rotated8(const T* row, int c, const dt_rope& r, int at, float (&x)[8]) {
-    dt_load8(row + 8 * c, x);
-    if (8 * c >= r.rot) return;
-    const int half = r.rot >> 1;
-    const float* cs = r.cos + (size_t)at * half;
-    const float* sn = r.sin + (size_t)at * half;
-    if (r.interleaved) {
-        const float4 co = *(const float4*)(cs + 4 * c), si = *(const float4*)(sn + 4 * c);
-        const float cv[4] = {co.x, co.y, co.z, co.w}, sv[4] = {si.x, si.y, si.z, si.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = __fsub_rn(__fmul_rn(a, cv[i]), __fmul_rn(b, sv[i]));
-            x[2 * i + 1] = __fadd_rn(__fmul_rn(b, cv[i]), __fmul_rn(a, sv[i]));
-        }
-    } else {
-        const bool second = 8 * c >= half;
-        const int i0 = second ? 8 * c - half : 8 * c;
-        float y[8], cv[8], sv[8];
-        dt_load8(second ? row + i0 : row + 8 * c + half, y);
-        dt_load8(cs + i0, cv);
-        dt_load8(sn + i0, sv);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float t = __fmul_rn(y[i], sv[i]);
-            x[i] = second ? __fadd_rn(__fmul_rn(x[i], cv[i]), t) : __fsub_rn(__fmul_rn(x[i], cv[i]), t);
-        }
-    }
-}
-
-// Two chunks of 8 elements of a head vector that rotate together, index p of
-// D / 16: split halves pair chunk p with chunk p + rot / 16; otherwise, and
-// past rot, neighbours.  c0, c1: which chunks they are.
-DT_DI void dt_pair_chunks(int p, const dt_rope& r, int& c0, int& c1) {
-    const bool halves = !r.interleaved && 16 * p < r.rot;
-    c0 = halves ? p : 2 * p;
-    c1 = halves ? p + (r.rot >> 4) : 2 * p + 1;
-}
 // Eight elements as they are stored.
 template <typename T>
 struct DtRaw8;
@@ -73,6 +31,60 @@ struct DtRaw8<float> {
         x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w, x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
     }
 };
+// Elements 8c .. 8c+7 of a head vector, rotated to position `at` (which must lie in
+// the tables): loads (no branch among them, so that several chunks' are in flight
+// together) and arithmetic apart.  The partner chunk of the split-halves form is
+// read again by the thread that owns it: both reads hit the same cache lines.
+template <typename T>
+struct DtTurned8 {
+    DtRaw8<T> own, other;
+    DtRaw8<float> c, s;
+    DT_DI void load(const T* row, int ch, const dt_rope& r, int at) {
+        const int half = r.rot >> 1;
+        const bool turn = 8 * ch < r.rot;
+        // where the angles are read: eight of them that lie in the row
+        const int i0 = r.interleaved ? min(4 * ch, half - 8) : 8 * ch >= half ? 8 * ch - half : 8 * ch;
+        const int mate = !turn || r.interleaved ? 8 * ch : 8 * ch >= half ? 8 * ch - half : 8 * ch + half;
+        own.load(row + 8 * ch);
+        other.load(row + mate);
+        c.load(turn ? r.cos + (size_t)at * half + i0 : (const float*)row);  // else any 32 bytes
+        s.load(turn ? r.sin + (size_t)at * half + i0 : (const float*)row);
+    }
+    DT_DI void values(int ch, const dt_rope& r, float (&x)[8]) const {
+        own.values(x);
+        if (8 * ch >= r.rot) return;
+        float cv[8], sv[8];
+        c.values(cv);
+        s.values(sv);
+        if (r.interleaved) {
+            const bool up = 4 * ch > (r.rot >> 1) - 8;  // the angles are the last four read
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float u = x[2 * i], v = x[2 * i + 1], co = up ? cv[4 + i] : cv[i], si = up ? sv[4 + i] : sv[i];
+                x[2 * i] = __fsub_rn(__fmul_rn(u, co), __fmul_rn(v, si));
+                x[2 * i + 1] = __fadd_rn(__fmul_rn(v, co), __fmul_rn(u, si));
+            }
+        } else {
+            const bool second = 8 * ch >= (r.rot >> 1);
+            float y[8];
+            other.values(y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float t = __fmul_rn(y[i], sv[i]);
+                x[i] = second ? __fadd_rn(__fmul_rn(x[i], cv[i]), t) : __fsub_rn(__fmul_rn(x[i], cv[i]), t);
+            }
+        }
+    }
+};
+
+// Two chunks of 8 elements of a head vector that rotate together, index p of
+// D / 16: split halves pair chunk p with chunk p + rot / 16; otherwise, and
+// past rot, neighbours.  c0, c1: which chunks they are.
+DT_DI void dt_pair_chunks(int p, const dt_rope& r, int& c0, int& c1) {
+    const bool halves = !r.interleaved && 16 * p < r.rot;
+    c0 = halves ? p : 2 * p;
+    c1 = halves ? p + (r.rot >> 4) : 2 * p + 1;
+}
 // Both chunks and their angles, loads (no branch among them, so that those of
 // several rows are in flight together) and arithmetic apart.
 template <typename T>

@@ -5,12 +5,14 @@
 // lane copies the bytes that it will need itself to its own places in shared
 // memory (cp.async, STAGES tiles ahead: up to 192 KB of an SM's loads are in
 // flight, and nothing is waited for but the lane's own copies), turns the e4m3
-// codes into fp16 in registers and feeds 16 x 8 x 16 MMAs:
-//   S = Q K^T   a lane's 32 bytes of a token serve as the K-fragment of all
-//               steps: which elements of the head a step takes is free, as long
-//               as Q's fragments are cut alike;
-//   O += P V    P's fragments are S's; a lane reads 16 columns of four tokens and
-//               pairs the tokens' bytes before it converts them.
+// codes into fp16 in registers and feeds 16 x 8 x 16 MMAs, tokens and columns on
+// the side of 16, NR groups of 8 query rows on the other:
+//   S' = K Q'    a lane's 32 bytes of a token serve as the K-fragment of all
+//                steps: which elements of the head a step takes is free, as long
+//                as Q's fragments are cut alike;
+//   O' += V' P'  P's fragments are S's, transposed 8 x 8 at a time; a lane reads 16
+//                columns of four tokens and pairs the tokens' bytes before it
+//                converts them.
 // (These narrow products cannot fill a tcgen05 tile: 16 rows of 128, and the
 // cache's bytes, not the products, bound the time.)  Scales as on the tensor
 // cores: P holds 2^(t + log2 vs - m), the row sum adds p / vs, and m moves only
@@ -76,23 +78,34 @@ DT_DI void lds(uint32_t addr, uint32_t (&w)[WORDS]) {
         asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
 }
 
-template <int D>
+// The transpose of an 8 x 8 matrix of 16-bit elements, two of a row to a lane.
+DT_DI uint32_t transposed8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int D, int NR>
 struct Stream {
     using L = Lay<D>;
     using Walk = AtWalk<ROWS, ATOM>;
-    static constexpr int KS = D / 16;  // steps of Q K^T
-    static constexpr int NV = D / 8;   // column tiles of P V; tile j has columns NV * g + j
+    static constexpr int KS = D / 16;  // steps of K Q'
+    static constexpr int NV = D / 8;   // columns of a lane in V' P': NV * g + j; two to an MMA
 
-    uint32_t qs;                       // Q's fragments in shared memory, [KS][32 lanes][4 words]
-    float rowc[2], m[2], l[2];
-    float o[NV][4];
+    uint32_t qs;  // Q's fragments in shared memory, [KS / 2][NR][32 lanes][4 words]
+    // of rows 2t + e + 8i (g, t: the lane's group of 4 and place in it)
+    float rowc[NR][2], m[NR][2], l[NR][2];
+    float o[NV / 2][NR][4];  // [j / 2][i][2 * (j % 2) + e]
 
-    // Two 8-element chunks (16 elements from 16 * c) of a head vector, rotated.
+    // 16 elements from 16 * c of a head vector, rotated.
     static DT_DI void pick16(const uint16_t* row, int c, const dt_rope& r, int at, float (&x)[16]) {
+        DtTurned8<uint16_t> raw[2];
         float y[8];
 #pragma unroll
+        for (int i = 0; i < 2; ++i) raw[i].load(row, 2 * c + i, r, at);
+#pragma unroll
         for (int i = 0; i < 2; ++i) {
-            dt_rotated8(row, 2 * c + i, r, at, y);
+            raw[i].values(2 * c + i, r, y);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[8 * i + e] = y[e];
         }
@@ -101,7 +114,7 @@ struct Stream {
     DT_DI void queries(const DtAttend& a, const Walk& u, int lane) {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NR; ++i) {
             const int r = g + 8 * i;
             float x[L::KC][16];
             uint32_t big = 0;
@@ -126,97 +139,105 @@ struct Stream {
             big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
             int ex = (int)(big >> 23) - 127;  // largest magnitude in [2^ex, 2^(ex+1))
             ex = big >= 0x7F800000u ? 0 : max(ex, -100);
-            const float f = dt_pow2(-ex);
-            rowc[i] = __fmul_rn(__fmul_rn(a.scale, LOG2E), dt_pow2(ex));
+            const float f = dt_pow2(-ex), rc = __fmul_rn(__fmul_rn(a.scale, LOG2E), dt_pow2(ex));
+            rowc[i][0] = __shfl_sync(0xffffffffu, rc, 8 * t);
+            rowc[i][1] = __shfl_sync(0xffffffffu, rc, 8 * t + 4);
             // every warp writes the same words
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 const float* y = x[s >> 2] + 4 * (s & 3);
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qs + s * 512 + lane * 16 + i * 8),
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qs + (((s >> 1) * NR + i) * 32 + lane) * 16 + (s & 1) * 8),
                              "r"(f16x2(__fmul_rn(y[0], f), __fmul_rn(y[1], f))),
                              "r"(f16x2(__fmul_rn(y[2], f), __fmul_rn(y[3], f)))
                              : "memory");
             }
         }
     }
-    // The fragments of step s: rows g, g + 8 of the first two elements, then of the others.
-    DT_DI void frag(int s, int lane, uint32_t (&f)[4]) const {
-        uint32_t w[4];
-        lds<4>(qs + s * 512 + lane * 16, w);
-        f[0] = w[0], f[2] = w[1], f[1] = w[2], f[3] = w[3];
-    }
 
-    // Scores of two groups of 8 tokens (columns 2t, 2t + 1 of each; rows g, g + 8),
-    // masked, to probabilities as the fragments of P; ks, lv, iv: the 16 tokens'.
-    DT_DI void weigh(float (&c)[2][4], float ks, float lv, float iv, uint32_t (&p)[4]) {
+    // Scores of 16 tokens, masked (c[i][2k + e]: token g + 8k, row 2t + e + 8i), to
+    // probabilities as the fragments of P'; ks, lv, iv: the 16 tokens'.
+    DT_DI void weigh(float (&c)[NR][4], float ks, float lv, float iv, uint32_t (&p)[NR][2]) {
         const float NEG_INF = -__int_as_float(0x7F800000);
-        const float k0 = __fmul_rn(rowc[0], ks), k1 = __fmul_rn(rowc[1], ks);
-        float t0 = fmaxf(fmaxf(c[0][0], c[0][1]), fmaxf(c[1][0], c[1][1]));
-        float t1 = fmaxf(fmaxf(c[0][2], c[0][3]), fmaxf(c[1][2], c[1][3]));
-        t0 = __fmaf_rn(t0, k0, lv);
-        t1 = __fmaf_rn(t1, k1, lv);
-        if (__any_sync(0xffffffffu, t0 > m[0] + (HEADROOM + LAZY) || t1 > m[1] + (HEADROOM + LAZY))) {
+        float k[NR][2], top[NR][2];
+        bool grown = false;
 #pragma unroll
-            for (int x = 1; x < 4; x <<= 1) {
-                t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
-                t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
-            }
-            const float n0 = t0 > m[0] + (HEADROOM + LAZY) ? t0 - HEADROOM : m[0];
-            const float n1 = t1 > m[1] + (HEADROOM + LAZY) ? t1 - HEADROOM : m[1];
-            const float f0 = n0 == m[0] ? 1.f : dt_ex2_approx(m[0] - n0);  // m = -inf: 0
-            const float f1 = n1 == m[1] ? 1.f : dt_ex2_approx(m[1] - n1);
-            m[0] = n0, m[1] = n1;
-            l[0] = __fmul_rn(l[0], f0), l[1] = __fmul_rn(l[1], f1);
+        for (int i = 0; i < NR; ++i) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                o[j][0] = __fmul_rn(o[j][0], f0), o[j][1] = __fmul_rn(o[j][1], f0);
-                o[j][2] = __fmul_rn(o[j][2], f1), o[j][3] = __fmul_rn(o[j][3], f1);
+            for (int e = 0; e < 2; ++e) {
+                k[i][e] = __fmul_rn(rowc[i][e], ks);
+                top[i][e] = __fmaf_rn(fmaxf(c[i][e], c[i][2 + e]), k[i][e], lv);
+                grown |= top[i][e] > m[i][e] + (HEADROOM + LAZY);
             }
         }
-        const float b0 = __fsub_rn(lv, m[0] == NEG_INF ? 0.f : m[0]), b1 = __fsub_rn(lv, m[1] == NEG_INF ? 0.f : m[1]);
+        if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+            for (int i = 0; i < NR; ++i) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) c[n][e] = dt_ex2_approx(__fmaf_rn(c[n][e], e < 2 ? k0 : k1, e < 2 ? b0 : b1));
+                for (int e = 0; e < 2; ++e) {
+                    float x = top[i][e];
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                    const float to = x > m[i][e] + (HEADROOM + LAZY) ? x - HEADROOM : m[i][e];
+                    const float f = to == m[i][e] ? 1.f : dt_ex2_approx(m[i][e] - to);  // m = -inf: 0
+                    m[i][e] = to;
+                    l[i][e] = __fmul_rn(l[i][e], f);
+#pragma unroll
+                    for (int j = 0; j < NV / 2; ++j) {
+                        o[j][i][e] = __fmul_rn(o[j][i][e], f);
+                        o[j][i][2 + e] = __fmul_rn(o[j][i][2 + e], f);
+                    }
+                }
+            }
         }
-        l[0] = __fmaf_rn(__fadd_rn(__fadd_rn(c[0][0], c[0][1]), __fadd_rn(c[1][0], c[1][1])), iv, l[0]);
-        l[1] = __fmaf_rn(__fadd_rn(__fadd_rn(c[0][2], c[0][3]), __fadd_rn(c[1][2], c[1][3])), iv, l[1]);
-        p[0] = f16x2(c[0][0], c[0][1]);
-        p[1] = f16x2(c[0][2], c[0][3]);
-        p[2] = f16x2(c[1][0], c[1][1]);
-        p[3] = f16x2(c[1][2], c[1][3]);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float b = __fsub_rn(lv, m[i][e] == NEG_INF ? 0.f : m[i][e]);
+                c[i][e] = dt_ex2_approx(__fmaf_rn(c[i][e], k[i][e], b));
+                c[i][2 + e] = dt_ex2_approx(__fmaf_rn(c[i][2 + e], k[i][e], b));
+                l[i][e] = __fmaf_rn(__fadd_rn(c[i][e], c[i][2 + e]), iv, l[i][e]);
+            }
+            p[i][0] = transposed8x8(f16x2(c[i][0], c[i][1]));
+            p[i][1] = transposed8x8(f16x2(c[i][2], c[i][3]));
+        }
     }
 
     // The staged 16 tokens at `st`, of which the first `left` exist.
     DT_DI void tile(uint32_t st, int lane, int left, float ks, float lv, float iv) {
-        const int t = lane & 3;
+        const int g = lane >> 2;
         const uint32_t my = st + lane * 16;
-        float c[2][4] = {};
+        float c[NR][4] = {};
 #pragma unroll
         for (int j = 0; j < L::KC; ++j) {
             uint32_t w[2][4];
             lds<4>(my + j * 512, w[0]);
             lds<4>(my + (L::KC + j) * 512, w[1]);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                uint32_t f[4], b0, b1;
-                frag(4 * j + s, lane, f);
+            for (int s = 0; s < 4; s += 2) {
+                uint32_t f[2][4], q[NR][4];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    dt_e4m3x4_to_f16x4(w[n][s], b0, b1);
-                    mma(c[n], f, b0, b1);
+                for (int k = 0; k < 2; ++k) {
+                    dt_e4m3x4_to_f16x4(w[0][s + k], f[k][0], f[k][2]);
+                    dt_e4m3x4_to_f16x4(w[1][s + k], f[k][1], f[k][3]);
+                }
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    lds<4>(qs + (((4 * j + s) / 2 * NR + i) * 32 + lane) * 16, q[i]);
+                    mma(c[i], f[0], q[i][0], q[i][1]);
+                    mma(c[i], f[1], q[i][2], q[i][3]);
                 }
             }
         }
         if (left < 16) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int i = 0; i < NR; ++i) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (8 * n + 2 * t + (e & 1) >= left) c[n][e] = -__int_as_float(0x7F800000);
+                for (int k = 0; k < 4; ++k)
+                    if (g + 8 * (k >> 1) >= left) c[i][k] = -__int_as_float(0x7F800000);
             }
         }
-        uint32_t p[4];
+        uint32_t p[NR][2];
         weigh(c, ks, lv, iv, p);
         // values of tokens 2t, 2t + 1, 2t + 8, 2t + 9
         constexpr int VW = L::VB / 4;
@@ -227,17 +248,30 @@ struct Stream {
         for (int j = 0; j < VW; ++j) {
             const uint32_t a0 = __byte_perm(w[0][j], w[1][j], 0x5140), a1 = __byte_perm(w[0][j], w[1][j], 0x7362);
             const uint32_t b0 = __byte_perm(w[2][j], w[3][j], 0x5140), b1 = __byte_perm(w[2][j], w[3][j], 0x7362);
-            uint32_t a[4], b[4];
-            dt_e4m3x4_to_f16x4(a0, a[0], a[1]);
-            dt_e4m3x4_to_f16x4(a1, a[2], a[3]);
-            dt_e4m3x4_to_f16x4(b0, b[0], b[1]);
-            dt_e4m3x4_to_f16x4(b1, b[2], b[3]);
+            uint32_t f[2][4];
+            dt_e4m3x4_to_f16x4(a0, f[0][0], f[0][1]);
+            dt_e4m3x4_to_f16x4(b0, f[0][2], f[0][3]);
+            dt_e4m3x4_to_f16x4(a1, f[1][0], f[1][1]);
+            dt_e4m3x4_to_f16x4(b1, f[1][2], f[1][3]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mma(o[4 * j + e], p, a[e], b[e]);
+            for (int i = 0; i < NR; ++i) {
+                mma(o[2 * j][i], f[0], p[i][0], p[i][1]);
+                mma(o[2 * j + 1][i], f[1], p[i][0], p[i][1]);
+            }
         }
     }
 
-    // Up to 16 new rows (one warp): rotated, scaled by powers of two to a largest
+    DT_DI void clear() {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+#pragma unroll
+            for (int j = 0; j < NV / 2; ++j) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
+            m[i][0] = m[i][1] = -__int_as_float(0x7F800000);
+            l[i][0] = l[i][1] = 0.f;
+        }
+    }
+
+    // The first of a warp's sums, from up to 16 new rows: rotated, scaled by powers of two to a largest
     // magnitude below 2, a row that is not finite replaced by zeros and reported
     // to those that see it.
     DT_DI void fresh(const DtAttend& a, const Walk& u, int lane) {
@@ -245,101 +279,120 @@ struct Stream {
         const uint16_t* kp = (const uint16_t*)a.k.ptr + u.b * a.k.stride_b + u.h * a.k.stride_h;
         const uint16_t* vp = (const uint16_t*)a.v.ptr + u.b * a.v.stride_b + u.h * a.v.stride_h;
         uint32_t bad = 0;  // bit per row
-        auto clean = [&](float (&x)[16], int row, uint32_t& big) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const uint32_t v = __float_as_uint(x[e]) & 0x7FFFFFFFu;
-                if (v >= 0x7F800000u) x[e] = 0.f, bad |= 1u << row;
-                else big = max(big, v);
-            }
-        };
         auto exponent = [](uint32_t big) {
             big = __reduce_max_sync(0xffffffffu, big);
             return max((int)(big >> 23) - 127, -57);
         };
-        float c[2][4] = {};
+        if (lane < n) {
+            for (int e = 0; e < D; e += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(vp + lane * a.v.stride_n + e));
+        }
+        float c[NR][4] = {};
         float k[2][L::KC][16];
         uint32_t big = 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int row = g + 8 * i;
+            const int at = a.rope.rot && row < n ? at_position(a, u.b, u.r.len, row) : 0;
 #pragma unroll
             for (int j = 0; j < L::KC; ++j) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) k[i][j][e] = 0.f;
-                if (row < n) {
-                    pick16(kp + row * a.k.stride_n, t + 4 * j, a.rope, at_position(a, u.b, u.r.len, row), k[i][j]);
-                    clean(k[i][j], row, big);
+                if (row < n) pick16(kp + row * a.k.stride_n, t + 4 * j, a.rope, at, k[i][j]);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const uint32_t w = __float_as_uint(k[i][j][e]) & 0x7FFFFFFFu;
+                    if (w >= 0x7F800000u) k[i][j][e] = 0.f, bad |= 1u << row;
+                    else big = max(big, w);
                 }
             }
         }
         const int ek = exponent(big);
         const float fk = dt_pow2(-ek);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int s = 0; s < KS; ++s) {
+            const float *y = k[0][s >> 2] + 4 * (s & 3), *z = k[1][s >> 2] + 4 * (s & 3);
+            const uint32_t f[4] = {f16x2(__fmul_rn(y[0], fk), __fmul_rn(y[1], fk)), f16x2(__fmul_rn(z[0], fk), __fmul_rn(z[1], fk)),
+                                   f16x2(__fmul_rn(y[2], fk), __fmul_rn(y[3], fk)), f16x2(__fmul_rn(z[2], fk), __fmul_rn(z[3], fk))};
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                const float* y = k[i][s >> 2] + 4 * (s & 3);
-                uint32_t f[4];
-                frag(s, lane, f);
-                mma(c[i], f, f16x2(__fmul_rn(y[0], fk), __fmul_rn(y[1], fk)), f16x2(__fmul_rn(y[2], fk), __fmul_rn(y[3], fk)));
+            for (int i = 0; i < NR; ++i) {
+                uint32_t q[2];
+                lds<2>(qs + (((s >> 1) * NR + i) * 32 + lane) * 16 + (s & 1) * 8, q);
+                mma(c[i], f, q[0], q[1]);
             }
         }
-        float v[4][L::VB];
+        uint32_t v[4][L::VB / 2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int row = 2 * t + (k & 1) + 8 * (k >> 1);
+#pragma unroll
+            for (int e = 0; e < L::VB / 2; e += 4) {
+                uint4 y = make_uint4(0u, 0u, 0u, 0u);
+                if (row < n) y = *(const uint4*)(vp + row * a.v.stride_n + L::VB * g + 2 * e);
+                v[k][e] = y.x, v[k][e + 1] = y.y, v[k][e + 2] = y.z, v[k][e + 3] = y.w;
+            }
+        }
         big = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = 2 * t + (i & 1) + 8 * (i >> 1);
+        for (int k4 = 0; k4 < 4; ++k4) {
+            const int row = 2 * t + (k4 & 1) + 8 * (k4 >> 1);
 #pragma unroll
-            for (int e = 0; e < L::VB; e += 8) {
-                float y[8] = {};
-                if (row < n) dt_load8(vp + row * a.v.stride_n + L::VB * g + e, y);
+            for (int e = 0; e < L::VB / 2; ++e) {
 #pragma unroll
-                for (int k8 = 0; k8 < 8; ++k8) {
-                    const uint32_t w = __float_as_uint(y[k8]) & 0x7FFFFFFFu;
-                    if (w >= 0x7F800000u) y[k8] = 0.f, bad |= 1u << row;
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t w = half ? v[k4][e] & 0x7FFF0000u : v[k4][e] << 16 & 0x7FFF0000u;  // magnitude as fp32
+                    if (w >= 0x7F800000u) v[k4][e] &= half ? 0x0000FFFFu : 0xFFFF0000u, bad |= 1u << row;
                     else big = max(big, w);
-                    v[i][e + k8] = y[k8];
                 }
             }
         }
         const int ev = exponent(big);
         const float fv = dt_pow2(-ev);
         bad = __reduce_or_sync(0xffffffffu, bad);
-        // what rows g and g + 8 see
-        bool poison[2];
+        // what the lane's rows see
+        bool poison[NR][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = g + 8 * i;
-            const uint32_t sees = r < u.rows ? at_mask_word(a, u.b, r / a.G, 0, n) : 0u;
-            poison[i] = (sees & bad) != 0u;
+        for (int i = 0; i < NR; ++i) {
 #pragma unroll
-            for (int k8 = 0; k8 < 2; ++k8) {
+            for (int e = 0; e < 2; ++e) {
+                const int r = 2 * t + e + 8 * i;
+                const uint32_t sees = r < u.rows ? at_mask_word(a, u.b, r / a.G, 0, n) : 0u;
+                poison[i][e] = (sees & bad) != 0u;
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (!((sees >> (8 * k8 + 2 * t + e)) & 1)) c[k8][2 * i + e] = -__int_as_float(0x7F800000);
+                for (int k8 = 0; k8 < 2; ++k8)
+                    if (!((sees >> (g + 8 * k8)) & 1)) c[i][2 * k8 + e] = -__int_as_float(0x7F800000);
             }
         }
-        uint32_t p[4];
+        uint32_t p[NR][2];
+        clear();
         weigh(c, dt_pow2(ek), (float)ev, dt_pow2(-ev), p);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (poison[i]) l[i] = __int_as_float(0x7FC00000);
+        for (int i = 0; i < NR; ++i) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            mma(o[j], p, f16x2(__fmul_rn(v[0][j], fv), __fmul_rn(v[1][j], fv)),
-                f16x2(__fmul_rn(v[2][j], fv), __fmul_rn(v[3][j], fv)));
+            for (int e = 0; e < 2; ++e)
+                if (poison[i][e]) l[i][e] = __int_as_float(0x7FC00000);
+        }
+        auto pair = [&](int x, int y, int j) {  // column j of rows v[x], v[y], scaled
+            const float lo = __uint_as_float(j & 1 ? v[x][j / 2] & 0xFFFF0000u : v[x][j / 2] << 16);
+            const float hi = __uint_as_float(j & 1 ? v[y][j / 2] & 0xFFFF0000u : v[y][j / 2] << 16);
+            return f16x2(__fmul_rn(lo, fv), __fmul_rn(hi, fv));
+        };
+#pragma unroll
+        for (int j = 0; j < NV; j += 2) {
+            const uint32_t f[4] = {pair(0, 1, j), pair(0, 1, j + 1), pair(2, 3, j), pair(2, 3, j + 1)};
+#pragma unroll
+            for (int i = 0; i < NR; ++i) mma(o[j / 2][i], f, p[i][0], p[i][1]);
+        }
     }
 };
 
-template <int D>
+template <int D, int NR>
 __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtAttend a, float* part, int* counters) {
     using L = Lay<D>;
-    using S = Stream<D>;
+    using S = Stream<D, NR>;
     constexpr int NV = S::NV;
     extern __shared__ __align__(128) unsigned char fifo[];
     __shared__ Shared sh;
-    __shared__ __align__(16) uint32_t qfrag[S::KS * 128];
+    __shared__ __align__(16) uint32_t qfrag[S::KS * NR * 64];
     const float NEG_INF = -__int_as_float(0x7F800000);
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int cta = blockIdx.x, ctas = gridDim.x;
@@ -427,10 +480,9 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
         for (int i = 0; i < L::STAGES - 1; ++i) issue();
         x.queries(a, u, lane);
         __syncwarp();
-#pragma unroll
-        for (int j = 0; j < NV; ++j) x.o[j][0] = x.o[j][1] = x.o[j][2] = x.o[j][3] = 0.f;
-        x.m[0] = x.m[1] = NEG_INF;
-        x.l[0] = x.l[1] = 0.f;
+        // new rows while the first copies are on their way
+        if (w == 0 && u.t1 > u.r.ctx) x.fresh(a, u, lane);
+        else x.clear();
         int slot = 0;  // of tile i
         for (int i = 0; i < n; ++i) {
             issue();
@@ -448,37 +500,39 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
             slot = slot + 1 == L::STAGES ? 0 : slot + 1;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        if (w == 0 && u.t1 > u.r.ctx) x.fresh(a, u, lane);
 
         // join the warps
 #pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-            x.l[0] = __fadd_rn(x.l[0], __shfl_xor_sync(0xffffffffu, x.l[0], d));
-            x.l[1] = __fadd_rn(x.l[1], __shfl_xor_sync(0xffffffffu, x.l[1], d));
-        }
-        if (t == 0) {
-            sh.m[w][g] = x.m[0], sh.m[w][g + 8] = x.m[1];
-            sh.l[w][g] = x.l[0], sh.l[w][g + 8] = x.l[1];
+        for (int i = 0; i < NR; ++i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1)
+                    x.l[i][e] = __fadd_rn(x.l[i][e], __shfl_xor_sync(0xffffffffu, x.l[i][e], d));
+                if (g == 0) {
+                    sh.m[w][2 * t + e + 8 * i] = x.m[i][e];
+                    sh.l[w][2 * t + e + 8 * i] = x.l[i][e];
+                }
+            }
         }
         __syncthreads();  // all copies have been read
-        // O as [warp][row][D]; a lane's columns NV * (2t + e) + j, j = 0 .. NV - 1
+        // O as [warp][row][D]
         float* all = (float*)fifo;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = g + 8 * i;
-            if (r < u.rows) {
+        for (int i = 0; i < NR; ++i) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float* dst = all + ((size_t)w * ROWS + r) * D + NV * (2 * t + e);
+            for (int e = 0; e < 2; ++e) {
+                const int r = 2 * t + e + 8 * i;
+                if (r < u.rows) {
+                    float* dst = all + ((size_t)w * ROWS + r) * D + NV * g;
 #pragma unroll
-                    for (int j = 0; j < NV; j += 4)
-                        *(float4*)(dst + j) = make_float4(x.o[j][2 * i + e], x.o[j + 1][2 * i + e], x.o[j + 2][2 * i + e],
-                                                          x.o[j + 3][2 * i + e]);
+                    for (int j = 0; j < NV / 2; j += 2)
+                        *(float4*)(dst + 2 * j) = make_float4(x.o[j][i][e], x.o[j][i][2 + e], x.o[j + 1][i][e], x.o[j + 1][i][2 + e]);
                 }
             }
         }
         const bool whole = u.t0 == 0 && u.t1 == u.nt;
-        if (tid < ROWS) {
+        if (tid < 8 * NR) {
             float M = NEG_INF, sum = 0.f;
 #pragma unroll
             for (int i = 0; i < NW; ++i) M = fmaxf(M, sh.m[i][tid]);
@@ -554,19 +608,20 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
     }
 }
 
-template <int D>
+template <int D, int NR>
 cudaError_t launch(const DtAttend& a, void* workspace, int ctas, cudaStream_t st) {
     constexpr size_t smem = Lay<D>::SMEM;
     static_assert(2 * (smem + sizeof(Shared) + 4096 + 1024) <= 228 * 1024, "two CTAs per SM");
-    cudaError_t e = cudaFuncSetAttribute(kn11_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kn11_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     DtLaunch lc(dim3(ctas), dim3(NT), smem, st);
-    return cudaLaunchKernelEx(&lc.cfg, kn11_kernel<D>, a, (float*)((char*)workspace + AT_MAX_CTAS * sizeof(int)),
+    return cudaLaunchKernelEx(&lc.cfg, kn11_kernel<D, NR>, a, (float*)((char*)workspace + AT_MAX_CTAS * sizeof(int)),
                               (int*)workspace);
 }
 
 }  // namespace
 
 cudaError_t dt_kn11_launch(const DtAttend& a, void* workspace, int ctas, cudaStream_t st) {
-    return a.c.D == 64 ? launch<64>(a, workspace, ctas, st) : launch<128>(a, workspace, ctas, st);
+    if (a.M * a.G <= 8) return a.c.D == 64 ? launch<64, 1>(a, workspace, ctas, st) : launch<128, 1>(a, workspace, ctas, st);
+    return a.c.D == 64 ? launch<64, 2>(a, workspace, ctas, st) : launch<128, 2>(a, workspace, ctas, st);
 }
