@@ -538,14 +538,13 @@ struct Soft {
 #pragma unroll
             for (int k = 0; k < U; ++k) {
                 const int r = r0 + k * RPI;
-                uint32_t big = 0;
                 float x[8], y[8];
                 raw[k].rotated(pr, a.rope, x, y);
+                // the row's largest magnitude (rows past the block's repeat its last one)
+                float top = fmaxf(fabsf(x[0]), fabsf(y[0]));
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (r >= u.rows) x[e] = y[e] = 0.f;
-                    big = max(big, max(__float_as_uint(x[e]) & 0x7FFFFFFFu, __float_as_uint(y[e]) & 0x7FFFFFFFu));
-                }
+                for (int e = 1; e < 8; ++e) top = max3(top, fabsf(x[e]), fabsf(y[e]));
+                uint32_t big = __float_as_uint(top);
 #pragma unroll
                 for (int o = PPR / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
                 int ex = (int)(big >> 23) - 127;  // largest magnitude in [2^ex, 2^(ex+1))
@@ -765,6 +764,11 @@ struct Soft {
                 const float inv = l == 0.f ? 0.f : 1.0f / l;
                 const float w0 = whole ? __fmul_rn(f0, inv) : f0, w1 = whole ? __fmul_rn(f1, inv) : f1;
                 uint16_t* out = out_row(a, u, row);
+                // a full block's rows go out by way of the query tiles, whole lines at a
+                // time: a warp's 32 rows in the place of its own slot's queries
+                const bool staged = whole && dual;
+                const uint32_t stage = dt_smem_addr(sm + L::Q) + (tid >> 5) * (32 * D * 2);
+                const int lane = tid & 31;
                 if (!whole) {
                     my[row] = m;
                     my[ROWS + row] = l;
@@ -787,22 +791,43 @@ struct Soft {
                         for (int e = 0; e < 4; ++e)
                             v[4 * i + e] = __float_as_uint(__fmaf_rn(__uint_as_float(v[4 * i + e]), w0, __fmul_rn(z[e], w1)));
                     }
-                    if (row < u.rows) {
-                        if (whole) {
-                            uint32_t o[8];
+                    if (whole) {
+                        uint32_t o[8];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) o[e] = bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+                        for (int e = 0; e < 8; ++e) o[e] = bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+                        if (staged) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t q[4] = {o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
+                                sts16(stage + lane * (D * 2) + (((2 * c + i) ^ (lane & 7)) << 4), q);
+                            }
+                        } else if (row < u.rows) {
                             *(uint4*)(out + 16 * c) = make_uint4(o[0], o[1], o[2], o[3]);
                             *(uint4*)(out + 16 * c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                *(uint4*)(my + 2 * ROWS + ((4 * c + i) * ROWS + row) * 4) =
-                                    make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                         }
+                    } else if (row < u.rows) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *(uint4*)(my + 2 * ROWS + ((4 * c + i) * ROWS + row) * 4) =
+                                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                     }
                 }
                 dt_tc_fence_before();
+                if (staged) {
+                    __syncwarp();
+                    constexpr int CPR = D / 8, RPI = 32 / CPR;  // 16-byte chunks of a row, rows at a time
+                    const int ch = lane % CPR;
+#pragma unroll 4
+                    for (int r0 = 0; r0 < 32; r0 += RPI) {
+                        const int r = r0 + lane / CPR;
+                        uint16_t* dst = (uint16_t*)__shfl_sync(0xffffffffu, (unsigned long long)out, r);
+                        uint4 q;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                                     : "r"(stage + r * (D * 2) + ((ch ^ (r & 7)) << 4)) : "memory");
+                        if ((row & ~31) + r < u.rows) *(uint4*)(dst + ch * 8) = q;
+                    }
+                }
             }
             if (!whole) {
                 // the CTA that finishes a unit's last part joins all of them, in their order
