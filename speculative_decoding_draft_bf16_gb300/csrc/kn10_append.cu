@@ -38,7 +38,7 @@ DT_DI uint2 codes8(const float (&x)[8], float inv) {
 }
 
 template <typename T, int CP>  // CP: pairs of 8-element chunks a thread may own
-__global__ void __launch_bounds__(NT) kn10_kernel(const __grid_constant__ dt_kv_cache c, const __grid_constant__ dt_rope kv_rope,
+__global__ void __launch_bounds__(NT, CP > 2 ? 2 : 4) kn10_kernel(const __grid_constant__ dt_kv_cache c, const __grid_constant__ dt_rope kv_rope,
                                                   int M, const __grid_constant__ dt_rows kr, const __grid_constant__ dt_rows vr,
                                                   const int32_t* rows, int N, const int32_t* count, int count_add,
                                                   int32_t* len_out, int32_t* status) {

@@ -23,8 +23,8 @@
 namespace {
 
 constexpr int ROWS = 16, NW = 8, NT = NW * 32;
-constexpr int ATOM = 10;             // tiles of the longest unit that is not split
-constexpr uint32_t MIN_SHARE = 8;    // least cost worth a CTA: the start and six tiles
+constexpr int ATOM = 4;              // tiles of the longest unit that is not split
+constexpr uint32_t MIN_SHARE = 4;    // least cost worth a CTA: the start and two tiles
 static_assert(MIN_SHARE >= AtPlan<ROWS>::HEAD + (AtPlan<ROWS>::SNAP + 1) * AtPlan<ROWS>::FULL,
               "every CTA between a unit's ends has a tile of it");
 constexpr float LOG2E = 1.44269504088896340736f;
