@@ -69,6 +69,7 @@ struct AtPlan {
 struct AtShare {
     uint32_t beg, end, b0_at, each, rest;
     int ctas, b0;
+    AtReq r0;  // of request b0
     DT_DI uint32_t start_of(uint32_t c) const { return c * each + min(c, rest); }
     DT_DI int owner(uint32_t x) const {  // of cost position x
         const uint32_t wide = rest * (each + 1);
@@ -82,12 +83,14 @@ DT_DI void at_share(const DtAttend& a, uint32_t c, uint32_t grid, uint32_t min_s
     using P = AtPlan<ROWS>;
     const int lane = threadIdx.x & 31;
     uint32_t total = 0;
+    AtReq r;
 #pragma unroll 1
     for (int b = lane; b < a.batch; b += 32) {
-        const AtReq r = P::req(a, b);
+        r = P::req(a, b);
         if (r.bad && c == 0) atomicOr(&a.status[b], DT_DEV_BAD_CACHE);
         total += P::cost(a, r);
     }
+    const uint32_t own = total;  // with up to 32 requests, of the lane's only one
     total = __reduce_add_sync(0xffffffffu, total);
     AtShare s;
     s.ctas = (int)max(1u, min(total / min_share, grid));
@@ -102,13 +105,25 @@ DT_DI void at_share(const DtAttend& a, uint32_t c, uint32_t grid, uint32_t min_s
 #pragma unroll 1
     for (int base = 0; base < a.batch && s.beg < s.end; base += 32) {
         const int b = base + lane;
-        const uint32_t mine = b < a.batch ? P::cost(a, P::req(a, b)) : 0;
+        uint32_t mine = own;
+        if (a.batch > 32) {
+            mine = 0;
+            if (b < a.batch) {
+                r = P::req(a, b);
+                mine = P::cost(a, r);
+            }
+        }
         const uint32_t inc = (uint32_t)dt_warp_incl_scan((int)mine);
         const unsigned m = __ballot_sync(0xffffffffu, at + inc > s.beg);
         if (m) {
             const int l = __ffs(m) - 1;
             s.b0 = base + l;
             s.b0_at = at + __shfl_sync(0xffffffffu, inc - mine, l);
+            s.r0.len = __shfl_sync(0xffffffffu, r.len, l);
+            s.r0.n = __shfl_sync(0xffffffffu, r.n, l);
+            s.r0.ctx = __shfl_sync(0xffffffffu, r.ctx, l);
+            s.r0.nqb = __shfl_sync(0xffffffffu, r.nqb, l);
+            s.r0.bad = false;
             break;
         }
         at += __shfl_sync(0xffffffffu, inc, 31);
@@ -137,7 +152,7 @@ struct AtWalk {
         qb = h = 0;
         at = s.b0_at;
         if (b >= a.batch) return;
-        r = P::req(a, b);
+        r = s.r0;
         unit(a);
         // whole blocks before the share (Hkv units of one cost each)
 #pragma unroll 1

@@ -292,11 +292,15 @@ struct Stream {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int row = g + 8 * i;
-            const int at = a.rope.rot && row < n ? at_position(a, u.b, u.r.len, row) : 0;
 #pragma unroll
             for (int j = 0; j < L::KC; ++j) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) k[i][j][e] = 0.f;
+            }
+            if (8 * i >= n) continue;  // short: code that runs once waits for its instructions
+            const int at = a.rope.rot && row < n ? at_position(a, u.b, u.r.len, row) : 0;
+#pragma unroll
+            for (int j = 0; j < L::KC; ++j) {
                 if (row < n) pick16(kp + row * a.k.stride_n, t + 4 * j, a.rope, at, k[i][j]);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
@@ -327,7 +331,7 @@ struct Stream {
 #pragma unroll
             for (int e = 0; e < L::VB / 2; e += 4) {
                 uint4 y = make_uint4(0u, 0u, 0u, 0u);
-                if (row < n) y = *(const uint4*)(vp + row * a.v.stride_n + L::VB * g + 2 * e);
+                if (row < n && (k < 2 || n > 8)) y = *(const uint4*)(vp + row * a.v.stride_n + L::VB * g + 2 * e);
                 v[k][e] = y.x, v[k][e + 1] = y.y, v[k][e + 2] = y.z, v[k][e + 3] = y.w;
             }
         }
@@ -335,6 +339,7 @@ struct Stream {
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
             const int row = 2 * t + (k4 & 1) + 8 * (k4 >> 1);
+            if (8 * (k4 >> 1) >= n) continue;
 #pragma unroll
             for (int e = 0; e < L::VB / 2; ++e) {
 #pragma unroll

@@ -173,6 +173,8 @@ def _dtype_code(t):
 def _need(t, dtype=None, name="tensor", numel=None):
     """A contiguous CUDA tensor (of dtype), holding at least numel elements: the
     C ABI takes bare pointers, so sizes are checked here, before any launch."""
+    if t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype == dtype) and (numel is None or t.numel() >= numel):
+        return t
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if not t.is_contiguous():
@@ -630,10 +632,6 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _need_status(status, batch):
-    return _need(status, torch.int32, "status", numel=batch)
-
-
 def kv_append(cache, k, v, rope=None, rows=None, count=None, count_add=0, len_out=None, status=None, stream=None):
     """Append rows of k, v [batch, M, Hkv, D] to the cache (dt_kv_append): keys rotated to their
     position on the way, both stored in e4m3.  rows [batch, N] int32 picks rows (the walk's acc_nodes),
@@ -654,7 +652,7 @@ def kv_append(cache, k, v, rope=None, rows=None, count=None, count_add=0, len_ou
         _need(count, torch.int32, "count", numel=batch)
     if len_out is not None:
         _need(len_out, torch.int32, "len_out", numel=batch)
-    status = torch.zeros((batch,), dtype=torch.int32, device=k.device) if status is None else _need_status(status, batch)
+    status = torch.zeros((batch,), dtype=torch.int32, device=k.device) if status is None else _need(status, torch.int32, "status", numel=batch)
     _check(lib().dt_kv_append(cache._ref, rope._ref if rope is not None else None, batch, M, _dtype_code(k),
                               ctypes.byref(kr), ctypes.byref(vr), _addr(rows), N, _addr(count), int(count_add),
                               _addr(len_out), _addr(status), _stream(stream)), "dt_kv_append")
@@ -693,7 +691,7 @@ def tree_attention(cache, q, k, v, mask=None, pos=None, n_nodes=None, rope=None,
     if status is None:
         status = torch.zeros((batch,), dtype=torch.int32, device=q.device)
     else:
-        _need_status(status, batch)
+        _need(status, torch.int32, "status", numel=batch)
     if workspace is None:
         workspace = attention_workspace(cache, M, Hq)
     ws, n = _need_workspace(workspace)
