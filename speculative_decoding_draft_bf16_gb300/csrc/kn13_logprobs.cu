@@ -3,10 +3,10 @@
 //
 // One pass over a row, by a cluster of S CTAs (S > 1 when there are few rows).
 // A thread keeps, for the elements x that it has read, sums relative to a
-// reference m of its own: s = sum e^(x-m) and u = sum (x-m) e^(x-m).  m is
-// its first vector's maximum and moves only when an element lies more than 20
-// above it.  Then lse = m + ln s and the entropy is ln s - u / s, without
-// cancellation between large numbers.
+// reference m of its own, with y = x log2(e) - m: s = sum 2^y and u = sum y 2^y.
+// m is its first vectors' maximum (times log2(e), rounded) and moves only when an
+// element lies more than 20 above it.  Then lse = m ln(2) + ln s and the entropy is
+// ln s - ln(2) u / s, without cancellation between large numbers.
 //
 // What concerns few elements is looked at once per 16-byte vector, by its
 // maximum: elements at least as large as the token (its rank), and elements at
@@ -15,7 +15,11 @@
 // when the list is cut back to its best; a round that overflows the list is read
 // again with a higher bound.
 //
-// Bound by the row's bytes: HBM for many rows, latency for few.
+// Many rows are bound by instruction issue and HBM together: 7.5 instructions per bf16
+// element, one of them the exponential.  4000 rows of 151936 bf16 logits with the
+// best alternative: 234 us, 5.2 TB/s (77% of a copy's rate); ten CTAs of 128 threads
+// on an SM (eight: 242 us; twelve spill: 276).  Few rows are bound by the latency of
+// their phases: one path of 17 rows 12 us, 16 paths of 17 fp32 rows 18 us.
 #include <type_traits>
 
 #include "dt_device.cuh"
@@ -23,14 +27,14 @@
 
 namespace {
 
-constexpr int U = 4;                // vectors in flight per thread
-constexpr int ROUND = 4;            // batches between two looks at the list
+constexpr int U = 6;                // vectors in flight per thread
+constexpr int ROUND = 6;            // batches between two looks at the list
 constexpr int CAP = 1024;           // list entries
-#ifndef DT_KN13_MANY
-#define DT_KN13_MANY 608
-#endif
 constexpr float FAR = 20.f;         // how far above its reference a thread lets an element lie
-constexpr float LOG2E = 1.44269504088896340736f;
+constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.693147180559945309417f;
+// What stands for -infinity, whose exponential has to be zero and its product with it
+// too, and the reference of a thread that has read nothing else.
+constexpr float LOWEST = -1.7014118346046923e38f, NO_REF = -1.0e38f;  // -2^127
 
 typedef unsigned long long u64;
 
@@ -44,11 +48,10 @@ DT_DI float key_value(u64 k) {
     return DtElem<T>::key_val((uint32_t)(k >> 32));
 }
 
-// The vector with -infinity replaced by a number so low that its exponential is
-// zero (0 times -infinity would be NaN); NaN stays.
+// The vector with LOWEST for -infinity; NaN stays.
 DT_DI uint32_t floor2(uint32_t w) {
     uint32_t r;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0xFF7FFF7Fu));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0xFF00FF00u));
     return r;
 }
 DT_DI void finite_vals(const uint4& q, float (&x)[8]) {
@@ -58,7 +61,7 @@ DT_DI void finite_vals(const uint4& q, float (&x)[8]) {
 DT_DI void finite_vals(const uint4& q, float (&x)[4]) {
     dt_vec_vals<float>(q, x);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(x[i]) : "f"(-3.0e38f));
+    for (int i = 0; i < 4; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(x[i]) : "f"(LOWEST));
 }
 
 struct Part {  // of a CTA, in rank 0's shared memory
@@ -83,29 +86,33 @@ template <typename T, bool TOP>
 struct Row {
     using E = DtElem<T>;
     static constexpr int EV = 16 / sizeof(T);  // elements of a vector
-    float m;         // reference
+    float m, lim;    // reference; what an element must exceed to move it
     u64 s2, u2;      // s and u, two fp32 parts each
     int before;
-    bool any;        // a value above -infinity
     float token;     // the token's logit
     typename std::conditional<sizeof(T) == 2, uint32_t, float>::type
         least_pre, least_post;  // what an element must reach to come before it, ahead of the token and
                                 // after it (bf16: in both halves)
-    __nv_bfloat162 count2;      // bf16: counts of even and odd elements since the last flush (whole to 256)
+    uint32_t masks;  // bf16: sum of masks (0xFFFF in each half that comes before), since the last flush
 
-    DT_DI void move(float to) {  // the reference
-        const float d = __fsub_rn(m, to), f = dt_ex2_approx(__fmul_rn(d, LOG2E));
+    DT_DI bool any() const { return lim > -__int_as_float(0x7F800000); }  // a value above -infinity
+    DT_DI void refer(float to) {  // the reference to `to`
+        const float d = __fsub_rn(m, to), f = dt_ex2_approx(d);
         u2 = dt_f2_mul(dt_f2_fma(s2, dt_f2_pack(d, d), u2), dt_f2_pack(f, f));
         s2 = dt_f2_mul(s2, dt_f2_pack(f, f));
         m = to;
     }
+    DT_DI void move(float x) {  // and to the element x
+        refer(__fmul_rn(x, LOG2E));
+        lim = __fadd_rn(x, FAR);
+    }
     DT_DI void add(float x0, float x1) {
-        const u64 d = dt_f2_add(dt_f2_pack(x0, x1), dt_f2_pack(-m, -m));
+        const u64 y = dt_f2_fma(dt_f2_pack(x0, x1), dt_f2_pack(LOG2E, LOG2E), dt_f2_pack(-m, -m));
         float y0, y1;
-        dt_f2_unpack(dt_f2_mul(d, dt_f2_pack(LOG2E, LOG2E)), y0, y1);
+        dt_f2_unpack(y, y0, y1);
         const u64 e = dt_f2_pack(dt_ex2_approx(y0), dt_ex2_approx(y1));
         s2 = dt_f2_add(s2, e);
-        u2 = dt_f2_fma(d, e, u2);
+        u2 = dt_f2_fma(y, e, u2);
     }
     // A vector's sums, and how many of its elements come before the token: those
     // not smaller when they precede it, the larger ones when they follow.
@@ -124,8 +131,8 @@ struct Row {
         } else if constexpr (sizeof(T) == 2) {
             const uint32_t t2 = id < tok ? least_pre : least_post;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)  // 1 or 0 each
-                count2 = __hadd2(count2, __hge2(*(const __nv_bfloat162*)&w[i], *(const __nv_bfloat162*)&t2));
+            for (int i = 0; i < 4; ++i)
+                masks += __hge2_mask(*(const __nv_bfloat162*)&w[i], *(const __nv_bfloat162*)&t2);
         } else {
             const float t = id < tok ? least_pre : least_post;
 #pragma unroll
@@ -134,8 +141,10 @@ struct Row {
     }
     DT_DI void flush() {
         if (sizeof(T) == 2) {
-            before += (int)(__low2float(count2) + __high2float(count2));
-            count2 = __nv_bfloat162(0.f, 0.f);
+            // with a low and b high halves set, masks = 2^16 (a - b) - a (mod 2^32); a, b < 2^16
+            const uint32_t a = -masks & 0xFFFFu, b = (a - ((masks + a) >> 16)) & 0xFFFFu;
+            before += (int)(a + b);
+            masks = 0u;
         }
     }
 };
@@ -201,14 +210,13 @@ DT_DI void cut_list(Shared<NT>* sh, int n, int k) {
 }
 
 template <typename T, bool TOP, int NT>
-__global__ void __launch_bounds__(NT, 1024 / NT) kn13_kernel(const __grid_constant__ DtLogprobs a, int S) {
+__global__ void __launch_bounds__(NT, NT == 128 ? 10 : 2) kn13_kernel(const __grid_constant__ DtLogprobs a, int S) {
     using E = DtElem<T>;
     using R = Row<T, TOP>;
     constexpr int EV = R::EV;
     __shared__ Shared<NT> sh;
     const float NEG_INF = -__int_as_float(0x7F800000), NaN = __int_as_float(0x7FC00000);
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    dt_pdl_trigger();
     dt_pdl_wait();
     const uint32_t c = blockIdx.x % (uint32_t)S;  // rank in the row's cluster
     const uint32_t e = blockIdx.x / (uint32_t)S;
@@ -237,7 +245,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) kn13_kernel(const __grid_consta
     R r;
     r.s2 = r.u2 = dt_f2_pack(0.f, 0.f);
     r.before = 0;
-    r.count2 = __nv_bfloat162(0.f, 0.f);
+    r.masks = 0u;
     uint4 q[U];
     const uint4 none = sizeof(T) == 2 ? make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u)
                                       : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
@@ -263,14 +271,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) kn13_kernel(const __grid_consta
     float first = NEG_INF;
 #pragma unroll
     for (int i = 0; i < U; ++i) first = fmaxf(first, dt_vec_max<T>(q[i]));
-    r.any = first > NEG_INF;
-    r.m = r.any ? first : 0.f;
+    r.m = NO_REF;
+    r.lim = NEG_INF;  // the first value that there is moves it
+    if (first > NEG_INF) r.move(first);
     float bound_val = __int_as_float(0x7F800000);
     if (TOP) {
         if (tid == 0) sh.count = 0;
         // the bound: the top-th best of the threads' maxima, with the last id (NaN: no
         // number, a lower bound all the same)
-        const u64 mine = (r.any ? (u64)dt_fkey(first) : 0ull) << 32 | (uint32_t)tid;
+        const u64 mine = (r.any() ? (u64)dt_fkey(first) : 0ull) << 32 | (uint32_t)tid;
         __syncthreads();
         const u64 best = dt_block_top32<NT>(NT, [&](int) { return mine; }, sh.scratch);  // asked for tid only
         if (tid == a.top - 1) {
@@ -293,8 +302,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) kn13_kernel(const __grid_consta
                     const int v = base + i * NT + tid;
                     const int id = v < v1 ? lead + v * EV : 0x7FFFFFFF;
                     const float vm = dt_vec_max<T>(q[i]);
-                    r.any |= vm > NEG_INF;
-                    const bool far = vm > r.m + FAR, hit = TOP && vm >= bound_val && v < v1;
+                    const bool far = vm > r.lim, hit = TOP && vm >= bound_val && v < v1;
                     if (__any_sync(0xffffffffu, far || hit)) {
                         if (far) r.move(vm);
                         __syncwarp();
@@ -305,8 +313,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) kn13_kernel(const __grid_consta
 #pragma unroll
                 for (int i = h; i < h + U / 2; ++i) fetch(base + U * NT, i);
             }
-            r.flush();
         }
+        r.flush();
         if (TOP) {
             const int kept = round == v0 ? 0 : sh.kept;
             __syncthreads();
@@ -341,6 +349,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) kn13_kernel(const __grid_consta
         if (tid == 0) sh.kept = 0;
         __syncthreads();
     }
+    // Not before: the next grid's CTAs would take their places among this one's, on
+    // some SMs more than on others.
+    dt_pdl_trigger();
     // the elements outside the vectors (fewer than 2 * EV, rank 0)
     if (c == 0) {
         const int n = lead + a.V - tail;
@@ -349,13 +360,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) kn13_kernel(const __grid_consta
             const T raw = x[id];
             float y = E::val(raw);
             r.before += named && (id < tok ? y >= r.token : y > r.token);
-            if (y > NEG_INF) {
-                if (!r.any) r.m = y;
-                r.any = true;
-            }
-            if (y > r.m + FAR) r.move(y);
-            if (y == NEG_INF) y = -3.0e38f;
-            const float d = y - r.m, ex = dt_ex2_approx(__fmul_rn(d, LOG2E));
+            if (y > r.lim) r.move(y);
+            if (y < LOWEST) y = LOWEST;
+            const float d = __fmaf_rn(y, LOG2E, -r.m), ex = dt_ex2_approx(d);
             r.s2 = dt_f2_add(r.s2, dt_f2_pack(ex, 0.f));
             r.u2 = dt_f2_add(r.u2, dt_f2_pack(__fmul_rn(d, ex), 0.f));
             if (TOP) sh.list[sh.kept + tid] = order_key<T>(raw, id);  // kept <= CAP / 2
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) kn13_kernel(const __grid_consta
         cut_list(&sh, n, a.top);
     }
     // the CTA's sums, relative to the largest reference among those with a value
-    float M = r.any ? r.m : NEG_INF;
+    float M = r.any() ? r.m : NEG_INF;
     M = dt_warp_max(M);
     if (lane == 0) sh.rm[w] = M;
     __syncthreads();
@@ -381,7 +388,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) kn13_kernel(const __grid_consta
     // a thread without a value has sums of zeros, or NaN
     float sa, sb, ua, ub;
     dt_f2_unpack(r.s2, sa, sb);
-    r.move(r.any || sa != sa || sb != sb ? ref : r.m);
+    r.refer(r.any() || sa != sa || sb != sb ? ref : r.m);
     dt_f2_unpack(r.s2, sa, sb);
     dt_f2_unpack(r.u2, ua, ub);
     const float s = dt_warp_sum(__fadd_rn(sa, sb)), u = dt_warp_sum(__fadd_rn(ua, ub));
@@ -417,15 +424,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) kn13_kernel(const __grid_consta
     for (int i = 0; i < S; ++i) {
         const Part& p = sh.part[i];
         tb += p.before;
-        const float d = p.any && any ? p.m - m : 0.f, f = dt_ex2_approx(__fmul_rn(d, LOG2E));
+        const float d = p.any && any ? p.m - m : 0.f, f = dt_ex2_approx(d);
         tu = __fmaf_rn(__fmaf_rn(p.s, d, p.u), f, tu);
         ts = __fmaf_rn(p.s, f, ts);
     }
     const float ln = logf(ts);
-    const float lse = any ? m + ln : NaN;
+    const float lse = any ? __fmaf_rn(m, LN2, ln) : NaN;
     if (lane == 0) {
         if (a.logprob) a.logprob[e] = named ? r.token - lse : tok < 0 ? 0.f : NaN;
-        if (a.entropy) a.entropy[e] = any ? ln - tu / ts : NaN;
+        if (a.entropy) a.entropy[e] = any ? __fmaf_rn(-LN2, tu / ts, ln) : NaN;
         if (a.rank) a.rank[e] = named ? tb : -1;
     }
     if (TOP) {
@@ -449,15 +456,18 @@ cudaError_t launch(const DtLogprobs& a, int S, cudaStream_t st) {
 }  // namespace
 
 cudaError_t dt_kn13_launch(const DtLogprobs& a, cudaStream_t st) {
-    // A cluster per row while rows alone leave SMs idle (two CTAs fit an SM), with
-    // a batch of vectors at least for every thread.
+    // A cluster per row while rows alone leave SMs idle (two CTAs of 512 threads fit an
+    // SM), with two vectors at least for every thread (one row of 151936 bf16: 8 CTAs;
+    // 17 rows by one CTA each 17.5 us, by 8 each 12.5).
     const long long rows = (long long)a.batch * a.N;
     const long long bytes = (long long)a.V * (a.dtype == DT_BF16 ? 2 : 4);
     int S = 1;
     while (S < 8 && rows * S < 2 * 152 && bytes >= (long long)S * 2 * 512 * 16 * 2) S *= 2;
     // Many rows: few threads to a row, so that what a row costs once is spread over
-    // more of its vectors.
-    if (rows >= DT_KN13_MANY)
+    // more of its vectors.  Measured, bf16, 128 threads against 512: 304 rows of 32000
+    // 13.7 : 13.6 us, 456 rows 15.2 : 19.7; of 151936, 456 rows 48.9 : 44.0, 608 rows
+    // 54.7 : 55.2, 2432 rows 151 : 202; of 262144, 760 rows 98 : 95, 912 rows 110 : 111.
+    if (rows >= 256 + bytes / 800)
         return a.dtype == DT_BF16 ? launch<uint16_t, 128>(a, S, st) : launch<float, 128>(a, S, st);
     return a.dtype == DT_BF16 ? launch<uint16_t, 512>(a, S, st) : launch<float, 512>(a, S, st);
 }

@@ -188,3 +188,20 @@ def test_refusals():
     for top in (-1, 33):
         with pytest.raises(dtree.DtError):
             dtree.token_logprobs(x, tok, top=top)
+
+
+@pytest.mark.parametrize("level", [-200.0, -4096.0, 512.0])
+@pytest.mark.parametrize("ruled_out", [5000, 40000, 150000])
+@pytest.mark.parametrize("dtype,rows", [(torch.bfloat16, 1), (torch.float32, 2), (torch.bfloat16, 700)])
+def test_far_values_behind_ruled_out_ones(dtype, rows, ruled_out, level):
+    """The first tokens ruled out, the others' logits far from zero: a common offset changes nothing."""
+    V = 151936
+    x, g = logits((1, rows, V), dtype, 5, scale=2.0)
+    x = (x.float() + level).to(dtype)
+    x[..., :ruled_out] = -math.inf
+    tok = torch.randint(ruled_out, V, (1, rows), generator=g, device="cuda").to(torch.int32)
+    pick = torch.arange(min(rows, 5), device="cuda")  # the 64-bit check of a few rows
+    o = dtree.token_logprobs(x, tok, top=4)
+    few = dtree.Logprobs(*(getattr(o, f)[:, pick] for f in ("logprob", "entropy", "rank", "top_id", "top_logprob")))
+    check(x[:, pick], None, tok[:, pick], 4, few)
+    assert torch.isfinite(o.logprob).all()
