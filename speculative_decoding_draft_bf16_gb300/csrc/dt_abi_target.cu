@@ -15,7 +15,10 @@ dt_status cuda_status(cudaError_t e) {
     return DT_ERR_CUDA;
 }
 
-// Rows per key head up to which attention streams the cache through registers.
+// Rows per key head up to which attention streams the cache through registers: two
+// groups of 8, which an MMA's side takes.  At 16 rows, 64 requests over 1000 to 16000 take
+// 264 us there and 364 on 128-row tiles, 16 requests of 16 heads of 64 38 and 61; more
+// rows would double the streaming kernel's MMAs, which fill half of the pipe at 8.
 constexpr long long kStreamRows = 16;
 
 int sm_count() {

@@ -6,14 +6,6 @@
 
 #include "dt_device.cuh"
 
-// Eight consecutive elements as fp32 (16-byte aligned).
-DT_DI void dt_load8(const uint16_t* p, float (&x)[8]) { dt_vec_vals<uint16_t>(*(const uint4*)p, x); }
-DT_DI void dt_load8(const float* p, float (&x)[8]) {
-    const float4 a = ((const float4*)p)[0], b = ((const float4*)p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-
 // Eight elements as they are stored.
 template <typename T>
 struct DtRaw8;

@@ -147,12 +147,7 @@ DT_DI void dt_tmem_ld_wait(uint32_t (&r)[16]) {
                  :
                  : "memory");
 }
-// 8 and 16 32-bit columns of this thread's lane to tensor memory.
-DT_DI void dt_tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
+// 16 32-bit columns of this thread's lane to tensor memory.
 DT_DI void dt_tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "

@@ -13,16 +13,26 @@
 //   O' += V' P'  P's fragments are S's, transposed 8 x 8 at a time; a lane reads 16
 //                columns of four tokens and pairs the tokens' bytes before it
 //                converts them.
-// (These narrow products cannot fill a tcgen05 tile: 16 rows of 128, and the
-// cache's bytes, not the products, bound the time.)  Scales as on the tensor
-// cores: P holds 2^(t + log2 vs - m), the row sum adds p / vs, and m moves only
-// when the maximum has grown by more than 8.  The warps' sums are joined in
-// shared memory, the CTAs' in the workspace.
+// These narrow products do not fill a tcgen05 tile (16 rows of 128), and the cache's
+// bytes are to bound the time; the same calls on 128-row tiles take 364 us against 264 at
+// 16 rows (64 requests, contexts to 16000), 31.6 against 22.9 for one request over 4000.
+// With the rows on the side of 16, single tokens paid for 12 idle rows and the MMA pipe was
+// full (one MMA takes 32 clocks of an SM's quarter): 276 us instead of 233.
+//   Scales: P holds 2^(t + log2 vs - m) for scores t in base 2, the row sum adds p / vs,
+// and m moves only when the maximum has grown by more than 8.  The warps' sums are joined
+// in shared memory, the CTAs' in the workspace.
+//
+// 64 single tokens, 32 heads on 8, over contexts of 1001 to 16384 (1.14 GB): 228 us, 5.0
+// TB/s (74% of a copy's rate).  Equal shares end between 165 and 228 us, by where on the
+// chip an SM lies: that spread, not the loop, is what is left.  One token over 1000: 15.6
+// us, the latency of the share, pages, copies, new row and join in turn.
 #include "dt_attend.cuh"
 
 namespace {
 
 constexpr int ROWS = 16, NW = 8, NT = NW * 32;
+// One token over 1000 with 4 and 4: 16.7 us; 6 and 6: 19.5; 10 and 8: 17.3; 8 and 8: 22.6
+// (long contexts do not notice).
 constexpr int ATOM = 4;              // tiles of the longest unit that is not split
 constexpr uint32_t MIN_SHARE = 4;    // least cost worth a CTA: the start and two tiles
 static_assert(MIN_SHARE >= AtPlan<ROWS>::HEAD + (AtPlan<ROWS>::SNAP + 1) * AtPlan<ROWS>::FULL,
@@ -30,6 +40,8 @@ static_assert(MIN_SHARE >= AtPlan<ROWS>::HEAD + (AtPlan<ROWS>::SNAP + 1) * AtPla
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float HEADROOM = 5.f, LAZY = 8.f;
 
+// Three tiles in flight of 4 KB to a warp, two CTAs to an SM; three CTAs with two tiles
+// each are slower (246 : 233 us).
 template <int D>
 struct Lay {
     static constexpr int KC = D / 64;             // 16-byte pieces of a token's keys per lane

@@ -21,6 +21,23 @@
 // maximum of t + log2 vs less 5 (fp16 then resolves probabilities down to 2^-29 of
 // the largest), moved -- and O rescaled -- only when the maximum has grown by
 // more than 8 since.
+//
+// Roundings: codes are exact in fp16; q, new k and v are scaled by powers of two into
+// fp16's range and rounded to 11 bits (bf16 has 8, rotation gives them more); P to 11
+// bits, below the 8 of the output; all sums fp32.
+//
+// What bounds it.  A tile of 256 rows and 128 tokens takes 2560 clocks of MMAs at D = 128
+// (64 clocks for 128 x 128 x 16; 48, not 32, for the 128 x 64 x 16 of the halves, which
+// read Q from shared memory each time) and 3200 to 4200 in all: a half's softmax takes
+// 1300 to 1500 clocks for 64 elements of 32 rows, in which two softmax and two converter
+// warps share an SM quarter's issue slots, and the slots' chains (scores, softmax,
+// products) overlap but do not fill each other's gaps.  Sixteen trees of 257 nodes, 64
+// heads on 8, contexts of 5000 to 16384: 1.13 ms, 0.98 PFLOP/s (51% of the measured bf16
+// rate).  Scores of a whole tile at a time (fewer, wider MMAs, but a slot's softmax then
+// waits for all of them): 1.27 ms.  Short contexts are bound by what a unit costs beside
+// its tiles: queries (9 thousand clocks), outputs (5), joins (15), the first tiles.
+// Code size matters as much: with unrolled tiles the roles' loops overflowed the
+// instruction caches (one tree of 257 nodes 125 us instead of 99).
 #include "dt_attend.cuh"
 #include "dt_tcgen05.cuh"
 
@@ -42,7 +59,7 @@ static_assert(NS * REG_SOFT + 2 * NC * REG_CONV + 128 * REG_MMA == NT * LAUNCH_R
 constexpr int STAGES = 2;       // K and V tiles in shared memory, each
 constexpr int RING = 8;         // tiles whose page ids and scales are kept
 constexpr int SEGS = 4;         // segments the walk may be ahead
-constexpr int ATOM = 4;         // tiles of the longest unit that is not split
+constexpr int ATOM = 4;         // tiles of the longest unit that is not split (8: 64 trees of 61 nodes 206 : 183 us)
 constexpr uint32_t MIN_SHARE = 36;    // least cost worth a CTA: the start and three tiles of a full block
 static_assert(MIN_SHARE >= AtPlan<ROWS>::HEAD + (AtPlan<ROWS>::SNAP + 1) * AtPlan<ROWS>::FULL,
               "every CTA between a unit's ends has a tile of it");
