@@ -17,8 +17,8 @@ dt_status cuda_status(cudaError_t e) {
 
 // Rows per key head up to which attention streams the cache through registers: two
 // groups of 8, which an MMA's side takes.  At 16 rows, 64 requests over 1000 to 16000 take
-// 264 us there and 364 on 128-row tiles, 16 requests of 16 heads of 64 38 and 61; more
-// rows would double the streaming kernel's MMAs, which fill half of the pipe at 8.
+// 264 us there and 364 on 128-row tiles, 16 requests of 16 heads of 64 38 and 61; with
+// more rows the streaming kernel's sums would leave its registers.
 constexpr long long kStreamRows = 16;
 
 int sm_count() {

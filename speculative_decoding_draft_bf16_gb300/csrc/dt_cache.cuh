@@ -113,10 +113,11 @@ struct DtPair {
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float u = x[i], v = y[i];
-                x[i] = __fsub_rn(__fmul_rn(u, cv[i]), __fmul_rn(v, sv[i]));
-                y[i] = __fadd_rn(__fmul_rn(v, cv[i]), __fmul_rn(u, sv[i]));
+            for (int i = 0; i < 8; i += 2) {  // two at a time, each step rounded as above
+                const unsigned long long u = dt_f2_pack(x[i], x[i + 1]), v = dt_f2_pack(y[i], y[i + 1]);
+                const unsigned long long co = dt_f2_pack(cv[i], cv[i + 1]), si = dt_f2_pack(sv[i], sv[i + 1]);
+                dt_f2_unpack(dt_f2_sub(dt_f2_mul(u, co), dt_f2_mul(v, si)), x[i], x[i + 1]);
+                dt_f2_unpack(dt_f2_add(dt_f2_mul(v, co), dt_f2_mul(u, si)), y[i], y[i + 1]);
             }
         }
     }

@@ -16,8 +16,8 @@
 // These narrow products do not fill a tcgen05 tile (16 rows of 128), and the cache's
 // bytes are to bound the time; the same calls on 128-row tiles take 364 us against 264 at
 // 16 rows (64 requests, contexts to 16000), 31.6 against 22.9 for one request over 4000.
-// With the rows on the side of 16, single tokens paid for 12 idle rows and the MMA pipe was
-// full (one MMA takes 32 clocks of an SM's quarter): 276 us instead of 233.
+// With the rows on the side of 16, single tokens paid for 12 idle rows in MMAs and
+// exponentials, a third of all instructions: 276 us instead of 233.
 //   Scales: P holds 2^(t + log2 vs - m) for scores t in base 2, the row sum adds p / vs,
 // and m moves only when the maximum has grown by more than 8.  The warps' sums are joined
 // in shared memory, the CTAs' in the workspace.

@@ -32,10 +32,11 @@
 // 1300 to 1500 clocks for 64 elements of 32 rows, in which two softmax and two converter
 // warps share an SM quarter's issue slots, and the slots' chains (scores, softmax,
 // products) overlap but do not fill each other's gaps.  Sixteen trees of 257 nodes, 64
-// heads on 8, contexts of 5000 to 16384: 1.13 ms, 0.98 PFLOP/s (51% of the measured bf16
+// heads on 8, contexts of 5000 to 16384: 1.12 ms, 0.99 PFLOP/s (51% of the measured bf16
 // rate).  Scores of a whole tile at a time (fewer, wider MMAs, but a slot's softmax then
 // waits for all of them): 1.27 ms.  Short contexts are bound by what a unit costs beside
-// its tiles: queries (9 thousand clocks), outputs (5), joins (15), the first tiles.
+// its tiles, in thousands of clocks: queries (8), outputs (3 to 5), joins (8 to 20), and
+// tiles of new rows, which take 9 (cached ones 4).
 // Code size matters as much: with unrolled tiles the roles' loops overflowed the
 // instruction caches (one tree of 257 nodes 125 us instead of 99).
 #include "dt_attend.cuh"
@@ -248,7 +249,7 @@ struct Conv {
         const int pr = ct % PPT;  // this thread's chunk pair of rows ct / PPT + i * TPI
         int c0, c1;
         dt_pair_chunks(pr, rope, c0, c1);
-        constexpr int U = 1;  // rows in flight
+        constexpr int U = D == 64 ? 2 : 1;  // rows in flight (two at D = 128 make the loop over cached tiles spill)
         int e = 0;
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {  // the second one when the tile needs another scale
@@ -256,6 +257,15 @@ struct Conv {
             uint32_t big = 0u;
 #pragma unroll 1
             for (int i0 = 0; i0 < NI; i0 += U) {
+                if (i0 * TPI >= left) {  // no row of these: zeros, which a weight of zero leaves zero
+                    const uint32_t zero[4] = {};
+#pragma unroll
+                    for (int k = 0; k < U; ++k) {
+                        sts16(tile + chunk_at(ct / PPT + (i0 + k) * TPI, c0), zero);
+                        sts16(tile + chunk_at(ct / PPT + (i0 + k) * TPI, c1), zero);
+                    }
+                    continue;
+                }
                 DtPair<uint16_t> raw[U];
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
