@@ -64,6 +64,7 @@ constexpr int ATOM = 4;         // tiles of the longest unit that is not split (
 constexpr uint32_t MIN_SHARE = 36;    // least cost worth a CTA: the start and three tiles of a full block
 static_assert(MIN_SHARE >= AtPlan<ROWS>::HEAD + (AtPlan<ROWS>::SNAP + 1) * AtPlan<ROWS>::FULL,
               "every CTA between a unit's ends has a tile of it");
+constexpr int OWN_PARTS = 8;    // most parts of a unit that its last CTA joins to its own
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float HEADROOM = 5.f, LAZY = 8.f;
 
@@ -97,6 +98,7 @@ struct Shared {
     int qpos[ROWS], kpos[AT_TILE];
     long long qoff[ROWS];
     float mrg_m[TQ], mrg_l[TQ];
+    float wt[OWN_PARTS][ROWS];
     uint32_t amax[2][NC / 32];
     uint64_t segfull[SEGS], segfree[SEGS];
     Seg seg[SEGS];
@@ -753,6 +755,20 @@ struct Soft {
             }
             g0 += nt;
             const bool whole = u.t0 == 0 && u.t1 == u.nt;
+            if (!whole && dual && u.segs <= OWN_PARTS) {
+                if (tid == 0) {  // are all other parts there?
+                    int done;
+                    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(done) : "l"(counters + u.first) : "memory");
+                    sh->last = done == u.segs - 1;
+                    if (done == u.segs - 1) counters[u.first] = 0;
+                }
+                asm volatile("bar.sync 2, 256;" ::: "memory");
+                if (sh->last) {
+                    join_own(a, u, sh, part, cta - u.first, to, row, m, l, dt_smem_addr(sm + L::Q) + (tid >> 5) * (32 * D * 2),
+                             out_row(a, u, row));
+                    continue;
+                }
+            }
             float* my = part + (size_t)(2 * cta + (u.t0 == 0)) * ROWS * (D + 2);
             float f0 = 1.f, f1 = 0.f;  // weights of this slot's and the other slot's sums
             const uint32_t xb = dt_smem_addr(sm + L::Q) + (tid % TQ) * (D * 4);
@@ -823,11 +839,7 @@ struct Soft {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) o[e] = bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
                         if (staged) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint32_t q[4] = {o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
-                                sts16(stage + lane * (D * 2) + (((2 * c + i) ^ (lane & 7)) << 4), q);
-                            }
+                            stage_row(stage, lane, c, o);
                         } else if (row < u.rows) {
                             *(uint4*)(out + 16 * c) = make_uint4(o[0], o[1], o[2], o[3]);
                             *(uint4*)(out + 16 * c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
@@ -840,21 +852,7 @@ struct Soft {
                     }
                 }
                 dt_tc_fence_before();
-                if (staged) {
-                    __syncwarp();
-                    constexpr int CPR = D / 8, RPI = 32 / CPR;  // 16-byte chunks of a row, rows at a time
-                    const int ch = lane % CPR;
-#pragma unroll 4
-                    for (int r0 = 0; r0 < 32; r0 += RPI) {
-                        const int r = r0 + lane / CPR;
-                        uint16_t* dst = (uint16_t*)__shfl_sync(0xffffffffu, (unsigned long long)out, r);
-                        uint4 q;
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                                     : "r"(stage + r * (D * 2) + ((ch ^ (r & 7)) << 4)) : "memory");
-                        if ((row & ~31) + r < u.rows) *(uint4*)(dst + ch * 8) = q;
-                    }
-                }
+                if (staged) send_rows(stage, lane, out, row & ~31, u.rows);
             }
             if (!whole) {
                 // the CTA that finishes a unit's last part joins all of them, in their order
@@ -870,6 +868,91 @@ struct Soft {
                 if (sh->last) join(a, sm, u, part, tid);
             }
         }
+    }
+
+    // 16 columns from 16c of the thread's row, in bf16, to its place in the staged rows.
+    static DT_DI void stage_row(uint32_t stage, int lane, int c, const uint32_t (&o)[8]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t q[4] = {o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
+            sts16(stage + lane * (D * 2) + (((2 * c + i) ^ (lane & 7)) << 4), q);
+        }
+    }
+    // The warp's 32 staged rows (from block row `first`) to memory, whole lines at a time.
+    static DT_DI void send_rows(uint32_t stage, int lane, uint16_t* out, int first, int rows) {
+        __syncwarp();
+        constexpr int CPR = D / 8, RPI = 32 / CPR;  // 16-byte chunks of a row, rows at a time
+        const int ch = lane % CPR;
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += RPI) {
+            const int r = r0 + lane / CPR;
+            uint16_t* dst = (uint16_t*)__shfl_sync(0xffffffffu, (unsigned long long)out, r);
+            uint4 q;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                         : "r"(stage + r * (D * 2) + ((ch ^ (r & 7)) << 4)) : "memory");
+            if (first + r < rows) *(uint4*)(dst + ch * 8) = q;
+        }
+    }
+
+    // The last CTA of a full block's unit: the other parts come from memory, its own
+    // straight from tensor memory; same sums in the same order as join().
+    static DT_DI void join_own(const DtAttend& a, const Seg& u, Shared* sh, const float* part, int own, uint32_t to, int row,
+                               float m, float l0, uint32_t stage, uint16_t* out) {
+        const float NEG_INF = -__int_as_float(0x7F800000);
+        const int first = u.first, segs = u.segs, lane = row & 31;
+        auto slot = [&](int i) { return part + (size_t)(2 * (first + i) + (i == 0)) * ROWS * (D + 2); };
+        float M = NEG_INF, l = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < segs; ++i) {
+            const float mi = i == own ? m : __ldcg(slot(i) + row), li = i == own ? l0 : __ldcg(slot(i) + ROWS + row);
+            sh->wt[i][row] = mi;
+            const float up = fmaxf(M, mi);
+            if (up != NEG_INF) l = __fmaf_rn(li, dt_ex2_approx(mi - up), __fmul_rn(l, dt_ex2_approx(M - up)));
+            else l = __fadd_rn(l, li);  // 0, or NaN
+            M = up;
+        }
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        for (int i = 0; i < segs; ++i) {
+            const float mi = sh->wt[i][row];
+            sh->wt[i][row] = mi == NEG_INF ? 0.f : __fmul_rn(dt_ex2_approx(mi - M), inv);
+        }
+#pragma unroll 1
+        for (int c = 0; c < D / 16; c += 2) {  // 32 columns
+            uint32_t v[2][16];
+            dt_tmem_ld16_async(to + 16 * c, v[0]);
+            dt_tmem_ld_wait(v[0]);
+            dt_tmem_ld16_async(to + 16 * c + 16, v[1]);
+            dt_tmem_ld_wait(v[1]);
+            float x[32] = {};
+#pragma unroll 1
+            for (int i = 0; i < segs; ++i) {
+                const float f = sh->wt[i][row];
+                if (i == own) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = __fmaf_rn(__uint_as_float(v[e >> 4][e & 15]), f, x[e]);
+                } else {
+                    const float4* o = (const float4*)(slot(i) + 2 * ROWS) + 4 * c * ROWS + row;
+                    float4 y[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] = __ldcg(o + k * ROWS);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        x[4 * k] = __fmaf_rn(y[k].x, f, x[4 * k]), x[4 * k + 1] = __fmaf_rn(y[k].y, f, x[4 * k + 1]);
+                        x[4 * k + 2] = __fmaf_rn(y[k].z, f, x[4 * k + 2]), x[4 * k + 3] = __fmaf_rn(y[k].w, f, x[4 * k + 3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = bf16x2(x[16 * h + 2 * e], x[16 * h + 2 * e + 1]);
+                stage_row(stage, lane, c + h, o);
+            }
+        }
+        dt_tc_fence_before();
+        send_rows(stage, lane, out, row & ~31, u.rows);
     }
 
     static DT_DI uint16_t* out_row(const DtAttend& a, const Seg& u, int r) {
