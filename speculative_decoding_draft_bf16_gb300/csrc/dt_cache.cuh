@@ -113,11 +113,17 @@ struct DtPair {
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {  // two at a time, each step rounded as above
+            // products two at a time; the sums are not, or they would be contracted with them
+            for (int i = 0; i < 8; i += 2) {
                 const unsigned long long u = dt_f2_pack(x[i], x[i + 1]), v = dt_f2_pack(y[i], y[i + 1]);
                 const unsigned long long co = dt_f2_pack(cv[i], cv[i + 1]), si = dt_f2_pack(sv[i], sv[i + 1]);
-                dt_f2_unpack(dt_f2_sub(dt_f2_mul(u, co), dt_f2_mul(v, si)), x[i], x[i + 1]);
-                dt_f2_unpack(dt_f2_add(dt_f2_mul(v, co), dt_f2_mul(u, si)), y[i], y[i + 1]);
+                float a0, a1, b0, b1, c0, c1, d0, d1;
+                dt_f2_unpack(dt_f2_mul(u, co), a0, a1);
+                dt_f2_unpack(dt_f2_mul(v, si), b0, b1);
+                dt_f2_unpack(dt_f2_mul(v, co), c0, c1);
+                dt_f2_unpack(dt_f2_mul(u, si), d0, d1);
+                x[i] = __fsub_rn(a0, b0), x[i + 1] = __fsub_rn(a1, b1);
+                y[i] = __fadd_rn(c0, d0), y[i + 1] = __fadd_rn(c1, d1);
             }
         }
     }

@@ -8,10 +8,10 @@
 //
 // A path's few rows cost a launch and the latency of three dependent reads (lengths,
 // rows, tables' ids): 2.6 us for 4 paths, 5 us for 64.  Prompts are bound by how many
-// rows are in flight: 8 prompts of up to 4000 bf16 rows, 160 MB, 36 us, 4.4 TB/s (65% of
+// rows are in flight: 8 prompts of up to 4000 bf16 rows, 160 MB, 37 us, 4.3 TB/s (64% of
 // a copy's rate), instructions issued in three of four clocks.  Rows read before the
 // verdict on the request, in pairs of chunks that rotate together, took 66 us to 43, four
-// CTAs per SM (64 registers) to 39, steps of two elements to 36; five CTAs spill (50 us),
+// CTAs per SM (64 registers) to 39, steps of two elements to 37; five CTAs spill (50 us),
 // 512 threads to a block leave them idle at short pages (50 us).
 #include "dt_cache.cuh"
 #include "dt_launch.h"

@@ -32,10 +32,10 @@
 // 1300 to 1500 clocks for 64 elements of 32 rows, in which two softmax and two converter
 // warps share an SM quarter's issue slots, and the slots' chains (scores, softmax,
 // products) overlap but do not fill each other's gaps.  Sixteen trees of 257 nodes, 64
-// heads on 8, contexts of 5000 to 16384: 1.12 ms, 0.99 PFLOP/s (51% of the measured bf16
+// heads on 8, contexts of 5000 to 16384: 1.10 ms, 1.01 PFLOP/s (52% of the measured bf16
 // rate).  Scores of a whole tile at a time (fewer, wider MMAs, but a slot's softmax then
 // waits for all of them): 1.27 ms.  Short contexts are bound by what a unit costs beside
-// its tiles, in thousands of clocks: queries (8), outputs (3 to 5), joins (8 to 20), and
+// its tiles, in thousands of clocks: queries (8), outputs (3 to 5), joins (5 to 15), and
 // tiles of new rows, which take 9 (cached ones 4).
 // Code size matters as much: with unrolled tiles the roles' loops overflowed the
 // instruction caches (one tree of 257 nodes 125 us instead of 99).
@@ -896,7 +896,8 @@ struct Soft {
     }
 
     // The last CTA of a full block's unit: the other parts come from memory, its own
-    // straight from tensor memory; same sums in the same order as join().
+    // straight from tensor memory; same sums in the same order as join(), which writes
+    // and reads all of them (64 trees of 61 nodes 174 us, this 166).
     static DT_DI void join_own(const DtAttend& a, const Seg& u, Shared* sh, const float* part, int own, uint32_t to, int row,
                                float m, float l0, uint32_t stage, uint16_t* out) {
         const float NEG_INF = -__int_as_float(0x7F800000);

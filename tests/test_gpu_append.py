@@ -239,3 +239,29 @@ def test_refusals():
     odd = torch.randn((2, 4, 2, 65), device="cuda")[..., 1:]
     with pytest.raises(dtree.DtError):  # off the 16-byte boundary
         dtree.kv_append(cache, odd, odd)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rotation_rounds_every_step(dtype, interleaved):
+    """Each product and each sum of the rotation is rounded once: with 2^24 keys the codes would
+    show some of the last-bit differences that a contracted product and sum makes."""
+    n, H, D, page = 8192, 16, 128, 128
+    g = torch.Generator(device="cuda").manual_seed(7)
+    k = torch.randn((1, n, H, D), generator=g, device="cuda").to(dtype)
+    cos, sin = ref.rope_tables(n, D, "cuda")
+    cache = dtree.PagedCache.empty(n // page, page, H, D, 1, n // page)
+    cache.table.copy_(torch.arange(n // page).view(1, -1))
+    assert not dtree.kv_append(cache, k, k, rope=dtree.Rope(cos, sin, interleaved)).any()
+    x = k[0].float()
+    a, b = (x[..., 0::2], x[..., 1::2]) if interleaved else (x[..., :D // 2], x[..., D // 2:])
+    c, s = cos[:, None], sin[:, None]
+    p, q, r, t = a * c, b * s, b * c, a * s
+    first, second = p - q, r + t
+    x = torch.stack((first, second), -1).flatten(-2) if interleaved else torch.cat((first, second), -1)
+    for codes, scale, y in ((cache.k, cache.k_scale, x), (cache.v, cache.v_scale, k[0].float())):
+        y = y.view(n // page, page, H, D).transpose(1, 2)
+        f, e = torch.frexp(y.abs().amax((2, 3)))
+        e = torch.where(f <= 0.875, e - 9, e - 8)
+        assert torch.equal(scale, torch.exp2(e.float()))
+        assert torch.equal(codes, (y / torch.exp2(e.float())[..., None, None]).to(torch.float8_e4m3fn).view(torch.uint8))
