@@ -338,7 +338,9 @@ DT_DI void dt_cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" 
 DT_DI void dt_cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // Packed fp32 pairs (one 64-bit register pair) for the two-lane f32x2
-// instructions; every operation is rounded to nearest on its own.
+// instructions, rounded to nearest.  A packed product that feeds a packed sum or
+// difference is contracted with it, .rn or not: where each step has to round, the
+// sums are taken apart.
 DT_DI unsigned long long dt_f2_pack(float a, float b) {
     unsigned long long r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
