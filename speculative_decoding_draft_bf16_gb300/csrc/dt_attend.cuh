@@ -211,6 +211,15 @@ struct AtWalk {
     }
 };
 
+// Factor from a product of codes to a score in base 2, as a normal number: a masked
+// score is -infinity, which a factor of zero would make NaN.  What the rounding up
+// adds to a score is below 2^-100.  NaN (a block that is not finite) stays.
+DT_DI float at_factor(float row, float keys) {
+    float f;
+    asm("max.NaN.f32 %0, %1, 0f00800000;" : "=f"(f) : "f"(__fmul_rn(row, keys)));
+    return f;
+}
+
 // The bits of new rows [m0, m0 + 32) that row `node` sees, rows below n only.
 DT_DI uint32_t at_mask_word(const DtAttend& a, int b, int node, int m0, int n) {
     uint32_t bits;

@@ -176,7 +176,7 @@ struct Stream {
         for (int i = 0; i < NR; ++i) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                k[i][e] = __fmul_rn(rowc[i][e], ks);
+                k[i][e] = at_factor(rowc[i][e], ks);
                 top[i][e] = __fmaf_rn(fmaxf(c[i][e], c[i][2 + e]), k[i][e], lv);
                 grown |= top[i][e] > m[i][e] + (HEADROOM + LAZY);
             }

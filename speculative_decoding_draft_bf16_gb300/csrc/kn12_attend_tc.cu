@@ -624,7 +624,7 @@ struct Soft {
         uint32_t x[64];
         const float4 ks = sc->ks, lv = sc->lv, iv = sc->iv;
         dt_tmem_ld64(ts, x);
-        const float ka[4] = {__fmul_rn(rowc, ks.x), __fmul_rn(rowc, ks.y), __fmul_rn(rowc, ks.z), __fmul_rn(rowc, ks.w)};
+        const float ka[4] = {at_factor(rowc, ks.x), at_factor(rowc, ks.y), at_factor(rowc, ks.z), at_factor(rowc, ks.w)};
         const float l4[4] = {lv.x, lv.y, lv.z, lv.w}, i4[4] = {iv.x, iv.y, iv.z, iv.w};
         if (masked) {
 #pragma unroll
