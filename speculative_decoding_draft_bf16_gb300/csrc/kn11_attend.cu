@@ -150,7 +150,7 @@ struct Stream {
             big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
             int ex = (int)(big >> 23) - 127;  // largest magnitude in [2^ex, 2^(ex+1))
-            ex = big >= 0x7F800000u ? 0 : max(ex, -100);
+            ex = big >= 0x7F800000u ? 0 : min(max(ex, -100), 126);  // 2^-ex is a normal number
             const float f = dt_pow2(-ex), rc = __fmul_rn(__fmul_rn(a.scale, LOG2E), dt_pow2(ex));
             rowc[i][0] = __shfl_sync(0xffffffffu, rc, 8 * t);
             rowc[i][1] = __shfl_sync(0xffffffffu, rc, 8 * t + 4);

@@ -577,7 +577,7 @@ struct Soft {
 #pragma unroll
                 for (int o = PPR / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
                 int ex = (int)(big >> 23) - 127;  // largest magnitude in [2^ex, 2^(ex+1))
-                ex = big >= 0x7F800000u ? 0 : max(ex, -100);
+                ex = big >= 0x7F800000u ? 0 : min(max(ex, -100), 126);  // 2^-ex is a normal number
                 const float f = dt_pow2(-ex);
                 uint32_t w[4], z[4];
 #pragma unroll

@@ -65,3 +65,15 @@ def test_factors_that_underflow(M, G, key_scale, scale):
     x[:, :, :2 * G] *= 2.0 ** -30
     q, k, v = x[:, :, :2 * G], x[:, :, 2 * G:2 * G + 2], x[:, :, 2 * G + 2:]
     compare(cache, q, k, v, dtree.tree_attention(cache, q, k, v, scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("M,G", SHAPES)
+def test_queries_near_the_largest_number(M, G):
+    """Queries of 2^127 and more over keys as small: ordinary scores.  No new row is seen."""
+    cache = make_cache([37, 130], 16, 2, 64, 3)
+    cache.k_scale[cache.k_scale.isfinite()] = 2.0 ** -126
+    x = torch.randn((2, M, 2 * G + 4, 64), generator=torch.Generator().manual_seed(M)).to(torch.bfloat16).cuda()
+    x[:, :, :2 * G, 7] = 2.5e38
+    q, k, v = x[:, :, :2 * G], x[:, :, 2 * G:2 * G + 2], x[:, :, 2 * G + 2:]
+    mask = torch.zeros((2, M, (M + 31) // 32), dtype=torch.int32, device="cuda")
+    compare(cache, q, k, v, dtree.tree_attention(cache, q, k, v, mask=mask), torch.zeros((M, M), dtype=torch.bool))
