@@ -569,8 +569,9 @@ dt_status dt_kv_append(const dt_kv_cache* c, const dt_rope* rope, int32_t batch,
  *      to be zero as they found it, for any later shapes.  Calls that may run
  *      at the same time need workspaces of their own.
  * Products are taken in fp16 with fp32 accumulation (e4m3 codes are exact in
- * fp16; q, new k and v are scaled by powers of two into its range); softmax
- * statistics are fp32.
+ * fp16; rows of q, new k and v are scaled by powers of two into its range, and
+ * keep what lies within 2^-20 of the row's largest magnitude; new values below
+ * 2^-57 may count as zero); softmax statistics are fp32.
  * A request whose len, n_nodes, pages or positions are out of range gets
  * DT_DEV_BAD_CACHE in status[b] (OR-ed) and undefined output rows. */
 size_t dt_tree_attention_workspace(const dt_kv_cache* c, int32_t batch, int32_t M, int32_t Hq);

@@ -220,6 +220,14 @@ DT_DI float at_factor(float row, float keys) {
     return f;
 }
 
+// Exponent by which a new row is scaled, from the bits of its largest magnitude: of
+// keys down to where it is a normal number; of values to 2^-57 (what lies below counts
+// as small against 1), so that sums over rows and pages keep their range; a row of
+// zeros, 0.
+DT_DI int at_row_exponent(uint32_t big, bool keys) {
+    return big == 0u ? 0 : min(max((int)(big >> 23) - 127, keys ? -126 : -57), 126);
+}
+
 // The bits of new rows [m0, m0 + 32) that row `node` sees, rows below n only.
 DT_DI uint32_t at_mask_word(const DtAttend& a, int b, int node, int m0, int n) {
     uint32_t bits;

@@ -167,17 +167,21 @@ struct Stream {
     }
 
     // Scores of 16 tokens, masked (c[i][2k + e]: token g + 8k, row 2t + e + 8i), to
-    // probabilities as the fragments of P'; ks, lv, iv: the 16 tokens'.
-    DT_DI void weigh(float (&c)[NR][4], float ks, float lv, float iv, uint32_t (&p)[NR][2]) {
+    // probabilities as the fragments of P'; ks, lv, iv: the 16 tokens', or (T = 2) of
+    // tokens g and g + 8.
+    template <int T>
+    DT_DI void weigh(float (&c)[NR][4], const float (&ks)[T], const float (&lv)[T], const float (&iv)[T], uint32_t (&p)[NR][2]) {
         const float NEG_INF = -__int_as_float(0x7F800000);
-        float k[NR][2], top[NR][2];
+        float k[NR][2][T], top[NR][2];
         bool grown = false;
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                k[i][e] = at_factor(rowc[i][e], ks);
-                top[i][e] = __fmaf_rn(fmaxf(c[i][e], c[i][2 + e]), k[i][e], lv);
+#pragma unroll
+                for (int h = 0; h < T; ++h) k[i][e][h] = at_factor(rowc[i][e], ks[h]);
+                if constexpr (T == 1) top[i][e] = __fmaf_rn(fmaxf(c[i][e], c[i][2 + e]), k[i][e][0], lv[0]);
+                else top[i][e] = fmaxf(__fmaf_rn(c[i][e], k[i][e][0], lv[0]), __fmaf_rn(c[i][2 + e], k[i][e][1], lv[1]));
                 grown |= top[i][e] > m[i][e] + (HEADROOM + LAZY);
             }
         }
@@ -205,10 +209,12 @@ struct Stream {
         for (int i = 0; i < NR; ++i) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float b = __fsub_rn(lv, m[i][e] == NEG_INF ? 0.f : m[i][e]);
-                c[i][e] = dt_ex2_approx(__fmaf_rn(c[i][e], k[i][e], b));
-                c[i][2 + e] = dt_ex2_approx(__fmaf_rn(c[i][2 + e], k[i][e], b));
-                l[i][e] = __fmaf_rn(__fadd_rn(c[i][e], c[i][2 + e]), iv, l[i][e]);
+                const float mu = m[i][e] == NEG_INF ? 0.f : m[i][e];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    c[i][2 * h + e] = dt_ex2_approx(__fmaf_rn(c[i][2 * h + e], k[i][e][h % T], __fsub_rn(lv[h % T], mu)));
+                if constexpr (T == 1) l[i][e] = __fmaf_rn(__fadd_rn(c[i][e], c[i][2 + e]), iv[0], l[i][e]);
+                else l[i][e] = __fmaf_rn(c[i][2 + e], iv[1], __fmaf_rn(c[i][e], iv[0], l[i][e]));
             }
             p[i][0] = transposed8x8(f16x2(c[i][0], c[i][1]));
             p[i][1] = transposed8x8(f16x2(c[i][2], c[i][3]));
@@ -250,7 +256,7 @@ struct Stream {
             }
         }
         uint32_t p[NR][2];
-        weigh(c, ks, lv, iv, p);
+        weigh<1>(c, {ks}, {lv}, {iv}, p);
         // values of tokens 2t, 2t + 1, 2t + 8, 2t + 9
         constexpr int VW = L::VB / 4;
         uint32_t w[4][VW];
@@ -283,33 +289,32 @@ struct Stream {
         }
     }
 
-    // The first of a warp's sums, from up to 16 new rows: rotated, scaled by powers of two to a largest
-    // magnitude below 2, a row that is not finite replaced by zeros and reported
-    // to those that see it.
+    // The first of a warp's sums, from up to 16 new rows: rotated, each scaled by a power of
+    // two to a largest magnitude below 4 (one of its own, so that what other rows hold does
+    // not matter), elements that are not finite replaced by zeros and reported to the rows
+    // that see them.
     DT_DI void fresh(const DtAttend& a, const Walk& u, int lane) {
         const int g = lane >> 2, t = lane & 3, n = u.r.n;
         const uint16_t* kp = (const uint16_t*)a.k.ptr + u.b * a.k.stride_b + u.h * a.k.stride_h;
         const uint16_t* vp = (const uint16_t*)a.v.ptr + u.b * a.v.stride_b + u.h * a.v.stride_h;
         uint32_t bad = 0;  // bit per row
-        auto exponent = [](uint32_t big) {
-            big = __reduce_max_sync(0xffffffffu, big);
-            return max((int)(big >> 23) - 127, -57);
-        };
         if (lane < n) {
             for (int e = 0; e < D; e += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(vp + lane * a.v.stride_n + e));
         }
         float c[NR][4] = {};
         float k[2][L::KC][16];
-        uint32_t big = 0;
+        float ks[2], fk[2];  // of rows g, g + 8
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int row = g + 8 * i;
+            ks[i] = fk[i] = 1.f;
 #pragma unroll
             for (int j = 0; j < L::KC; ++j) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) k[i][j][e] = 0.f;
             }
             if (8 * i >= n) continue;  // short: code that runs once waits for its instructions
+            uint32_t big = 0;
             const int at = a.rope.rot && row < n ? at_position(a, u.b, u.r.len, row) : 0;
 #pragma unroll
             for (int j = 0; j < L::KC; ++j) {
@@ -321,14 +326,16 @@ struct Stream {
                     else big = max(big, w);
                 }
             }
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            const int ek = at_row_exponent(big, true);
+            ks[i] = dt_pow2(ek), fk[i] = dt_pow2(-ek);
         }
-        const int ek = exponent(big);
-        const float fk = dt_pow2(-ek);
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const float *y = k[0][s >> 2] + 4 * (s & 3), *z = k[1][s >> 2] + 4 * (s & 3);
-            const uint32_t f[4] = {f16x2(__fmul_rn(y[0], fk), __fmul_rn(y[1], fk)), f16x2(__fmul_rn(z[0], fk), __fmul_rn(z[1], fk)),
-                                   f16x2(__fmul_rn(y[2], fk), __fmul_rn(y[3], fk)), f16x2(__fmul_rn(z[2], fk), __fmul_rn(z[3], fk))};
+            const uint32_t f[4] = {f16x2(__fmul_rn(y[0], fk[0]), __fmul_rn(y[1], fk[0])), f16x2(__fmul_rn(z[0], fk[1]), __fmul_rn(z[1], fk[1])),
+                                   f16x2(__fmul_rn(y[2], fk[0]), __fmul_rn(y[3], fk[0])), f16x2(__fmul_rn(z[2], fk[1]), __fmul_rn(z[3], fk[1]))};
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
                 uint32_t q[2];
@@ -347,11 +354,14 @@ struct Stream {
                 v[k][e] = y.x, v[k][e + 1] = y.y, v[k][e + 2] = y.z, v[k][e + 3] = y.w;
             }
         }
-        big = 0;
+        float fv[4];  // of rows as v's
+        int ev[4];
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
             const int row = 2 * t + (k4 & 1) + 8 * (k4 >> 1);
+            ev[k4] = 0, fv[k4] = 1.f;
             if (8 * (k4 >> 1) >= n) continue;
+            uint32_t big = 0;
 #pragma unroll
             for (int e = 0; e < L::VB / 2; ++e) {
 #pragma unroll
@@ -361,9 +371,18 @@ struct Stream {
                     else big = max(big, w);
                 }
             }
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, d));
+            ev[k4] = at_row_exponent(big, false);
+            fv[k4] = dt_pow2(-ev[k4]);
         }
-        const int ev = exponent(big);
-        const float fv = dt_pow2(-ev);
+        float lv[2], iv[2];  // of rows g, g + 8, which lanes with t = g / 2 hold
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e0 = __shfl_sync(0xffffffffu, ev[2 * i], g >> 1), e1 = __shfl_sync(0xffffffffu, ev[2 * i + 1], g >> 1);
+            const int e = g & 1 ? e1 : e0;
+            lv[i] = (float)e, iv[i] = dt_pow2(-e);
+        }
         bad = __reduce_or_sync(0xffffffffu, bad);
         // what the lane's rows see
         bool poison[NR][2];
@@ -381,7 +400,7 @@ struct Stream {
         }
         uint32_t p[NR][2];
         clear();
-        weigh(c, dt_pow2(ek), (float)ev, dt_pow2(-ev), p);
+        weigh<2>(c, ks, lv, iv, p);
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
 #pragma unroll
@@ -391,7 +410,7 @@ struct Stream {
         auto pair = [&](int x, int y, int j) {  // column j of rows v[x], v[y], scaled
             const float lo = __uint_as_float(j & 1 ? v[x][j / 2] & 0xFFFF0000u : v[x][j / 2] << 16);
             const float hi = __uint_as_float(j & 1 ? v[y][j / 2] & 0xFFFF0000u : v[y][j / 2] << 16);
-            return f16x2(__fmul_rn(lo, fv), __fmul_rn(hi, fv));
+            return f16x2(__fmul_rn(lo, fv[x]), __fmul_rn(hi, fv[y]));
         };
 #pragma unroll
         for (int j = 0; j < NV; j += 2) {

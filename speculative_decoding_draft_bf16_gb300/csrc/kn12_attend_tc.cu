@@ -20,7 +20,9 @@
 // so the products need no scaling, and the row sum adds p / vs.  m is the running
 // maximum of t + log2 vs less 5 (fp16 then resolves probabilities down to 2^-29 of
 // the largest), moved -- and O rescaled -- only when the maximum has grown by
-// more than 8 since.
+// more than 8 since.  A tile of new rows has one scale, or, when the rows'
+// magnitudes lie too far apart for fp16, one for each row: such tiles go through
+// a short loop of their own, and what a row does not see never matters to it.
 //
 // Roundings: codes are exact in fp16; q, new k and v are scaled by powers of two into
 // fp16's range and rounded to 11 bits (bf16 has 8, rotation gives them more); P to 11
@@ -68,6 +70,10 @@ constexpr int OWN_PARTS = 8;    // most parts of a unit that its last CTA joins 
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float HEADROOM = 5.f, LAZY = 8.f;
 
+struct Apart {  // of a tile of new rows, keys and values: each row's exponent, and whether rows have their own
+    int8_t e[2][AT_TILE];
+    int yes[2];
+};
 struct Scales {  // of four groups of 16 tokens: key scale, log2 and inverse of the value scale
     float4 ks, lv, iv;
 };
@@ -94,12 +100,13 @@ struct Shared {
     int fail, last;
     AtShare share;
     Ring ring[RING];
+    Apart apart[RING];
     float qscale[ROWS];
     int qpos[ROWS], kpos[AT_TILE];
     long long qoff[ROWS];
     float mrg_m[TQ], mrg_l[TQ];
     float wt[OWN_PARTS][ROWS];
-    uint32_t amax[2][NC / 32];
+    int emax[2][NC / 32], emin[2][NC / 32];
     uint64_t segfull[SEGS], segfree[SEGS];
     Seg seg[SEGS];
 };
@@ -178,6 +185,12 @@ DT_DI float max3(float a, float b, float c) {
     return r;
 }
 
+DT_DI float max3_nan(float a, float b, float c) {  // NaN if one is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Streamed codes: read once by this CTA, not kept in L1.
 DT_DI uint4 ldg16(const void* p) {
     uint4 v;
@@ -235,10 +248,17 @@ struct Conv {
         else asm volatile("bar.sync 3, 128;" ::: "memory");
     }
 
-    // One tile of new rows, from row m0: keys rotated, scaled by a power of two
-    // when the largest magnitude leaves fp16's comfortable range.
-    static DT_DI void fresh(const DtAttend& a, const Seg& u, bool keys, int m0, int ct, Shared* sh, Ring* ring,
+    static constexpr float INF = __builtin_huge_valf();
+    static constexpr int8_t NONE = 127;  // in place of the exponent of a row of zeros
+
+    // One tile of new rows, from row m0: keys rotated, and scaled by powers of two when
+    // the rows' largest magnitudes are not all in [2^-4, 2^15), where fp16 is exact enough:
+    // by one for the tile when that brings them there, else by one for each row, so that
+    // what other rows hold does not matter.
+    static DT_DI void fresh(const DtAttend& a, const Seg& u, bool keys, int m0, int ct, Shared* sh, uint32_t g,
                             uint32_t tile) {
+        Ring* ring = &sh->ring[g % RING];
+        Apart* ap = &sh->apart[g % RING];
         const int which = keys ? 0 : 1, b = u.b, n = u.n, len = u.len, left = min(AT_TILE, n - m0);
         const dt_rows& src = keys ? a.k : a.v;
         const uint16_t* p = (const uint16_t*)src.ptr + b * src.stride_b + u.h * src.stride_h;
@@ -246,17 +266,15 @@ struct Conv {
         dt_rope rope = a.rope;
         if (!keys) rope.rot = 0;
         if (ct < 4) ring->bad[which][ct] = 0u;
+        ap->e[which][ct] = NONE;
         if (keys) sh->kpos[ct] = rope.rot && ct < left ? at_position(a, b, len, m0 + ct) : 0;
         group_sync(keys);
         const int pr = ct % PPT;  // this thread's chunk pair of rows ct / PPT + i * TPI
         int c0, c1;
         dt_pair_chunks(pr, rope, c0, c1);
         constexpr int U = D == 64 ? 2 : 1;  // rows in flight (two at D = 128 make the loop over cached tiles spill)
-        int e = 0;
 #pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {  // the second one when the tile needs another scale
-            const float f = dt_pow2(-e);
-            uint32_t big = 0u;
+        for (int pass = 0; pass < 2; ++pass) {  // the second one when the tile needs scales
 #pragma unroll 1
             for (int i0 = 0; i0 < NI; i0 += U) {
                 if (i0 * TPI >= left) {  // no row of these: zeros, which a weight of zero leaves zero
@@ -277,22 +295,25 @@ struct Conv {
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
                     const int r = ct / PPT + (i0 + k) * TPI;
-                    bool bad = false;
                     uint32_t o[4], w[4];
                     float x[8], y[8];
                     raw[k].rotated(pr, rope, x, y);
+                    float top = max3_nan(fabsf(x[0]), fabsf(y[0]), 0.f);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        float& u0 = x[q];
-                        float& u1 = y[q];
-                        const bool b0 = (__float_as_uint(u0) & 0x7FFFFFFFu) >= 0x7F800000u;
-                        const bool b1 = (__float_as_uint(u1) & 0x7FFFFFFFu) >= 0x7F800000u;
-                        bad |= b0 | b1;
-                        u0 = b0 || r >= left ? 0.f : __fmul_rn(u0, f);
-                        u1 = b1 || r >= left ? 0.f : __fmul_rn(u1, f);
-                        big = max(big, max(__float_as_uint(u0) & 0x7FFFFFFFu, __float_as_uint(u1) & 0x7FFFFFFFu));
+                    for (int q = 1; q < 8; ++q) top = max3_nan(top, fabsf(x[q]), fabsf(y[q]));
+                    if (__float_as_uint(top) >= 0x7F800000u) {  // zeros for what is not finite
+                        top = 0.f;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            x[q] = fabsf(x[q]) < INF ? x[q] : 0.f;
+                            y[q] = fabsf(y[q]) < INF ? y[q] : 0.f;
+                            top = max3_nan(top, fabsf(x[q]), fabsf(y[q]));
+                        }
+                        if (r < left) atomicOr(&ring->bad[which][r >> 5], 1u << (r & 31));
                     }
-                    if (bad && r < left) atomicOr(&ring->bad[which][r >> 5], 1u << (r & 31));
+                    const float f = r >= left ? 0.f : pass ? dt_pow2(-ap->e[which][r]) : 1.f;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) x[q] = __fmul_rn(x[q], f), y[q] = __fmul_rn(y[q], f);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         o[q] = f16x2(x[2 * q], x[2 * q + 1]);
@@ -300,25 +321,35 @@ struct Conv {
                     }
                     sts16(tile + chunk_at(r, c0), o);
                     sts16(tile + chunk_at(r, c1), w);
+                    if (pass == 0) {
+#pragma unroll
+                        for (int d = 1; d < PPT; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        if (pr == 0 && top > 0.f && r < left) ap->e[which][r] = (int8_t)at_row_exponent(__float_as_uint(top), keys);
+                    }
                 }
             }
             if (pass) break;
-            big = dt_warp_max_u32(big);
-            if ((ct & 31) == 0) sh->amax[which][ct >> 5] = big;
             group_sync(keys);
-            for (int i = 0; i < NC / 32; ++i) big = max(big, sh->amax[which][i]);
-            // as they are in [2^-4, 2^15), else scaled to below 2^9; none or very small: 2^-57
-            e = (int)(big >> 23) - 127;
-            e = e >= -4 && e < 15 ? 0 : max(e - 8, -57);
-            if (e == 0) break;
-        }
-        if (ct < 8) {
-            if (keys) {
-                *ring->ks(ct) = dt_pow2(e);
-            } else {
-                *ring->lv(ct) = (float)e;
-                *ring->iv(ct) = dt_pow2(-e);
+            const int own = ap->e[which][ct];
+            int hi = __reduce_max_sync(0xffffffffu, own == NONE ? -128 : own), lo = __reduce_min_sync(0xffffffffu, own);
+            if ((ct & 31) == 0) sh->emax[which][ct >> 5] = hi, sh->emin[which][ct >> 5] = lo;
+            group_sync(keys);
+            for (int i = 0; i < NC / 32; ++i) hi = max(hi, sh->emax[which][i]), lo = min(lo, sh->emin[which][i]);
+            const bool apart = hi - lo > 18 && hi != -128;
+            const int e = apart || hi == -128 || (lo >= -4 && hi < 15) ? 0 : max(hi - 14, keys ? -126 : -57);
+            if (!apart) ap->e[which][ct] = (int8_t)e;
+            else if (own == NONE) ap->e[which][ct] = 0;
+            if (ct == 0) ap->yes[which] = apart;
+            if (ct < 8) {
+                if (keys) {
+                    *ring->ks(ct) = dt_pow2(e);
+                } else {
+                    *ring->lv(ct) = (float)e;
+                    *ring->iv(ct) = dt_pow2(-e);
+                }
             }
+            group_sync(keys);
+            if (e == 0 && !apart) return;
         }
         group_sync(keys);
     }
@@ -382,7 +413,7 @@ struct Conv {
                 const int s = g % STAGES;
                 wait(&free_[s], (g / STAGES + 1) & 1, &sh->fail);
                 wait(&sh->idfull[g % RING], (g / RING) & 1, &sh->fail);  // the ring's slot is free
-                fresh(a, u, keys, (j - u.ctx) * AT_TILE, ct, sh, &sh->ring[g % RING], base + s * L::TILE);
+                fresh(a, u, keys, (j - u.ctx) * AT_TILE, ct, sh, g, base + s * L::TILE);
                 if (ct == 0) dt_mbar_arrive(&sh->scfull[g % RING]);
                 stored(s);
             }
@@ -607,6 +638,33 @@ struct Soft {
         return make_uint2(at_mask_word(a, u.b, node, m0, u.n), at_mask_word(a, u.b, node, m0 + 32, u.n));
     }
 
+    // A maximum that has grown moves the reference, and O when it has sums; rows of a
+    // warp do so together.
+    static DT_DI void follow(float mx, float& m, float& l, uint32_t to, bool has_o, uint64_t* other, uint32_t other_ph,
+                             int* fail) {
+        const bool grown = mx > m + (HEADROOM + LAZY);
+        if (__any_sync(0xffffffffu, grown)) {
+            const float to_m = grown ? mx - HEADROOM : m;
+            const float f = grown ? dt_ex2_approx(m - to_m) : 1.f;  // m = -inf: 0
+            m = to_m;
+            l = __fmul_rn(l, f);
+            if (has_o) {
+                wait(other, other_ph, fail);
+                __syncwarp();
+                dt_tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t o[16];
+                    dt_tmem_ld16_async(to + 16 * c, o);
+                    dt_tmem_ld_wait(o);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__fmul_rn(__uint_as_float(o[i]), f));
+                    dt_tmem_st16(to + 16 * c, o);
+                }
+            }
+        }
+    }
+
     // 64 tokens of a row: their scores at ts become probabilities in place, the
     // running reference m and sum l move on, and O is rescaled when it has sums;
     // before that every product of the slot must be done: `other` is the barrier
@@ -645,28 +703,7 @@ struct Soft {
             tg[g] = __fmaf_rn(fmaxf(q0, q1), ka[g], l4[g]);
         }
         const float mx = fmaxf(max3(tg[0], tg[1], tg[2]), tg[3]);
-        // a maximum that has grown moves the reference; rows of a warp do so together
-        const bool grown = mx > m + (HEADROOM + LAZY);
-        if (__any_sync(0xffffffffu, grown)) {
-            const float to_m = grown ? mx - HEADROOM : m;
-            const float f = grown ? dt_ex2_approx(m - to_m) : 1.f;  // m = -inf: 0
-            m = to_m;
-            l = __fmul_rn(l, f);
-            if (has_o) {
-                wait(other, other_ph, fail);
-                __syncwarp();
-                dt_tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {
-                    uint32_t o[16];
-                    dt_tmem_ld16_async(to + 16 * c, o);
-                    dt_tmem_ld_wait(o);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__fmul_rn(__uint_as_float(o[i]), f));
-                    dt_tmem_st16(to + 16 * c, o);
-                }
-            }
-        }
+        follow(mx, m, l, to, has_o, other, other_ph, fail);
         const float mu = m == NEG_INF ? 0.f : m;
 #pragma unroll
         for (int g2 = 0; g2 < 4; g2 += 2) {
@@ -695,6 +732,49 @@ struct Soft {
         dt_tmem_st_wait();
     }
 
+    // The same for tokens with scales of their own: key exponents ek, value exponents ev.
+    // Rare, so short: 16 tokens at a time, their scores read twice.
+    static DT_DI void half_apart(const Apart* ap, int h, uint32_t ts, uint32_t to, bool has_o, float rowc,
+                                 uint2 mk, float& m, float& l, uint64_t* other, uint32_t other_ph, int* fail) {
+        const float NEG_INF = -__int_as_float(0x7F800000);
+        const int8_t *ek = ap->e[0] + 64 * h, *ev = ap->e[1] + 64 * h;
+        float mx = NEG_INF, mu = 0.f;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t bits = (g < 2 ? mk.x : mk.y) >> (16 * (g & 1));
+                uint32_t x[16], p[8];
+                dt_tmem_ld16_async(ts + 16 * g, x);
+                dt_tmem_ld_wait(x);
+                float y[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    y[i] = (bits >> i) & 1 ? __fmaf_rn(__uint_as_float(x[i]), at_factor(rowc, dt_pow2(ek[16 * g + i])),
+                                                       __fsub_rn((float)ev[16 * g + i], mu))
+                                           : NEG_INF;
+                if (pass == 0) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) mx = fmaxf(mx, y[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        y[i] = dt_ex2_approx(y[i]);
+                        l = __fmaf_rn(y[i], dt_pow2(-ev[16 * g + i]), l);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) p[i] = f16x2(y[2 * i], y[2 * i + 1]);
+                    dt_tmem_st8(ts + 8 * g, p);  // over scores that have been read
+                }
+            }
+            if (pass == 0) {
+                follow(mx, m, l, to, has_o, other, other_ph, fail);
+                mu = m == NEG_INF ? 0.f : m;
+            }
+        }
+        dt_tmem_st_wait();
+    }
+
     static DT_DI void run(const DtAttend& a, unsigned char* sm, Shared* sh, uint32_t tmem, int tid, int cta,
                           float* part, int* counters) {
         const int s = tid / TQ, w4 = (tid >> 5) & 3;
@@ -716,11 +796,14 @@ struct Soft {
             bool poison = false;
             const int clear = len / AT_TILE - u.t0;  // tiles before this one are wholly visible
             uint32_t pa = ph & 1;                    // phase of both halves' scores
+            int lt = dual ? 0 : s;
 #pragma unroll 1
-            for (int lt = dual ? 0 : s; lt < nt; lt += hop, pa ^= 1) {
+            for (; lt < nt; lt += hop, pa ^= 1) {
                 const uint32_t g = g0 + lt;
                 const Ring* ring = &sh->ring[g % RING];
                 wait(&sh->scfull[g % RING], (g / RING) & 1, &sh->fail);
+                // (under `clear`, known already: without it 16 trees of 257 nodes 1.14 ms instead of 1.13)
+                if (lt >= clear && u.t0 + lt >= u.ctx && (sh->apart[g % RING].yes[0] | sh->apart[g % RING].yes[1])) break;
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     uint64_t* other = &sh->sfull[s][h ^ 1];  // of half 0: waited for next; of half 1: of the next tile
@@ -738,6 +821,28 @@ struct Soft {
                     __syncwarp();
                     dt_tc_fence_after();
                     half(&ring->half[h], st, to, has_o, rowc, masked, mk, m, l, other, other_ph, &sh->fail);
+                    dt_tc_fence_before();
+                    __syncwarp();
+                    if ((tid & 31) == 0) dt_mbar_arrive(&sh->pfull[s][h]);
+                }
+            }
+            // new rows from a tile on whose rows have scales of their own (rare: short code, apart
+            // from the loop above)
+#pragma unroll 1
+            for (; lt < nt; lt += hop, pa ^= 1) {
+                const uint32_t g = g0 + lt;
+                const Ring* ring = &sh->ring[g % RING];
+                wait(&sh->scfull[g % RING], (g / RING) & 1, &sh->fail);
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const uint2 mk = mask_words(a, u, u.t0 + lt, h, row);
+                    poison |= ((mk.x & (ring->bad[0][2 * h] | ring->bad[1][2 * h])) |
+                               (mk.y & (ring->bad[0][2 * h + 1] | ring->bad[1][2 * h + 1]))) != 0u;
+                    wait(&sh->sfull[s][h], pa, &sh->fail);
+                    __syncwarp();
+                    dt_tc_fence_after();
+                    half_apart(&sh->apart[g % RING], h, ts + 64 * h, to, lt >= hop || h, rowc, mk, m, l, &sh->sfull[s][h ^ 1],
+                               pa ^ h, &sh->fail);
                     dt_tc_fence_before();
                     __syncwarp();
                     if ((tid & 31) == 0) dt_mbar_arrive(&sh->pfull[s][h]);
