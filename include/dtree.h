@@ -583,10 +583,10 @@ dt_status dt_tree_attention(const dt_kv_cache* c, const dt_rope* rope, int32_t b
 /* Log-probabilities of given tokens ([Unit11] temperature 1), with the rank of
  * the token, the entropy of the row and its best alternatives.
  *   logits: [batch][M][V] in dtype, row m of request b at b * stride_b +
- *      m * stride elements (stride >= V, stride_b >= 0).  Magnitudes up to
- *      2^127, or -inf, one finite value per row at least (else logprob, entropy
- *      and top_logprob of that row are NaN or infinite, ids and ranks
- *      unspecified).
+ *      m * stride elements (stride >= V, stride_b >= 0).  Any finite numbers
+ *      (masks of the type's lowest value among them) or -inf, one finite value
+ *      per row at least; for a row without one, or with NaN or +inf, logprob,
+ *      entropy and top_logprob are NaN or infinite, ids and ranks unspecified.
  *   rows:   NULL (row j, N <= M) or [batch][N]: entry j is about logits row
  *      rows[b][j]; a negative entry is about no row: logprob, entropy and
  *      top_logprob 0, rank and top_id -1; an entry >= M: the same with NaN.

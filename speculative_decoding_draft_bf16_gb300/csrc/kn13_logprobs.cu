@@ -35,6 +35,11 @@ constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.693147180559945309417f;
 // What stands for -infinity, whose exponential has to be zero and its product with it
 // too, and the reference of a thread that has read nothing else.
 constexpr float LOWEST = -1.7014118346046923e38f, NO_REF = -1.0e38f;  // -2^127
+// A reference of this magnitude or more is too coarse: x log2(e) - m of the element it was
+// taken from is 2^6 off, and beyond that its exponential underflows.  But logits so large
+// lie 32 apart at least, and only ties with the row's largest have a weight: a CTA with such
+// a largest reference counts them.
+constexpr float FLAT = 536870912.f;  // 2^29, in base 2
 
 typedef unsigned long long u64;
 
@@ -66,6 +71,7 @@ DT_DI void finite_vals(const uint4& q, float (&x)[4]) {
 
 struct Part {  // of a CTA, in rank 0's shared memory
     float m, s, u;
+    float flat;      // beyond FLAT: its largest logit (s counts the ties), else 0
     int before, any;
     u64 top[32];
 };
@@ -96,14 +102,16 @@ struct Row {
     uint32_t masks;  // bf16: sum of masks (0xFFFF in each half that comes before), since the last flush
 
     DT_DI bool any() const { return lim > -__int_as_float(0x7F800000); }  // a value above -infinity
-    DT_DI void refer(float to) {  // the reference to `to`
-        const float d = __fsub_rn(m, to), f = dt_ex2_approx(d);
+    DT_DI void refer(float to) {  // the reference to `to`, which is not below it (or there are no sums)
+        const float d = fminf(fmaxf(__fsub_rn(m, to), -200.f), 0.f), f = dt_ex2_approx(d);  // far: 0, with finite terms
         u2 = dt_f2_mul(dt_f2_fma(s2, dt_f2_pack(d, d), u2), dt_f2_pack(f, f));
         s2 = dt_f2_mul(s2, dt_f2_pack(f, f));
         m = to;
     }
     DT_DI void move(float x) {  // and to the element x
-        refer(__fmul_rn(x, LOG2E));
+        // above x log2(e) by more than it is rounded, so that no exponential overflows, and
+        // not below what stands for -infinity
+        refer(__fmaf_rn(fabsf(x), 0x1p-22f, __fmul_rn(fmaxf(x, LOWEST), LOG2E)));
         lim = __fadd_rn(x, FAR);
     }
     DT_DI void add(float x0, float x1) {
@@ -405,34 +413,69 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 10 : 2) kn13_kernel(const __gr
         to->m = ref;
         to->s = ss;
         to->u = uu;
+        to->flat = 0.f;
         to->before = bb;
         to->any = M > NEG_INF;
+    }
+    if (fabsf(M) >= FLAT && M > NEG_INF) {  // (all threads) the largest logit, and how many there are of it
+        float flat = 0.f, ties = 0.f;
+        for (int pass = 0; pass < 2; ++pass) {
+            float best = NEG_INF, n = 0.f;
+            auto look = [&](T raw) {
+                const float y = E::val(raw);
+                best = fmaxf(best, y);
+                n += y != y || y == __int_as_float(0x7F800000) ? NaN : y == flat ? 1.f : 0.f;  // no figures, as elsewhere
+            };
+#pragma unroll 1
+            for (const T* p = (const T*)(vec + v0) + tid; p < (const T*)(vec + v1); p += NT) look(*p);
+            if (c == 0 && tid < lead) look(x[tid]);
+            if (c == 0 && tid < a.V - tail) look(x[tail + tid]);
+            const float part = pass ? dt_warp_sum(n) : dt_warp_max(best);
+            __syncthreads();  // rm has been read
+            if (lane == 0) sh.rm[w] = part;
+            __syncthreads();
+            if (pass == 0) flat = sh.rm[0];
+#pragma unroll 1
+            for (int i = 0; i < NT / 32; ++i) {
+                if (pass) ties += sh.rm[i];
+                else flat = fmaxf(flat, sh.rm[i]);
+            }
+        }
+        if (tid == 0) to->s = ties, to->u = 0.f, to->flat = flat;
     }
     if (TOP && tid < 32) to->top[tid] = tid < sh.count ? sh.list[tid] : 0ull;
     if (S > 1) cluster.sync();
     else __syncthreads();
     if (c != 0 || w != 0) return;
     // rank 0's first warp: the CTAs' parts in their order
-    float m = NEG_INF;
+    float m = NEG_INF, X = NEG_INF;
     bool any = false;
     for (int i = 0; i < S; ++i) {
         if (sh.part[i].any) m = fmaxf(m, sh.part[i].m);
         any |= sh.part[i].any != 0;
+    }
+    const bool flat_row = any && fabsf(m) >= FLAT;
+    if (flat_row) {
+        for (int i = 0; i < S; ++i)
+            if (sh.part[i].flat != 0.f) X = fmaxf(X, sh.part[i].flat);
     }
     float ts = 0.f, tu = 0.f;
     int tb = 0;
     for (int i = 0; i < S; ++i) {
         const Part& p = sh.part[i];
         tb += p.before;
-        const float d = p.any && any ? p.m - m : 0.f, f = dt_ex2_approx(d);
+        const float d = p.any && any ? fmaxf(p.m - m, -200.f) : 0.f;
+        const float f = flat_row ? (p.flat == X ? 1.f : 0.f) : dt_ex2_approx(d);
         tu = __fmaf_rn(__fmaf_rn(p.s, d, p.u), f, tu);
         ts = __fmaf_rn(p.s, f, ts);
     }
     const float ln = logf(ts);
     const float lse = any ? __fmaf_rn(m, LN2, ln) : NaN;
+    // in a flat row the difference from the largest logit comes first, or it would absorb the logarithm
+    auto logprob_of = [&](float y) { return flat_row ? (y - X) - ln : y - lse; };
     if (lane == 0) {
-        if (a.logprob) a.logprob[e] = named ? r.token - lse : tok < 0 ? 0.f : NaN;
-        if (a.entropy) a.entropy[e] = any ? __fmaf_rn(-LN2, tu / ts, ln) : NaN;
+        if (a.logprob) a.logprob[e] = named ? logprob_of(r.token) : tok < 0 ? 0.f : NaN;
+        if (a.entropy) a.entropy[e] = !any ? NaN : flat_row ? ln : __fmaf_rn(-LN2, tu / ts, ln);
         if (a.rank) a.rank[e] = named ? tb : -1;
     }
     if (TOP) {
@@ -440,7 +483,7 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 10 : 2) kn13_kernel(const __gr
         for (int i = 1; i < S; ++i) best = dt_warp_top32_merge(best, sh.part[i].top[lane]);
         if (lane < a.top) {
             a.top_id[(size_t)e * a.top + lane] = (int)~(uint32_t)best;
-            a.top_logprob[(size_t)e * a.top + lane] = key_value<T>(best) - lse;
+            a.top_logprob[(size_t)e * a.top + lane] = logprob_of(key_value<T>(best));
         }
     }
 }
