@@ -5,8 +5,9 @@
 // A thread keeps, for the elements x that it has read, sums relative to a
 // reference m of its own, with y = x log2(e) - m: s = sum 2^y and u = sum y 2^y.
 // m is its first vectors' maximum (times log2(e), rounded) and moves only when an
-// element lies more than 20 above it.  Then lse = m ln(2) + ln s and the entropy is
-// ln s - ln(2) u / s, without cancellation between large numbers.
+// element lies more than 6 above it.  Then lse = m ln(2) + ln s and the entropy is
+// ln s - ln(2) u / s, whose terms cancel in a row that is certain: they are at most
+// some 6 there, and the difference is off by less than 2e-6.
 //
 // What concerns few elements is looked at once per 16-byte vector, by its
 // maximum: elements at least as large as the token (its rank), and elements at
@@ -30,7 +31,11 @@ namespace {
 constexpr int U = 6;                // vectors in flight per thread
 constexpr int ROUND = 6;            // batches between two looks at the list
 constexpr int CAP = 1024;           // list entries
-constexpr float FAR = 20.f;         // how far above its reference a thread lets an element lie
+// How far above its reference a thread lets an element lie.  Entropy of rows of 151936 normal
+// logits with one up to 25 above the others, largest error with 20, 12, 8, 6, 4: 13, 10, 4.6,
+// 2.1, 1.7e-6 (in 32 bits from the row's maximum 1.1); 4000 rows: 236.1, 236.0, 236.3, 237.5,
+// 239.9 us.
+constexpr float FAR = 6.f;
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.693147180559945309417f;
 // What stands for -infinity, whose exponential has to be zero and its product with it
 // too, and the reference of a thread that has read nothing else.
@@ -475,7 +480,8 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 10 : 2) kn13_kernel(const __gr
     auto logprob_of = [&](float y) { return flat_row ? (y - X) - ln : y - lse; };
     if (lane == 0) {
         if (a.logprob) a.logprob[e] = named ? logprob_of(r.token) : tok < 0 ? 0.f : NaN;
-        if (a.entropy) a.entropy[e] = !any ? NaN : flat_row ? ln : __fmaf_rn(-LN2, tu / ts, ln);
+        const float h = flat_row ? ln : __fmaf_rn(-LN2, tu / ts, ln);
+        if (a.entropy) a.entropy[e] = !any ? NaN : h < 0.f ? 0.f : h;  // rounding alone takes it below 0
         if (a.rank) a.rank[e] = named ? tb : -1;
     }
     if (TOP) {

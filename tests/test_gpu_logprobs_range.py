@@ -111,3 +111,21 @@ def test_levels_around_the_limit(dtype):
         x[0, r, 30000:60000] = (bits - 1).view(dtype)
     tok = torch.full((1, 17), 510, dtype=torch.int32, device="cuda")
     check(x, tok, 4, dtree.token_logprobs(x, tok, top=4))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_entropy_of_certain_rows(dtype):
+    """Two numbers in one thread's share, the later one up to 30 above the earlier: the reference that
+    a thread keeps may lag its largest value, and what that costs the entropy stays below 2e-6 (log and
+    quotient of some 6 each, to 2^-23 of it, and an exponential to 2^-22); it is not negative."""
+    rows = 400  # a CTA to a row
+    x = torch.full((1, rows, V), -math.inf, device="cuda")
+    x[0, :, 3] = torch.linspace(-40.0, 10.0, rows, device="cuda")
+    x[0, :, 3 + 512 * 8 * 12] = x[0, :, 3] + torch.linspace(0.0, 30.0, rows, device="cuda")
+    x = x.to(dtype)
+    o = dtree.token_logprobs(x, torch.full((1, rows), 3, dtype=torch.int32, device="cuda"), top=2)
+    lp = torch.log_softmax(x.double(), -1)
+    ent = -torch.where(lp > -700, lp.exp() * lp, 0.0).sum(-1)
+    assert (o.entropy >= 0).all()
+    worst = (o.entropy.double() - ent).abs().max().item()
+    assert worst <= 2e-6, worst
