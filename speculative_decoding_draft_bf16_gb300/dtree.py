@@ -6,6 +6,7 @@ documented dtype; the library writes into caller-owned buffers on the current
 torch stream (or the stream given).  A missing or unloadable library raises --
 there is no other code path.
 """
+import contextlib
 import ctypes
 import dataclasses
 import math
@@ -160,6 +161,12 @@ def _stream(stream):
         return ctypes.c_void_p(stream.cuda_stream)
     # the current stream's handle, without a Stream object (4 us of host time per call)
     return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+
+
+def _on(stream):
+    """Context in which a call allocates what its caller did not bring: on the stream that the call
+    runs on, so that fills come before it and freed memory is not handed out while it runs."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
 def _dtype_code(t):
@@ -481,7 +488,8 @@ def verify(tree, target, temperature=0.0, draft=None, uniforms=None, out=None, v
         # the walk reads both row sets with the target's element type
         raise TypeError("draft logits (%s) and target logits (%s) must share one dtype" % (draft.dtype, target.dtype))
     if out is None:
-        out = alloc_verify_out(tree)
+        with _on(stream):
+            out = alloc_verify_out(tree)
     acc_nodes, acc_len, next_tok = out
     _need_verify_io(tree, batch, V, draft, uniforms, target_lse, out, visited_lse)
     if rule is not None:
@@ -508,7 +516,8 @@ def verify_markov(p, tree, target, draft, znorm, uniforms, out=None, visited_lse
         raise TypeError("target logits must be %s for dtype=%r, got %s" % (draft.dtype, p.dtype, target.dtype))
     _need(znorm, torch.float32, "znorm", numel=p.batch * p.L * p.K)
     if out is None:
-        out = alloc_verify_out(tree)
+        with _on(stream):
+            out = alloc_verify_out(tree)
     acc_nodes, acc_len, next_tok = out
     _need_verify_io(tree, p.batch, p.V, None, uniforms, target_lse, out, visited_lse)
     if uniforms is None:
@@ -636,7 +645,7 @@ def kv_append(cache, k, v, rope=None, rows=None, count=None, count_add=0, len_ou
     """Append rows of k, v [batch, M, Hkv, D] to the cache (dt_kv_append): keys rotated to their
     position on the way, both stored in e4m3.  rows [batch, N] int32 picks rows (the walk's acc_nodes),
     count [batch] int32 + count_add says how many (its acc_len, 1); len_out [batch] gets the new lengths;
-    status [batch] int32 is OR-ed with DT_DEV_BAD_CACHE for a request that does not fit."""
+    status [batch] int32 is OR-ed with DT_DEV_BAD_CACHE for a request that does not fit; returned."""
     batch, M = cache.batch, k.shape[1]
     if k.dtype != v.dtype:
         raise TypeError("k (%s) and v (%s) must share one dtype" % (k.dtype, v.dtype))
@@ -652,7 +661,11 @@ def kv_append(cache, k, v, rope=None, rows=None, count=None, count_add=0, len_ou
         _need(count, torch.int32, "count", numel=batch)
     if len_out is not None:
         _need(len_out, torch.int32, "len_out", numel=batch)
-    status = torch.zeros((batch,), dtype=torch.int32, device=k.device) if status is None else _need(status, torch.int32, "status", numel=batch)
+    if status is None:
+        with _on(stream):
+            status = torch.zeros((batch,), dtype=torch.int32, device=k.device)
+    else:
+        _need(status, torch.int32, "status", numel=batch)
     _check(lib().dt_kv_append(cache._ref, rope._ref if rope is not None else None, batch, M, _dtype_code(k),
                               ctypes.byref(kr), ctypes.byref(vr), _addr(rows), N, _addr(count), int(count_add),
                               _addr(len_out), _addr(status), _stream(stream)), "dt_kv_append")
@@ -670,7 +683,8 @@ def tree_attention(cache, q, k, v, mask=None, pos=None, n_nodes=None, rope=None,
                    status=None, stream=None):
     """Attention of the tree's rows over the cache and over the tree (dt_tree_attention).
     q [batch, M, Hq, D], k, v [batch, M, Hkv, D] bf16, not rotated; mask, pos as dt_tree_mask writes
-    them with pos_offset 0 (None: a chain); returns out [batch, M, Hq, D] bf16."""
+    them with pos_offset 0 (None: a chain); returns out [batch, M, Hq, D] bf16.  status [batch] int32
+    is OR-ed with DT_DEV_BAD_CACHE for a request out of range: bring one to see it."""
     batch, M, Hq = cache.batch, q.shape[1], q.shape[2]
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if t.dtype != torch.bfloat16:
@@ -684,16 +698,18 @@ def tree_attention(cache, q, k, v, mask=None, pos=None, n_nodes=None, rope=None,
         _need(pos, torch.int32, "pos", numel=batch * M)
     if n_nodes is not None:
         _need(n_nodes, torch.int32, "n_nodes", numel=batch)
-    if out is None:
-        out = torch.empty((batch, M, Hq, cache.D), dtype=torch.bfloat16, device=q.device)
-    else:
+    if out is not None:
         _need(out, torch.bfloat16, "out", numel=batch * M * Hq * cache.D)
-    if status is None:
-        status = torch.zeros((batch,), dtype=torch.int32, device=q.device)
-    else:
+    if status is not None:
         _need(status, torch.int32, "status", numel=batch)
-    if workspace is None:
-        workspace = attention_workspace(cache, M, Hq)
+    if out is None or status is None or workspace is None:
+        with _on(stream):
+            if out is None:
+                out = torch.empty((batch, M, Hq, cache.D), dtype=torch.bfloat16, device=q.device)
+            if status is None:
+                status = torch.zeros((batch,), dtype=torch.int32, device=q.device)
+            if workspace is None:
+                workspace = attention_workspace(cache, M, Hq)
     ws, n = _need_workspace(workspace)
     if scale is None:
         scale = 1.0 / math.sqrt(cache.D)
@@ -743,7 +759,8 @@ def token_logprobs(logits, tokens, top=0, rows=None, out=None, stream=None):
         if rows.shape != tokens.shape:
             raise ValueError("rows must be shaped as tokens, got %s and %s" % (tuple(rows.shape), tuple(tokens.shape)))
     if out is None:
-        out = alloc_logprobs(batch, N, top, logits.device)
+        with _on(stream):
+            out = alloc_logprobs(batch, N, top, logits.device)
     else:
         _need(out.logprob, torch.float32, "logprob", numel=batch * N)
         _need(out.entropy, torch.float32, "entropy", numel=batch * N)
