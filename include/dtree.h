@@ -566,14 +566,16 @@ dt_status dt_kv_append(const dt_kv_cache* c, const dt_rope* rope, int32_t batch,
  *   out: [batch][M][Hq][D] bf16, dense, 16-byte aligned.
  *   workspace: dt_tree_attention_workspace bytes of device memory, 16-byte
  *      aligned, zeroed before its first use; the calls leave the part that has
- *      to be zero as they found it, for any later shapes.  Calls that may run
- *      at the same time need workspaces of their own.
+ *      to be zero as they found it, for any later shapes; after DT_DEV_TIMEOUT
+ *      it has to be zeroed again.  Calls that may run at the same time need
+ *      workspaces of their own.
  * Products are taken in fp16 with fp32 accumulation (e4m3 codes are exact in
  * fp16; rows of q, new k and v are scaled by powers of two into its range, and
  * keep what lies within 2^-20 of the row's largest magnitude; new values below
  * 2^-57 may count as zero); softmax statistics are fp32.
  * A request whose len, n_nodes, pages or positions are out of range gets
- * DT_DEV_BAD_CACHE in status[b] (OR-ed) and undefined output rows. */
+ * DT_DEV_BAD_CACHE in status[b] (OR-ed) and undefined output rows; when a wait
+ * of the kernel runs out, every request gets DT_DEV_TIMEOUT, and all rows are. */
 size_t dt_tree_attention_workspace(const dt_kv_cache* c, int32_t batch, int32_t M, int32_t Hq);
 dt_status dt_tree_attention(const dt_kv_cache* c, const dt_rope* rope, int32_t batch, int32_t M, int32_t Hq,
                             const dt_rows* q, const dt_rows* k, const dt_rows* v, const uint32_t* mask,
@@ -607,18 +609,22 @@ dt_status dt_token_logprobs(const void* logits, int32_t dtype, int32_t batch, in
  * Every mbarrier wait in the library is bounded; when a bound runs out the
  * kernel records it and carries on (stage 1: the row's lse becomes NaN and the
  * selection sets DT_DEV_TIMEOUT; the walk sets DT_DEV_TIMEOUT in the status
- * word; the normaliser writes NaN, which the selection reports the same way).
+ * word; the normaliser writes NaN, which the selection reports the same way; tree
+ * attention sets DT_DEV_TIMEOUT for every request).
  * For the kernels named in `kernels` (DT_PROBE_* bits, 0 = off) this makes
  * the staging wait first wait on a barrier that nothing ever completes, bounded
  * by budget_cycles SM clock cycles (1 .. DT_PROBE_MAX_BUDGET), so that path
  * runs; the real wait follows unchanged, so every copy lands before its data
- * is read and outputs other than the flags are the usual ones.  Applies to the
- * current device; synchronous (a copy to device symbols): call it outside
+ * is read and outputs other than the flags are the usual ones.  For tree
+ * attention a role of the kernel gives up for good while the others are at
+ * work, so that all of them stop: outputs and workspace are undefined.  Applies
+ * to the current device (tree attention: to the calls made while it is on); synchronous (a copy to device symbols): call it outside
  * stream capture and with no library kernel running.  Not for production use.
  * Returns DT_ERR_INVALID_ARG for unknown bits or a budget out of range. */
 #define DT_PROBE_STAGE1 0x1      /* the cluster stage-1 kernel (dt_candidates, few rows) */
 #define DT_PROBE_WALK 0x2        /* the acceptance walk (dt_verify, dt_verify_rule, dt_verify_markov) */
 #define DT_PROBE_NORMALISER 0x4  /* the tensor-core normaliser (dt_markov_norm) */
+#define DT_PROBE_ATTENTION 0x10  /* tree attention on the tensor cores (more than 16 rows per key head) */
 #define DT_PROBE_MAX_BUDGET (1ll << 28)
 dt_status dt_test_wait_fault(int32_t kernels, int64_t budget_cycles);
 

@@ -514,12 +514,13 @@ dt_status dt_saba_budget(const dt_saba_params* q, const dt_tree* t, int32_t batc
 }
 
 dt_status dt_test_wait_fault(int32_t kernels, int64_t budget_cycles) {
-    if (kernels & ~(DT_PROBE_STAGE1 | DT_PROBE_WALK | DT_PROBE_NORMALISER)) return DT_ERR_INVALID_ARG;
+    if (kernels & ~(DT_PROBE_STAGE1 | DT_PROBE_WALK | DT_PROBE_NORMALISER | DT_PROBE_ATTENTION)) return DT_ERR_INVALID_ARG;
     if (kernels && (budget_cycles < 1 || budget_cycles > DT_PROBE_MAX_BUDGET)) return DT_ERR_INVALID_ARG;
     const long long on = kernels ? (long long)budget_cycles : 0;
     cudaError_t e = dt_kn1_set_probe((kernels & DT_PROBE_STAGE1) ? on : 0);
     if (e == cudaSuccess) e = dt_kn6_set_probe((kernels & DT_PROBE_WALK) ? on : 0);
     if (e == cudaSuccess) e = dt_kn3n_set_probe((kernels & DT_PROBE_NORMALISER) ? on : 0);
+    dt_kn12_set_probe((kernels & DT_PROBE_ATTENTION) ? on : 0);
     return cuda_status(e);
 }
 

@@ -191,6 +191,7 @@ cudaError_t dt_kn11_launch(const DtAttend& a, void* workspace, int ctas, cudaStr
 // The same for many rows per key head, on the tensor cores (kn12_attend_tc.cu),
 // with ctas CTAs and dt_kn12_workspace bytes.
 size_t dt_kn12_workspace(int D, int ctas);
+void dt_kn12_set_probe(long long budget);
 cudaError_t dt_kn12_launch(const DtAttend& a, void* workspace, int ctas, cudaStream_t st);
 
 // Log-probabilities of given tokens (kn13_logprobs.cu).

@@ -41,6 +41,8 @@
 // tiles of new rows, which take 9 (cached ones 4).
 // Code size matters as much: with unrolled tiles the roles' loops overflowed the
 // instruction caches (one tree of 257 nodes 125 us instead of 99).
+#include <atomic>
+
 #include "dt_attend.cuh"
 #include "dt_tcgen05.cuh"
 
@@ -96,8 +98,9 @@ struct Seg {
 struct Shared {
     uint64_t kfull[STAGES], kfree[STAGES], vfull[STAGES], vfree[STAGES];
     uint64_t sfull[2][2], pfull[2][2], qfull, scfull[RING], idfull[RING], ringfree[RING];
+    uint64_t drain[2], probe;
     uint32_t tmem;
-    int fail, last;
+    int fail, drain_fail[2], last;
     AtShare share;
     Ring ring[RING];
     Apart apart[RING];
@@ -119,16 +122,30 @@ struct Lay {
     static constexpr size_t SMEM = 1024 + SH + sizeof(Shared);
 };
 
-// Bounded wait (some 10^8 to 10^9 clocks); once one has run out, `fail` is set and
-// later ones give up at their first look.  Short code: it stands in every role.
+// Bounded wait (about a second); once one has run out, `fail` is set and later ones give
+// up at their first look.  Short code: it stands in every role.
 DT_DI void wait(uint64_t* bar, uint32_t phase, int* fail) {
     asm volatile(
-        "{\n .reg .pred p;\n .reg .u32 n, f;\n mov.u32 n, 4194304;\n"
+        "{\n .reg .pred p;\n .reg .u32 n, f;\n mov.u32 n, 1048576;\n"
         "AGAIN:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1, 1000;\n @p bra DONE;\n"
         " sub.u32 n, n, 1;\n setp.ne.u32 p, n, 0;\n @!p st.volatile.shared.u32 [%2], 1;\n"
         " ld.volatile.shared.u32 f, [%2];\n setp.eq.u32 p, f, 0;\n @p bra AGAIN;\nDONE:\n}\n" ::"r"(dt_smem_addr(bar)),
         "r"(phase), "r"(dt_smem_addr(fail))
         : "memory");
+}
+
+// The same, four times as long and whatever has run out elsewhere: for segments, which come
+// in the end, because every role then runs on without waiting.  False when it has run out.
+DT_DI bool wait_long(uint64_t* bar, uint32_t phase, int* fail) {
+    uint32_t n = 4194304;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        "AGAIN:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n @p bra DONE;\n"
+        " sub.u32 %0, %0, 1;\n setp.ne.u32 p, %0, 0;\n @p bra AGAIN;\n st.volatile.shared.u32 [%3], 1;\nDONE:\n}\n"
+        : "+r"(n)
+        : "r"(dt_smem_addr(bar)), "r"(phase), "r"(dt_smem_addr(fail))
+        : "memory");
+    return n != 0;
 }
 
 DT_DI bool elect_one() {  // one lane of a converged warp
@@ -146,26 +163,32 @@ DT_DI void set_regs() {
     if constexpr (R < LAUNCH_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// The thread that walks the share, up to SEGS segments ahead of the roles.
+DT_DI bool failed(const Shared* sh) { return *(const volatile int*)&sh->fail != 0; }
+
+// The thread that walks the share, up to SEGS segments ahead of the roles.  When a wait
+// of a role has run out, it ends the walk.
 DT_DI void walk_share(const DtAttend& a, Shared* sh, int cta) {
     AtWalk<ROWS, ATOM> u;
     u.start(a, sh->share);
     uint32_t i = 0;
     for (bool more = true; more; ++i) {
         more = u.next(a, sh->share, cta);
-        wait(&sh->segfree[i % SEGS], (i / SEGS + 1) & 1, &sh->fail);
+        if (!wait_long(&sh->segfree[i % SEGS], (i / SEGS + 1) & 1, &sh->fail)) return;  // it may still be read
+        more = more && !failed(sh);
         Seg* s = &sh->seg[i % SEGS];
         *s = more ? Seg{u.b, u.h, u.qb, u.t0, u.t1, u.nt, u.rows, u.r.len, u.r.n, u.r.ctx, u.first, u.segs} : Seg{-1};
         dt_mbar_arrive(&sh->segfull[i % SEGS]);
         if (more) u.step(a);
     }
 }
-// Segment i of the share, or null after the last one.  Every thread of a role
-// gets each segment and releases it when it has read what it needs.
+// Segment i of the share, or null after the last one.  Every thread of a role gets each
+// segment and releases it when it has read what it needs.  The threads of a role wait for
+// each other within a segment, so all have to come to one answer whatever has run out: it
+// depends on what the walk has published alone.
 DT_DI const Seg* get_segment(Shared* sh, uint32_t i) {
-    wait(&sh->segfull[i % SEGS], (i / SEGS) & 1, &sh->fail);
+    const bool there = wait_long(&sh->segfull[i % SEGS], (i / SEGS) & 1, &sh->fail);
     const Seg* s = &sh->seg[i % SEGS];
-    return sh->fail || s->b < 0 ? nullptr : s;
+    return !there || s->b < 0 ? nullptr : s;
 }
 DT_DI void release_segment(Shared* sh, uint32_t i) { dt_mbar_arrive(&sh->segfree[i % SEGS]); }
 
@@ -566,6 +589,11 @@ DT_DI void issue_slot(unsigned char* sm, Shared* sh, uint32_t tmem, int s) {
         }
         g0 += nt;
     }
+    if (el && failed(sh)) {  // otherwise the softmax warps have waited for every product
+        dt_mma_commit(&sh->drain[s]);
+        wait(&sh->drain[s], 0, &sh->drain_fail[s]);
+    }
+    __syncwarp();
 }
 
 // A slot's softmax: 128 threads, one per row.
@@ -1156,7 +1184,8 @@ struct Soft {
 };
 
 template <int D>
-__global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtAttend a, float* part, int* counters) {
+__global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtAttend a, float* part, int* counters,
+                                                          long long probe) {
     using L = Lay<D>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -1185,9 +1214,13 @@ __global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtA
             dt_mbar_init(&sh->segfree[i], NS + 2 * NC + 2 + 32);
         }
         dt_mbar_init(&sh->qfull, NS);
+        dt_mbar_init(&sh->drain[0], 1);
+        dt_mbar_init(&sh->drain[1], 1);
+        dt_mbar_init(&sh->probe, 1);
         dt_fence_mbar_init();
-        sh->fail = 0;
+        sh->fail = sh->drain_fail[0] = sh->drain_fail[1] = 0;
     }
+    if (tid < RING * 8) sh->ring[tid >> 3].id[tid & 7] = 0;  // a page for whoever gives up waiting for one
     dt_pdl_trigger();
     dt_pdl_wait();
     if (wid == 1) at_share<ROWS>(a, cta, ctas, MIN_SHARE, &sh->share);
@@ -1208,10 +1241,15 @@ __global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtA
         if (wid == W0 || wid == W0 + 3)
             issue_slot<D>(sm, sh, __shfl_sync(0xffffffffu, tmem, 0), __shfl_sync(0xffffffffu, wid != W0, 0));
         if (tid == NS + 2 * NC + 32) walk_share(a, sh, cta);
-        if (wid == W0 + 2) look_up<D>(a, sh, tid & 31);
+        if (wid == W0 + 2) {
+            if ((tid & 31) == 0 && !dt_probe_wait(&sh->probe, probe)) sh->fail = 1;
+            __syncwarp();
+            look_up<D>(a, sh, tid & 31);
+        }
     }
     dt_tc_fence_before();
     __syncthreads();
+    // The outputs are undefined then, and so are the counters in the workspace.
     if (tid == 0 && sh->fail)
         for (int b = 0; b < a.batch; ++b) atomicOr(&a.status[b], DT_DEV_TIMEOUT);
     if (wid == 0) {
@@ -1219,6 +1257,9 @@ __global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtA
         dt_tmem_dealloc(tmem, 512);
     }
 }
+
+// Probe budget of the timeout path's test hook (0: off) in the calls made from now on.
+std::atomic<long long> g_probe{0};
 
 template <int D>
 cudaError_t launch(const DtAttend& a, void* workspace, int ctas, cudaStream_t st) {
@@ -1231,10 +1272,12 @@ cudaError_t launch(const DtAttend& a, void* workspace, int ctas, cudaStream_t st
     if (e != cudaSuccess) return e;
     DtLaunch lc(dim3(ctas), dim3(NT), ask, st);
     return cudaLaunchKernelEx(&lc.cfg, kn12_kernel<D>, a, (float*)((char*)workspace + AT_MAX_CTAS * sizeof(int)),
-                              (int*)workspace);
+                              (int*)workspace, g_probe.load(std::memory_order_relaxed));
 }
 
 }  // namespace
+
+void dt_kn12_set_probe(long long budget) { g_probe.store(budget, std::memory_order_relaxed); }
 
 size_t dt_kn12_workspace(int D, int ctas) {
     return AT_MAX_CTAS * sizeof(int) + (size_t)ctas * 2 * ROWS * (D + 2) * sizeof(float);

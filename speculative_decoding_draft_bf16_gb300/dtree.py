@@ -131,7 +131,7 @@ def lib():
     return _LIB
 
 
-PROBE = {"stage1": 0x1, "walk": 0x2, "normaliser": 0x4}
+PROBE = {"stage1": 0x1, "walk": 0x2, "normaliser": 0x4, "attention": 0x10}
 
 
 def set_test_wait_fault(kernels=(), budget_cycles=2_000_000):
