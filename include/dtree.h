@@ -484,9 +484,12 @@ dt_status dt_select_dartree_noalloc(const dt_build_params* p, dt_tree* tree, dt_
  * key head), for keys and values apart: an element is code * scale.  dt_kv_append
  * writes scales that are powers of two: e4m3 is a floating format, so a finer
  * scale would buy no precision, and a block whose scale grows is rescaled
- * exactly (outside e4m3's subnormals).  dt_tree_attention takes any positive
- * finite scale.  A scale that is NaN stands for a block that holds a value that
- * is not finite: every row that attends to it becomes NaN. */
+ * exactly (outside e4m3's subnormals).  dt_tree_attention takes scales that are
+ * powers of two or not: of keys any positive normal number, of values 2^-100 to
+ * 2^120, those that one row attends to up to 2^96 apart (a new row's is its
+ * largest magnitude, from 2^-57 on); further apart, tokens with the smaller
+ * ones may lose their weight.  A scale that is NaN stands for a block that
+ * holds a value that is not finite: every row that attends to it becomes NaN. */
 typedef struct {
     int32_t n_pages;      /* physical pages */
     int32_t page;         /* tokens per page: 16, 32, 64 or 128 */

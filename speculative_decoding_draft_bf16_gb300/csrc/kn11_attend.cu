@@ -18,9 +18,10 @@
 // 16 rows (64 requests, contexts to 16000), 31.6 against 22.9 for one request over 4000.
 // With the rows on the side of 16, single tokens paid for 12 idle rows in MMAs and
 // exponentials, a third of all instructions: 276 us instead of 233.
-//   Scales: P holds 2^(t + log2 vs - m) for scores t in base 2, the row sum adds p / vs,
-// and m moves only when the maximum has grown by more than 8.  The warps' sums are joined
-// in shared memory, the CTAs' in the workspace.
+//   Scales: P holds 2^(t + log2 vs - m) for scores t in base 2, the row sum adds p / vs
+// (value scales from 2^-100 on, or the sum leaves fp32), and m moves only when the maximum
+// has grown by more than 8.  The warps' sums are joined in shared memory, the CTAs' in the
+// workspace.
 //
 // 64 single tokens, 32 heads on 8, over contexts of 1001 to 16384 (1.14 GB): 228 us, 5.0
 // TB/s (74% of a copy's rate).  Equal shares end between 165 and 228 us, by where on the

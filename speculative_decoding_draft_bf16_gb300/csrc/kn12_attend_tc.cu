@@ -244,7 +244,7 @@ DT_DI void store_codes(uint32_t a0, uint32_t a1, const uint4& q) {
     sts16(a1, w);
 }
 
-// log2 of a positive normal number, and its inverse: exact for powers of two.
+// log2 of a value scale (2^-100 to 2^120), and its inverse: exact for powers of two.
 DT_DI void scale_parts(float s, float& lg, float& inv) {
     lg = log2f(s);
     inv = 1.0f / s;
