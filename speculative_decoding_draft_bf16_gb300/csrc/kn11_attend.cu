@@ -23,10 +23,11 @@
 // has grown by more than 8.  The warps' sums are joined in shared memory, the CTAs' in the
 // workspace.
 //
-// 64 single tokens, 32 heads on 8, over contexts of 1001 to 16384 (1.14 GB): 228 us, 5.0
-// TB/s (74% of a copy's rate).  Equal shares end between 165 and 228 us, by where on the
-// chip an SM lies: that spread, not the loop, is what is left.  One token over 1000: 15.6
-// us, the latency of the share, pages, copies, new row and join in turn.
+// On the device (calls in a graph): 64 single tokens, 32 heads on 8, over contexts of 1001
+// to 16384 (1.14 GB) 228 to 231 us, 4.9 TB/s (73% of a copy's rate).  Equal shares end
+// between 165 and 228 us, by where on the chip an SM lies: that spread, not the loop, is
+// what is left.  One token over 1000: 15.9 us, the latency of the share, pages, copies, new
+// row and join in turn (15.6 before each new row had a scale of its own).
 #include "dt_attend.cuh"
 
 namespace {

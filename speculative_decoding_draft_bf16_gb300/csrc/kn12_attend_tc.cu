@@ -34,11 +34,12 @@
 // 1300 to 1500 clocks for 64 elements of 32 rows, in which two softmax and two converter
 // warps share an SM quarter's issue slots, and the slots' chains (scores, softmax,
 // products) overlap but do not fill each other's gaps.  Sixteen trees of 257 nodes, 64
-// heads on 8, contexts of 5000 to 16384: 1.10 ms, 1.01 PFLOP/s (52% of the measured bf16
+// heads on 8, contexts of 5000 to 16384: 1.12 ms, 0.98 PFLOP/s (51% of the measured bf16
 // rate).  Scores of a whole tile at a time (fewer, wider MMAs, but a slot's softmax then
-// waits for all of them): 1.27 ms.  Short contexts are bound by what a unit costs beside
-// its tiles, in thousands of clocks: queries (8), outputs (3 to 5), joins (5 to 15), and
-// tiles of new rows, which take 9 (cached ones 4).
+// waits for all of them): 1.27 ms against 1.10 then.  Short contexts are bound by what a
+// unit costs beside its tiles, in thousands of clocks: queries (8), outputs (3 to 5), joins
+// (5 to 15), and tiles of new rows, which take 9 in trees and 20 in prompts (cached ones
+// 4): one prompt of 4000 rows over an empty cache, 32 heads on 8, 542 us (13% of the rate).
 // Code size matters as much: with unrolled tiles the roles' loops overflowed the
 // instruction caches (one tree of 257 nodes 125 us instead of 99).
 #include <atomic>

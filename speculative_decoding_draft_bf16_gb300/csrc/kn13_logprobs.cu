@@ -16,11 +16,15 @@
 // when the list is cut back to its best; a round that overflows the list is read
 // again with a higher bound.
 //
-// Many rows are bound by instruction issue and HBM together: 7.5 instructions per bf16
-// element, one of them the exponential.  4000 rows of 151936 bf16 logits with the
-// best alternative: 234 us, 5.2 TB/s (77% of a copy's rate); ten CTAs of 128 threads
-// on an SM (eight: 242 us; twelve spill: 276).  Few rows are bound by the latency of
-// their phases: one path of 17 rows 12 us, 16 paths of 17 fp32 rows 18 us.
+// Rows whose largest logit is so large that only ties with it have a weight count those
+// instead (see FLAT).
+//
+// Many rows are bound by instruction issue and HBM together: 10 instructions per bf16
+// element, one of them the exponential; with 1, 5, 20 alternatives 11.3, 11.9, 14.1.  4000
+// rows of 151936 bf16 logits with the best alternative: 237 us, 5.1 TB/s (76% of a copy's
+// rate), fp32 401 us, 6.1 TB/s (89%); ten CTAs of 128 threads on an SM (eight: 242 us
+// against 234 then; twelve spill: 276).  Few rows are bound by the latency of their phases,
+// on the device: one path of 17 rows 12.8 us, 16 paths of 17 fp32 rows 18.3 us.
 #include <type_traits>
 
 #include "dt_device.cuh"

@@ -8,7 +8,7 @@ from test_gpu_attention import make_cache
 
 pytestmark = pytest.mark.gpu
 
-CLOCKS = 100_000_000  # some 50 ms
+CLOCKS = 200_000_000  # some 100 ms
 
 
 @pytest.fixture(autouse=True)
