@@ -505,6 +505,29 @@ typedef struct {
                              j % page of its logical page j / page */
 } dt_kv_cache;
 
+/* The same context in 4 bits: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign)
+ * with a scale for each 16 neighbouring elements of a token's head, 4.5 bits for an
+ * element in all.  Element 2i lies in the lower four bits of byte i, element 2i + 1
+ * in the upper ones.  A scale byte holds five exponent bits (bias 15) and three of
+ * the fraction, the upper half of an fp16 number without its sign: bytes 1 to 226
+ * stand for 2^-17 to 10240, so that a code times its scale is exact in fp16; 0
+ * stands for zeros; 255 for a block that holds a value that is not finite: its 16
+ * elements are NaN, and so is every row that attends to it.  Other bytes are not
+ * written, and may not be there.  Rows do not depend on each other. */
+typedef struct {
+    int32_t n_pages;      /* physical pages */
+    int32_t page;         /* tokens per page: 16, 32, 64 or 128 */
+    int32_t Hkv;          /* key heads */
+    int32_t D;            /* head size: 64 or 128 */
+    int32_t max_pages;    /* columns of the page table */
+    uint8_t* k;           /* [n_pages][Hkv][page][D / 2] codes of the rotated keys; 16-byte aligned */
+    uint8_t* v;           /* the same for values */
+    uint8_t* k_scale;     /* [n_pages][Hkv][page][D / 16] scale bytes; 16-byte aligned */
+    uint8_t* v_scale;     /* the same for values */
+    const int32_t* table; /* as in dt_kv_cache */
+    const int32_t* len;
+} dt_kv_cache4;
+
 /* Position rotation: pair (a, b) of a head's first `rot` elements becomes
  * (a cos - b sin, b cos + a sin) with entry [position][i] of the tables; pairs
  * are (x[i], x[i + rot/2]), or (x[2i], x[2i+1]) when interleaved. */
@@ -551,6 +574,57 @@ dt_status dt_kv_append(const dt_kv_cache* c, const dt_rope* rope, int32_t batch,
                        const dt_rows* k, const dt_rows* v, const int32_t* rows, int32_t N, const int32_t* count,
                        int32_t count_add, int32_t* len_out, int32_t* status, dt_stream_t stream);
 
+/* The same for a 4-bit cache.  The scale of 16 elements is the smallest one, from 2^-17
+ * to 10240, that their largest magnitude is at most 6 times; codes are the rotated
+ * fp32 values over the scale, to the nearest number of e2m1, ties to the even code,
+ * at most 6; the sign of a zero stays.  Older tokens keep their codes. */
+dt_status dt_kv_append4(const dt_kv_cache4* c, const dt_rope* rope, int32_t batch, int32_t M, int32_t dtype,
+                        const dt_rows* k, const dt_rows* v, const int32_t* rows, int32_t N, const int32_t* count,
+                        int32_t count_add, int32_t* len_out, int32_t* status, dt_stream_t stream);
+
+/* Reads tokens back out of a cache, for a drafter that works on the target's keys and
+ * values, or to move a request: row j < n_b of request b of k and v becomes token
+ * rows[b][j], or start[b] + j when rows is NULL.
+ *   k, v: outputs [batch][N][Hkv][D] in dtype (DT_BF16 or DT_F32); code times scale in fp32,
+ *         then in dtype (exact from 4 bits); rows from n_b on are left alone.  Keys come as
+ *         they are held, rotated.
+ *   rows: NULL or [batch][N] token numbers in [0, len[b]), in any order and any number of
+ *         times; entries from n_b on are not read.
+ *   start: NULL (0) or [batch]; NULL when there are rows.
+ *   count: n_b = count[b] + count_add, in [0, N]; NULL: n_b = N with rows, and all of
+ *         the rest, len[b] - start[b], without (count_add is ignored).
+ * A request whose len, start or count is out of range is left alone; a row number or a page
+ * out of range makes its row zeros; both set DT_DEV_BAD_CACHE in status[b] (OR-ed). */
+dt_status dt_kv_read(const dt_kv_cache* c, int32_t batch, const int32_t* rows, int32_t N, const int32_t* start,
+                     const int32_t* count, int32_t count_add, int32_t dtype, const dt_rows* k, const dt_rows* v,
+                     int32_t* status, dt_stream_t stream);
+dt_status dt_kv_read4(const dt_kv_cache4* c, int32_t batch, const int32_t* rows, int32_t N, const int32_t* start,
+                      const int32_t* count, int32_t count_add, int32_t dtype, const dt_rows* k, const dt_rows* v,
+                      int32_t* status, dt_stream_t stream);
+
+/* Root-mean-square norms of query and key heads, for models that normalise each head
+ * before its rotation, with the rotation in the same pass:
+ *   y = R(x / sqrt(mean(x^2) + eps) * w), the mean over a head's D elements (64 or 128).
+ * Row n < n_nodes[b] of request b has position len[b] + pos[b][n]; tree attention and
+ * append then take the outputs without a rotation of their own.
+ *   q: [batch][M][Hq][D], k: [batch][M][Hk][D] in dtype (DT_BF16 or DT_F32); Hq or Hk may
+ *      be 0 (its pointers are not read then).
+ *   q_weight, k_weight: NULL (ones), or fp32, 16-byte aligned: [D] with stride 0, or
+ *      [heads][D] with stride D.
+ *   rope: NULL: no rotation.  len: NULL (0) or [batch]; pos: NULL (n) or [batch][M];
+ *   n_nodes: NULL (M) or [batch] in [0, M].
+ *   q_out, k_out: as q and k; may be q and k themselves.  Rows from n_nodes[b] on are left
+ *      alone.
+ * Everything is fp32 up to the one rounding at the end.  A row with a value that is not
+ * finite becomes NaN where that value takes part.  A request with n_nodes out of range, and
+ * a row with its position outside the tables, is left alone and sets DT_DEV_BAD_CACHE in
+ * status[b] (OR-ed). */
+dt_status dt_qk_norm(int32_t batch, int32_t M, int32_t Hq, int32_t Hk, int32_t D, int32_t dtype, const dt_rows* q,
+                     const dt_rows* k, const float* q_weight, int32_t q_weight_stride, const float* k_weight,
+                     int32_t k_weight_stride, float eps, const dt_rope* rope, const int32_t* len, const int32_t* pos,
+                     const int32_t* n_nodes, const dt_rows* q_out, const dt_rows* k_out, int32_t* status,
+                     dt_stream_t stream);
+
 /* Attention of a tree's rows over the cached context and the tree itself.
  * Row n < n_nodes[b] of query head h (key head h / (Hq / Hkv)) has position
  * len[b] + pos[b][n]; it sees every cached token j < len[b] and those new rows
@@ -584,6 +658,14 @@ dt_status dt_tree_attention(const dt_kv_cache* c, const dt_rope* rope, int32_t b
                             const dt_rows* q, const dt_rows* k, const dt_rows* v, const uint32_t* mask,
                             const int32_t* pos, const int32_t* n_nodes, float scale, void* out, void* workspace,
                             size_t workspace_bytes, int32_t* status, dt_stream_t stream);
+
+/* The same over a 4-bit cache (codes times scales are exact in fp16, too); new values
+ * below 2^-24 may count as zero.  A workspace serves calls of both kinds. */
+size_t dt_tree_attention4_workspace(const dt_kv_cache4* c, int32_t batch, int32_t M, int32_t Hq);
+dt_status dt_tree_attention4(const dt_kv_cache4* c, const dt_rope* rope, int32_t batch, int32_t M, int32_t Hq,
+                             const dt_rows* q, const dt_rows* k, const dt_rows* v, const uint32_t* mask,
+                             const int32_t* pos, const int32_t* n_nodes, float scale, void* out, void* workspace,
+                             size_t workspace_bytes, int32_t* status, dt_stream_t stream);
 
 /* Log-probabilities of given tokens ([Unit11] temperature 1), with the rank of
  * the token, the entropy of the row and its best alternatives.

@@ -1,5 +1,5 @@
-// dt_abi_target.cu -- C ABI of the target-side calls: the paged cache, tree
-// attention and token log-probabilities (include/dtree.h).  Argument checks only.
+// dt_abi_target.cu -- C ABI of the target-side calls: the paged caches, tree
+// attention, head norms and token log-probabilities (include/dtree.h).  Argument checks only.
 #include <cmath>
 
 #include <cuda_runtime.h>
@@ -46,6 +46,14 @@ dt_status check_cache(const dt_kv_cache* c, int32_t batch) {
     return DT_OK;
 }
 
+dt_status check_cache(const dt_kv_cache4* c, int32_t batch) {
+    if (!c) return DT_ERR_INVALID_ARG;
+    const dt_kv_cache f = dt_cache_of(*c);
+    const dt_status s = check_cache(&f, batch);
+    if (s != DT_OK) return s;
+    return aligned16(c->k_scale) && aligned16(c->v_scale) ? DT_OK : DT_ERR_INVALID_ARG;
+}
+
 dt_status check_rope(const dt_rope* r, int32_t D) {
     if (!r) return DT_OK;
     if (r->rot < 16 || r->rot > D || (r->rot & 15) || r->max_pos < 1) return DT_ERR_INVALID_ARG;
@@ -62,13 +70,12 @@ bool rows_ok(const dt_rows* r, int esize) {
     return true;
 }
 
-}  // namespace
+const dt_rope kNoRope = {nullptr, nullptr, 0, 0, 0};
 
-extern "C" {
-
-dt_status dt_kv_append(const dt_kv_cache* c, const dt_rope* rope, int32_t batch, int32_t M, int32_t dtype,
-                       const dt_rows* k, const dt_rows* v, const int32_t* rows, int32_t N, const int32_t* count,
-                       int32_t count_add, int32_t* len_out, int32_t* status, dt_stream_t stream) {
+template <typename C, typename F>
+dt_status append(const C* c, F launch, const dt_rope* rope, int32_t batch, int32_t M, int32_t dtype, const dt_rows* k,
+                 const dt_rows* v, const int32_t* rows, int32_t N, const int32_t* count, int32_t count_add,
+                 int32_t* len_out, int32_t* status, dt_stream_t stream) {
     dt_status s = check_cache(c, batch);
     if (s != DT_OK) return s;
     if ((s = check_rope(rope, c->D)) != DT_OK) return s;
@@ -78,12 +85,81 @@ dt_status dt_kv_append(const dt_kv_cache* c, const dt_rope* rope, int32_t batch,
     if (N > (1 << 30)) return DT_ERR_UNSUPPORTED;
     if (count && (count_add < -(1 << 30) || count_add > (1 << 30))) return DT_ERR_INVALID_ARG;
     if (!status || len_out == c->len) return DT_ERR_INVALID_ARG;
-    const dt_rope none = {nullptr, nullptr, 0, 0, 0};
-    return cuda_status(dt_kn10_launch(*c, rope ? *rope : none, batch, M, dtype, *k, *v, rows, N, count, count_add,
-                                      len_out, status, (cudaStream_t)stream));
+    return cuda_status(launch(*c, rope ? *rope : kNoRope, batch, M, dtype, *k, *v, rows, N, count, count_add, len_out,
+                              status, (cudaStream_t)stream));
+}
+
+dt_status attend(const dt_kv_cache& c, int bits, const dt_rope* rope, int32_t batch, int32_t M, int32_t Hq,
+                 const dt_rows* q, const dt_rows* k, const dt_rows* v, const uint32_t* mask, const int32_t* pos,
+                 const int32_t* n_nodes, float scale, void* out, void* workspace, size_t workspace_bytes, int32_t* status,
+                 dt_stream_t stream) {
+    const dt_status s = check_rope(rope, c.D);
+    if (s != DT_OK) return s;
+    if (M < 1 || Hq < 1 || Hq % c.Hkv != 0) return DT_ERR_INVALID_ARG;
+    if (Hq / c.Hkv > 128 || Hq > 65535 || M > (1 << 20)) return DT_ERR_UNSUPPORTED;
+    // the work division counts tiles in 32 bits
+    const long long rows = (long long)M * (Hq / c.Hkv);
+    const double tiles = (double)c.max_pages * c.page / 128 + M / 128 + 2;
+    if ((double)batch * c.Hkv * (rows / 256 + 1) * tiles * 5 > 4.2e9) return DT_ERR_UNSUPPORTED;
+    if (!rows_ok(q, 2) || !rows_ok(k, 2) || !rows_ok(v, 2)) return DT_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return DT_ERR_INVALID_ARG;
+    if (!out || !aligned16(out) || !status) return DT_ERR_INVALID_ARG;
+    const size_t need = dt_kn12_workspace(c.D, sm_count());
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return DT_ERR_INVALID_ARG;
+    const DtAttend a{c, rope ? *rope : kNoRope, batch, M, Hq, Hq / c.Hkv, *q, *k, *v, mask, pos, n_nodes, scale, out, status};
+    if (rows <= kStreamRows) return cuda_status(dt_kn11_launch(a, bits, workspace, 2 * sm_count(), (cudaStream_t)stream));
+    return cuda_status(dt_kn12_launch(a, bits, workspace, sm_count(), (cudaStream_t)stream));
+}
+
+dt_status read(const dt_kv_cache& c, int bits, int32_t batch, const int32_t* rows, int32_t N, const int32_t* start,
+               const int32_t* count, int32_t count_add, int32_t dtype, const dt_rows* k, const dt_rows* v,
+               int32_t* status, dt_stream_t stream) {
+    if (dtype != DT_BF16 && dtype != DT_F32) return DT_ERR_INVALID_ARG;
+    const int esize = dtype == DT_BF16 ? 2 : 4;
+    if (N < 1 || (rows && start) || !rows_ok(k, esize) || !rows_ok(v, esize) || !status) return DT_ERR_INVALID_ARG;
+    if (N > (1 << 30) || c.Hkv > 32767) return DT_ERR_UNSUPPORTED;
+    if (count && (count_add < -(1 << 30) || count_add > (1 << 30))) return DT_ERR_INVALID_ARG;
+    return cuda_status(dt_kn15_launch(c, bits, batch, rows, N, start, count, count_add, dtype, *k, *v, status,
+                                      (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+dt_status dt_kv_append(const dt_kv_cache* c, const dt_rope* rope, int32_t batch, int32_t M, int32_t dtype,
+                       const dt_rows* k, const dt_rows* v, const int32_t* rows, int32_t N, const int32_t* count,
+                       int32_t count_add, int32_t* len_out, int32_t* status, dt_stream_t stream) {
+    return append(c, dt_kn10_launch, rope, batch, M, dtype, k, v, rows, N, count, count_add, len_out, status, stream);
+}
+
+dt_status dt_kv_append4(const dt_kv_cache4* c, const dt_rope* rope, int32_t batch, int32_t M, int32_t dtype,
+                        const dt_rows* k, const dt_rows* v, const int32_t* rows, int32_t N, const int32_t* count,
+                        int32_t count_add, int32_t* len_out, int32_t* status, dt_stream_t stream) {
+    if (c && c->Hkv > 32767) return DT_ERR_UNSUPPORTED;
+    return append(c, dt_kn14_launch, rope, batch, M, dtype, k, v, rows, N, count, count_add, len_out, status, stream);
+}
+
+dt_status dt_kv_read(const dt_kv_cache* c, int32_t batch, const int32_t* rows, int32_t N, const int32_t* start,
+                     const int32_t* count, int32_t count_add, int32_t dtype, const dt_rows* k, const dt_rows* v,
+                     int32_t* status, dt_stream_t stream) {
+    const dt_status s = check_cache(c, batch);
+    return s != DT_OK ? s : read(*c, 8, batch, rows, N, start, count, count_add, dtype, k, v, status, stream);
+}
+
+dt_status dt_kv_read4(const dt_kv_cache4* c, int32_t batch, const int32_t* rows, int32_t N, const int32_t* start,
+                      const int32_t* count, int32_t count_add, int32_t dtype, const dt_rows* k, const dt_rows* v,
+                      int32_t* status, dt_stream_t stream) {
+    const dt_status s = check_cache(c, batch);
+    return s != DT_OK ? s : read(dt_cache_of(*c), 4, batch, rows, N, start, count, count_add, dtype, k, v, status, stream);
 }
 
 size_t dt_tree_attention_workspace(const dt_kv_cache* c, int32_t batch, int32_t M, int32_t Hq) {
+    if (check_cache(c, batch) != DT_OK || M < 1 || Hq < 1) return 0;
+    return dt_kn12_workspace(c->D, sm_count());
+}
+
+size_t dt_tree_attention4_workspace(const dt_kv_cache4* c, int32_t batch, int32_t M, int32_t Hq) {
     if (check_cache(c, batch) != DT_OK || M < 1 || Hq < 1) return 0;
     return dt_kn12_workspace(c->D, sm_count());
 }
@@ -92,24 +168,44 @@ dt_status dt_tree_attention(const dt_kv_cache* c, const dt_rope* rope, int32_t b
                             const dt_rows* q, const dt_rows* k, const dt_rows* v, const uint32_t* mask,
                             const int32_t* pos, const int32_t* n_nodes, float scale, void* out, void* workspace,
                             size_t workspace_bytes, int32_t* status, dt_stream_t stream) {
-    dt_status s = check_cache(c, batch);
+    const dt_status s = check_cache(c, batch);
     if (s != DT_OK) return s;
-    if ((s = check_rope(rope, c->D)) != DT_OK) return s;
-    if (M < 1 || Hq < 1 || Hq % c->Hkv != 0) return DT_ERR_INVALID_ARG;
-    if (Hq / c->Hkv > 128 || Hq > 65535 || M > (1 << 20)) return DT_ERR_UNSUPPORTED;
-    // the work division counts tiles in 32 bits
-    const long long rows = (long long)M * (Hq / c->Hkv);
-    const double tiles = (double)c->max_pages * c->page / 128 + M / 128 + 2;
-    if ((double)batch * c->Hkv * (rows / 256 + 1) * tiles * 5 > 4.2e9) return DT_ERR_UNSUPPORTED;
-    if (!rows_ok(q, 2) || !rows_ok(k, 2) || !rows_ok(v, 2)) return DT_ERR_INVALID_ARG;
-    if (!(scale > 0.f) || !std::isfinite(scale)) return DT_ERR_INVALID_ARG;
-    if (!out || !aligned16(out) || !status) return DT_ERR_INVALID_ARG;
-    const size_t need = dt_tree_attention_workspace(c, batch, M, Hq);
-    if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return DT_ERR_INVALID_ARG;
-    const dt_rope none = {nullptr, nullptr, 0, 0, 0};
-    const DtAttend a{*c, rope ? *rope : none, batch, M, Hq, Hq / c->Hkv, *q, *k, *v, mask, pos, n_nodes, scale, out, status};
-    if (rows <= kStreamRows) return cuda_status(dt_kn11_launch(a, workspace, 2 * sm_count(), (cudaStream_t)stream));
-    return cuda_status(dt_kn12_launch(a, workspace, sm_count(), (cudaStream_t)stream));
+    return attend(*c, 8, rope, batch, M, Hq, q, k, v, mask, pos, n_nodes, scale, out, workspace, workspace_bytes, status,
+                  stream);
+}
+
+dt_status dt_tree_attention4(const dt_kv_cache4* c, const dt_rope* rope, int32_t batch, int32_t M, int32_t Hq,
+                             const dt_rows* q, const dt_rows* k, const dt_rows* v, const uint32_t* mask,
+                             const int32_t* pos, const int32_t* n_nodes, float scale, void* out, void* workspace,
+                             size_t workspace_bytes, int32_t* status, dt_stream_t stream) {
+    const dt_status s = check_cache(c, batch);
+    if (s != DT_OK) return s;
+    return attend(dt_cache_of(*c), 4, rope, batch, M, Hq, q, k, v, mask, pos, n_nodes, scale, out, workspace,
+                  workspace_bytes, status, stream);
+}
+
+dt_status dt_qk_norm(int32_t batch, int32_t M, int32_t Hq, int32_t Hk, int32_t D, int32_t dtype, const dt_rows* q,
+                     const dt_rows* k, const float* q_weight, int32_t q_weight_stride, const float* k_weight,
+                     int32_t k_weight_stride, float eps, const dt_rope* rope, const int32_t* len, const int32_t* pos,
+                     const int32_t* n_nodes, const dt_rows* q_out, const dt_rows* k_out, int32_t* status,
+                     dt_stream_t stream) {
+    if (batch < 1 || M < 1 || Hq < 0 || Hk < 0 || Hq + (long long)Hk < 1 || D < 1) return DT_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return DT_ERR_UNSUPPORTED;
+    if (batch > 65535 || M > (1 << 20) || Hq > 65535 || Hk > 65535) return DT_ERR_UNSUPPORTED;
+    if (dtype != DT_BF16 && dtype != DT_F32) return DT_ERR_INVALID_ARG;
+    const int esize = dtype == DT_BF16 ? 2 : 4;
+    if (Hq > 0 && (!rows_ok(q, esize) || !rows_ok(q_out, esize))) return DT_ERR_INVALID_ARG;
+    if (Hk > 0 && (!rows_ok(k, esize) || !rows_ok(k_out, esize))) return DT_ERR_INVALID_ARG;
+    if (!aligned16(q_weight) || !aligned16(k_weight)) return DT_ERR_INVALID_ARG;
+    if ((q_weight_stride != 0 && q_weight_stride != D) || (k_weight_stride != 0 && k_weight_stride != D)) return DT_ERR_INVALID_ARG;
+    if (!(eps >= 0.f) || !std::isfinite(eps) || !status) return DT_ERR_INVALID_ARG;
+    const dt_status s = check_rope(rope, D);
+    if (s != DT_OK) return s;
+    const dt_rows none = {nullptr, 0, 0, 0};
+    const DtNorm a{rope ? *rope : kNoRope, batch, M, Hq, Hk, D, dtype, Hq ? *q : none, Hk ? *k : none,
+                   Hq ? *q_out : none, Hk ? *k_out : none, q_weight, k_weight, q_weight_stride, k_weight_stride, eps,
+                   len, pos, n_nodes, status, 0};
+    return cuda_status(dt_kn16_launch(a, (cudaStream_t)stream));
 }
 
 dt_status dt_token_logprobs(const void* logits, int32_t dtype, int32_t batch, int32_t M, int32_t V, int64_t stride_b,

@@ -220,12 +220,18 @@ DT_DI float at_factor(float row, float keys) {
     return f;
 }
 
-// Exponent by which a new row is scaled, from the bits of its largest magnitude: of
-// keys down to where it is a normal number; of values to 2^-57 (what lies below counts
-// as small against 1), so that sums over rows and pages keep their range; a row of
-// zeros, 0.
+// Least exponent by which new rows are scaled: of keys down to where it is a normal
+// number; of values to 2^-57 (what lies below counts as small against 1), so that sums over
+// rows and pages keep their range.  Beside a 4-bit cache to 2^-13: its values have their
+// scales in them (from 2^-18 on), so P does not follow their magnitude, and a new row's P is
+// smaller by its scale.  With 2^-13 equal weights are 2^-8 at least, a normal number of
+// fp16, and values down to 2^-24 keep their bits.
+template <int BITS>
+DT_DI int at_least_exponent(bool keys) { return keys ? -126 : BITS == 4 ? -13 : -57; }
+// Exponent of a row from the bits of its largest magnitude; of a row of zeros, 0.
+template <int BITS>
 DT_DI int at_row_exponent(uint32_t big, bool keys) {
-    return big == 0u ? 0 : min(max((int)(big >> 23) - 127, keys ? -126 : -57), 126);
+    return big == 0u ? 0 : min(max((int)(big >> 23) - 127, at_least_exponent<BITS>(keys)), 126);
 }
 
 // The bits of new rows [m0, m0 + 32) that row `node` sees, rows below n only.

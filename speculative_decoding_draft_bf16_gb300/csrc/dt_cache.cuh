@@ -1,10 +1,13 @@
-// dt_cache.cuh -- device helpers of the paged e4m3 cache and its rotation.
+// dt_cache.cuh -- device helpers of the paged caches (e4m3, e2m1) and their rotation.
 #pragma once
 
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "dt_device.cuh"
+
+// 2^e for -126 <= e <= 127.
+DT_DI float dt_pow2(int e) { return __int_as_float((e + 127) << 23); }
 
 // Eight elements as they are stored.
 template <typename T>
@@ -98,6 +101,10 @@ struct DtPair {
     DT_DI void rotated(int p, const dt_rope& r, float (&x)[8], float (&y)[8]) const {
         a.values(x);
         b.values(y);
+        turn(p, r, x, y);
+    }
+    // The rotation alone.
+    DT_DI void turn(int p, const dt_rope& r, float (&x)[8], float (&y)[8]) const {
         if (16 * p >= r.rot) return;
         float cv[8], sv[8];
         c.values(cv);
@@ -152,5 +159,44 @@ DT_DI uint32_t dt_f32x2_to_e4m3x2(float lo, float hi) {
     return d;
 }
 
-// 2^e for -126 <= e <= 127.
-DT_DI float dt_pow2(int e) { return __int_as_float((e + 127) << 23); }
+// Eight e2m1 codes (elements 2i, 2i + 1 in byte i) as exact fp16 pairs.
+DT_DI void dt_e2m1x8_to_f16x8(uint32_t codes, uint32_t (&h)[4]) {
+    asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(codes));
+}
+// Eight fp32 values to e2m1 (to nearest, ties to even, saturating), the first one lowest.
+DT_DI uint32_t dt_f32x8_to_e2m1x8(const float (&x)[8]) {
+    uint32_t r;
+    asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
+        : "=r"(r)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+    return r;
+}
+// Scale bytes of the 4-bit cache: the upper halves of fp16 numbers without their sign
+// (five exponent bits, three of the fraction).  DT_E5M3_TOP: 10240, the largest one whose
+// sixfold fp16 holds; DT_E5M3_NAN: a block with a value that is not finite.
+constexpr int DT_E5M3_TOP = 226, DT_E5M3_NAN = 255;
+// Scale byte i of a word, twice, as fp16.
+DT_DI uint32_t dt_e5m3_pair(uint32_t bytes, int i) { return __byte_perm(bytes, 0u, i == 0 ? 0x4040 : i == 1 ? 0x4141 : i == 2 ? 0x4242 : 0x4343) << 7; }
+DT_DI uint32_t dt_f16x2_mul(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+DT_DI float dt_e5m3_to_f32(int b) {
+    return __half2float(__ushort_as_half((unsigned short)(b << 7)));
+}
+// The byte of the smallest scale, from 2^-17 to 10240, with top <= 6 * scale; top finite.
+DT_DI int dt_e5m3_for(float top) {
+    // top / 6 from above; below 2^-14 the numbers lie as far apart as from 2^-14 on
+    const float y = __fmul_ru(top, 0.16666667163372039795f);
+    const bool sub = y < dt_pow2(-14);
+    const uint32_t bits = __float_as_uint(sub ? __fadd_ru(y, dt_pow2(-14)) : y);
+    int b = (int)((bits + 0xFFFFFu) >> 20) - (112 << 3) - (sub ? 8 : 0);
+    b = min(b, DT_E5M3_TOP + 1);
+    if (b > 1 && __fmul_rn(dt_e5m3_to_f32(b - 1), 6.f) >= top) --b;
+    return min(max(b, 1), DT_E5M3_TOP);
+}

@@ -174,7 +174,41 @@ cudaError_t dt_kn10_launch(const dt_kv_cache& c, const dt_rope& rope, int batch,
                            const dt_rows& v, const int32_t* rows, int N, const int32_t* count, int count_add,
                            int32_t* len_out, int32_t* status, cudaStream_t st);
 
-// Tree attention over the paged cache (kn11_attend.cu).
+// Appending to the 4-bit cache (kn14_append4.cu).
+cudaError_t dt_kn14_launch(const dt_kv_cache4& c, const dt_rope& rope, int batch, int M, int dtype, const dt_rows& k,
+                           const dt_rows& v, const int32_t* rows, int N, const int32_t* count, int count_add,
+                           int32_t* len_out, int32_t* status, cudaStream_t st);
+
+// A 4-bit cache in the form the kernels of both forms take: k_scale and v_scale then
+// point to its scale bytes.
+inline dt_kv_cache dt_cache_of(const dt_kv_cache4& c) {
+    return dt_kv_cache{c.n_pages, c.page, c.Hkv, c.D, c.max_pages, c.k, c.v, (float*)c.k_scale, (float*)c.v_scale,
+                       c.table, c.len};
+}
+
+// Reading back tokens (kn15_read.cu); bits: 4 or 8.
+cudaError_t dt_kn15_launch(const dt_kv_cache& c, int bits, int batch, const int32_t* rows, int N, const int32_t* start,
+                           const int32_t* count, int count_add, int dtype, const dt_rows& k, const dt_rows& v,
+                           int32_t* status, cudaStream_t st);
+
+// Norms of query and key heads (kn16_qk_norm.cu).
+struct DtNorm {
+    dt_rope rope;  // rot = 0: none
+    int batch, M, Hq, Hk, D, dtype;
+    dt_rows q, k, q_out, k_out;
+    const float* q_weight;  // or NULL
+    const float* k_weight;
+    int q_weight_stride, k_weight_stride;  // elements between heads
+    float eps;
+    const int32_t* len;  // or NULL
+    const int32_t* pos;
+    const int32_t* n_nodes;
+    int32_t* status;
+    int parts;  // warps that share a token (set by the launch)
+};
+cudaError_t dt_kn16_launch(const DtNorm& a, cudaStream_t st);
+
+// Tree attention over the paged caches (kn11_attend.cu); bits: 8 (e4m3) or 4.
 struct DtAttend {
     dt_kv_cache c;
     dt_rope rope;  // rot = 0: none
@@ -187,12 +221,12 @@ struct DtAttend {
     void* out;
     int32_t* status;
 };
-cudaError_t dt_kn11_launch(const DtAttend& a, void* workspace, int ctas, cudaStream_t st);
+cudaError_t dt_kn11_launch(const DtAttend& a, int bits, void* workspace, int ctas, cudaStream_t st);
 // The same for many rows per key head, on the tensor cores (kn12_attend_tc.cu),
 // with ctas CTAs and dt_kn12_workspace bytes.
 size_t dt_kn12_workspace(int D, int ctas);
 void dt_kn12_set_probe(long long budget);
-cudaError_t dt_kn12_launch(const DtAttend& a, void* workspace, int ctas, cudaStream_t st);
+cudaError_t dt_kn12_launch(const DtAttend& a, int bits, void* workspace, int ctas, cudaStream_t st);
 
 // Log-probabilities of given tokens (kn13_logprobs.cu).
 struct DtLogprobs {

@@ -44,12 +44,14 @@ constexpr float HEADROOM = 5.f, LAZY = 8.f;
 
 // Three tiles in flight of 4 KB to a warp, two CTAs to an SM; three CTAs with two tiles
 // each are slower (246 : 233 us).
-template <int D>
+template <int D, int BITS>
 struct Lay {
-    static constexpr int KC = D / 64;             // 16-byte pieces of a token's keys per lane
-    static constexpr int VB = D / 8;              // bytes of a token's values per lane
-    static constexpr int STAGES = D == 128 ? 3 : 6;
-    static constexpr int KBYTES = 2 * KC * 512, BYTES = KBYTES + 4 * VB * 32;  // per warp and stage
+    static constexpr int KC = D / 64;             // runs of 16 elements of a token's keys per lane
+    static constexpr int VB = D / 8;              // elements of a token's values per lane
+    static constexpr int STAGES = BITS == 4 ? (D == 128 ? 5 : 10) : D == 128 ? 3 : 6;
+    static constexpr int KBYTES = D * 2 * BITS;   // per warp and stage: 16 tokens' codes
+    static constexpr int SCALES = 2 * KBYTES;     // where a stage's scale bytes lie
+    static constexpr int BYTES = SCALES + (BITS == 4 ? 2 * D : 0);
     static constexpr size_t FIFO = (size_t)NW * STAGES * BYTES;
     static constexpr size_t JOIN = (size_t)NW * ROWS * D * 4;
     static constexpr size_t SMEM = FIFO > JOIN ? FIFO : JOIN;
@@ -86,10 +88,21 @@ DT_DI void copy_async(uint32_t dst, const void* src) {
 }
 template <int WORDS>
 DT_DI void lds(uint32_t addr, uint32_t (&w)[WORDS]) {
-    if constexpr (WORDS == 4)
+    if constexpr (WORDS == 1)
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+    else if constexpr (WORDS == 4)
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
     else
         asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+}
+
+// One or two bytes.
+template <int BYTES>
+DT_DI uint32_t lds_bytes(uint32_t addr) {
+    uint32_t v;
+    if constexpr (BYTES == 1) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    else asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // The transpose of an 8 x 8 matrix of 16-bit elements, two of a row to a lane.
@@ -99,9 +112,9 @@ DT_DI uint32_t transposed8x8(uint32_t x) {
     return y;
 }
 
-template <int D, int NR>
+template <int D, int NR, int BITS>
 struct Stream {
-    using L = Lay<D>;
+    using L = Lay<D, BITS>;
     using Walk = AtWalk<ROWS, ATOM>;
     static constexpr int KS = D / 16;  // steps of K Q'
     static constexpr int NV = D / 8;   // columns of a lane in V' P': NV * g + j; two to an MMA
@@ -110,6 +123,10 @@ struct Stream {
     // of rows 2t + e + 8i (g, t: the lane's group of 4 and place in it)
     float rowc[NR][2], m[NR][2], l[NR][2];
     float o[NV / 2][NR][4];  // [j / 2][i][2 * (j % 2) + e]
+
+    // Which run of 16 elements of a head is the j-th of a lane with place t: the ones whose
+    // codes it reads at once.
+    static DT_DI int run_of(int t, int j) { return BITS == 8 ? t + 4 * j : L::KC * t + j; }
 
     // 16 elements from 16 * c of a head vector, rotated.
     static DT_DI void pick16(const uint16_t* row, int c, const dt_rope& r, int at, float (&x)[16]) {
@@ -144,7 +161,7 @@ struct Stream {
                 const int at = a.rope.rot ? at_position(a, u.b, u.r.len, n) : 0;
 #pragma unroll
                 for (int j = 0; j < L::KC; ++j) {
-                    pick16(p, t + 4 * j, a.rope, at, x[j]);
+                    pick16(p, run_of(t, j), a.rope, at, x[j]);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) big = max(big, __float_as_uint(x[j][e]) & 0x7FFFFFFFu);
                 }
@@ -170,7 +187,7 @@ struct Stream {
 
     // Scores of 16 tokens, masked (c[i][2k + e]: token g + 8k, row 2t + e + 8i), to
     // probabilities as the fragments of P'; ks, lv, iv: the 16 tokens', or (T = 2) of
-    // tokens g and g + 8.
+    // tokens g and g + 8.  (T = 1 with constants ones and zeros costs the 4-bit form nothing.)
     template <int T>
     DT_DI void weigh(float (&c)[NR][4], const float (&ks)[T], const float (&lv)[T], const float (&iv)[T], uint32_t (&p)[NR][2]) {
         const float NEG_INF = -__int_as_float(0x7F800000);
@@ -220,6 +237,77 @@ struct Stream {
             }
             p[i][0] = transposed8x8(f16x2(c[i][0], c[i][1]));
             p[i][1] = transposed8x8(f16x2(c[i][2], c[i][3]));
+        }
+    }
+
+    // The same of a 4-bit cache.  The codes' scales go into the fragments: a lane's keys have
+    // KC scales per token, its values one per token, and the products are exact in fp16.
+    DT_DI void tile4(uint32_t st, int lane, int left) {
+        const int g = lane >> 2, t = lane & 3;
+        constexpr int NB = D / 16;  // scales of a token
+        const uint32_t sk = st + L::SCALES, sv = sk + 16 * NB;
+        float c[NR][4] = {};
+        uint32_t w[2][2 * L::KC], ks[2];
+        lds<2 * L::KC>(st + lane * (8 * L::KC), w[0]);
+        lds<2 * L::KC>(st + L::KBYTES / 2 + lane * (8 * L::KC), w[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) ks[i] = lds_bytes<L::KC>(sk + (g + 8 * i) * NB + L::KC * t);
+#pragma unroll
+        for (int j = 0; j < 2 * L::KC; ++j) {  // 8 elements of both tokens
+            uint32_t f[2][4], q[NR][4], h[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t s = dt_e5m3_pair(ks[i], j >> 1);
+                dt_e2m1x8_to_f16x8(w[i][j], h[i]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f[k >> 1][2 * (k & 1) + i] = dt_f16x2_mul(h[i][k], s);
+            }
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                lds<4>(qs + ((j * NR + i) * 32 + lane) * 16, q[i]);
+                mma(c[i], f[0], q[i][0], q[i][1]);
+                mma(c[i], f[1], q[i][2], q[i][3]);
+            }
+        }
+        // values of tokens 2t, 2t + 1, 2t + 8, 2t + 9
+        constexpr int VW = L::VB / 8;
+        uint32_t v[4][VW], vs[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int row = (k & 1) * 8 + t + 4 * (k >> 1);  // where token 2t + k % 2 + 8 (k / 2) lies
+            lds<VW>(st + L::KBYTES + (D == 128 ? row * 64 + ((((g >> 1) ^ (row & 2)) << 4) | ((g & 1) << 3)) : row * 32 + g * 4), v[k]);
+            vs[k] = lds_bytes<1>(sv + (2 * t + (k & 1) + 8 * (k >> 1)) * NB + (D == 128 ? g : g >> 1));
+        }
+        if (left < 16) {
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (g + 8 * (k >> 1) >= left) c[i][k] = -__int_as_float(0x7F800000);
+            }
+            // whatever lies behind the last token counts as zeros
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (2 * t + (k & 1) + 8 * (k >> 1) >= left) vs[k] = 0u;
+        }
+        uint32_t p[NR][2];
+        weigh<1>(c, {1.f}, {0.f}, {1.f}, p);
+        const uint32_t s0 = (vs[0] | vs[1] << 16) << 7, s1 = (vs[2] | vs[3] << 16) << 7;
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+            // columns 2n and 2n + 1 of two tokens in byte n
+            constexpr uint32_t LOW = 0x0F0F0F0Fu;
+            uint32_t e0[4], e1[4], o0[4], o1[4];
+            dt_e2m1x8_to_f16x8((v[0][j] & LOW) | (v[1][j] << 4 & ~LOW), e0);
+            dt_e2m1x8_to_f16x8((v[0][j] >> 4 & LOW) | (v[1][j] & ~LOW), o0);
+            dt_e2m1x8_to_f16x8((v[2][j] & LOW) | (v[3][j] << 4 & ~LOW), e1);
+            dt_e2m1x8_to_f16x8((v[2][j] >> 4 & LOW) | (v[3][j] & ~LOW), o1);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const uint32_t f[4] = {dt_f16x2_mul(e0[n], s0), dt_f16x2_mul(o0[n], s0), dt_f16x2_mul(e1[n], s1), dt_f16x2_mul(o1[n], s1)};
+#pragma unroll
+                for (int i = 0; i < NR; ++i) mma(o[4 * j + n][i], f, p[i][0], p[i][1]);
+            }
         }
     }
 
@@ -320,7 +408,7 @@ struct Stream {
             const int at = a.rope.rot && row < n ? at_position(a, u.b, u.r.len, row) : 0;
 #pragma unroll
             for (int j = 0; j < L::KC; ++j) {
-                if (row < n) pick16(kp + row * a.k.stride_n, t + 4 * j, a.rope, at, k[i][j]);
+                if (row < n) pick16(kp + row * a.k.stride_n, run_of(t, j), a.rope, at, k[i][j]);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const uint32_t w = __float_as_uint(k[i][j][e]) & 0x7FFFFFFFu;
@@ -330,7 +418,7 @@ struct Stream {
             }
             big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            const int ek = at_row_exponent(big, true);
+            const int ek = at_row_exponent<BITS>(big, true);
             ks[i] = dt_pow2(ek), fk[i] = dt_pow2(-ek);
         }
 #pragma unroll
@@ -375,7 +463,7 @@ struct Stream {
             }
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, d));
-            ev[k4] = at_row_exponent(big, false);
+            ev[k4] = at_row_exponent<BITS>(big, false);
             fv[k4] = dt_pow2(-ev[k4]);
         }
         float lv[2], iv[2];  // of rows g, g + 8, which lanes with t = g / 2 hold
@@ -423,10 +511,10 @@ struct Stream {
     }
 };
 
-template <int D, int NR>
+template <int D, int NR, int BITS>
 __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtAttend a, float* part, int* counters) {
-    using L = Lay<D>;
-    using S = Stream<D, NR>;
+    using L = Lay<D, BITS>;
+    using S = Stream<D, NR, BITS>;
     constexpr int NV = S::NV;
     extern __shared__ __align__(128) unsigned char fifo[];
     __shared__ Shared sh;
@@ -441,7 +529,8 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
     __syncthreads();
     const AtShare share = sh.share;
     const int lp = 31 - __clz(a.c.page), low = a.c.page - 1;
-    const uint32_t page_bytes = ((uint32_t)a.c.Hkv << lp) * D;
+    constexpr int ROW = D * BITS / 8;  // bytes of a token
+    const uint32_t page_bytes = ((uint32_t)a.c.Hkv << lp) * ROW;
     const uint32_t my_fifo = dt_smem_addr(fifo) + w * L::STAGES * L::BYTES;
     AtWalk<ROWS, ATOM> u;
     u.start(a, share);
@@ -450,8 +539,8 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
     for (; u.next(a, share, cta); u.step(a)) {
         const int len = u.r.len, cend = min(u.t1, u.r.ctx), n = max(0, cend - u.t0);
         const int* table = a.c.table + (size_t)u.b * a.c.max_pages;
-        const uint8_t* kbase = a.c.k + ((size_t)u.h << lp) * D + t * 16;
-        const uint8_t* vbase = a.c.v + ((size_t)u.h << lp) * D + g * L::VB;
+        const uint8_t* kbase = a.c.k + ((size_t)u.h << lp) * ROW + (BITS == 8 ? t * 16 : 0);
+        const uint8_t* vbase = a.c.v + ((size_t)u.h << lp) * ROW + (BITS == 8 ? g * L::VB : 0);
         // Pages and scales of this warp's 16 tokens of 32 tiles at a time, one
         // tile to a lane; the next batch's pages are loaded a batch ahead.
         auto page_at = [&](int i) {  // of tile t0 + i (past the end: of the last token)
@@ -475,15 +564,37 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
             if (issued < n) {
                 if ((issued & 31) == 0 && issued > 0) {
                     id = id_next;
-                    if ((issued >> 5) & 1) scales_of(id, ks[1], vs[1]);
-                    else scales_of(id, ks[0], vs[0]);
+                    if constexpr (BITS == 8) {
+                        if ((issued >> 5) & 1) scales_of(id, ks[1], vs[1]);
+                        else scales_of(id, ks[0], vs[0]);
+                    }
                     id_next = page_at(issued + 32 + lane);
                 }
                 const uint32_t p = __shfl_sync(0xffffffffu, id, issued & 31);
                 const int tok0 = (u.t0 + issued) * AT_TILE + w * 16;
                 const uint32_t st = my_fifo + put * L::BYTES + lane * 16, sv = my_fifo + put * L::BYTES + L::KBYTES + lane * L::VB;
-                const size_t o = (size_t)p * page_bytes + (uint32_t)(tok0 & low) * D;
-                if (tok0 + 16 <= len) {  // 16 tokens lie in one page
+                const size_t o = (size_t)p * page_bytes + (uint32_t)(tok0 & low) * ROW;
+                if constexpr (BITS == 4) {
+                    // the 16 tokens' codes and scales lie in one piece each, whatever of them exists
+                    if (tok0 < len) {
+                        const uint8_t *k = kbase + o + lane * 16, *v = vbase + o + lane * 16;
+                        constexpr int PPT = D / 32;  // 16-byte pieces of a token
+                        const int r = lane / PPT;    // token; even ones lie before odd ones, see tile4
+                        const int at = D == 128 ? ((r & 1) * 8 + (r >> 1)) * 64 + (((lane & 3) ^ (r >> 1 & 2)) << 4)
+                                                : ((r & 1) * 8 + (r >> 1)) * 32 + (lane & 1) * 16;
+                        const uint32_t sv4 = my_fifo + put * L::BYTES + L::KBYTES + at;
+#pragma unroll
+                        for (int i = 0; i < L::KC; ++i) {
+                            copy_async<16>(st + i * 512, k + i * 512);
+                            copy_async<16>(sv4 + i * (8 / 2 * 64), v + i * 512);
+                        }
+                        if (lane < D / 8) {  // D bytes of key scales, then as many of value scales
+                            const uint8_t* s = (const uint8_t*)(lane < D / 16 ? a.c.k_scale : a.c.v_scale) +
+                                               ((size_t)u.h << lp) * (D / 16) + o / 8 + (lane & (D / 16 - 1)) * 16;
+                            copy_async<16>(st + L::SCALES, s);
+                        }
+                    }
+                } else if (tok0 + 16 <= len) {  // 16 tokens lie in one page
                     const uint8_t* k = kbase + o + g * D;
                     const uint8_t* v = vbase + o + 2 * t * D;
 #pragma unroll
@@ -513,7 +624,7 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
         if (n > 0) {
             id = page_at(lane);
             id_next = page_at(32 + lane);
-            scales_of(id, ks[0], vs[0]);
+            if constexpr (BITS == 8) scales_of(id, ks[0], vs[0]);
         }
         for (int i = 0; i < L::STAGES - 1; ++i) issue();
         x.queries(a, u, lane);
@@ -525,6 +636,14 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
         for (int i = 0; i < n; ++i) {
             issue();
             asm volatile("cp.async.wait_group %0;" ::"n"(L::STAGES - 1) : "memory");
+            const int left = len - (u.t0 + i) * AT_TILE - w * 16, at = my_fifo + slot * L::BYTES;
+            slot = slot + 1 == L::STAGES ? 0 : slot + 1;
+            if constexpr (BITS == 4) {
+                __syncwarp();  // lanes read what others have copied
+                if (left > 0) x.tile4(at, lane, left);
+                __syncwarp();  // before the next copies there
+                continue;
+            }
             const bool odd = (i >> 5) & 1;
             if ((i & 31) == 0) {
                 const float v = odd ? vs[1] : vs[0];
@@ -533,9 +652,7 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
             }
             const float k = __shfl_sync(0xffffffffu, odd ? ks[1] : ks[0], i & 31);
             const float v = __shfl_sync(0xffffffffu, lv, i & 31), r = __shfl_sync(0xffffffffu, iv, i & 31);
-            const int left = len - (u.t0 + i) * AT_TILE - w * 16;
-            if (left > 0) x.tile(my_fifo + slot * L::BYTES, lane, left, k, v, r);
-            slot = slot + 1 == L::STAGES ? 0 : slot + 1;
+            if (left > 0) x.tile(at, lane, left, k, v, r);
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
 
@@ -646,20 +763,22 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
     }
 }
 
-template <int D, int NR>
+template <int D, int NR, int BITS>
 cudaError_t launch(const DtAttend& a, void* workspace, int ctas, cudaStream_t st) {
-    constexpr size_t smem = Lay<D>::SMEM;
+    constexpr size_t smem = Lay<D, BITS>::SMEM;
     static_assert(2 * (smem + sizeof(Shared) + 4096 + 1024) <= 228 * 1024, "two CTAs per SM");
-    cudaError_t e = cudaFuncSetAttribute(kn11_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kn11_kernel<D, NR, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     DtLaunch lc(dim3(ctas), dim3(NT), smem, st);
-    return cudaLaunchKernelEx(&lc.cfg, kn11_kernel<D, NR>, a, (float*)((char*)workspace + AT_MAX_CTAS * sizeof(int)),
+    return cudaLaunchKernelEx(&lc.cfg, kn11_kernel<D, NR, BITS>, a, (float*)((char*)workspace + AT_MAX_CTAS * sizeof(int)),
                               (int*)workspace);
 }
 
 }  // namespace
 
-cudaError_t dt_kn11_launch(const DtAttend& a, void* workspace, int ctas, cudaStream_t st) {
-    if (a.M * a.G <= 8) return a.c.D == 64 ? launch<64, 1>(a, workspace, ctas, st) : launch<128, 1>(a, workspace, ctas, st);
-    return a.c.D == 64 ? launch<64, 2>(a, workspace, ctas, st) : launch<128, 2>(a, workspace, ctas, st);
+cudaError_t dt_kn11_launch(const DtAttend& a, int bits, void* workspace, int ctas, cudaStream_t st) {
+    const bool narrow = a.M * a.G <= 8;
+    auto f = bits == 4 ? (a.c.D == 64 ? (narrow ? launch<64, 1, 4> : launch<64, 2, 4>) : (narrow ? launch<128, 1, 4> : launch<128, 2, 4>))
+                       : (a.c.D == 64 ? (narrow ? launch<64, 1, 8> : launch<64, 2, 8>) : (narrow ? launch<128, 1, 8> : launch<128, 2, 8>));
+    return f(a, workspace, ctas, st);
 }

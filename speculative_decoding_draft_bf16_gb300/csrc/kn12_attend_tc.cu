@@ -3,10 +3,10 @@
 //
 // A CTA works on a block of up to 256 query rows (two slots of 128, the rows of
 // an MMA) and a run of 128-token tiles:
-//   converter warps  read e4m3 codes (or new rows, which they rotate) into
-//                    registers and write exact fp16 tiles, 128-byte swizzled, to
-//                    shared memory: keys K-major, values MN-major -- the same
-//                    physical layout, so neither is transposed;
+//   converter warps  read e4m3 codes, or e2m1 codes and their scales (or new rows, which
+//                    they rotate) into registers and write exact fp16 tiles, 128-byte
+//                    swizzled, to shared memory: keys K-major, values MN-major -- the
+//                    same physical layout, so neither is transposed;
 //   MMA warp         S = Q K^T (128 x 128 per slot) and O += P V, accumulators
 //                    in tensor memory, P read from tensor memory;
 //   softmax warps    one thread per row: row maximum, exponentials, P in fp16
@@ -15,7 +15,8 @@
 // most 128 rows puts the same rows in both slots, which then take every other
 // tile and are joined at the end.
 //
-// Scales.  A tile has a key scale ks and a value scale vs for each 16 tokens.
+// Scales.  An e4m3 tile has a key scale ks and a value scale vs for each 16 tokens (those
+// of e2m1 codes go into the fp16 tiles, and these are 1 then).
 // Scores in base 2 are t = s * (row factor * ks); P holds p = 2^(t + log2 vs - m),
 // so the products need no scaling, and the row sum adds p / vs.  m is the running
 // maximum of t + log2 vs less 5 (fp16 then resolves probabilities down to 2^-29 of
@@ -226,6 +227,12 @@ DT_DI uint4 ldg16(const void* p) {
     return v;
 }
 
+DT_DI uint32_t ldg2(const void* p) {
+    uint16_t v;
+    asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // Byte offset of the 16-byte chunk c (8 fp16) of row r in a tile of D columns.
 DT_DI uint32_t chunk_at(int r, int c) {
     return (uint32_t)((c >> 3) * (AT_TILE * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
@@ -252,20 +259,43 @@ DT_DI void scale_parts(float s, float& lg, float& inv) {
     inv = 1.0f / s;
 }
 
+// 32 e2m1 codes and their two scale bytes to four fp16 chunks at a, a ^ 16, a ^ 32 and
+// a ^ 48.  The products are exact.
+DT_DI void store_codes4(uint32_t a, const uint4& q, uint32_t scales) {
+    const uint32_t c[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+        const uint32_t s = dt_e5m3_pair(scales, i >> 1);
+        dt_e2m1x8_to_f16x8(c[i], w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = dt_f16x2_mul(w[k], s);
+        sts16(a ^ (i << 4), w);
+    }
+}
+
 // The converter warps: 128 threads for the keys, 128 for the values, one code (the
 // instruction caches nearest the SM's quarters hold little more than the loops of
-// the roles that run there).
-template <int D>
+// the roles that run there).  BITS: of a code, e4m3 or e2m1.
+template <int D, int BITS>
 struct Conv {
-    // A thread reads 16-byte piece `piece` (of D / 16) of token i * TPI + `tok`
-    // in iteration i.  Four lanes read half a row of 128 columns; eight lanes of
-    // a store phase then hold two tokens, whose chunks swizzle to eight
-    // different 16-byte columns.
-    static constexpr int PPT = D / 16;
-    static constexpr int TPI = NC / PPT;      // tokens per iteration
-    static DT_DI int piece_of(int ct) { return D == 128 ? (ct & 3) + ((ct >> 4) & 1) * 4 : ct & 3; }
-    static DT_DI int tok_of(int ct) { return D == 128 ? ((ct >> 2) & 3) + (ct >> 5) * 4 : ct >> 2; }
+    // A thread reads 16-byte piece `piece` of token i * TPI + `tok` in iteration i:
+    // 16 codes of e4m3 or 32 of e2m1.  Lanes next to each other read half a row of 128
+    // columns; eight lanes of a store phase then hold two or four tokens, whose chunks
+    // swizzle to eight different 16-byte columns.
+    static constexpr int PPR = D / 16;             // chunk pairs of a new row
+    static constexpr int PPT = D * BITS / 128;     // pieces of a token
+    static constexpr int RPI = NC / PPR, TPI = NC / PPT;  // new rows, tokens per iteration
+    static DT_DI int piece_of(int ct) {
+        return BITS == 8 ? (D == 128 ? (ct & 3) + ((ct >> 4) & 1) * 4 : ct & 3)
+                         : (D == 128 ? (ct & 1) + ((ct >> 3) & 1) * 2 : ct & 1);
+    }
+    static DT_DI int tok_of(int ct) {
+        return BITS == 8 ? (D == 128 ? ((ct >> 2) & 3) + (ct >> 5) * 4 : ct >> 2)
+                         : (D == 128 ? ((ct >> 1) & 3) + (ct >> 4) * 4 : ct >> 1);
+    }
     static constexpr int NI = AT_TILE / TPI;  // iterations per tile
+    static constexpr int NF = AT_TILE / RPI;  // the same for new rows
     using L = Lay<D>;
 
     static DT_DI void group_sync(bool keys) {
@@ -294,32 +324,32 @@ struct Conv {
         ap->e[which][ct] = NONE;
         if (keys) sh->kpos[ct] = rope.rot && ct < left ? at_position(a, b, len, m0 + ct) : 0;
         group_sync(keys);
-        const int pr = ct % PPT;  // this thread's chunk pair of rows ct / PPT + i * TPI
+        const int pr = ct % PPR;  // this thread's chunk pair of rows ct / PPR + i * RPI
         int c0, c1;
         dt_pair_chunks(pr, rope, c0, c1);
         constexpr int U = D == 64 ? 2 : 1;  // rows in flight (two at D = 128 make the loop over cached tiles spill)
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {  // the second one when the tile needs scales
 #pragma unroll 1
-            for (int i0 = 0; i0 < NI; i0 += U) {
-                if (i0 * TPI >= left) {  // no row of these: zeros, which a weight of zero leaves zero
+            for (int i0 = 0; i0 < NF; i0 += U) {
+                if (i0 * RPI >= left) {  // no row of these: zeros, which a weight of zero leaves zero
                     const uint32_t zero[4] = {};
 #pragma unroll
                     for (int k = 0; k < U; ++k) {
-                        sts16(tile + chunk_at(ct / PPT + (i0 + k) * TPI, c0), zero);
-                        sts16(tile + chunk_at(ct / PPT + (i0 + k) * TPI, c1), zero);
+                        sts16(tile + chunk_at(ct / PPR + (i0 + k) * RPI, c0), zero);
+                        sts16(tile + chunk_at(ct / PPR + (i0 + k) * RPI, c1), zero);
                     }
                     continue;
                 }
                 DtPair<uint16_t> raw[U];
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
-                    const int r = min(ct / PPT + (i0 + k) * TPI, left - 1);
+                    const int r = min(ct / PPR + (i0 + k) * RPI, left - 1);
                     raw[k].load(p + (m0 + r) * stride, pr, rope, sh->kpos[r]);
                 }
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
-                    const int r = ct / PPT + (i0 + k) * TPI;
+                    const int r = ct / PPR + (i0 + k) * RPI;
                     uint32_t o[4], w[4];
                     float x[8], y[8];
                     raw[k].rotated(pr, rope, x, y);
@@ -348,8 +378,8 @@ struct Conv {
                     sts16(tile + chunk_at(r, c1), w);
                     if (pass == 0) {
 #pragma unroll
-                        for (int d = 1; d < PPT; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        if (pr == 0 && top > 0.f && r < left) ap->e[which][r] = (int8_t)at_row_exponent(__float_as_uint(top), keys);
+                        for (int d = 1; d < PPR; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        if (pr == 0 && top > 0.f && r < left) ap->e[which][r] = (int8_t)at_row_exponent<BITS>(__float_as_uint(top), keys);
                     }
                 }
             }
@@ -361,7 +391,7 @@ struct Conv {
             group_sync(keys);
             for (int i = 0; i < NC / 32; ++i) hi = max(hi, sh->emax[which][i]), lo = min(lo, sh->emin[which][i]);
             const bool apart = hi - lo > 18 && hi != -128;
-            const int e = apart || hi == -128 || (lo >= -4 && hi < 15) ? 0 : max(hi - 14, keys ? -126 : -57);
+            const int e = apart || hi == -128 || (lo >= -4 && hi < 15) ? 0 : max(hi - 14, at_least_exponent<BITS>(keys));
             if (!apart) ap->e[which][ct] = (int8_t)e;
             else if (own == NONE) ap->e[which][ct] = 0;
             if (ct == 0) ap->yes[which] = apart;
@@ -382,27 +412,32 @@ struct Conv {
     static DT_DI void run(const DtAttend& a, unsigned char* sm, Shared* sh, int ct, bool keys) {
         const int lp = 31 - __clz(a.c.page), low = a.c.page - 1;
         const uint32_t base = dt_smem_addr(sm + (keys ? L::K : L::V));
-        const uint32_t a0 = base + chunk_at(tok_of(ct), 2 * piece_of(ct)),
-                       a1 = base + chunk_at(tok_of(ct), 2 * piece_of(ct) + 1);
-        const uint32_t page_bytes = ((uint32_t)a.c.Hkv << lp) * D;
+        const uint32_t a0 = base + chunk_at(tok_of(ct), 16 / BITS * piece_of(ct)),
+                       a1 = a0 ^ 16;
+        constexpr int ROW = D * BITS / 8;  // bytes of a token
+        const uint32_t page_bytes = ((uint32_t)a.c.Hkv << lp) * ROW;
         uint64_t* full = keys ? sh->kfull : sh->vfull;
         uint64_t* free_ = keys ? sh->kfree : sh->vfree;
         uint32_t g = 0, i = 0;  // tiles, segments done
         for (const Seg* sg; (sg = get_segment(sh, i)) != nullptr; release_segment(sh, i++)) {
             const Seg& u = *sg;
             const int t1 = u.t1, cend = min(t1, u.ctx), last = u.len - 1;
-            const uint8_t* codes = (keys ? a.c.k : a.c.v) + (((size_t)u.h << lp) * D + piece_of(ct) * 16);
+            const uint8_t* codes = (keys ? a.c.k : a.c.v) + (((size_t)u.h << lp) * ROW + piece_of(ct) * 16);
+            const uint8_t* scales = (const uint8_t*)(keys ? a.c.k_scale : a.c.v_scale) + (((size_t)u.h << lp) * (D / 16) + piece_of(ct) * 2);
             // The next tile's codes are loaded in two batches, each when this
             // tile's have left its registers.  Page ids come from shared memory:
             // loads that wait for loads would share their scoreboards.  Past len,
             // the last token's.
             uint4 q[NI];
+            uint32_t sc[BITS == 4 ? NI : 1];
             auto load = [&](int j, uint32_t g, int i0) {
                 const Ring* ring = &sh->ring[g % RING];
 #pragma unroll
                 for (int i = i0; i < i0 + NI / 2; ++i) {
                     const int r = tok_of(ct) + i * TPI, tok = min(j * AT_TILE + r, last);
-                    q[i] = ldg16(codes + (size_t)ring->id[r >> 4] * page_bytes + (uint32_t)(tok & low) * D);
+                    q[i] = ldg16(codes + (size_t)ring->id[r >> 4] * page_bytes + (uint32_t)(tok & low) * ROW);
+                    if constexpr (BITS == 4)
+                        sc[i] = ldg2(scales + (size_t)ring->id[r >> 4] * (page_bytes / 8) + (uint32_t)(tok & low) * (D / 16));
                 }
             };
             int j = u.t0;
@@ -427,8 +462,10 @@ struct Conv {
 #pragma unroll
                 for (int i0 = 0; i0 < NI; i0 += NI / 2) {
 #pragma unroll
-                    for (int i = i0; i < i0 + NI / 2; ++i)  // rows TPI apart, a multiple of 8, swizzle alike
-                        store_codes(a0 + o + i * (TPI * 128), a1 + o + i * (TPI * 128), q[i]);
+                    for (int i = i0; i < i0 + NI / 2; ++i) {  // rows TPI apart, a multiple of 8, swizzle alike
+                        if constexpr (BITS == 8) store_codes(a0 + o + i * (TPI * 128), a1 + o + i * (TPI * 128), q[i]);
+                        else store_codes4(a0 + o + i * (TPI * 128), q[i], sc[i]);
+                    }
                     if (more) load(j + 1, g + 1, i0);
                 }
                 stored(s);
@@ -451,10 +488,11 @@ DT_DI void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" 
 // The warp that looks up pages and scales, four tiles at a time (eight lanes,
 // of 16 tokens each, to a tile), up to RING tiles ahead of their use, and asks
 // L2 for the codes.  A page id out of range is reported and reads another page.
-template <int D>
+template <int D, int BITS>
 DT_DI void look_up(const DtAttend& a, Shared* sh, int lane) {
     const int lp = 31 - __clz(a.c.page), grp = lane & 7;
-    const uint32_t page_bytes = ((uint32_t)a.c.Hkv << lp) * D;
+    constexpr int ROW = D * BITS / 8;  // bytes of a token
+    const uint32_t page_bytes = ((uint32_t)a.c.Hkv << lp) * ROW;
     uint32_t g = 0, i = 0;
     for (const Seg* sg; (sg = get_segment(sh, i)) != nullptr; release_segment(sh, i++)) {
         const int t0 = sg->t0, nt = sg->t1 - t0, ctx = min(sg->t1, sg->ctx) - t0, len = sg->len, b = sg->b, h = sg->h;
@@ -472,14 +510,20 @@ DT_DI void look_up(const DtAttend& a, Shared* sh, int lane) {
                 }
             }
             if (in && tok < len) {
-                ks = a.c.k_scale[(size_t)id * a.c.Hkv + h];
-                vs = a.c.v_scale[(size_t)id * a.c.Hkv + h];
-                // the 16 tokens' codes: 16 D bytes of keys and of values
-                const size_t o = (size_t)id * page_bytes + ((size_t)h << lp) * D + (tok & (a.c.page - 1)) * D;
+                if constexpr (BITS == 8) {
+                    ks = a.c.k_scale[(size_t)id * a.c.Hkv + h];
+                    vs = a.c.v_scale[(size_t)id * a.c.Hkv + h];
+                }
+                // the 16 tokens' codes, of keys and of values
+                const size_t o = (size_t)id * page_bytes + ((size_t)h << lp) * ROW + (tok & (a.c.page - 1)) * ROW;
 #pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
+                for (int c = 0; c < ROW / 8; ++c) {
                     prefetch_l2(a.c.k + o + c * 128);
                     prefetch_l2(a.c.v + o + c * 128);
+                }
+                if constexpr (BITS == 4) {  // and scales, D bytes
+                    prefetch_l2((const uint8_t*)a.c.k_scale + o / 8);
+                    prefetch_l2((const uint8_t*)a.c.v_scale + o / 8);
                 }
             }
             if (t >= ctx && t < nt) {  // 16 new rows
@@ -1185,7 +1229,7 @@ struct Soft {
     }
 };
 
-template <int D>
+template <int D, int BITS>
 __global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtAttend a, float* part, int* counters,
                                                           long long probe) {
     using L = Lay<D>;
@@ -1235,7 +1279,7 @@ __global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtA
         Soft<D>::run(a, sm, sh, tmem, tid, cta, part, counters);
     } else if (tid < NS + 2 * NC) {
         set_regs<REG_CONV>();
-        Conv<D>::run(a, sm, sh, (tid - NS) % NC, tid < NS + NC);
+        Conv<D, BITS>::run(a, sm, sh, (tid - NS) % NC, tid < NS + NC);
         at_zero_rest(a, cta, ctas, tid - NS, 2 * NC);
     } else {
         set_regs<REG_MMA>();
@@ -1246,7 +1290,7 @@ __global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtA
         if (wid == W0 + 2) {
             if ((tid & 31) == 0 && !dt_probe_wait(&sh->probe, probe)) sh->fail = 1;
             __syncwarp();
-            look_up<D>(a, sh, tid & 31);
+            look_up<D, BITS>(a, sh, tid & 31);
         }
     }
     dt_tc_fence_before();
@@ -1263,17 +1307,17 @@ __global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtA
 // Probe budget of the timeout path's test hook (0: off) in the calls made from now on.
 std::atomic<long long> g_probe{0};
 
-template <int D>
+template <int D, int BITS>
 cudaError_t launch(const DtAttend& a, void* workspace, int ctas, cudaStream_t st) {
     constexpr size_t smem = Lay<D>::SMEM;
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     // more than half of an SM's shared memory: one CTA per SM, as its 512 TMEM columns need
     static_assert(2 * (smem + 1024) > 233472 || D == 64, "one CTA per SM");
     constexpr size_t ask = smem > 116 * 1024 ? smem : 116 * 1024;
-    cudaError_t e = cudaFuncSetAttribute(kn12_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ask);
+    cudaError_t e = cudaFuncSetAttribute(kn12_kernel<D, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ask);
     if (e != cudaSuccess) return e;
     DtLaunch lc(dim3(ctas), dim3(NT), ask, st);
-    return cudaLaunchKernelEx(&lc.cfg, kn12_kernel<D>, a, (float*)((char*)workspace + AT_MAX_CTAS * sizeof(int)),
+    return cudaLaunchKernelEx(&lc.cfg, kn12_kernel<D, BITS>, a, (float*)((char*)workspace + AT_MAX_CTAS * sizeof(int)),
                               (int*)workspace, g_probe.load(std::memory_order_relaxed));
 }
 
@@ -1285,6 +1329,7 @@ size_t dt_kn12_workspace(int D, int ctas) {
     return AT_MAX_CTAS * sizeof(int) + (size_t)ctas * 2 * ROWS * (D + 2) * sizeof(float);
 }
 
-cudaError_t dt_kn12_launch(const DtAttend& a, void* workspace, int ctas, cudaStream_t st) {
-    return a.c.D == 64 ? launch<64>(a, workspace, ctas, st) : launch<128>(a, workspace, ctas, st);
+cudaError_t dt_kn12_launch(const DtAttend& a, int bits, void* workspace, int ctas, cudaStream_t st) {
+    if (bits == 4) return a.c.D == 64 ? launch<64, 4>(a, workspace, ctas, st) : launch<128, 4>(a, workspace, ctas, st);
+    return a.c.D == 64 ? launch<64, 8>(a, workspace, ctas, st) : launch<128, 8>(a, workspace, ctas, st);
 }

@@ -1,0 +1,165 @@
+// kn15_read.cu -- reading back tokens of the paged caches, in 4 bits and in e4m3
+// (dt_kv_read4, dt_kv_read).
+//
+// A thread turns 16 elements of a token's head (one scale of the 4-bit cache) into bf16 or
+// fp32 and writes them at once; a CTA keeps to one head, whose tokens lie together in a page.
+#include "dt_cache.cuh"
+#include "dt_launch.h"
+
+namespace {
+
+constexpr int NT = 256;
+constexpr int U = 4;  // blocks of 16 in flight per thread
+
+DT_DI uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *(const uint32_t*)&v;
+}
+DT_DI void store32(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+DT_DI void store16(void* p, const uint32_t (&w)[8]) {
+    ((uint4*)p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    ((uint4*)p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <int BITS>
+struct Raw {  // 16 codes and their scale
+    uint4 q;
+    float s;
+    DT_DI void load(const uint8_t* codes, const void* scales, size_t slot, size_t blk, int nb, int at) {
+        if (BITS == 4) {
+            const uint2 w = *(const uint2*)(codes + (slot * nb + at) * 8);
+            q = make_uint4(w.x, w.y, 0u, 0u);
+            s = __int_as_float(((const uint8_t*)scales)[slot * nb + at]);
+        } else {
+            q = *(const uint4*)(codes + (slot * nb + at) * 16);
+            s = ((const float*)scales)[blk];
+        }
+    }
+    DT_DI void values(float (&x)[16]) const {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        const float f = BITS == 4 ? dt_e5m3_to_f32(__float_as_int(s)) : s;
+#pragma unroll
+        for (int i = 0; i < 4; i += (BITS == 4 ? 2 : 1)) {
+            uint32_t h[4];
+            if (BITS == 4) {
+                dt_e2m1x8_to_f16x8(w[i / 2], h);
+            } else {
+                dt_e4m3x4_to_f16x4(w[i], h[0], h[1]);
+            }
+#pragma unroll
+            for (int k = 0; k < (BITS == 4 ? 4 : 2); ++k) {
+                const float2 v = __half22float2(*(const __half2*)&h[k]);
+                x[4 * i + 2 * k] = __fmul_rn(v.x, f);
+                x[4 * i + 2 * k + 1] = __fmul_rn(v.y, f);
+            }
+        }
+    }
+};
+
+// OUT: bytes of an output element.  WIDE: outputs start on 32 bytes.
+template <int BITS, int OUT, bool WIDE>
+__global__ void __launch_bounds__(NT, 4) kn15_kernel(const __grid_constant__ dt_kv_cache c, const int32_t* rows, int N,
+                                                     const int32_t* start, const int32_t* count, int count_add,
+                                                     const __grid_constant__ dt_rows ko, const __grid_constant__ dt_rows vo,
+                                                     int32_t* status) {
+    dt_pdl_trigger();
+    dt_pdl_wait();
+    const int tid = threadIdx.x, b = blockIdx.z, h = blockIdx.y >> 1;
+    const bool keys = (blockIdx.y & 1) == 0;
+    const int len = c.len[b], s0 = !rows && start ? start[b] : 0;
+    const long long want = count ? (long long)count[b] + count_add : rows ? N : (long long)len - s0;
+    const bool bad = len < 0 || (long long)len > (long long)c.max_pages * c.page || s0 < 0 || want < 0 || want > N ||
+                     (!rows && s0 + want > len);
+    if (bad) {
+        if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) atomicOr(&status[b], DT_DEV_BAD_CACHE);
+        return;
+    }
+    const int n = (int)want;
+    const int sh = c.D == 128 ? 3 : 2, nb = 1 << sh, blk = tid & (nb - 1);  // blocks of a head
+    const int lp = 31 - __clz(c.page);
+    const int32_t* table = c.table + (size_t)b * c.max_pages;
+    const uint8_t* codes = keys ? c.k : c.v;
+    const void* scales = keys ? c.k_scale : c.v_scale;
+    const dt_rows& dst = keys ? ko : vo;
+    char* out = (char*)dst.ptr + (b * dst.stride_b + h * dst.stride_h + blk * 16) * OUT;
+    const int per = NT >> sh;  // tokens of a pass
+    for (int j0 = (int)blockIdx.x * U * per + (tid >> sh); j0 < n; j0 += (int)gridDim.x * U * per) {
+        Raw<BITS> raw[U];
+        bool off[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int j = j0 + i * per;
+            off[i] = false;
+            if (j < n) {
+                int tok = rows ? rows[(size_t)b * N + j] : s0 + j;
+                uint32_t id = 0;
+                off[i] = (unsigned)tok >= (unsigned)len;
+                if (!off[i]) {
+                    id = (uint32_t)table[tok >> lp];
+                    off[i] = id >= (uint32_t)c.n_pages;
+                }
+                if (!off[i]) {
+                    const size_t k = (size_t)id * c.Hkv + h;
+                    raw[i].load(codes, scales, (k << lp) + (tok & (c.page - 1)), k, nb, blk);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int j = j0 + i * per;
+            if (j >= n) continue;
+            float x[16];
+            if (off[i]) {
+                atomicOr(&status[b], DT_DEV_BAD_CACHE);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = 0.f;
+            } else {
+                raw[i].values(x);
+            }
+            char* o = out + j * dst.stride_n * OUT;
+#pragma unroll
+            for (int part = 0; part < OUT / 2; ++part) {
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    w[e] = OUT == 2 ? bf16x2(x[2 * e], x[2 * e + 1]) : __float_as_uint(x[8 * part + e]);
+                if (WIDE) store32(o + 32 * part, w);
+                else store16(o + 32 * part, w);
+            }
+        }
+    }
+}
+
+template <int BITS, int OUT, bool WIDE>
+cudaError_t launch(const dt_kv_cache& c, int batch, const int32_t* rows, int N, const int32_t* start, const int32_t* count,
+                   int count_add, const dt_rows& k, const dt_rows& v, int32_t* status, cudaStream_t st) {
+    const int per = NT * 16 / c.D * U;  // tokens of a CTA
+    DtLaunch lc(dim3((N + per - 1) / per, 2 * c.Hkv, batch), dim3(NT), 0, st);
+    return cudaLaunchKernelEx(&lc.cfg, kn15_kernel<BITS, OUT, WIDE>, c, rows, N, start, count, count_add, k, v, status);
+}
+
+bool aligned32(const dt_rows& r, int size) {
+    return (((uintptr_t)r.ptr | (uintptr_t)(r.stride_b * size) | (uintptr_t)(r.stride_n * size) | (uintptr_t)(r.stride_h * size)) & 31) == 0;
+}
+
+template <int BITS>
+cudaError_t launch_bits(const dt_kv_cache& c, int batch, const int32_t* rows, int N, const int32_t* start, const int32_t* count,
+                        int count_add, int dtype, const dt_rows& k, const dt_rows& v, int32_t* status, cudaStream_t st) {
+    const int size = dtype == DT_BF16 ? 2 : 4;
+    const bool wide = aligned32(k, size) && aligned32(v, size);
+    auto f = dtype == DT_BF16 ? (wide ? launch<BITS, 2, true> : launch<BITS, 2, false>)
+                              : (wide ? launch<BITS, 4, true> : launch<BITS, 4, false>);
+    return f(c, batch, rows, N, start, count, count_add, k, v, status, st);
+}
+
+}  // namespace
+
+cudaError_t dt_kn15_launch(const dt_kv_cache& c, int bits, int batch, const int32_t* rows, int N, const int32_t* start,
+                           const int32_t* count, int count_add, int dtype, const dt_rows& k, const dt_rows& v,
+                           int32_t* status, cudaStream_t st) {
+    return (bits == 4 ? launch_bits<4> : launch_bits<8>)(c, batch, rows, N, start, count, count_add, dtype, k, v, status, st);
+}

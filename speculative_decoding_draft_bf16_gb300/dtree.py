@@ -121,6 +121,17 @@ def lib():
         L.dt_tree_attention.restype = _i32
         L.dt_tree_attention.argtypes = [cp, rp, _i32, _i32, _i32, xp, xp, xp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp,
                                         ctypes.c_size_t, _vp, _vp]
+        # a 4-bit cache has the same fields, k_scale and v_scale pointing to bytes
+        L.dt_kv_append4.restype = L.dt_tree_attention4.restype = _i32
+        L.dt_kv_append4.argtypes = L.dt_kv_append.argtypes
+        L.dt_tree_attention4.argtypes = L.dt_tree_attention.argtypes
+        L.dt_tree_attention4_workspace.restype = ctypes.c_size_t
+        L.dt_tree_attention4_workspace.argtypes = L.dt_tree_attention_workspace.argtypes
+        L.dt_kv_read.restype = L.dt_kv_read4.restype = _i32
+        L.dt_kv_read.argtypes = L.dt_kv_read4.argtypes = [cp, _i32, _vp, _i32, _vp, _vp, _i32, _i32, xp, xp, _vp, _vp]
+        L.dt_qk_norm.restype = _i32
+        L.dt_qk_norm.argtypes = [_i32, _i32, _i32, _i32, _i32, _i32, xp, xp, _vp, _i32, _vp, _i32, ctypes.c_float, rp,
+                                 _vp, _vp, _vp, xp, xp, _vp, _vp]
         L.dt_token_logprobs.restype = _i32
         L.dt_token_logprobs.argtypes = [_vp, _i32, _i32, _i32, _i32, _i64, _i64, _vp, _vp, _i32, _i32, _vp, _vp,
                                         _vp, _vp, _vp, _vp]
@@ -567,8 +578,8 @@ def saba_budget(tree, st, c_verify, c_fixed, B_min, B_max, budget, state, hidden
 
 
 # ---------------------------------------------------------------------------
-# The target model's side of a round: paged e4m3 cache, tree attention over it,
-# and log-probabilities of what was emitted.
+# The target model's side of a round: norms of its heads, paged caches in e4m3 or 4 bits,
+# tree attention over them, and log-probabilities of what was emitted.
 # ---------------------------------------------------------------------------
 
 class PagedCache:
@@ -611,6 +622,45 @@ class PagedCache:
                    torch.full((batch, max_pages), -1, **i32), torch.zeros((batch,), **i32))
 
 
+class PagedCache4:
+    """Keys and values in pages of e2m1 numbers, 4.5 bits an element (dt_kv_cache4): append, attention and
+    reading take it in place of a PagedCache.
+
+    k, v: [n_pages, Hkv, page, D / 2] uint8 codes, element 2i in the lower half of byte i; k_scale, v_scale:
+    [n_pages, Hkv, page, D / 16] uint8, a scale for each 16 elements (the upper half of an fp16 number without
+    its sign); table: [batch, max_pages] int32; len: [batch] int32.  The caller owns all of them, as there."""
+
+    def __init__(self, k, v, k_scale, v_scale, table, len):
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError("k and v must be [n_pages, Hkv, page, D / 2] of one shape, got %s and %s"
+                             % (tuple(k.shape), tuple(v.shape)))
+        self.n_pages, self.Hkv, self.page, self.D = *k.shape[:3], 2 * k.shape[3]
+        for t, name in ((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+            _need(t, torch.uint8, name)
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t.shape != (*k.shape[:3], self.D // 16):
+                raise ValueError("%s must be %s, got %s" % (name, (*k.shape[:3], self.D // 16), tuple(t.shape)))
+        _need(table, torch.int32, "table")
+        if table.dim() != 2:
+            raise ValueError("table must be [batch, max_pages], got %s" % (tuple(table.shape),))
+        self.batch, self.max_pages = table.shape
+        _need(len, torch.int32, "len", numel=self.batch)
+        self.k, self.v, self.k_scale, self.v_scale, self.table, self.len = k, v, k_scale, v_scale, table, len
+        self._struct = CacheStruct(self.n_pages, self.page, self.Hkv, self.D, self.max_pages, k.data_ptr(),
+                                   v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
+                                   len.data_ptr())
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def empty(cls, n_pages, page, Hkv, D, batch, max_pages, device="cuda"):
+        """A cache with nothing in it: every length 0, every table entry -1."""
+        u8 = dict(dtype=torch.uint8, device=device)
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.zeros((n_pages, Hkv, page, D // 2), **u8), torch.zeros((n_pages, Hkv, page, D // 2), **u8),
+                   torch.zeros((n_pages, Hkv, page, D // 16), **u8), torch.zeros((n_pages, Hkv, page, D // 16), **u8),
+                   torch.full((batch, max_pages), -1, **i32), torch.zeros((batch,), **i32))
+
+
 class Rope:
     """Rotation tables (dt_rope): cos, sin [max_pos, rot / 2] fp32."""
 
@@ -627,8 +677,8 @@ class Rope:
 
 def _head_rows(t, batch, M, H, D, name):
     """dt_rows of [batch, M, H, D]: any strides with dense, 16-byte aligned head vectors."""
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError("%s must be a CUDA tensor on the current device" % name)
     if t.shape != (batch, M, H, D):
         raise ValueError("%s must be %s, got %s" % (name, (batch, M, H, D), tuple(t.shape)))
     sb, sn, sh, sd = t.stride()
@@ -642,8 +692,8 @@ def _addr(t):
 
 
 def kv_append(cache, k, v, rope=None, rows=None, count=None, count_add=0, len_out=None, status=None, stream=None):
-    """Append rows of k, v [batch, M, Hkv, D] to the cache (dt_kv_append): keys rotated to their
-    position on the way, both stored in e4m3.  rows [batch, N] int32 picks rows (the walk's acc_nodes),
+    """Append rows of k, v [batch, M, Hkv, D] to the cache (dt_kv_append, dt_kv_append4): keys rotated to
+    their position on the way, both stored in the cache's form.  rows [batch, N] int32 picks rows (the walk's acc_nodes),
     count [batch] int32 + count_add says how many (its acc_len, 1); len_out [batch] gets the new lengths;
     status [batch] int32 is OR-ed with DT_DEV_BAD_CACHE for a request that does not fit; returned."""
     batch, M = cache.batch, k.shape[1]
@@ -666,22 +716,120 @@ def kv_append(cache, k, v, rope=None, rows=None, count=None, count_add=0, len_ou
             status = torch.zeros((batch,), dtype=torch.int32, device=k.device)
     else:
         _need(status, torch.int32, "status", numel=batch)
-    _check(lib().dt_kv_append(cache._ref, rope._ref if rope is not None else None, batch, M, _dtype_code(k),
-                              ctypes.byref(kr), ctypes.byref(vr), _addr(rows), N, _addr(count), int(count_add),
-                              _addr(len_out), _addr(status), _stream(stream)), "dt_kv_append")
+    call = lib().dt_kv_append4 if isinstance(cache, PagedCache4) else lib().dt_kv_append
+    _check(call(cache._ref, rope._ref if rope is not None else None, batch, M, _dtype_code(k),
+                ctypes.byref(kr), ctypes.byref(vr), _addr(rows), N, _addr(count), int(count_add), _addr(len_out),
+                _addr(status), _stream(stream)), "dt_kv_append")
     return status
+
+
+def kv_read(cache, N=None, rows=None, start=None, count=None, count_add=0, dtype=torch.bfloat16, k=None, v=None,
+            status=None, stream=None):
+    """Read tokens back out of a PagedCache or PagedCache4 (dt_kv_read, dt_kv_read4): row j of request b is
+    token rows[b, j] (rows [batch, N] int32), or start[b] + j (start [batch] int32; None: 0).
+    count [batch] int32 + count_add says how many rows a request gets, in [0, N]; without it, all of `rows`,
+    or all tokens from start on.  k, v: outputs [batch, N, Hkv, D] bf16 or fp32, any strides with dense heads
+    (None: zeros of `dtype`; N is needed then when there are no rows).  status [batch] int32 is OR-ed with
+    DT_DEV_BAD_CACHE for a request out of range.  Returns (k, v)."""
+    batch, Hkv, D = cache.batch, cache.Hkv, cache.D
+    if rows is not None:
+        _need(rows, torch.int32, "rows")
+        if rows.dim() != 2 or rows.shape[0] != batch:
+            raise ValueError("rows must be [batch, N], got %s" % (tuple(rows.shape),))
+        if start is not None:
+            raise ValueError("rows and start exclude each other")
+    given = [x for x in (N, None if rows is None else rows.shape[1], None if k is None else k.shape[1],
+                         None if v is None else v.shape[1]) if x is not None]
+    if not given:
+        raise ValueError("N is needed without rows and outputs")
+    N = given[0]
+    if any(x != N for x in given):
+        raise ValueError("N, rows and outputs speak of %s rows" % (sorted(set(given)),))
+    if start is not None:
+        _need(start, torch.int32, "start", numel=batch)
+    if count is not None:
+        _need(count, torch.int32, "count", numel=batch)
+    if k is None or v is None or status is None:
+        with _on(stream):
+            held = dict(dtype=dtype if k is None and v is None else (v if k is None else k).dtype, device=cache.k.device)
+            if k is None:
+                k = torch.zeros((batch, N, Hkv, D), **held)
+            if v is None:
+                v = torch.zeros((batch, N, Hkv, D), **held)
+            if status is None:
+                status = torch.zeros((batch,), dtype=torch.int32, device=cache.k.device)
+    _need(status, torch.int32, "status", numel=batch)
+    if k.dtype != v.dtype:
+        raise TypeError("k (%s) and v (%s) must share one dtype" % (k.dtype, v.dtype))
+    kr, vr = _head_rows(k, batch, N, Hkv, D, "k"), _head_rows(v, batch, N, Hkv, D, "v")
+    call = lib().dt_kv_read4 if isinstance(cache, PagedCache4) else lib().dt_kv_read
+    _check(call(cache._ref, batch, _addr(rows), N, _addr(start), _addr(count), int(count_add), _dtype_code(k),
+                ctypes.byref(kr), ctypes.byref(vr), _addr(status), _stream(stream)), "dt_kv_read")
+    return k, v
+
+
+def _norm_weight(w, H, D, name):
+    """(address, stride between heads) of weights [D] or [H, D]."""
+    if w is None:
+        return None, 0
+    _need(w, torch.float32, name)
+    if w.shape not in ((D,), (H, D)):
+        raise ValueError("%s must be %s or %s, got %s" % (name, (D,), (H, D), tuple(w.shape)))
+    return w.data_ptr(), D if w.dim() == 2 else 0
+
+
+def qk_norm(q, k, q_weight=None, k_weight=None, eps=1e-6, rope=None, len=None, pos=None, n_nodes=None, q_out=None,
+            k_out=None, status=None, stream=None):
+    """Root-mean-square norms of query and key heads, rotated in the same pass (dt_qk_norm): q [batch, M, Hq, D],
+    k [batch, M, Hk, D] bf16 or fp32 (k None: queries alone); weights fp32 [D] or [heads, D] (None: ones).
+    Row n of request b has position len[b] + pos[b, n] (len None: 0; pos None: n).  Outputs are like q and k and
+    may be q and k themselves; rows from n_nodes[b] on are left alone in outputs that the caller brings, and
+    undefined in others.  tree_attention and kv_append then take the results with rope None.  status [batch]
+    int32 is OR-ed with DT_DEV_BAD_CACHE for a position or count out of range.  Returns (q_out, k_out)."""
+    batch, M, Hq, D = q.shape
+    Hk = 0 if k is None else k.shape[2]
+    if k is not None and k.dtype != q.dtype:
+        raise TypeError("q (%s) and k (%s) must share one dtype" % (q.dtype, k.dtype))
+    if k is None and k_out is not None:
+        raise ValueError("k_out needs k")
+    if q_out is None or (k_out is None and k is not None) or status is None:
+        with _on(stream):
+            if q_out is None:
+                q_out = torch.empty((batch, M, Hq, D), dtype=q.dtype, device=q.device)
+            if k_out is None and k is not None:
+                k_out = torch.empty((batch, M, Hk, D), dtype=q.dtype, device=q.device)
+            if status is None:
+                status = torch.zeros((batch,), dtype=torch.int32, device=q.device)
+    refs = []
+    for x, H, name in ((q, Hq, "q"), (k, Hk, "k"), (q_out, Hq, "q_out"), (k_out, Hk, "k_out")):
+        if x is None:
+            refs.append(None)
+            continue
+        if x.dtype != q.dtype:
+            raise TypeError("%s must be %s, got %s" % (name, q.dtype, x.dtype))
+        refs.append(ctypes.byref(_head_rows(x, batch, M, H, D, name)))
+    for x, name, n in ((len, "len", batch), (pos, "pos", batch * M), (n_nodes, "n_nodes", batch), (status, "status", batch)):
+        if x is not None:
+            _need(x, torch.int32, name, numel=n)
+    qw, qs = _norm_weight(q_weight, Hq, D, "q_weight")
+    kw, ks = _norm_weight(k_weight, Hk, D, "k_weight")
+    _check(lib().dt_qk_norm(batch, M, Hq, Hk, D, _dtype_code(q), refs[0], refs[1], qw, qs, kw, ks, float(eps),
+                            rope._ref if rope is not None else None, _addr(len), _addr(pos), _addr(n_nodes), refs[2],
+                            refs[3], _addr(status), _stream(stream)), "dt_qk_norm")
+    return q_out, k_out
 
 
 def attention_workspace(cache, M, Hq):
     """Zeroed workspace of tree_attention calls on this cache with M rows and Hq query heads (or
     fewer of either): (tensor, bytes).  Calls that may run at the same time need one each."""
-    n = int(lib().dt_tree_attention_workspace(cache._ref, cache.batch, M, Hq))
+    size = lib().dt_tree_attention4_workspace if isinstance(cache, PagedCache4) else lib().dt_tree_attention_workspace
+    n = int(size(cache._ref, cache.batch, M, Hq))
     return torch.zeros(max(n, 16), dtype=torch.uint8, device=cache.k.device), n
 
 
 def tree_attention(cache, q, k, v, mask=None, pos=None, n_nodes=None, rope=None, scale=None, out=None, workspace=None,
                    status=None, stream=None):
-    """Attention of the tree's rows over the cache and over the tree (dt_tree_attention).
+    """Attention of the tree's rows over the cache and over the tree (dt_tree_attention, dt_tree_attention4).
     q [batch, M, Hq, D], k, v [batch, M, Hkv, D] bf16, not rotated; mask, pos as dt_tree_mask writes
     them with pos_offset 0 (None: a chain); returns out [batch, M, Hq, D] bf16.  status [batch] int32
     is OR-ed with DT_DEV_BAD_CACHE for a request out of range: bring one to see it."""
@@ -713,10 +861,10 @@ def tree_attention(cache, q, k, v, mask=None, pos=None, n_nodes=None, rope=None,
     ws, n = _need_workspace(workspace)
     if scale is None:
         scale = 1.0 / math.sqrt(cache.D)
-    _check(lib().dt_tree_attention(cache._ref, rope._ref if rope is not None else None, batch, M, Hq,
-                                   ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), _addr(mask), _addr(pos),
-                                   _addr(n_nodes), scale, _addr(out), _addr(ws), n, _addr(status), _stream(stream)),
-           "dt_tree_attention")
+    call = lib().dt_tree_attention4 if isinstance(cache, PagedCache4) else lib().dt_tree_attention
+    _check(call(cache._ref, rope._ref if rope is not None else None, batch, M, Hq, ctypes.byref(qr), ctypes.byref(kr),
+                ctypes.byref(vr), _addr(mask), _addr(pos), _addr(n_nodes), scale, _addr(out), _addr(ws), n,
+                _addr(status), _stream(stream)), "dt_tree_attention")
     return out
 
 
