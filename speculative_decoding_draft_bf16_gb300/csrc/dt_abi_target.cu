@@ -204,8 +204,8 @@ dt_status dt_qk_norm(int32_t batch, int32_t M, int32_t Hq, int32_t Hk, int32_t D
     const dt_rows none = {nullptr, 0, 0, 0};
     const DtNorm a{rope ? *rope : kNoRope, batch, M, Hq, Hk, D, dtype, Hq ? *q : none, Hk ? *k : none,
                    Hq ? *q_out : none, Hk ? *k_out : none, q_weight, k_weight, q_weight_stride, k_weight_stride, eps,
-                   len, pos, n_nodes, status, 0};
-    return cuda_status(dt_kn16_launch(a, (cudaStream_t)stream));
+                   len, pos, n_nodes, status, 0, 0, 0, 0};
+    return cuda_status(dt_kn16_launch(a, sm_count(), (cudaStream_t)stream));
 }
 
 dt_status dt_token_logprobs(const void* logits, int32_t dtype, int32_t batch, int32_t M, int32_t V, int64_t stride_b,

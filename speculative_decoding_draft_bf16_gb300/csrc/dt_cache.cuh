@@ -190,13 +190,11 @@ DT_DI float dt_e5m3_to_f32(int b) {
     return __half2float(__ushort_as_half((unsigned short)(b << 7)));
 }
 // The byte of the smallest scale, from 2^-17 to 10240, with top <= 6 * scale; top finite.
+// y = top / 6 to nearest, with the constant a quarter of a step above 1 / 6, is larger than
+// a scale s exactly when top > 6 s: for top = 6 s it is off by a quarter of a step at most,
+// for the next number up it lies 2/3 of a step above.  Rounding up to fp16, then to three
+// bits of fraction, finds the next scale.
 DT_DI int dt_e5m3_for(float top) {
-    // top / 6 from above; below 2^-14 the numbers lie as far apart as from 2^-14 on
-    const float y = __fmul_ru(top, 0.16666667163372039795f);
-    const bool sub = y < dt_pow2(-14);
-    const uint32_t bits = __float_as_uint(sub ? __fadd_ru(y, dt_pow2(-14)) : y);
-    int b = (int)((bits + 0xFFFFFu) >> 20) - (112 << 3) - (sub ? 8 : 0);
-    b = min(b, DT_E5M3_TOP + 1);
-    if (b > 1 && __fmul_rn(dt_e5m3_to_f32(b - 1), 6.f) >= top) --b;
-    return min(max(b, 1), DT_E5M3_TOP);
+    const unsigned short h = __half_as_ushort(__float2half_ru(__fmul_rn(top, 0.16666667163372039795f)));
+    return min(max((h + 127) >> 7, 1), DT_E5M3_TOP);
 }

@@ -204,9 +204,9 @@ struct DtNorm {
     const int32_t* pos;
     const int32_t* n_nodes;
     int32_t* status;
-    int parts;  // warps that share a token (set by the launch)
+    int q_steps, k_steps, per, parts;  // set by the launch: steps of a token, steps of a unit of work, units of a token
 };
-cudaError_t dt_kn16_launch(const DtNorm& a, cudaStream_t st);
+cudaError_t dt_kn16_launch(const DtNorm& a, int sms, cudaStream_t st);
 
 // Tree attention over the paged caches (kn11_attend.cu); bits: 8 (e4m3) or 4.
 struct DtAttend {

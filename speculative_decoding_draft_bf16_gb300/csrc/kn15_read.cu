@@ -3,6 +3,11 @@
 //
 // A thread turns 16 elements of a token's head (one scale of the 4-bit cache) into bf16 or
 // fp32 and writes them at once; a CTA keeps to one head, whose tokens lie together in a page.
+//
+// Bound by HBM, mostly writes: 8 contexts of 500 to 8000 tokens of 8 heads of 128 to bf16,
+// 178 MB, 31 us, 5.8 TB/s (85% of a copy's rate).  With 1, 2, 4, 8 blocks in flight per
+// thread 61, 40, 33, 31 us at four CTAs to an SM; four at six CTAs 31.  Picked rows take the
+// latency of four dependent reads: 16 requests' 129 tokens of e4m3 4.5 us.
 #include "dt_cache.cuh"
 #include "dt_launch.h"
 
@@ -62,7 +67,7 @@ struct Raw {  // 16 codes and their scale
 
 // OUT: bytes of an output element.  WIDE: outputs start on 32 bytes.
 template <int BITS, int OUT, bool WIDE>
-__global__ void __launch_bounds__(NT, 4) kn15_kernel(const __grid_constant__ dt_kv_cache c, const int32_t* rows, int N,
+__global__ void __launch_bounds__(NT, 6) kn15_kernel(const __grid_constant__ dt_kv_cache c, const int32_t* rows, int N,
                                                      const int32_t* start, const int32_t* count, int count_add,
                                                      const __grid_constant__ dt_rows ko, const __grid_constant__ dt_rows vo,
                                                      int32_t* status) {
