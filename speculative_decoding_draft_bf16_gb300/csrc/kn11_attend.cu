@@ -96,12 +96,9 @@ DT_DI void lds(uint32_t addr, uint32_t (&w)[WORDS]) {
         asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
 }
 
-// One or two bytes.
-template <int BYTES>
-DT_DI uint32_t lds_bytes(uint32_t addr) {
+DT_DI uint32_t lds_byte(uint32_t addr) {
     uint32_t v;
-    if constexpr (BYTES == 1) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    else asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
 
@@ -117,6 +114,7 @@ struct Stream {
     using L = Lay<D, BITS>;
     using Walk = AtWalk<ROWS, ATOM>;
     static constexpr int KS = D / 16;  // steps of K Q'
+    static constexpr int TP = NR == 1 ? 2 : 1;  // tiles at a time of a 4-bit cache (two groups of rows and two tiles spill)
     static constexpr int NV = D / 8;   // columns of a lane in V' P': NV * g + j; two to an MMA
 
     uint32_t qs;  // Q's fragments in shared memory, [KS / 2][NR][32 lanes][4 words]
@@ -170,7 +168,9 @@ struct Stream {
             big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
             int ex = (int)(big >> 23) - 127;  // largest magnitude in [2^ex, 2^(ex+1))
             ex = big >= 0x7F800000u ? 0 : min(max(ex, -100), 126);  // 2^-ex is a normal number
-            const float f = dt_pow2(-ex), rc = __fmul_rn(__fmul_rn(a.scale, LOG2E), dt_pow2(ex));
+            const float f = dt_pow2(-ex);
+            float rc = __fmul_rn(__fmul_rn(a.scale, LOG2E), dt_pow2(ex));
+            if (BITS == 4) rc = at_factor(rc, 1.f);  // what the loop over cached tokens multiplies with
             rowc[i][0] = __shfl_sync(0xffffffffu, rc, 8 * t);
             rowc[i][1] = __shfl_sync(0xffffffffu, rc, 8 * t + 4);
             // every warp writes the same words
@@ -185,9 +185,31 @@ struct Stream {
         }
     }
 
+    // Moves the references of rows whose maximum has grown, and their sums.
+    DT_DI void follow(const float (&top)[NR][2]) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = top[i][e];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                const float to = x > m[i][e] + (HEADROOM + LAZY) ? x - HEADROOM : m[i][e];
+                const float f = to == m[i][e] ? 1.f : dt_ex2_approx(m[i][e] - to);  // m = -inf: 0
+                m[i][e] = to;
+                l[i][e] = __fmul_rn(l[i][e], f);
+#pragma unroll
+                for (int j = 0; j < NV / 2; ++j) {
+                    o[j][i][e] = __fmul_rn(o[j][i][e], f);
+                    o[j][i][2 + e] = __fmul_rn(o[j][i][2 + e], f);
+                }
+            }
+        }
+    }
+
     // Scores of 16 tokens, masked (c[i][2k + e]: token g + 8k, row 2t + e + 8i), to
     // probabilities as the fragments of P'; ks, lv, iv: the 16 tokens', or (T = 2) of
-    // tokens g and g + 8.  (T = 1 with constants ones and zeros costs the 4-bit form nothing.)
+    // tokens g and g + 8.
     template <int T>
     DT_DI void weigh(float (&c)[NR][4], const float (&ks)[T], const float (&lv)[T], const float (&iv)[T], uint32_t (&p)[NR][2]) {
         const float NEG_INF = -__int_as_float(0x7F800000);
@@ -204,26 +226,7 @@ struct Stream {
                 grown |= top[i][e] > m[i][e] + (HEADROOM + LAZY);
             }
         }
-        if (__any_sync(0xffffffffu, grown)) {
-#pragma unroll
-            for (int i = 0; i < NR; ++i) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x = top[i][e];
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                    const float to = x > m[i][e] + (HEADROOM + LAZY) ? x - HEADROOM : m[i][e];
-                    const float f = to == m[i][e] ? 1.f : dt_ex2_approx(m[i][e] - to);  // m = -inf: 0
-                    m[i][e] = to;
-                    l[i][e] = __fmul_rn(l[i][e], f);
-#pragma unroll
-                    for (int j = 0; j < NV / 2; ++j) {
-                        o[j][i][e] = __fmul_rn(o[j][i][e], f);
-                        o[j][i][2 + e] = __fmul_rn(o[j][i][2 + e], f);
-                    }
-                }
-            }
-        }
+        if (__any_sync(0xffffffffu, grown)) follow(top);
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
 #pragma unroll
@@ -240,27 +243,29 @@ struct Stream {
         }
     }
 
-    // The same of a 4-bit cache.  The codes' scales go into the fragments: a lane's keys have
-    // KC scales per token, its values one per token, and the products are exact in fp16.
-    DT_DI void tile4(uint32_t st, int lane, int left) {
+    // Scores of the staged 16 tokens of a 4-bit cache.  The codes' scales go into the
+    // fragments: a lane's keys have KC scales per token, and the products are exact in fp16.
+    DT_DI void scores4(uint32_t st, int lane, float (&c)[NR][4]) {
         const int g = lane >> 2, t = lane & 3;
         constexpr int NB = D / 16;  // scales of a token
-        const uint32_t sk = st + L::SCALES, sv = sk + 16 * NB;
-        float c[NR][4] = {};
-        uint32_t w[2][2 * L::KC], ks[2];
+        uint32_t w[2][2 * L::KC], ks[2][L::KC];
         lds<2 * L::KC>(st + lane * (8 * L::KC), w[0]);
         lds<2 * L::KC>(st + L::KBYTES / 2 + lane * (8 * L::KC), w[1]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) ks[i] = lds_bytes<L::KC>(sk + (g + 8 * i) * NB + L::KC * t);
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int j = 0; j < L::KC; ++j) ks[i][j] = lds_byte(st + L::SCALES + (g + 8 * i) * NB + L::KC * t + j) * 0x00800080u;
+        }
+#pragma unroll
+        for (int i = 0; i < NR; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
 #pragma unroll
         for (int j = 0; j < 2 * L::KC; ++j) {  // 8 elements of both tokens
             uint32_t f[2][4], q[NR][4], h[2][4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint32_t s = dt_e5m3_pair(ks[i], j >> 1);
                 dt_e2m1x8_to_f16x8(w[i][j], h[i]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) f[k >> 1][2 * (k & 1) + i] = dt_f16x2_mul(h[i][k], s);
+                for (int k = 0; k < 4; ++k) f[k >> 1][2 * (k & 1) + i] = dt_f16x2_mul(h[i][k], ks[i][j >> 1]);
             }
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
@@ -269,30 +274,35 @@ struct Stream {
                 mma(c[i], f[1], q[i][2], q[i][3]);
             }
         }
-        // values of tokens 2t, 2t + 1, 2t + 8, 2t + 9
-        constexpr int VW = L::VB / 8;
+    }
+    // Scores of tokens from `left` on count as -infinity.
+    DT_DI void hide(float (&c)[NR][4], int g, int left) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (g + 8 * (k >> 1) >= left) c[i][k] = -__int_as_float(0x7F800000);
+        }
+    }
+    // The staged 16 values, of which `left` exist, weighted by P': a lane's columns have one
+    // scale per token (whatever lies behind the last token: zero).
+    DT_DI void values4(uint32_t st, int lane, int left, const uint32_t (&p)[NR][2]) {
+        const int g = lane >> 2, t = lane & 3;
+        constexpr int NB = D / 16, VW = L::VB / 8;
+        const uint32_t sv = st + L::SCALES + 16 * NB + 2 * t * NB + (D == 128 ? g : g >> 1);
         uint32_t v[4][VW], vs[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int row = (k & 1) * 8 + t + 4 * (k >> 1);  // where token 2t + k % 2 + 8 (k / 2) lies
+        for (int k = 0; k < 4; ++k) {  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+            const int row = (k & 1) * 8 + t + 4 * (k >> 1);  // where it lies
             lds<VW>(st + L::KBYTES + (D == 128 ? row * 64 + ((((g >> 1) ^ (row & 2)) << 4) | ((g & 1) << 3)) : row * 32 + g * 4), v[k]);
-            vs[k] = lds_bytes<1>(sv + (2 * t + (k & 1) + 8 * (k >> 1)) * NB + (D == 128 ? g : g >> 1));
+            vs[k] = lds_byte(sv + ((k & 1) + 8 * (k >> 1)) * NB);
         }
         if (left < 16) {
-#pragma unroll
-            for (int i = 0; i < NR; ++i) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (g + 8 * (k >> 1) >= left) c[i][k] = -__int_as_float(0x7F800000);
-            }
-            // whatever lies behind the last token counts as zeros
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (2 * t + (k & 1) + 8 * (k >> 1) >= left) vs[k] = 0u;
         }
-        uint32_t p[NR][2];
-        weigh<1>(c, {1.f}, {0.f}, {1.f}, p);
-        const uint32_t s0 = (vs[0] | vs[1] << 16) << 7, s1 = (vs[2] | vs[3] << 16) << 7;
+        const uint32_t s0 = vs[0] * 0x80u + vs[1] * 0x800000u, s1 = vs[2] * 0x80u + vs[3] * 0x800000u;
 #pragma unroll
         for (int j = 0; j < VW; ++j) {
             // columns 2n and 2n + 1 of two tokens in byte n
@@ -309,6 +319,48 @@ struct Stream {
                 for (int i = 0; i < NR; ++i) mma(o[4 * j + n][i], f, p[i][0], p[i][1]);
             }
         }
+    }
+    // TP groups of 16 tokens of a 4-bit cache, whose first left[k] tokens exist, left[0] > 0.
+    // Cached tokens have no scales beside their values, so scores are moved by the reference
+    // alone; with a token there it is finite (or all of the row is NaN).
+    DT_DI void tiles4(const uint32_t (&st)[TP], int lane, const int (&left)[TP]) {
+        float c[TP][NR][4];
+#pragma unroll
+        for (int k = 0; k < TP; ++k) scores4(st[k], lane, c[k]);
+        if (left[TP - 1] < 16) {  // then those before it may be, too
+#pragma unroll
+            for (int k = 0; k < TP; ++k) hide(c[k], lane >> 2, left[k]);
+        }
+        float top[NR][2];
+        bool grown = false;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = fmaxf(c[0][i][e], c[0][i][2 + e]);
+#pragma unroll
+                for (int k = 1; k < TP; ++k) x = fmaxf(x, fmaxf(c[k][i][e], c[k][i][2 + e]));
+                top[i][e] = __fmul_rn(x, rowc[i][e]);
+                grown |= top[i][e] > m[i][e] + (HEADROOM + LAZY);
+            }
+        }
+        if (__any_sync(0xffffffffu, grown)) follow(top);
+        uint32_t p[TP][NR][2];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+#pragma unroll
+            for (int k = 0; k < TP; ++k) {
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = dt_ex2_approx(__fmaf_rn(c[k][i][e], rowc[i][e & 1], -m[i][e & 1]));
+                l[i][0] = __fadd_rn(l[i][0], __fadd_rn(x[0], x[2]));
+                l[i][1] = __fadd_rn(l[i][1], __fadd_rn(x[1], x[3]));
+                p[k][i][0] = transposed8x8(f16x2(x[0], x[1]));
+                p[k][i][1] = transposed8x8(f16x2(x[2], x[3]));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < TP; ++k) values4(st[k], lane, left[k], p[k]);
     }
 
     // The staged 16 tokens at `st`, of which the first `left` exist.
@@ -539,8 +591,8 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
     for (; u.next(a, share, cta); u.step(a)) {
         const int len = u.r.len, cend = min(u.t1, u.r.ctx), n = max(0, cend - u.t0);
         const int* table = a.c.table + (size_t)u.b * a.c.max_pages;
-        const uint8_t* kbase = a.c.k + ((size_t)u.h << lp) * ROW + (BITS == 8 ? t * 16 : 0);
-        const uint8_t* vbase = a.c.v + ((size_t)u.h << lp) * ROW + (BITS == 8 ? g * L::VB : 0);
+        const uint8_t* kbase = a.c.k + ((size_t)u.h << lp) * ROW + (BITS == 8 ? t * 16 : lane * 16);
+        const uint8_t* vbase = a.c.v + ((size_t)u.h << lp) * ROW + (BITS == 8 ? g * L::VB : lane * 16);
         // Pages and scales of this warp's 16 tokens of 32 tiles at a time, one
         // tile to a lane; the next batch's pages are loaded a batch ahead.
         auto page_at = [&](int i) {  // of tile t0 + i (past the end: of the last token)
@@ -564,37 +616,15 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
             if (issued < n) {
                 if ((issued & 31) == 0 && issued > 0) {
                     id = id_next;
-                    if constexpr (BITS == 8) {
-                        if ((issued >> 5) & 1) scales_of(id, ks[1], vs[1]);
-                        else scales_of(id, ks[0], vs[0]);
-                    }
+                    if ((issued >> 5) & 1) scales_of(id, ks[1], vs[1]);
+                    else scales_of(id, ks[0], vs[0]);
                     id_next = page_at(issued + 32 + lane);
                 }
                 const uint32_t p = __shfl_sync(0xffffffffu, id, issued & 31);
                 const int tok0 = (u.t0 + issued) * AT_TILE + w * 16;
                 const uint32_t st = my_fifo + put * L::BYTES + lane * 16, sv = my_fifo + put * L::BYTES + L::KBYTES + lane * L::VB;
-                const size_t o = (size_t)p * page_bytes + (uint32_t)(tok0 & low) * ROW;
-                if constexpr (BITS == 4) {
-                    // the 16 tokens' codes and scales lie in one piece each, whatever of them exists
-                    if (tok0 < len) {
-                        const uint8_t *k = kbase + o + lane * 16, *v = vbase + o + lane * 16;
-                        constexpr int PPT = D / 32;  // 16-byte pieces of a token
-                        const int r = lane / PPT;    // token; even ones lie before odd ones, see tile4
-                        const int at = D == 128 ? ((r & 1) * 8 + (r >> 1)) * 64 + (((lane & 3) ^ (r >> 1 & 2)) << 4)
-                                                : ((r & 1) * 8 + (r >> 1)) * 32 + (lane & 1) * 16;
-                        const uint32_t sv4 = my_fifo + put * L::BYTES + L::KBYTES + at;
-#pragma unroll
-                        for (int i = 0; i < L::KC; ++i) {
-                            copy_async<16>(st + i * 512, k + i * 512);
-                            copy_async<16>(sv4 + i * (8 / 2 * 64), v + i * 512);
-                        }
-                        if (lane < D / 8) {  // D bytes of key scales, then as many of value scales
-                            const uint8_t* s = (const uint8_t*)(lane < D / 16 ? a.c.k_scale : a.c.v_scale) +
-                                               ((size_t)u.h << lp) * (D / 16) + o / 8 + (lane & (D / 16 - 1)) * 16;
-                            copy_async<16>(st + L::SCALES, s);
-                        }
-                    }
-                } else if (tok0 + 16 <= len) {  // 16 tokens lie in one page
+                const size_t o = (size_t)p * page_bytes + (uint32_t)(tok0 & low) * D;
+                if (tok0 + 16 <= len) {  // 16 tokens lie in one page
                     const uint8_t* k = kbase + o + g * D;
                     const uint8_t* v = vbase + o + 2 * t * D;
 #pragma unroll
@@ -621,38 +651,91 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
             ++issued;
             put = put + 1 == L::STAGES ? 0 : put + 1;
         };
+        // The same for a 4-bit cache: the 16 tokens' codes and scales lie in one piece each,
+        // whatever of them exists, in the same slots of each page (tiles are whole pages).
+        constexpr int PPT = ROW / 16;  // 16-byte pieces of a token
+        const int r16 = lane / PPT;    // token of a lane's piece; even ones lie before odd ones, see values4
+        const uint32_t to_k = my_fifo + lane * 16, slot0 = (uint32_t)(w * 16 & low) * ROW;
+        const uint32_t to_v = my_fifo + L::KBYTES + ((r16 & 1) * 8 + (r16 >> 1)) * ROW +
+                              (D == 128 ? ((lane & 3) ^ (r16 >> 1 & 2)) << 4 : (lane & 1) << 4);
+        const uint8_t *k4 = kbase + slot0, *v4 = vbase + slot0;
+        const uint8_t* s4 = (const uint8_t*)(lane < D / 16 ? a.c.k_scale : a.c.v_scale) +  // D bytes each
+                            (((size_t)u.h << lp) * ROW + slot0) / 8 + (lane & (D / 16 - 1)) * 16;
+        int ahead = len - u.t0 * AT_TILE - w * 16;  // tokens from the next tile's on
+        uint32_t put4 = 0;
+        auto issue4 = [&]() {
+            if (issued < n) {
+                if ((issued & 31) == 0 && issued > 0) {
+                    id = id_next;
+                    id_next = page_at(issued + 32 + lane);
+                }
+                const uint32_t p = __shfl_sync(0xffffffffu, id, issued & 31);
+                if (ahead > 0) {
+                    const uint8_t *k = k4 + (size_t)p * page_bytes, *v = v4 + (size_t)p * page_bytes;
+#pragma unroll
+                    for (int i = 0; i < L::KC; ++i) {
+                        copy_async<16>(to_k + put4 + i * 512, k + i * 512);
+                        copy_async<16>(to_v + put4 + i * (4 * ROW), v + i * 512);
+                    }
+                    if (lane < D / 8) copy_async<16>(to_k + put4 + L::SCALES, s4 + (size_t)p * (page_bytes / 8));
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            ++issued;
+            ahead -= AT_TILE;
+            put4 = put4 == (L::STAGES - 1) * L::BYTES ? 0u : put4 + L::BYTES;
+        };
         if (n > 0) {
             id = page_at(lane);
             id_next = page_at(32 + lane);
             if constexpr (BITS == 8) scales_of(id, ks[0], vs[0]);
         }
-        for (int i = 0; i < L::STAGES - 1; ++i) issue();
+        if constexpr (BITS == 8) {
+            for (int i = 0; i < L::STAGES - 1; ++i) issue();
+        } else {
+            for (int i = 0; i < L::STAGES - S::TP; ++i) issue4();
+        }
         x.queries(a, u, lane);
         __syncwarp();
         // new rows while the first copies are on their way
         if (w == 0 && u.t1 > u.r.ctx) x.fresh(a, u, lane);
         else x.clear();
-        int slot = 0;  // of tile i
-        for (int i = 0; i < n; ++i) {
-            issue();
-            asm volatile("cp.async.wait_group %0;" ::"n"(L::STAGES - 1) : "memory");
-            const int left = len - (u.t0 + i) * AT_TILE - w * 16, at = my_fifo + slot * L::BYTES;
-            slot = slot + 1 == L::STAGES ? 0 : slot + 1;
-            if constexpr (BITS == 4) {
+        if constexpr (BITS == 4) {
+            int left = len - u.t0 * AT_TILE - w * 16;
+            uint32_t got = my_fifo;
+#pragma unroll 1
+            for (int i = 0; i < n; i += S::TP, left -= S::TP * AT_TILE) {
+                uint32_t at[S::TP];
+                int there[S::TP];
+#pragma unroll
+                for (int k = 0; k < S::TP; ++k) {
+                    issue4();
+                    at[k] = got;
+                    got = got == my_fifo + (L::STAGES - 1) * L::BYTES ? my_fifo : got + L::BYTES;
+                    there[k] = i + k < n ? max(left - k * AT_TILE, 0) : 0;
+                }
+                asm volatile("cp.async.wait_group %0;" ::"n"(L::STAGES - S::TP) : "memory");
                 __syncwarp();  // lanes read what others have copied
-                if (left > 0) x.tile4(at, lane, left);
+                if (left > 0) x.tiles4(at, lane, there);
                 __syncwarp();  // before the next copies there
-                continue;
             }
-            const bool odd = (i >> 5) & 1;
-            if ((i & 31) == 0) {
-                const float v = odd ? vs[1] : vs[0];
-                lv = log2f(v);
-                iv = 1.0f / v;
+        } else {
+            int slot = 0;  // of tile i
+            for (int i = 0; i < n; ++i) {
+                issue();
+                asm volatile("cp.async.wait_group %0;" ::"n"(L::STAGES - 1) : "memory");
+                const int left = len - (u.t0 + i) * AT_TILE - w * 16, at = my_fifo + slot * L::BYTES;
+                slot = slot + 1 == L::STAGES ? 0 : slot + 1;
+                const bool odd = (i >> 5) & 1;
+                if ((i & 31) == 0) {
+                    const float v = odd ? vs[1] : vs[0];
+                    lv = log2f(v);
+                    iv = 1.0f / v;
+                }
+                const float k = __shfl_sync(0xffffffffu, odd ? ks[1] : ks[0], i & 31);
+                const float v = __shfl_sync(0xffffffffu, lv, i & 31), r = __shfl_sync(0xffffffffu, iv, i & 31);
+                if (left > 0) x.tile(at, lane, left, k, v, r);
             }
-            const float k = __shfl_sync(0xffffffffu, odd ? ks[1] : ks[0], i & 31);
-            const float v = __shfl_sync(0xffffffffu, lv, i & 31), r = __shfl_sync(0xffffffffu, iv, i & 31);
-            if (left > 0) x.tile(at, lane, left, k, v, r);
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
 
