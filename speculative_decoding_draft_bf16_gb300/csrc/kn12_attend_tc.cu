@@ -643,7 +643,7 @@ DT_DI void issue_slot(unsigned char* sm, Shared* sh, uint32_t tmem, int s) {
 }
 
 // A slot's softmax: 128 threads, one per row.
-template <int D>
+template <int D, int BITS>
 struct Soft {
     using L = Lay<D>;
 
@@ -806,6 +806,44 @@ struct Soft {
         dt_tmem_st_wait();
     }
 
+    // The same for cached tokens of a 4-bit cache that are all visible: their scales are in the
+    // tiles, so nothing is left but the products' and the exponentials' work.  ka: the row's
+    // factor, a normal number.
+    static DT_DI void half_clear(uint32_t ts, uint32_t to, bool has_o, float ka, float& m, float& l, uint64_t* other,
+                                 uint32_t other_ph, int* fail) {
+        uint32_t x[64];
+        dt_tmem_ld64(ts, x);
+        float q[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            q[g] = fmaxf(__uint_as_float(x[16 * g]), __uint_as_float(x[16 * g + 1]));
+#pragma unroll
+            for (int i = 2; i < 16; i += 2) q[g] = max3(q[g], __uint_as_float(x[16 * g + i]), __uint_as_float(x[16 * g + i + 1]));
+        }
+        follow(__fmul_rn(fmaxf(max3(q[0], q[1], q[2]), q[3]), ka), m, l, to, has_o, other, other_ph, fail);
+        const float kb = m == -__int_as_float(0x7F800000) ? 0.f : -m;
+        const unsigned long long ka2 = dt_f2_pack(ka, ka), kb2 = dt_f2_pack(kb, kb);
+        unsigned long long sum[2] = {dt_f2_pack(0.f, 0.f), dt_f2_pack(0.f, 0.f)};
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                float e0, e1;
+                dt_f2_unpack(dt_f2_fma(dt_f2_pack(__uint_as_float(x[16 * g + i]), __uint_as_float(x[16 * g + i + 1])), ka2, kb2), e0, e1);
+                e0 = dt_ex2_approx(e0);
+                e1 = dt_ex2_approx(e1);
+                sum[(i >> 1) & 1] = dt_f2_add(sum[(i >> 1) & 1], dt_f2_pack(e0, e1));
+                p[i / 2] = f16x2(e0, e1);
+            }
+            dt_tmem_st16(ts + 8 * g, p);  // over columns that are in registers
+        }
+        float s0, s1;
+        dt_f2_unpack(dt_f2_add(sum[0], sum[1]), s0, s1);
+        l = __fadd_rn(__fadd_rn(s0, s1), l);
+        dt_tmem_st_wait();
+    }
+
     // The same for tokens with scales of their own: key exponents ek, value exponents ev.
     // Rare, so short: 16 tokens at a time, their scores read twice.
     static DT_DI void half_apart(const Apart* ap, int h, uint32_t ts, uint32_t to, bool has_o, float rowc,
@@ -871,6 +909,23 @@ struct Soft {
             const int clear = len / AT_TILE - u.t0;  // tiles before this one are wholly visible
             uint32_t pa = ph & 1;                    // phase of both halves' scores
             int lt = dual ? 0 : s;
+            if constexpr (BITS == 4) {
+                const float ka = at_factor(rowc, 1.f);
+                const int last = min(clear, nt);
+#pragma unroll 1
+                for (; lt < last; lt += hop, pa ^= 1) {
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        wait(&sh->sfull[s][h], pa, &sh->fail);
+                        __syncwarp();
+                        dt_tc_fence_after();
+                        half_clear(ts + 64 * h, to, lt >= hop || h, ka, m, l, &sh->sfull[s][h ^ 1], pa ^ h, &sh->fail);
+                        dt_tc_fence_before();
+                        __syncwarp();
+                        if ((tid & 31) == 0) dt_mbar_arrive(&sh->pfull[s][h]);
+                    }
+                }
+            }
 #pragma unroll 1
             for (; lt < nt; lt += hop, pa ^= 1) {
                 const uint32_t g = g0 + lt;
@@ -1276,7 +1331,7 @@ __global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtA
     const uint32_t tmem = sh->tmem;
     if (tid < NS) {
         set_regs<REG_SOFT>();
-        Soft<D>::run(a, sm, sh, tmem, tid, cta, part, counters);
+        Soft<D, BITS>::run(a, sm, sh, tmem, tid, cta, part, counters);
     } else if (tid < NS + 2 * NC) {
         set_regs<REG_CONV>();
         Conv<D, BITS>::run(a, sm, sh, (tid - NS) % NC, tid < NS + NC);
