@@ -100,7 +100,7 @@ dt_status attend(const dt_kv_cache& c, int bits, const dt_rope* rope, int32_t ba
     // the work division counts tiles in 32 bits
     const long long rows = (long long)M * (Hq / c.Hkv);
     const double tiles = (double)c.max_pages * c.page / 128 + M / 128 + 2;
-    if ((double)batch * c.Hkv * (rows / 256 + 1) * tiles * 5 > 4.2e9) return DT_ERR_UNSUPPORTED;
+    if ((double)batch * c.Hkv * (rows / 256 + 1) * (tiles * 6 + 30) > 4.2e9) return DT_ERR_UNSUPPORTED;
     if (!rows_ok(q, 2) || !rows_ok(k, 2) || !rows_ok(v, 2)) return DT_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !std::isfinite(scale)) return DT_ERR_INVALID_ARG;
     if (!out || !aligned16(out) || !status) return DT_ERR_INVALID_ARG;

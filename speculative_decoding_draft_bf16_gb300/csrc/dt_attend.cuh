@@ -22,14 +22,16 @@ struct AtReq {  // one request
     bool bad;
 };
 
-template <int ROWS>
+// BITS: of the cache's codes.
+template <int ROWS, int BITS = 8>
 struct AtPlan {
-    // Cost of a tile of a block; one of at most half of 256 rows costs less (3.5
-    // against 4.2 thousand clocks measured).
-    static constexpr uint32_t FULL = ROWS == 256 ? 5 : 1, PART = ROWS == 256 ? 4 : 1;
-    // What starting on a unit costs: its queries, its sums' way out.  64 trees of 61
-    // nodes with 14, 20, 26: 208, 183, 188 us; 64 single tokens with 1, 2, 3: 240, 233, 234.
-    static constexpr uint32_t HEAD = ROWS == 256 ? 20 : 2;
+    // Cost of a tile of a block; one of at most half of 256 rows costs less (of e4m3 3.5
+    // against 4.2 thousand clocks measured, of 4 bits 2.2 against 3.3).
+    static constexpr uint32_t FULL = ROWS == 256 ? (BITS == 4 ? 6 : 5) : 1, PART = ROWS == 256 ? 4 : 1;
+    // What starting on a unit costs: its queries, its new rows, its sums' way out.  64 trees
+    // of 61 nodes with 14, 20, 26: 208, 183, 188 us; 64 single tokens with 1, 2, 3: 240, 233,
+    // 234.
+    static constexpr uint32_t HEAD = ROWS == 256 ? (BITS == 4 ? 30 : 20) : 2;
     // Pieces of so few tiles at a unit's end are not worth starting on (one tree of 257
     // nodes over 8000 tokens without this 92 us, with 2 77, with 4 81).
     static constexpr int SNAP = ROWS == 256 ? 2 : 1;
@@ -80,9 +82,9 @@ struct AtShare {
 };
 
 // One warp: the share of CTA c of grid.  min_share: least cost worth a CTA.
-template <int ROWS>
+template <int ROWS, int BITS = 8>
 DT_DI void at_share(const DtAttend& a, uint32_t c, uint32_t grid, uint32_t min_share, AtShare* sh) {
-    using P = AtPlan<ROWS>;
+    using P = AtPlan<ROWS, BITS>;
     const int lane = threadIdx.x & 31;
     uint32_t total = 0;
     AtReq r;
@@ -134,9 +136,9 @@ DT_DI void at_share(const DtAttend& a, uint32_t c, uint32_t grid, uint32_t min_s
 }
 
 // Walks a CTA's segments: the tiles [t0, t1) of one unit each.
-template <int ROWS, int ATOM>
+template <int ROWS, int ATOM, int BITS = 8>
 struct AtWalk {
-    using P = AtPlan<ROWS>;
+    using P = AtPlan<ROWS, BITS>;
     int b, qb, h;       // the unit
     AtReq r;
     int rows, nt;       // its rows and tiles

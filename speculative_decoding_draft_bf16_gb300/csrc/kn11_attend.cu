@@ -37,8 +37,14 @@ constexpr int ROWS = 16, NW = 8, NT = NW * 32;
 // (long contexts do not notice).
 constexpr int ATOM = 4;              // tiles of the longest unit that is not split
 constexpr uint32_t MIN_SHARE = 4;    // least cost worth a CTA: the start and two tiles
-static_assert(MIN_SHARE >= AtPlan<ROWS>::HEAD + (AtPlan<ROWS>::SNAP + 1) * AtPlan<ROWS>::FULL,
-              "every CTA between a unit's ends has a tile of it");
+constexpr uint32_t MIN_SHARE4 = 4;   // the same over 4 bits
+template <int BITS>
+struct Division {
+    using Plan = AtPlan<ROWS, BITS>;
+    using Walk = AtWalk<ROWS, ATOM, BITS>;
+    static constexpr uint32_t LEAST = BITS == 4 ? MIN_SHARE4 : MIN_SHARE;
+    static_assert(LEAST >= Plan::HEAD + (Plan::SNAP + 1) * Plan::FULL, "every CTA between a unit's ends has a tile of it");
+};
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float HEADROOM = 5.f, LAZY = 8.f;
 
@@ -112,7 +118,7 @@ DT_DI uint32_t transposed8x8(uint32_t x) {
 template <int D, int NR, int BITS>
 struct Stream {
     using L = Lay<D, BITS>;
-    using Walk = AtWalk<ROWS, ATOM>;
+    using Walk = typename Division<BITS>::Walk;
     static constexpr int KS = D / 16;  // steps of K Q'
     static constexpr int TP = NR == 1 ? 2 : 1;  // tiles at a time of a 4-bit cache (two groups of rows and two tiles spill)
     static constexpr int NV = D / 8;   // columns of a lane in V' P': NV * g + j; two to an MMA
@@ -576,7 +582,7 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
     const int cta = blockIdx.x, ctas = gridDim.x;
     dt_pdl_trigger();
     dt_pdl_wait();
-    if (w == 0) at_share<ROWS>(a, cta, ctas, MIN_SHARE, &sh.share);
+    if (w == 0) at_share<ROWS, BITS>(a, cta, ctas, Division<BITS>::LEAST, &sh.share);
     at_zero_rest(a, cta, ctas, tid, NT);
     __syncthreads();
     const AtShare share = sh.share;
@@ -584,7 +590,7 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
     constexpr int ROW = D * BITS / 8;  // bytes of a token
     const uint32_t page_bytes = ((uint32_t)a.c.Hkv << lp) * ROW;
     const uint32_t my_fifo = dt_smem_addr(fifo) + w * L::STAGES * L::BYTES;
-    AtWalk<ROWS, ATOM> u;
+    typename Division<BITS>::Walk u;
     u.start(a, share);
     S x;
     x.qs = dt_smem_addr(qfrag);

@@ -68,8 +68,14 @@ constexpr int RING = 8;         // tiles whose page ids and scales are kept
 constexpr int SEGS = 4;         // segments the walk may be ahead
 constexpr int ATOM = 4;         // tiles of the longest unit that is not split (8: 64 trees of 61 nodes 206 : 183 us)
 constexpr uint32_t MIN_SHARE = 36;    // least cost worth a CTA: the start and three tiles of a full block
-static_assert(MIN_SHARE >= AtPlan<ROWS>::HEAD + (AtPlan<ROWS>::SNAP + 1) * AtPlan<ROWS>::FULL,
-              "every CTA between a unit's ends has a tile of it");
+constexpr uint32_t MIN_SHARE4 = 48;   // the same over 4 bits
+template <int BITS>
+struct Division {
+    using Plan = AtPlan<ROWS, BITS>;
+    using Walk = AtWalk<ROWS, ATOM, BITS>;
+    static constexpr uint32_t LEAST = BITS == 4 ? MIN_SHARE4 : MIN_SHARE;
+    static_assert(LEAST >= Plan::HEAD + (Plan::SNAP + 1) * Plan::FULL, "every CTA between a unit's ends has a tile of it");
+};
 constexpr int OWN_PARTS = 8;    // most parts of a unit that its last CTA joins to its own
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float HEADROOM = 5.f, LAZY = 8.f;
@@ -130,7 +136,7 @@ struct Lay {
 DT_DI void wait(uint64_t* bar, uint32_t phase, int* fail) {
     asm volatile(
         "{\n .reg .pred p;\n .reg .u32 n, f;\n mov.u32 n, 262144;\n"
-        "AGAIN:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1, 1000;\n @p bra DONE;\n"
+        "AGAIN:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n @p bra DONE;\n"
         " sub.u32 n, n, 1;\n setp.ne.u32 p, n, 0;\n @!p st.volatile.shared.u32 [%2], 1;\n"
         " ld.volatile.shared.u32 f, [%2];\n setp.eq.u32 p, f, 0;\n @p bra AGAIN;\nDONE:\n}\n" ::"r"(dt_smem_addr(bar)),
         "r"(phase), "r"(dt_smem_addr(fail))
@@ -143,7 +149,7 @@ DT_DI bool wait_long(uint64_t* bar, uint32_t phase, int* fail) {
     uint32_t n = 1048576;
     asm volatile(
         "{\n .reg .pred p;\n"
-        "AGAIN:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n @p bra DONE;\n"
+        "AGAIN:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
         " sub.u32 %0, %0, 1;\n setp.ne.u32 p, %0, 0;\n @p bra AGAIN;\n st.volatile.shared.u32 [%3], 1;\nDONE:\n}\n"
         : "+r"(n)
         : "r"(dt_smem_addr(bar)), "r"(phase), "r"(dt_smem_addr(fail))
@@ -170,8 +176,9 @@ DT_DI bool failed(const Shared* sh) { return *(const volatile int*)&sh->fail != 
 
 // The thread that walks the share, up to SEGS segments ahead of the roles.  When a wait
 // of a role has run out, it ends the walk.
+template <int BITS>
 DT_DI void walk_share(const DtAttend& a, Shared* sh, int cta) {
-    AtWalk<ROWS, ATOM> u;
+    typename Division<BITS>::Walk u;
     u.start(a, sh->share);
     uint32_t i = 0;
     for (bool more = true; more; ++i) {
@@ -274,6 +281,20 @@ DT_DI void store_codes4(uint32_t a, const uint4& q, uint32_t scales) {
     }
 }
 
+// A chunk pair that is not rotated, in place of a DtPair: half the registers, so that more
+// rows are in flight.
+struct Straight {
+    DtRaw8<uint16_t> a, b;
+    DT_DI void load(const uint16_t* row, int p, const dt_rope&, int) {
+        a.load(row + 16 * p);
+        b.load(row + 16 * p + 8);
+    }
+    DT_DI void rotated(int, const dt_rope&, float (&x)[8], float (&y)[8]) const {
+        a.values(x);
+        b.values(y);
+    }
+};
+
 // The converter warps: 128 threads for the keys, 128 for the values, one code (the
 // instruction caches nearest the SM's quarters hold little more than the loops of
 // the roles that run there).  BITS: of a code, e4m3 or e2m1.
@@ -309,7 +330,9 @@ struct Conv {
     // One tile of new rows, from row m0: keys rotated, and scaled by powers of two when
     // the rows' largest magnitudes are not all in [2^-4, 2^15), where fp16 is exact enough:
     // by one for the tile when that brings them there, else by one for each row, so that
-    // what other rows hold does not matter.
+    // what other rows hold does not matter.  Pair: how chunk pairs are read (DtPair, Straight),
+    // U: rows in flight.
+    template <class Pair, int U>
     static DT_DI void fresh(const DtAttend& a, const Seg& u, bool keys, int m0, int ct, Shared* sh, uint32_t g,
                             uint32_t tile) {
         Ring* ring = &sh->ring[g % RING];
@@ -327,7 +350,6 @@ struct Conv {
         const int pr = ct % PPR;  // this thread's chunk pair of rows ct / PPR + i * RPI
         int c0, c1;
         dt_pair_chunks(pr, rope, c0, c1);
-        constexpr int U = D == 64 ? 2 : 1;  // rows in flight (two at D = 128 make the loop over cached tiles spill)
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {  // the second one when the tile needs scales
 #pragma unroll 1
@@ -341,7 +363,7 @@ struct Conv {
                     }
                     continue;
                 }
-                DtPair<uint16_t> raw[U];
+                Pair raw[U];
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
                     const int r = min(ct / PPR + (i0 + k) * RPI, left - 1);
@@ -475,7 +497,12 @@ struct Conv {
                 const int s = g % STAGES;
                 wait(&free_[s], (g / STAGES + 1) & 1, &sh->fail);
                 wait(&sh->idfull[g % RING], (g / RING) & 1, &sh->fail);  // the ring's slot is free
-                fresh(a, u, keys, (j - u.ctx) * AT_TILE, ct, sh, g, base + s * L::TILE);
+                // (rows loaded before these waits take registers that the loop over cached tiles
+                // needs: 16 trees of 257 nodes 881 us instead of 869)
+                if (BITS == 4 && (!keys || a.rope.rot == 0))
+                    fresh<Straight, 4>(a, u, keys, (j - u.ctx) * AT_TILE, ct, sh, g, base + s * L::TILE);
+                else  // two rotating rows in flight at D = 128 make that loop spill
+                    fresh<DtPair<uint16_t>, D == 64 ? 2 : 1>(a, u, keys, (j - u.ctx) * AT_TILE, ct, sh, g, base + s * L::TILE);
                 if (ct == 0) dt_mbar_arrive(&sh->scfull[g % RING]);
                 stored(s);
             }
@@ -648,8 +675,10 @@ struct Soft {
     using L = Lay<D>;
 
     // The block's rows, rotated, scaled by a power of two and converted.
+    template <class Pair, int U>
     static DT_DI void queries(const DtAttend& a, const Seg& u, unsigned char* sm, Shared* sh, int tid) {
-        constexpr int PPR = D / 16, RPI = NS / PPR, U = 2;  // chunk pairs per row, rows per pass
+        constexpr int PPR = D / 16, RPI = NS / PPR;  // chunk pairs per row, rows per pass
+        static_assert(TQ % (U * RPI) == 0, "whole slots");
         const uint32_t G = a.G;
         const int tiles = u.rows > TQ ? 2 : 1;
         const uint32_t qb = dt_smem_addr(sm + L::Q);
@@ -665,7 +694,7 @@ struct Soft {
         const uint16_t* base = (const uint16_t*)a.q.ptr + u.b * a.q.stride_b + (size_t)u.h * G * a.q.stride_h;
 #pragma unroll 1
         for (int r0 = tid / PPR; r0 < tiles * TQ; r0 += U * RPI) {
-            DtPair<uint16_t> raw[U];
+            Pair raw[U];
 #pragma unroll
             for (int k = 0; k < U; ++k)  // U rows in flight
                 raw[k].load(base + sh->qoff[r0 + k * RPI], pr, a.rope, sh->qpos[r0 + k * RPI]);
@@ -700,14 +729,16 @@ struct Soft {
     }
 
     // The row's mask of 64 tokens of a tile that is not wholly visible.
-    static DT_DI uint2 mask_words(const DtAttend& a, const Seg& u, int t, int h, int row) {
+    static DT_DI int node_of(const DtAttend& a, const Seg& u, int row) {
+        return (int)(((uint32_t)u.qb * ROWS + row) / (uint32_t)(a.G));
+    }
+    static DT_DI uint2 mask_words(const DtAttend& a, const Seg& u, int t, int h, int row, int node) {
         if (t < u.ctx) {
             const int left = u.len - t * AT_TILE - 64 * h;
             return make_uint2(left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u,
                               left >= 64 ? ~0u : left <= 32 ? 0u : (1u << (left - 32)) - 1u);
         }
         if (row >= u.rows) return make_uint2(0u, 0u);
-        const int node = (int)(((uint32_t)u.qb * ROWS + row) / (uint32_t)(a.G));
         const int m0 = (t - u.ctx) * AT_TILE + 64 * h;
         return make_uint2(at_mask_word(a, u.b, node, m0, u.n), at_mask_word(a, u.b, node, m0 + 32, u.n));
     }
@@ -754,7 +785,12 @@ struct Soft {
             return;
         }
         uint32_t x[64];
-        const float4 ks = sc->ks, lv = sc->lv, iv = sc->iv;
+        float4 ks = sc->ks, lv = sc->lv, iv = sc->iv;
+        if constexpr (BITS == 4) {  // one scale for the tile
+            ks.y = ks.z = ks.w = ks.x;
+            lv.y = lv.z = lv.w = lv.x;
+            iv.y = iv.z = iv.w = iv.x;
+        }
         dt_tmem_ld64(ts, x);
         const float ka[4] = {at_factor(rowc, ks.x), at_factor(rowc, ks.y), at_factor(rowc, ks.z), at_factor(rowc, ks.w)};
         const float l4[4] = {lv.x, lv.y, lv.z, lv.w}, i4[4] = {iv.x, iv.y, iv.z, iv.w};
@@ -901,7 +937,8 @@ struct Soft {
             const bool dual = u.rows > TQ;
             const int nt = u.t1 - u.t0, hop = dual ? 1 : 2, len = u.len;
             const int row = dual ? tid : tid % TQ;  // within the block
-            queries(a, u, sm, sh, tid);
+            if (BITS == 4 && a.rope.rot == 0) queries<Straight, D == 64 ? 2 : 4>(a, u, sm, sh, tid);
+            else queries<DtPair<uint16_t>, 2>(a, u, sm, sh, tid);
             asm volatile("bar.sync 2, 256;" ::: "memory");
             const float rowc = sh->qscale[row];
             float m = NEG_INF, l = 0.f;
@@ -909,6 +946,7 @@ struct Soft {
             const int clear = len / AT_TILE - u.t0;  // tiles before this one are wholly visible
             uint32_t pa = ph & 1;                    // phase of both halves' scores
             int lt = dual ? 0 : s;
+            const int node = BITS == 4 ? node_of(a, u, row) : 0;
             if constexpr (BITS == 4) {
                 const float ka = at_factor(rowc, 1.f);
                 const int last = min(clear, nt);
@@ -930,6 +968,11 @@ struct Soft {
             for (; lt < nt; lt += hop, pa ^= 1) {
                 const uint32_t g = g0 + lt;
                 const Ring* ring = &sh->ring[g % RING];
+                uint2 mk2[2];  // of a 4-bit cache: both halves' masks, on their way while the scales are waited for
+                if constexpr (BITS == 4) {
+                    mk2[0] = mask_words(a, u, u.t0 + lt, 0, row, node);
+                    mk2[1] = mask_words(a, u, u.t0 + lt, 1, row, node);
+                }
                 wait(&sh->scfull[g % RING], (g / RING) & 1, &sh->fail);
                 // (under `clear`, known already: without it 16 trees of 257 nodes 1.14 ms instead of 1.13)
                 if (lt >= clear && u.t0 + lt >= u.ctx && (sh->apart[g % RING].yes[0] | sh->apart[g % RING].yes[1])) break;
@@ -941,7 +984,7 @@ struct Soft {
                     const bool masked = lt >= clear;
                     uint2 mk = make_uint2(0u, 0u);
                     if (masked) {
-                        mk = mask_words(a, u, u.t0 + lt, h, row);
+                        mk = BITS == 4 ? (h ? mk2[1] : mk2[0]) : mask_words(a, u, u.t0 + lt, h, row, node_of(a, u, row));
                         if (u.t0 + lt >= u.ctx)
                             poison |= ((mk.x & (ring->bad[0][2 * h] | ring->bad[1][2 * h])) |
                                        (mk.y & (ring->bad[0][2 * h + 1] | ring->bad[1][2 * h + 1]))) != 0u;
@@ -964,7 +1007,7 @@ struct Soft {
                 wait(&sh->scfull[g % RING], (g / RING) & 1, &sh->fail);
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
-                    const uint2 mk = mask_words(a, u, u.t0 + lt, h, row);
+                    const uint2 mk = mask_words(a, u, u.t0 + lt, h, row, node_of(a, u, row));
                     poison |= ((mk.x & (ring->bad[0][2 * h] | ring->bad[1][2 * h])) |
                                (mk.y & (ring->bad[0][2 * h + 1] | ring->bad[1][2 * h + 1]))) != 0u;
                     wait(&sh->sfull[s][h], pa, &sh->fail);
@@ -1324,7 +1367,7 @@ __global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtA
     if (tid < RING * 8) sh->ring[tid >> 3].id[tid & 7] = 0;  // a page for whoever gives up waiting for one
     dt_pdl_trigger();
     dt_pdl_wait();
-    if (wid == 1) at_share<ROWS>(a, cta, ctas, MIN_SHARE, &sh->share);
+    if (wid == 1) at_share<ROWS, BITS>(a, cta, ctas, Division<BITS>::LEAST, &sh->share);
     dt_tc_fence_before();
     __syncthreads();
     dt_tc_fence_after();
@@ -1341,7 +1384,7 @@ __global__ void __launch_bounds__(NT, 1) kn12_kernel(const __grid_constant__ DtA
         constexpr int W0 = (NS + 2 * NC) / 32;
         if (wid == W0 || wid == W0 + 3)
             issue_slot<D>(sm, sh, __shfl_sync(0xffffffffu, tmem, 0), __shfl_sync(0xffffffffu, wid != W0, 0));
-        if (tid == NS + 2 * NC + 32) walk_share(a, sh, cta);
+        if (tid == NS + 2 * NC + 32) walk_share<BITS>(a, sh, cta);
         if (wid == W0 + 2) {
             if ((tid & 31) == 0 && !dt_probe_wait(&sh->probe, probe)) sh->fail = 1;
             __syncwarp();
