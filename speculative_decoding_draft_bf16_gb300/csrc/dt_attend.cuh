@@ -32,6 +32,9 @@ struct AtPlan {
     // of 61 nodes with 14, 20, 26: 208, 183, 188 us; 64 single tokens with 1, 2, 3: 240, 233,
     // 234.
     static constexpr uint32_t HEAD = ROWS == 256 ? (BITS == 4 ? 30 : 20) : 2;
+    // The same of 16 rows over 4 bits when every CTA has work (see AtShareLead): a unit's start
+    // and end take the time of so many tiles then.
+    static constexpr uint32_t HEAD_FULL = 6;
     // Pieces of so few tiles at a unit's end are not worth starting on (one tree of 257
     // nodes over 8000 tokens without this 92 us, with 2 77, with 4 81).
     static constexpr int SNAP = ROWS == 256 ? 2 : 1;
@@ -54,9 +57,9 @@ struct AtPlan {
     static DT_DI int block_tiles(const DtAttend& a, const AtReq& r, int qb) {
         return r.ctx + (block_new(a, r, qb) + AT_TILE - 1) / AT_TILE;
     }
-    static DT_DI uint32_t cost(const DtAttend& a, const AtReq& r) {
+    static DT_DI uint32_t cost(const DtAttend& a, const AtReq& r, uint32_t head = HEAD) {
         if (r.nqb == 0) return 0;
-        uint32_t s = block_tiles(a, r, r.nqb - 1) * weight(block_rows(a, r, r.nqb - 1)) + r.nqb * HEAD;
+        uint32_t s = block_tiles(a, r, r.nqb - 1) * weight(block_rows(a, r, r.nqb - 1)) + r.nqb * head;
         if (a.mask) {
             s += (r.nqb - 1) * block_tiles(a, r, 0) * FULL;
         } else {
@@ -81,23 +84,67 @@ struct AtShare {
     }
 };
 
+// The cost of starting on a unit that the walk counts with.
+template <class Plan>
+DT_DI uint32_t at_head(const AtShare&) { return Plan::HEAD; }
+
+// A division with a choice of HEAD, and with LEAD / 256 of a share more for each CTA of the
+// first half when all of a grid of two CTAs to an SM work: of two CTAs on an SM the one that
+// came first issues first.
+template <int LEAD>
+struct AtShareLead : AtShare {
+    uint32_t half;  // CTAs of the first half; 0: shares are equal
+    uint32_t head;
+    DT_DI uint32_t more() const { return each * LEAD / 256; }
+    DT_DI uint32_t start_of(uint32_t c) const { return AtShare::start_of(c) + (c < half ? c : 2 * half - c) * (half ? more() : 0u); }
+    DT_DI int owner(uint32_t x) const {
+        if (half == 0) return AtShare::owner(x);
+        const uint32_t wide = half * (each + more());
+        int c = (int)(x < wide ? x / (each + more() + 1) : half + (x - wide) / (each - more() + 1));  // near it
+        c = min(c, ctas - 1);
+        while (start_of(c) > x) --c;
+        while (c + 1 < ctas && start_of(c + 1) <= x) ++c;
+        return c;
+    }
+};
+template <class Plan, int LEAD>
+DT_DI uint32_t at_head(const AtShareLead<LEAD>& s) { return s.head; }
+
+// How many CTAs work, and the cost of all units (whose tiles cost `tiles`).  A division with
+// a choice takes the larger head when that still gives every CTA of the grid a share.
+template <class Plan>
+DT_DI void at_choose(AtShare& s, uint32_t tiles, uint32_t units, uint32_t grid, uint32_t min_share, uint32_t& total) {
+    total = tiles + units * Plan::HEAD;
+    s.ctas = (int)max(1u, min(total / min_share, grid));
+}
+template <class Plan, int LEAD>
+DT_DI void at_choose(AtShareLead<LEAD>& s, uint32_t tiles, uint32_t units, uint32_t grid, uint32_t min_share, uint32_t& total) {
+    const uint32_t more = Plan::HEAD_FULL - Plan::HEAD;
+    const bool full = tiles + units * Plan::HEAD_FULL >= grid * (min_share + more);
+    s.head = full ? Plan::HEAD_FULL : Plan::HEAD;
+    total = tiles + units * s.head;
+    s.ctas = (int)max(1u, min(total / (min_share + (full ? more : 0u)), grid));
+    s.half = full && grid % 2 == 0 ? grid / 2 : 0;
+}
+
 // One warp: the share of CTA c of grid.  min_share: least cost worth a CTA.
-template <int ROWS, int BITS = 8>
-DT_DI void at_share(const DtAttend& a, uint32_t c, uint32_t grid, uint32_t min_share, AtShare* sh) {
+template <int ROWS, int BITS = 8, class Share>
+DT_DI void at_share(const DtAttend& a, uint32_t c, uint32_t grid, uint32_t min_share, Share* sh) {
     using P = AtPlan<ROWS, BITS>;
     const int lane = threadIdx.x & 31;
-    uint32_t total = 0;
+    uint32_t tiles = 0, units = 0, total;
     AtReq r;
 #pragma unroll 1
     for (int b = lane; b < a.batch; b += 32) {
         r = P::req(a, b);
         if (r.bad && c == 0) atomicOr(&a.status[b], DT_DEV_BAD_CACHE);
-        total += P::cost(a, r);
+        tiles += P::cost(a, r, 0);
+        units += r.nqb * a.c.Hkv;
     }
-    const uint32_t own = total;  // with up to 32 requests, of the lane's only one
-    total = __reduce_add_sync(0xffffffffu, total);
-    AtShare s;
-    s.ctas = (int)max(1u, min(total / min_share, grid));
+    const uint32_t own_tiles = tiles, own_units = units;  // with up to 32 requests, of the lane's only one
+    Share s;
+    at_choose<P>(s, __reduce_add_sync(0xffffffffu, tiles), __reduce_add_sync(0xffffffffu, units), grid, min_share, total);
+    const uint32_t head = at_head<P>(s), own = own_tiles + own_units * head;
     s.each = total / s.ctas;
     s.rest = total % s.ctas;
     s.beg = c < s.ctas ? s.start_of(c) : total;
@@ -114,7 +161,7 @@ DT_DI void at_share(const DtAttend& a, uint32_t c, uint32_t grid, uint32_t min_s
             mine = 0;
             if (b < a.batch) {
                 r = P::req(a, b);
-                mine = P::cost(a, r);
+                mine = P::cost(a, r, head);
             }
         }
         const uint32_t inc = (uint32_t)dt_warp_incl_scan((int)mine);
@@ -142,7 +189,8 @@ struct AtWalk {
     int b, qb, h;       // the unit
     AtReq r;
     int rows, nt;       // its rows and tiles
-    uint32_t w, at;     // its tile cost and first cost position; tile 0 costs P::HEAD more
+    uint32_t head;      // what starting on a unit costs
+    uint32_t w, at;     // its tile cost and first cost position; tile 0 costs `head` more
     int t0, t1;         // this CTA's tiles of it
     int first, segs;    // the CTA that holds tile 0, and how many CTAs share it
 
@@ -151,7 +199,9 @@ struct AtWalk {
         nt = P::block_tiles(a, r, qb);
         w = P::weight(rows);
     }
-    DT_DI void start(const DtAttend& a, const AtShare& s) {
+    template <class Share>
+    DT_DI void start(const DtAttend& a, const Share& s) {
+        head = at_head<P>(s);
         b = s.b0;
         qb = h = 0;
         at = s.b0_at;
@@ -160,23 +210,24 @@ struct AtWalk {
         unit(a);
         // whole blocks before the share (Hkv units of one cost each)
 #pragma unroll 1
-        while (at + a.c.Hkv * (nt * w + P::HEAD) <= s.beg) {
-            at += a.c.Hkv * (nt * w + P::HEAD);
+        while (at + a.c.Hkv * (nt * w + head) <= s.beg) {
+            at += a.c.Hkv * (nt * w + head);
             ++qb;
             unit(a);
         }
-        h = (int)((s.beg - at) / (nt * w + P::HEAD));
-        at += h * (nt * w + P::HEAD);
+        h = (int)((s.beg - at) / (nt * w + head));
+        at += h * (nt * w + head);
     }
     // The first tile that starts at cost position x or later; no cut leaves a piece
     // of SNAP tiles or fewer at either end of the unit.
     DT_DI int tile_from(uint32_t x) const {
-        if (x <= at + P::HEAD + P::SNAP * w) return 0;
-        const int t = (int)((x - at - P::HEAD + w - 1) / w);
+        if (x <= at + head + P::SNAP * w) return 0;
+        const int t = (int)((x - at - head + w - 1) / w);
         return t >= nt - P::SNAP ? nt : t;
     }
     // The next segment, or false.  A unit of at most ATOM tiles is not split.
-    DT_DI bool next(const DtAttend& a, const AtShare& s, int c) {
+    template <class Share>
+    DT_DI bool next(const DtAttend& a, const Share& s, int c) {
         static_assert(ATOM >= 2 * P::SNAP, "a cut is near one end of a unit only");
 #pragma unroll 1
         while (b < a.batch && at < s.end) {
@@ -188,7 +239,7 @@ struct AtWalk {
             } else {
                 t0 = tile_from(s.beg);
                 t1 = tile_from(s.end);
-                int last = s.owner(at + P::HEAD + w * (nt - 1));
+                int last = s.owner(at + head + w * (nt - 1));
                 if (tile_from(s.start_of(first + 1)) == 0) ++first;
                 if (tile_from(s.start_of(last)) == nt) --last;
                 segs = last - first + 1;
@@ -199,7 +250,7 @@ struct AtWalk {
         return false;
     }
     DT_DI void step(const DtAttend& a) {  // to the next unit
-        at += nt * w + P::HEAD;
+        at += nt * w + head;
         if (++h < a.c.Hkv) return;
         h = 0;
         ++qb;

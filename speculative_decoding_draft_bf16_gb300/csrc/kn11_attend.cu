@@ -28,6 +28,8 @@
 // between 165 and 228 us, by where on the chip an SM lies: that spread, not the loop, is
 // what is left.  One token over 1000: 15.9 us, the latency of the share, pages, copies, new
 // row and join in turn (15.6 before each new row had a scale of its own).
+#include <type_traits>
+
 #include "dt_attend.cuh"
 
 namespace {
@@ -38,10 +40,12 @@ constexpr int ROWS = 16, NW = 8, NT = NW * 32;
 constexpr int ATOM = 4;              // tiles of the longest unit that is not split
 constexpr uint32_t MIN_SHARE = 4;    // least cost worth a CTA: the start and two tiles
 constexpr uint32_t MIN_SHARE4 = 4;   // the same over 4 bits
+constexpr int LEAD = 8;
 template <int BITS>
 struct Division {
     using Plan = AtPlan<ROWS, BITS>;
     using Walk = AtWalk<ROWS, ATOM, BITS>;
+    using Share = std::conditional_t<BITS == 4, AtShareLead<LEAD>, AtShare>;
     static constexpr uint32_t LEAST = BITS == 4 ? MIN_SHARE4 : MIN_SHARE;
     static_assert(LEAST >= Plan::HEAD + (Plan::SNAP + 1) * Plan::FULL, "every CTA between a unit's ends has a tile of it");
 };
@@ -63,8 +67,9 @@ struct Lay {
     static constexpr size_t SMEM = FIFO > JOIN ? FIFO : JOIN;
 };
 
+template <int BITS>
 struct Shared {
-    AtShare share;
+    typename Division<BITS>::Share share;
     float m[NW][ROWS], l[NW][ROWS], w[NW][ROWS];
     int last;
 };
@@ -134,6 +139,17 @@ struct Stream {
 
     // 16 elements from 16 * c of a head vector, rotated.
     static DT_DI void pick16(const uint16_t* row, int c, const dt_rope& r, int at, float (&x)[16]) {
+        if (BITS == 4 && r.rot == 0) {  // short and with few loads: where it is called, their latency counts
+            DtRaw8<uint16_t> lo, hi;
+            float u[8], v[8];
+            lo.load(row + 16 * c);
+            hi.load(row + 16 * c + 8);
+            lo.values(u);
+            hi.values(v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = u[e], x[8 + e] = v[e];
+            return;
+        }
         DtTurned8<uint16_t> raw[2];
         float y[8];
 #pragma unroll
@@ -437,6 +453,73 @@ struct Stream {
         }
     }
 
+    // The first of a warp's sums, from one new row that is not rotated: its score in fp32, its
+    // weight 2^HEADROOM.  A single token's own row comes once to every unit and is work for one
+    // warp, so this is short: fresh() takes 6000 clocks, most of them to fetch its instructions.
+    DT_DI void fresh_one(const DtAttend& a, const Walk& u, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+        const uint16_t* kp = (const uint16_t*)a.k.ptr + u.b * a.k.stride_b + u.h * a.k.stride_h;
+        const uint16_t* vp = (const uint16_t*)a.v.ptr + u.b * a.v.stride_b + u.h * a.v.stride_h;
+        uint4 kw[2 * L::KC], vw[L::VB / 8];
+#pragma unroll
+        for (int j = 0; j < 2 * L::KC; ++j) kw[j] = *(const uint4*)(kp + run_of(t, 0) * 16 + 8 * j);  // KC runs in a row
+#pragma unroll
+        for (int j = 0; j < L::VB / 8; ++j) vw[j] = *(const uint4*)(vp + L::VB * g + 8 * j);
+        bool bad = false;
+        float v[L::VB], dot[NR];
+        auto finite = [&](float x) {  // zeros for what is not, which `bad` reports
+            const bool odd = !(fabsf(x) < __int_as_float(0x7F800000));
+            bad |= odd;
+            return odd ? 0.f : x;
+        };
+#pragma unroll
+        for (int j = 0; j < L::VB / 8; ++j) {
+            float y[8];
+            dt_vec_vals<uint16_t>(vw[j], y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[8 * j + e] = finite(y[e]);
+        }
+#pragma unroll
+        for (int i = 0; i < NR; ++i) dot[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2 * L::KC; ++j) {
+            float y[8];
+            dt_vec_vals<uint16_t>(kw[j], y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = finite(y[e]);
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                uint32_t q[4];  // the row's elements 8 j on of the lane's run
+                lds<4>(qs + ((j * NR + i) * 32 + lane) * 16, q);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 z = __half22float2(*(const __half2*)&q[e]);
+                    dot[i] = __fmaf_rn(z.y, y[2 * e + 1], __fmaf_rn(z.x, y[2 * e], dot[i]));
+                }
+            }
+        }
+        bad = __any_sync(0xffffffffu, bad);
+        clear();
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {  // of row g + 8 i
+            dot[i] = __fadd_rn(dot[i], __shfl_xor_sync(0xffffffffu, dot[i], 1));
+            dot[i] = __fadd_rn(dot[i], __shfl_xor_sync(0xffffffffu, dot[i], 2));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float s = __fmul_rn(__shfl_sync(0xffffffffu, dot[i], 8 * t + 4 * e), rowc[i][e]);
+                const int r = 2 * t + e + 8 * i;
+                if (r >= u.rows || !(at_mask_word(a, u.b, r / a.G, 0, 1) & 1)) continue;
+                const float w = s == s ? 32.f : s;
+                m[i][e] = s == s ? s - HEADROOM : -__int_as_float(0x7F800000);
+                if (g == 0) l[i][e] = w;
+                if (bad) l[i][e] = __int_as_float(0x7FC00000);
+#pragma unroll
+                for (int j = 0; j < NV; ++j) o[j / 2][i][2 * (j & 1) + e] = __fmul_rn(w, v[j]);
+            }
+        }
+    }
+    static_assert(HEADROOM == 5.f, "2^HEADROOM above");
+
     // The first of a warp's sums, from up to 16 new rows: rotated, each scaled by a power of
     // two to a largest magnitude below 4 (one of its own, so that what other rows hold does
     // not matter), elements that are not finite replaced by zeros and reported to the rows
@@ -446,7 +529,21 @@ struct Stream {
         const uint16_t* kp = (const uint16_t*)a.k.ptr + u.b * a.k.stride_b + u.h * a.k.stride_h;
         const uint16_t* vp = (const uint16_t*)a.v.ptr + u.b * a.v.stride_b + u.h * a.v.stride_h;
         uint32_t bad = 0;  // bit per row
-        if (lane < n) {
+        uint32_t v[4][L::VB / 2];
+        auto values = [&]() {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int row = 2 * t + (k & 1) + 8 * (k >> 1);
+#pragma unroll
+                for (int e = 0; e < L::VB / 2; e += 4) {
+                    uint4 y = make_uint4(0u, 0u, 0u, 0u);
+                    if (row < n && (k < 2 || n > 8)) y = *(const uint4*)(vp + row * a.v.stride_n + L::VB * g + 2 * e);
+                    v[k][e] = y.x, v[k][e + 1] = y.y, v[k][e + 2] = y.z, v[k][e + 3] = y.w;
+                }
+            }
+        };
+        if (BITS == 4) values();  // with the keys, whose products they wait for
+        if (BITS == 8 && lane < n) {
             for (int e = 0; e < D; e += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(vp + lane * a.v.stride_n + e));
         }
         float c[NR][4] = {};
@@ -491,17 +588,7 @@ struct Stream {
                 mma(c[i], f, q[0], q[1]);
             }
         }
-        uint32_t v[4][L::VB / 2];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int row = 2 * t + (k & 1) + 8 * (k >> 1);
-#pragma unroll
-            for (int e = 0; e < L::VB / 2; e += 4) {
-                uint4 y = make_uint4(0u, 0u, 0u, 0u);
-                if (row < n && (k < 2 || n > 8)) y = *(const uint4*)(vp + row * a.v.stride_n + L::VB * g + 2 * e);
-                v[k][e] = y.x, v[k][e + 1] = y.y, v[k][e + 2] = y.z, v[k][e + 3] = y.w;
-            }
-        }
+        if (BITS == 8) values();
         float fv[4];  // of rows as v's
         int ev[4];
 #pragma unroll
@@ -575,7 +662,7 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
     using S = Stream<D, NR, BITS>;
     constexpr int NV = S::NV;
     extern __shared__ __align__(128) unsigned char fifo[];
-    __shared__ Shared sh;
+    __shared__ Shared<BITS> sh;
     __shared__ __align__(16) uint32_t qfrag[S::KS * NR * 64];
     const float NEG_INF = -__int_as_float(0x7F800000);
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -585,7 +672,7 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
     if (w == 0) at_share<ROWS, BITS>(a, cta, ctas, Division<BITS>::LEAST, &sh.share);
     at_zero_rest(a, cta, ctas, tid, NT);
     __syncthreads();
-    const AtShare share = sh.share;
+    const auto share = sh.share;
     const int lp = 31 - __clz(a.c.page), low = a.c.page - 1;
     constexpr int ROW = D * BITS / 8;  // bytes of a token
     const uint32_t page_bytes = ((uint32_t)a.c.Hkv << lp) * ROW;
@@ -704,7 +791,10 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
         x.queries(a, u, lane);
         __syncwarp();
         // new rows while the first copies are on their way
-        if (w == 0 && u.t1 > u.r.ctx) x.fresh(a, u, lane);
+        if (w == 0 && u.t1 > u.r.ctx) {
+            if (BITS == 4 && u.r.n == 1 && a.rope.rot == 0) x.fresh_one(a, u, lane);
+            else x.fresh(a, u, lane);
+        }
         else x.clear();
         if constexpr (BITS == 4) {
             int left = len - u.t0 * AT_TILE - w * 16;
@@ -855,7 +945,7 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
 template <int D, int NR, int BITS>
 cudaError_t launch(const DtAttend& a, void* workspace, int ctas, cudaStream_t st) {
     constexpr size_t smem = Lay<D, BITS>::SMEM;
-    static_assert(2 * (smem + sizeof(Shared) + 4096 + 1024) <= 228 * 1024, "two CTAs per SM");
+    static_assert(2 * (smem + sizeof(Shared<BITS>) + 4096 + 1024) <= 228 * 1024, "two CTAs per SM");
     cudaError_t e = cudaFuncSetAttribute(kn11_kernel<D, NR, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     DtLaunch lc(dim3(ctas), dim3(NT), smem, st);

@@ -20,9 +20,18 @@ def test_every_tile_falls_to_one_cta(kernel, tmp_path):
     (tmp_path / "division_body.h").write_text(body)
     with open(os.path.join(HERE, "attention_division.cpp")) as f:
         program = f.read()
-    for form in ("AtPlan<K_ROWS", "AtWalk<K_ROWS, K_ATOM"):
-        assert form + ">" in program
-        program = program.replace(form + ">", form + ", 4>")
+    forms = [("AtPlan<K_ROWS>", "AtPlan<K_ROWS, 4>"), ("AtWalk<K_ROWS, K_ATOM>", "AtWalk<K_ROWS, K_ATOM, 4>")]
+    if kernel == "kn11_attend.cu":
+        # the larger head, and shares of two sizes, in every second batch
+        forms += [("AtShare s;", "AtShareLead<%s> s; s.head = head, s.half = lead ? grid / 2 : 0;" % constant(kernel, "LEAD")),
+                  ("long long total = 0;", "const bool full = it % 2; const uint32_t head = full ? Plan::HEAD_FULL : Plan::HEAD;"
+                   " const uint32_t least = K_MIN_SHARE + head - Plan::HEAD; long long total = 0;"),
+                  ("Plan::req(a, b));", "Plan::req(a, b), head);"), ("Plan::cost(a, r)", "Plan::cost(a, r, head)"),
+                  ("total / K_MIN_SHARE", "total / least"),
+                  ("std::map<std::tuple", "const bool lead = full && ctas == grid && grid % 2 == 0; std::map<std::tuple")]
+    for old, new in forms:
+        assert old in program, old
+        program = program.replace(old, new)
     (tmp_path / "division.cpp").write_text(program)
     exe = str(tmp_path / "division")
     flags = ["-DK_%s=%s" % (n, constant(kernel, c)) for n, c in (("ROWS", "ROWS"), ("ATOM", "ATOM"), ("MIN_SHARE", "MIN_SHARE4"))]
