@@ -1,5 +1,6 @@
 // dt_abi_target.cu -- C ABI of the target-side calls: the paged caches, tree
 // attention, head norms and token log-probabilities (include/dtree.h).  Argument checks only.
+#include <atomic>
 #include <cmath>
 
 #include <cuda_runtime.h>
@@ -21,14 +22,19 @@ dt_status cuda_status(cudaError_t e) {
 // more rows the streaming kernel's sums would leave its registers.
 constexpr long long kStreamRows = 16;
 
+// SMs of the current device, asked for once per device.
 int sm_count() {
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+    const bool here = cudaGetDevice(&dev) == cudaSuccess;
+    if (here && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (!here || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
         (void)cudaGetLastError();
         return 152;
     }
-    return n < 512 ? n : 512;
+    n = n < 512 ? n : 512;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }

@@ -171,7 +171,10 @@ def _stream(stream):
     if stream is not None:
         return ctypes.c_void_p(stream.cuda_stream)
     # the current stream's handle, without a Stream object (4 us of host time per call)
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _on(stream):
@@ -675,12 +678,13 @@ class Rope:
         self._ref = ctypes.byref(self._struct)
 
 
-def _head_rows(t, batch, M, H, D, name):
-    """dt_rows of [batch, M, H, D]: any strides with dense, 16-byte aligned head vectors."""
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+def _head_rows(t, shape, name, device):
+    """dt_rows of [batch, M, H, D]: any strides with dense, 16-byte aligned head vectors.
+    device: the current one (torch.cuda.current_device(), read once per call)."""
+    if t.get_device() != device:
         raise ValueError("%s must be a CUDA tensor on the current device" % name)
-    if t.shape != (batch, M, H, D):
-        raise ValueError("%s must be %s, got %s" % (name, (batch, M, H, D), tuple(t.shape)))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, shape, tuple(t.shape)))
     sb, sn, sh, sd = t.stride()
     if sd != 1:
         raise ValueError("%s must be dense in its last dimension" % name)
@@ -696,11 +700,11 @@ def kv_append(cache, k, v, rope=None, rows=None, count=None, count_add=0, len_ou
     their position on the way, both stored in the cache's form.  rows [batch, N] int32 picks rows (the walk's acc_nodes),
     count [batch] int32 + count_add says how many (its acc_len, 1); len_out [batch] gets the new lengths;
     status [batch] int32 is OR-ed with DT_DEV_BAD_CACHE for a request that does not fit; returned."""
-    batch, M = cache.batch, k.shape[1]
+    batch, M, device = cache.batch, k.shape[1], torch.cuda.current_device()
     if k.dtype != v.dtype:
         raise TypeError("k (%s) and v (%s) must share one dtype" % (k.dtype, v.dtype))
-    kr = _head_rows(k, batch, M, cache.Hkv, cache.D, "k")
-    vr = _head_rows(v, batch, M, cache.Hkv, cache.D, "v")
+    shape = (batch, M, cache.Hkv, cache.D)
+    kr, vr = _head_rows(k, shape, "k", device), _head_rows(v, shape, "v", device)
     N = M
     if rows is not None:
         _need(rows, torch.int32, "rows")
@@ -717,9 +721,9 @@ def kv_append(cache, k, v, rope=None, rows=None, count=None, count_add=0, len_ou
     else:
         _need(status, torch.int32, "status", numel=batch)
     call = lib().dt_kv_append4 if isinstance(cache, PagedCache4) else lib().dt_kv_append
-    _check(call(cache._ref, rope._ref if rope is not None else None, batch, M, _dtype_code(k),
-                ctypes.byref(kr), ctypes.byref(vr), _addr(rows), N, _addr(count), int(count_add), _addr(len_out),
-                _addr(status), _stream(stream)), "dt_kv_append")
+    _check(call(cache._ref, rope._ref if rope is not None else None, batch, M, _dtype_code(k), kr, vr, _addr(rows), N,
+                _addr(count), int(count_add), _addr(len_out), status.data_ptr(),
+                _raw_stream(device) if stream is None else stream.cuda_stream), "dt_kv_append")
     return status
 
 
@@ -731,20 +735,22 @@ def kv_read(cache, N=None, rows=None, start=None, count=None, count_add=0, dtype
     or all tokens from start on.  k, v: outputs [batch, N, Hkv, D] bf16 or fp32, any strides with dense heads
     (None: zeros of `dtype`; N is needed then when there are no rows).  status [batch] int32 is OR-ed with
     DT_DEV_BAD_CACHE for a request out of range.  Returns (k, v)."""
-    batch, Hkv, D = cache.batch, cache.Hkv, cache.D
+    batch, Hkv, D, device = cache.batch, cache.Hkv, cache.D, torch.cuda.current_device()
     if rows is not None:
         _need(rows, torch.int32, "rows")
         if rows.dim() != 2 or rows.shape[0] != batch:
             raise ValueError("rows must be [batch, N], got %s" % (tuple(rows.shape),))
         if start is not None:
             raise ValueError("rows and start exclude each other")
-    given = [x for x in (N, None if rows is None else rows.shape[1], None if k is None else k.shape[1],
-                         None if v is None else v.shape[1]) if x is not None]
-    if not given:
+    for x in (rows, k, v):
+        if x is None:
+            continue
+        if N is None:
+            N = x.shape[1]
+        if x.shape[1] != N:
+            raise ValueError("N, rows and outputs speak of %d and %d rows" % (N, x.shape[1]))
+    if N is None:
         raise ValueError("N is needed without rows and outputs")
-    N = given[0]
-    if any(x != N for x in given):
-        raise ValueError("N, rows and outputs speak of %s rows" % (sorted(set(given)),))
     if start is not None:
         _need(start, torch.int32, "start", numel=batch)
     if count is not None:
@@ -761,10 +767,11 @@ def kv_read(cache, N=None, rows=None, start=None, count=None, count_add=0, dtype
     _need(status, torch.int32, "status", numel=batch)
     if k.dtype != v.dtype:
         raise TypeError("k (%s) and v (%s) must share one dtype" % (k.dtype, v.dtype))
-    kr, vr = _head_rows(k, batch, N, Hkv, D, "k"), _head_rows(v, batch, N, Hkv, D, "v")
+    shape = (batch, N, Hkv, D)
+    kr, vr = _head_rows(k, shape, "k", device), _head_rows(v, shape, "v", device)
     call = lib().dt_kv_read4 if isinstance(cache, PagedCache4) else lib().dt_kv_read
-    _check(call(cache._ref, batch, _addr(rows), N, _addr(start), _addr(count), int(count_add), _dtype_code(k),
-                ctypes.byref(kr), ctypes.byref(vr), _addr(status), _stream(stream)), "dt_kv_read")
+    _check(call(cache._ref, batch, _addr(rows), N, _addr(start), _addr(count), int(count_add), _dtype_code(k), kr, vr,
+                status.data_ptr(), _raw_stream(device) if stream is None else stream.cuda_stream), "dt_kv_read")
     return k, v
 
 
@@ -787,9 +794,7 @@ def qk_norm(q, k, q_weight=None, k_weight=None, eps=1e-6, rope=None, len=None, p
     undefined in others.  tree_attention and kv_append then take the results with rope None.  status [batch]
     int32 is OR-ed with DT_DEV_BAD_CACHE for a position or count out of range.  Returns (q_out, k_out)."""
     batch, M, Hq, D = q.shape
-    Hk = 0 if k is None else k.shape[2]
-    if k is not None and k.dtype != q.dtype:
-        raise TypeError("q (%s) and k (%s) must share one dtype" % (q.dtype, k.dtype))
+    Hk, device, dtype = 0 if k is None else k.shape[2], torch.cuda.current_device(), q.dtype
     if k is None and k_out is not None:
         raise ValueError("k_out needs k")
     if q_out is None or (k_out is None and k is not None) or status is None:
@@ -800,22 +805,28 @@ def qk_norm(q, k, q_weight=None, k_weight=None, eps=1e-6, rope=None, len=None, p
                 k_out = torch.empty((batch, M, Hk, D), dtype=q.dtype, device=q.device)
             if status is None:
                 status = torch.zeros((batch,), dtype=torch.int32, device=q.device)
-    refs = []
-    for x, H, name in ((q, Hq, "q"), (k, Hk, "k"), (q_out, Hq, "q_out"), (k_out, Hk, "k_out")):
-        if x is None:
-            refs.append(None)
-            continue
-        if x.dtype != q.dtype:
-            raise TypeError("%s must be %s, got %s" % (name, q.dtype, x.dtype))
-        refs.append(ctypes.byref(_head_rows(x, batch, M, H, D, name)))
-    for x, name, n in ((len, "len", batch), (pos, "pos", batch * M), (n_nodes, "n_nodes", batch), (status, "status", batch)):
-        if x is not None:
-            _need(x, torch.int32, name, numel=n)
+    shape = (batch, M, Hq, D)
+    qr, qo = _head_rows(q, shape, "q", device), _head_rows(q_out, shape, "q_out", device)
+    kr = ko = None
+    if q_out.dtype != dtype:
+        raise TypeError("q_out must be %s, got %s" % (dtype, q_out.dtype))
+    if k is not None:
+        shape = (batch, M, Hk, D)
+        kr, ko = _head_rows(k, shape, "k", device), _head_rows(k_out, shape, "k_out", device)
+        if k.dtype != dtype or k_out.dtype != dtype:
+            raise TypeError("k and k_out must be %s, got %s and %s" % (dtype, k.dtype, k_out.dtype))
+    if len is not None:
+        _need(len, torch.int32, "len", numel=batch)
+    if pos is not None:
+        _need(pos, torch.int32, "pos", numel=batch * M)
+    if n_nodes is not None:
+        _need(n_nodes, torch.int32, "n_nodes", numel=batch)
+    _need(status, torch.int32, "status", numel=batch)
     qw, qs = _norm_weight(q_weight, Hq, D, "q_weight")
     kw, ks = _norm_weight(k_weight, Hk, D, "k_weight")
-    _check(lib().dt_qk_norm(batch, M, Hq, Hk, D, _dtype_code(q), refs[0], refs[1], qw, qs, kw, ks, float(eps),
-                            rope._ref if rope is not None else None, _addr(len), _addr(pos), _addr(n_nodes), refs[2],
-                            refs[3], _addr(status), _stream(stream)), "dt_qk_norm")
+    _check(lib().dt_qk_norm(batch, M, Hq, Hk, D, _dtype_code(q), qr, kr, qw, qs, kw, ks, eps,
+                            rope._ref if rope is not None else None, _addr(len), _addr(pos), _addr(n_nodes), qo, ko,
+                            status.data_ptr(), _raw_stream(device) if stream is None else stream.cuda_stream), "dt_qk_norm")
     return q_out, k_out
 
 
@@ -833,13 +844,13 @@ def tree_attention(cache, q, k, v, mask=None, pos=None, n_nodes=None, rope=None,
     q [batch, M, Hq, D], k, v [batch, M, Hkv, D] bf16, not rotated; mask, pos as dt_tree_mask writes
     them with pos_offset 0 (None: a chain); returns out [batch, M, Hq, D] bf16.  status [batch] int32
     is OR-ed with DT_DEV_BAD_CACHE for a request out of range: bring one to see it."""
-    batch, M, Hq = cache.batch, q.shape[1], q.shape[2]
+    batch, M, Hq, device = cache.batch, q.shape[1], q.shape[2], torch.cuda.current_device()
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if t.dtype != torch.bfloat16:
             raise TypeError("%s must be bfloat16, got %s" % (name, t.dtype))
-    qr = _head_rows(q, batch, M, Hq, cache.D, "q")
-    kr = _head_rows(k, batch, M, cache.Hkv, cache.D, "k")
-    vr = _head_rows(v, batch, M, cache.Hkv, cache.D, "v")
+    qr = _head_rows(q, (batch, M, Hq, cache.D), "q", device)
+    shape = (batch, M, cache.Hkv, cache.D)
+    kr, vr = _head_rows(k, shape, "k", device), _head_rows(v, shape, "v", device)
     if mask is not None:
         _need(mask, torch.int32, "mask", numel=batch * M * ((M + 31) // 32))
     if pos is not None:
@@ -862,9 +873,9 @@ def tree_attention(cache, q, k, v, mask=None, pos=None, n_nodes=None, rope=None,
     if scale is None:
         scale = 1.0 / math.sqrt(cache.D)
     call = lib().dt_tree_attention4 if isinstance(cache, PagedCache4) else lib().dt_tree_attention
-    _check(call(cache._ref, rope._ref if rope is not None else None, batch, M, Hq, ctypes.byref(qr), ctypes.byref(kr),
-                ctypes.byref(vr), _addr(mask), _addr(pos), _addr(n_nodes), scale, _addr(out), _addr(ws), n,
-                _addr(status), _stream(stream)), "dt_tree_attention")
+    _check(call(cache._ref, rope._ref if rope is not None else None, batch, M, Hq, qr, kr, vr, _addr(mask), _addr(pos),
+                _addr(n_nodes), scale, out.data_ptr(), _addr(ws), n, status.data_ptr(),
+                _raw_stream(device) if stream is None else stream.cuda_stream), "dt_tree_attention")
     return out
 
 
