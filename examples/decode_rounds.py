@@ -10,7 +10,11 @@ A round for a batch of requests of different lengths:
 Prompts go through the same attention (mask None: a chain) and the same append, and
 plain decoding is the tree of one node.  The model's own products are torch's.
 
-    python examples/decode_rounds.py [--rounds N]
+With --normed the model normalises its query and key heads: qk_norm does so and rotates
+them, and attention and append take them as they are.  With --bits 4 the context is held
+in 4 bits; kv_read shows what it stands for.
+
+    python examples/decode_rounds.py [--rounds N] [--bits 4] [--normed]
 """
 import argparse
 import math
@@ -29,7 +33,7 @@ L, K, BUDGET = 8, 16, 40
 class Model:
     """Attention layers between an embedding and a head; follow[token] is a likely next token."""
 
-    def __init__(self, seed=0, device="cuda"):
+    def __init__(self, seed=0, device="cuda", normed=False):
         g = torch.Generator().manual_seed(seed)
         bf16 = dict(dtype=torch.bfloat16, device=device)
         self.emb = torch.randn((V, H), generator=g).to(**bf16)
@@ -39,6 +43,8 @@ class Model:
         self.follow = torch.randperm(V, generator=g).to(device)
         at = torch.arange(4096, dtype=torch.float64)[:, None] * 1e4 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)
         self.rope = dtree.Rope(at.cos().float().to(device), at.sin().float().to(device))
+        self.norms = [[(1 + 0.2 * torch.randn(D, generator=g)).to(device) for _ in range(2)] for _ in range(LAYERS)] if normed else None
+        self.later = None if normed else self.rope  # the rotation that attention and append have to do
 
     def forward(self, tokens, caches, workspace, status, **tree):
         """Logits [b, M, V] of the rows `tokens` [b, M] and each layer's keys and values, not in the caches yet."""
@@ -47,7 +53,10 @@ class Model:
         for i in range(LAYERS):
             y = torch.nn.functional.rms_norm(x, (H,)) @ self.qkv[i]
             q, k, v = (t.unflatten(-1, (-1, D)) for t in y.split((HQ * D, HKV * D, HKV * D), -1))  # slices, no copies
-            o = dtree.tree_attention(caches[i], q, k, v, rope=self.rope, workspace=workspace, status=status, **tree)
+            if self.norms:
+                q, k = dtree.qk_norm(q, k, *self.norms[i], rope=self.rope, len=caches[i].len, pos=tree.get("pos"),
+                                     n_nodes=tree.get("n_nodes"), status=status)
+            o = dtree.tree_attention(caches[i], q, k, v, rope=self.later, workspace=workspace, status=status, **tree)
             x = x + o.view(b, M, HQ * D) @ self.out[i]
             kv.append((k, v))
         logits = torch.nn.functional.rms_norm(x, (H,)) @ self.head
@@ -63,10 +72,11 @@ class Model:
         return (torch.stack(rows, 1) + noise).to(torch.bfloat16)
 
 
-def new_caches(batch, tokens, device="cuda"):
+def new_caches(batch, tokens, device="cuda", bits=8):
     """A cache per layer with pages for `tokens` tokens of each request; they share lengths and pages' numbers."""
     pages = -(-tokens // PAGE)
-    caches = [dtree.PagedCache.empty(batch * pages, PAGE, HKV, D, batch, pages, device) for _ in range(LAYERS)]
+    form = dtree.PagedCache4 if bits == 4 else dtree.PagedCache
+    caches = [form.empty(batch * pages, PAGE, HKV, D, batch, pages, device) for _ in range(LAYERS)]
     for c in caches:
         c.table.copy_(torch.randperm(batch * pages, generator=torch.Generator().manual_seed(1)).view(batch, pages))
     return caches
@@ -75,7 +85,7 @@ def new_caches(batch, tokens, device="cuda"):
 def append(model, caches, kv, length, status, **rows):
     """Every layer appends at the same length, which moves on once they all have."""
     for c, (k, v) in zip(caches, kv):
-        dtree.kv_append(c, k, v, rope=model.rope, len_out=length, status=status, **rows)
+        dtree.kv_append(c, k, v, rope=model.later, len_out=length, status=status, **rows)
     for c in caches:
         c.len.copy_(length)
 
@@ -90,11 +100,11 @@ def prefill(model, prompts, caches, status):
     return prompts.gather(1, count[:, None].long())[:, 0]
 
 
-def decode(model, prompts, rounds, top=4, seed=0):
+def decode(model, prompts, rounds, top=4, seed=0, bits=8):
     """Rounds of draft, verify and append.  Returns, per request, the emitted tokens and their
     log-probabilities and ranks, the caches, and the status words (all zero)."""
     b, dev = prompts.shape[0], prompts.device
-    caches = new_caches(b, prompts.shape[1] + rounds * (L + 1), dev)
+    caches = new_caches(b, prompts.shape[1] + rounds * (L + 1), dev, bits)
     status = torch.zeros((b,), dtype=torch.int32, device=dev)
     length = torch.empty((b,), dtype=torch.int32, device=dev)
     last = prefill(model, prompts, caches, status)
@@ -128,13 +138,18 @@ def decode(model, prompts, rounds, top=4, seed=0):
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--rounds", type=int, default=8)
-    rounds = ap.parse_args().rounds
-    model = Model()
+    ap.add_argument("--bits", type=int, default=8, choices=(4, 8), help="of an element of the context")
+    ap.add_argument("--normed", action="store_true", help="a model that normalises its heads")
+    args = ap.parse_args()
+    rounds = args.rounds
+    model = Model(normed=args.normed)
     prompts = torch.full((3, 50), -1, device="cuda")
     for i, n in enumerate((1, 17, 50)):
         prompts[i, :n] = torch.randint(0, V, (n,), generator=torch.Generator().manual_seed(i)).cuda()
-    got, caches, status = decode(model, prompts, rounds)
+    got, caches, status = decode(model, prompts, rounds, bits=args.bits)
     print("status", status.tolist(), "tokens held", caches[0].len.tolist())
+    keys, values = dtree.kv_read(caches[0], N=int(caches[0].len.max()))
+    print("largest key and value of the first layer", float(keys.abs().max()), float(values.abs().max()))
     for i, g in enumerate(got):
         print("request %d: %d tokens in %d rounds, mean log-probability %.3f: %s"
               % (i, len(g), rounds, sum(x[1] for x in g) / len(g), [x[0] for x in g]))

@@ -76,6 +76,11 @@ bool rows_ok(const dt_rows* r, int esize) {
     return true;
 }
 
+// Rows that a call writes: heads of D elements that lie apart.
+bool rows_apart(const dt_rows* r, int esize, int64_t batch, int64_t n, int64_t heads, int D) {
+    return rows_ok(r, esize) && (batch < 2 || r->stride_b >= D) && (n < 2 || r->stride_n >= D) && (heads < 2 || r->stride_h >= D);
+}
+
 const dt_rope kNoRope = {nullptr, nullptr, 0, 0, 0};
 
 template <typename C, typename F>
@@ -122,7 +127,8 @@ dt_status read(const dt_kv_cache& c, int bits, int32_t batch, const int32_t* row
                int32_t* status, dt_stream_t stream) {
     if (dtype != DT_BF16 && dtype != DT_F32) return DT_ERR_INVALID_ARG;
     const int esize = dtype == DT_BF16 ? 2 : 4;
-    if (N < 1 || (rows && start) || !rows_ok(k, esize) || !rows_ok(v, esize) || !status) return DT_ERR_INVALID_ARG;
+    if (N < 1 || (rows && start) || !status) return DT_ERR_INVALID_ARG;
+    if (!rows_apart(k, esize, batch, N, c.Hkv, c.D) || !rows_apart(v, esize, batch, N, c.Hkv, c.D)) return DT_ERR_INVALID_ARG;
     if (N > (1 << 30) || c.Hkv > 32767) return DT_ERR_UNSUPPORTED;
     if (count && (count_add < -(1 << 30) || count_add > (1 << 30))) return DT_ERR_INVALID_ARG;
     return cuda_status(dt_kn15_launch(c, bits, batch, rows, N, start, count, count_add, dtype, *k, *v, status,
@@ -198,10 +204,11 @@ dt_status dt_qk_norm(int32_t batch, int32_t M, int32_t Hq, int32_t Hk, int32_t D
     if (batch < 1 || M < 1 || Hq < 0 || Hk < 0 || Hq + (long long)Hk < 1 || D < 1) return DT_ERR_INVALID_ARG;
     if (D != 64 && D != 128) return DT_ERR_UNSUPPORTED;
     if (batch > 65535 || M > (1 << 20) || Hq > 65535 || Hk > 65535) return DT_ERR_UNSUPPORTED;
+    if ((long long)batch * M > 0x7fffffffll) return DT_ERR_UNSUPPORTED;
     if (dtype != DT_BF16 && dtype != DT_F32) return DT_ERR_INVALID_ARG;
     const int esize = dtype == DT_BF16 ? 2 : 4;
-    if (Hq > 0 && (!rows_ok(q, esize) || !rows_ok(q_out, esize))) return DT_ERR_INVALID_ARG;
-    if (Hk > 0 && (!rows_ok(k, esize) || !rows_ok(k_out, esize))) return DT_ERR_INVALID_ARG;
+    if (Hq > 0 && (!rows_ok(q, esize) || !rows_apart(q_out, esize, batch, M, Hq, D))) return DT_ERR_INVALID_ARG;
+    if (Hk > 0 && (!rows_ok(k, esize) || !rows_apart(k_out, esize, batch, M, Hk, D))) return DT_ERR_INVALID_ARG;
     if (!aligned16(q_weight) || !aligned16(k_weight)) return DT_ERR_INVALID_ARG;
     if ((q_weight_stride != 0 && q_weight_stride != D) || (k_weight_stride != 0 && k_weight_stride != D)) return DT_ERR_INVALID_ARG;
     if (!(eps >= 0.f) || !std::isfinite(eps) || !status) return DT_ERR_INVALID_ARG;

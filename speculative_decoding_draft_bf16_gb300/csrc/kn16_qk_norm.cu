@@ -243,7 +243,6 @@ cudaError_t launch(DtNorm a, int sms, cudaStream_t st) {
     a.parts = a.parts < most ? a.parts : most;
     a.per = (most + a.parts - 1) / a.parts;
     const long long units = tokens * a.parts, need = (units + NT / 32 - 1) / (NT / 32);
-    if (units > 0xfffffff0ll - NT) return cudaErrorInvalidValue;
     // whole tokens: two steps at a time (the prompts 87 us, one at a time 91); parts of
     // tokens have few steps (3904 short rows 12.6 us with two, 10.9 with one)
     return (a.parts == 1 ? launch_u<T, D, 2> : launch_u<T, D, 1>)(a, (unsigned)need, st);

@@ -613,6 +613,7 @@ class PagedCache:
                                    v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
                                    len.data_ptr())
         self._ref = ctypes.byref(self._struct)
+        self._device = table.get_device()
 
     @classmethod
     def empty(cls, n_pages, page, Hkv, D, batch, max_pages, device="cuda"):
@@ -653,6 +654,7 @@ class PagedCache4:
                                    v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
                                    len.data_ptr())
         self._ref = ctypes.byref(self._struct)
+        self._device = table.get_device()
 
     @classmethod
     def empty(cls, n_pages, page, Hkv, D, batch, max_pages, device="cuda"):
@@ -676,6 +678,7 @@ class Rope:
         self.cos, self.sin, self.interleaved = cos, sin, bool(interleaved)
         self._struct = RopeStruct(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], int(self.interleaved))
         self._ref = ctypes.byref(self._struct)
+        self._device = cos.get_device()
 
 
 def _head_rows(t, shape, name, device):
@@ -691,6 +694,12 @@ def _head_rows(t, shape, name, device):
     return RowsStruct(t.data_ptr(), sb, sn, sh)
 
 
+def _need_here(x, name, device):
+    """A cache or rotation tables on the current device (None: nothing to check)."""
+    if x is not None and x._device != device:
+        raise ValueError("%s must be on the current device" % name)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -701,6 +710,8 @@ def kv_append(cache, k, v, rope=None, rows=None, count=None, count_add=0, len_ou
     count [batch] int32 + count_add says how many (its acc_len, 1); len_out [batch] gets the new lengths;
     status [batch] int32 is OR-ed with DT_DEV_BAD_CACHE for a request that does not fit; returned."""
     batch, M, device = cache.batch, k.shape[1], torch.cuda.current_device()
+    _need_here(cache, "cache", device)
+    _need_here(rope, "rope", device)
     if k.dtype != v.dtype:
         raise TypeError("k (%s) and v (%s) must share one dtype" % (k.dtype, v.dtype))
     shape = (batch, M, cache.Hkv, cache.D)
@@ -736,6 +747,7 @@ def kv_read(cache, N=None, rows=None, start=None, count=None, count_add=0, dtype
     (None: zeros of `dtype`; N is needed then when there are no rows).  status [batch] int32 is OR-ed with
     DT_DEV_BAD_CACHE for a request out of range.  Returns (k, v)."""
     batch, Hkv, D, device = cache.batch, cache.Hkv, cache.D, torch.cuda.current_device()
+    _need_here(cache, "cache", device)
     if rows is not None:
         _need(rows, torch.int32, "rows")
         if rows.dim() != 2 or rows.shape[0] != batch:
@@ -795,6 +807,7 @@ def qk_norm(q, k, q_weight=None, k_weight=None, eps=1e-6, rope=None, len=None, p
     int32 is OR-ed with DT_DEV_BAD_CACHE for a position or count out of range.  Returns (q_out, k_out)."""
     batch, M, Hq, D = q.shape
     Hk, device, dtype = 0 if k is None else k.shape[2], torch.cuda.current_device(), q.dtype
+    _need_here(rope, "rope", device)
     if k is None and k_out is not None:
         raise ValueError("k_out needs k")
     if q_out is None or (k_out is None and k is not None) or status is None:
@@ -845,6 +858,8 @@ def tree_attention(cache, q, k, v, mask=None, pos=None, n_nodes=None, rope=None,
     them with pos_offset 0 (None: a chain); returns out [batch, M, Hq, D] bf16.  status [batch] int32
     is OR-ed with DT_DEV_BAD_CACHE for a request out of range: bring one to see it."""
     batch, M, Hq, device = cache.batch, q.shape[1], q.shape[2], torch.cuda.current_device()
+    _need_here(cache, "cache", device)
+    _need_here(rope, "rope", device)
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if t.dtype != torch.bfloat16:
             raise TypeError("%s must be bfloat16, got %s" % (name, t.dtype))

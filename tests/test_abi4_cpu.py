@@ -83,6 +83,7 @@ def test_attention():
 def test_read(four):
     for kw in (dict(batch=0), dict(N=0), dict(dtype=2), dict(status=None), dict(rows=0x8000, start=0x9000),
                dict(k=_rows(ptr=None)), dict(v=_rows(ptr=0x1008)), dict(v=_rows(stride_n=100)),
+               dict(k=_rows(stride_n=0)), dict(v=_rows(stride_h=56)), dict(k=_rows(stride_b=0), batch=2),
                dict(count=0x8000, count_add=-(1 << 30) - 1)):
         assert _read(four, **kw) == -1, kw
     assert _read(four, N=(1 << 30) + 1) == -2 and _read(four, cache=_cache(Hkv=32768)) == -2
@@ -93,9 +94,10 @@ def test_norm():
     for kw in (dict(batch=0), dict(M=0), dict(Hq=-1), dict(Hk=-1), dict(Hq=0, Hk=0), dict(D=0), dict(dtype=2),
                dict(eps=-1e-6), dict(eps=nan), dict(eps=inf), dict(status=None), dict(qw=0x2004), dict(qs=63), dict(ks=128),
                dict(q=_rows(ptr=None)), dict(k=_rows(ptr=0x1004)), dict(q_out=_rows(stride_h=60)),
-               dict(k_out=_rows(ptr=None))):
+               dict(k_out=_rows(ptr=None)), dict(q_out=_rows(stride_h=0)), dict(k_out=_rows(stride_n=32)),
+               dict(q_out=_rows(stride_b=0), batch=2)):
         assert _norm(**kw) == -1, kw
-    for kw in (dict(D=96), dict(D=256), dict(batch=65536), dict(M=(1 << 20) + 1), dict(Hq=65536)):
+    for kw in (dict(D=96), dict(D=256), dict(batch=65536), dict(M=(1 << 20) + 1), dict(Hq=65536), dict(batch=2048, M=1 << 20)):
         assert _norm(**kw) == -2, kw
 
 

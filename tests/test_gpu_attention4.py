@@ -149,6 +149,54 @@ def test_rotations_and_strides(rot, interleaved, layout):
     run([40, 333], 3, 6, 2, 128, 64, rot=rot, interleaved=interleaved, layout=layout, seed=rot + 1)
 
 
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_that_are_rotated_already(page, D):
+    """Without a rotation new rows take shorter paths: single tokens, small trees, large ones, chains."""
+    lens = [0, 1, 15, 16, 17, 127, 128, 129, 300]
+    for G in (1, 4, 7, 12):
+        run(lens, 1, 2 * G, 2, D, page, tree=False, rot=0, seed=G)
+    run(lens, 5, 6, 2, D, page, rot=0, n_nodes=[5, 1, 2, 0, 5, 1, 3, 4, 5], seed=20)
+    run(lens, 61, 6, 2, D, page, rot=0, n_nodes=[61, 1, 2, 0, 60, 33, 32, 31, 61], seed=21)
+    run([100, 0], 290, 2, 1, D, page, rot=0, n_nodes=[290, 257], seed=22)
+    run([100, 0], 150, 3, 1, D, page, tree=False, rot=0, seed=23)
+
+
+def test_single_tokens_among_many():
+    """Enough units that every CTA has work (shares of two sizes), with more and fewer rows than one."""
+    lens = [(577 * i) % 3000 for i in range(48)]
+    run(lens, 1, 8, 8, 64, 16, tree=False, rot=0, seed=31)
+    run(lens, 3, 8, 4, 128, 64, rot=0, n_nodes=[(i % 3) + 1 for i in range(48)], seed=32)
+
+
+@pytest.mark.parametrize("G", [2, 12])
+def test_a_single_row_of_its_own(G):
+    """One new row: not finite, hidden by its mask, or far from the cache's magnitudes."""
+    cache = make_cache([100, 0, 30], 32, 2, 128, 5)
+    g = torch.Generator().manual_seed(G)
+    q, k, v = inputs(3, 1, 2 * G, 2, 128, g)
+    see, none = [torch.ones((1, 1), dtype=torch.bool)] * 3, [torch.zeros((1, 1), dtype=torch.bool)] * 3
+    at = [torch.arange(1)] * 3
+    for size in (2.0 ** -30, 2.0 ** -12, 1.0, 2.0 ** 12):
+        out = dtree.tree_attention(cache, q, k, v * size)
+        check(cache, q, k, v * size, see, at, [1] * 3, None, 1 / math.sqrt(128), out)
+    bad = v.clone()
+    bad[:, 0, 0, 7], bad[:, 0, 1, 100] = math.nan, -math.inf
+    hidden = torch.zeros((3, 1, 1), **I32)
+    out = dtree.tree_attention(cache, q, bad, bad, mask=hidden)
+    assert (out[1] == 0).all()  # sees nothing at all
+    for b in (0, 2):
+        one = dtree.PagedCache4(cache.k, cache.v, cache.k_scale, cache.v_scale, cache.table[b:b + 1].contiguous(), cache.len[b:b + 1].contiguous())
+        check(one, q[b:b + 1], k[b:b + 1], v[b:b + 1], none[:1], at[:1], [1], None, 1 / math.sqrt(128), out[b:b + 1])
+    for kk, vv in ((bad, v), (k, bad)):
+        assert torch.isnan(dtree.tree_attention(cache, q, kk, vv)).all()
+    qn = q.clone()
+    qn[0, 0, 0, 3] = math.nan
+    out = dtree.tree_attention(cache, qn, k, v)
+    nan = torch.isnan(out).all(-1)
+    assert nan[0, 0, 0] and int(nan.sum()) == 1
+
+
 def test_long_contexts_are_split():
     run([9000, 5, 3001], 1, 16, 2, 128, 64, tree=False, seed=5)
     run([7001], 40, 16, 2, 128, 128, seed=6)
