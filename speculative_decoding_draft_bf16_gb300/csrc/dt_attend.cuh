@@ -29,11 +29,13 @@ struct AtPlan {
     // against 4.2 thousand clocks measured, of 4 bits 2.2 against 3.3).
     static constexpr uint32_t FULL = ROWS == 256 ? (BITS == 4 ? 6 : 5) : 1, PART = ROWS == 256 ? 4 : 1;
     // What starting on a unit costs: its queries, its new rows, its sums' way out.  64 trees
-    // of 61 nodes with 14, 20, 26: 208, 183, 188 us; 64 single tokens with 1, 2, 3: 240, 233,
-    // 234.
+    // of 61 nodes with 14, 20, 26: 208, 183, 188 us, over 4 bits with 24, 30, 34: 132, 128,
+    // 127; 64 single tokens with 1, 2, 3: 240, 233, 234.
     static constexpr uint32_t HEAD = ROWS == 256 ? (BITS == 4 ? 30 : 20) : 2;
     // The same of 16 rows over 4 bits when every CTA has work (see AtShareLead): a unit's start
-    // and end take the time of so many tiles then.
+    // and end take the time of so many tiles then.  64 single tokens with 2, 5, 6, 7, 8: 144,
+    // 129, 129, 130, 136 us; calls that do not fill the GPU need the smaller one (one token
+    // 12.5 us, 15 with 6).
     static constexpr uint32_t HEAD_FULL = 6;
     // Pieces of so few tiles at a unit's end are not worth starting on (one tree of 257
     // nodes over 8000 tokens without this 92 us, with 2 77, with 4 81).

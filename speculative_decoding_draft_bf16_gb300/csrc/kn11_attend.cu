@@ -1,5 +1,6 @@
 // kn11_attend.cu -- tree attention for up to 16 query rows per key head (single
-// tokens and small trees), bound by the reading of the cache (dt_tree_attention).
+// tokens and small trees), over an e4m3 cache bound by its reading (dt_tree_attention,
+// dt_tree_attention4).
 //
 // A CTA streams runs of 128-token tiles, 16 tokens to each of its 8 warps.  A
 // lane copies the bytes that it will need itself to its own places in shared
@@ -28,6 +29,20 @@
 // between 165 and 228 us, by where on the chip an SM lies: that spread, not the loop, is
 // what is left.  One token over 1000: 15.9 us, the latency of the share, pages, copies, new
 // row and join in turn (15.6 before each new row had a scale of its own).
+//
+// Over 4 bits (e2m1 codes, a scale for each 16 elements of a token) a token has 144 bytes
+// in place of 256, and the conversion is what bounds the time.  The 16 tokens' codes and
+// scales lie in one piece each and are copied as they lie; scales meet the codes as fp16
+// pairs, where products are exact: a lane's keys are runs of 16, its values one run of four
+// tokens.  Of a group of 16 tokens a lane converts 128 codes to 64 pairs, multiplies them
+// and issues 16 MMAs: 64 conversions at two clocks each in one pipe, 64 products at two
+// clocks in another and MMAs at eight, 320 clocks of an SM quarter when nothing else
+// runs, and 450 to 530 with the nibbles' pairing, loads, addresses and exponentials around
+// them.  64 single tokens as above (0.64 GB): 129 us, 5.0 TB/s (74% of a copy's rate); 16 of
+// them 43 us; one over 1000 12.5 us.  Steps on the way: 158 us with a group at a time, 144
+// with two (votes, references and addresses shared); loops of less code were slower (153),
+// as were three CTAs per SM (152); the division's weights (see AtShareLead) 133; a path of
+// its own for a token's own row 129.
 #include <type_traits>
 
 #include "dt_attend.cuh"
@@ -40,6 +55,8 @@ constexpr int ROWS = 16, NW = 8, NT = NW * 32;
 constexpr int ATOM = 4;              // tiles of the longest unit that is not split
 constexpr uint32_t MIN_SHARE = 4;    // least cost worth a CTA: the start and two tiles
 constexpr uint32_t MIN_SHARE4 = 4;   // the same over 4 bits
+// What the CTA that came first gets more, in 256ths of a share: of the two on an SM it takes
+// 1400 clocks for a tile, the other 1700.  With 0, 8, 12, 16, 24: 135, 133, 135, 136, 141 us.
 constexpr int LEAD = 8;
 template <int BITS>
 struct Division {
@@ -53,7 +70,7 @@ constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float HEADROOM = 5.f, LAZY = 8.f;
 
 // Three tiles in flight of 4 KB to a warp, two CTAs to an SM; three CTAs with two tiles
-// each are slower (246 : 233 us).
+// each are slower (246 : 233 us).  Of 4 bits five of 2.3 KB (four and six are alike).
 template <int D, int BITS>
 struct Lay {
     static constexpr int KC = D / 64;             // runs of 16 elements of a token's keys per lane

@@ -1,5 +1,5 @@
 // kn12_attend_tc.cu -- tree attention on the tensor cores, for many query rows
-// per key head (dt_tree_attention).
+// per key head (dt_tree_attention, dt_tree_attention4).
 //
 // A CTA works on a block of up to 256 query rows (two slots of 128, the rows of
 // an MMA) and a run of 128-token tiles:
@@ -43,6 +43,17 @@
 // 4): one prompt of 4000 rows over an empty cache, 32 heads on 8, 542 us (13% of the rate).
 // Code size matters as much: with unrolled tiles the roles' loops overflowed the
 // instruction caches (one tree of 257 nodes 125 us instead of 99).
+//
+// Over 4 bits the scales are in the tiles, so tiles that are wholly visible, nearly all of
+// a long context, go through a loop of their own without scales, masks or their waits: a
+// tile of 256 rows takes 3300 clocks instead of 4200 (1.5 PFLOP/s over a context of 65536,
+// 79% of the measured rate; the MMAs' 2560 bound it), the sixteen trees 1.09 ms with the
+// common loop and 0.90 with this.  Tiles of new rows and the context's last one take 6000
+// to 7500.  Rows without a rotation are read four at a time (queries 8 to 5 thousand clocks,
+// new rows 9 to 7), masks before the waits; with weights of its own for the division the
+// sixteen trees take 0.85 ms (68%), 64 trees of 61 nodes 128 us, 8 of 513 with D = 64 73 us.
+// What did not help: new rows' loads or the next half's scores ahead (registers), waits that
+// look without sleeping (882 to 896 us), a short rolled loop for tiles with masks (961).
 #include <atomic>
 
 #include "dt_attend.cuh"
