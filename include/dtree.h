@@ -587,7 +587,7 @@ dt_status dt_kv_append4(const dt_kv_cache4* c, const dt_rope* rope, int32_t batc
  * rows[b][j], or start[b] + j when rows is NULL.
  *   k, v: outputs [batch][N][Hkv][D] in dtype (DT_BF16 or DT_F32); code times scale in fp32,
  *         then in dtype (exact from 4 bits); rows from n_b on are left alone.  Keys come as
- *         they are held, rotated.  Strides of outputs are D at least.
+ *         they are held, rotated.  Strides of outputs are D at least, and they do not overlap.
  *   rows: NULL or [batch][N] token numbers in [0, len[b]), in any order and any number of
  *         times; entries from n_b on are not read.
  *   start: NULL (0) or [batch]; NULL when there are rows.
@@ -613,8 +613,8 @@ dt_status dt_kv_read4(const dt_kv_cache4* c, int32_t batch, const int32_t* rows,
  *      [heads][D] with stride D.
  *   rope: NULL: no rotation.  len: NULL (0) or [batch]; pos: NULL (n) or [batch][M];
  *   n_nodes: NULL (M) or [batch] in [0, M].
- *   q_out, k_out: as q and k; may be q and k themselves.  Strides are D at least.  Rows from
- *      n_nodes[b] on are left alone.
+ *   q_out, k_out: as q and k; may be q and k themselves, but not overlap else.  Strides are D
+ *      at least.  Rows from n_nodes[b] on are left alone.
  * Everything is fp32 up to the one rounding at the end.  A row with a value that is not
  * finite becomes NaN where that value takes part.  A request with n_nodes out of range, and
  * a row with its position outside the tables, is left alone and sets DT_DEV_BAD_CACHE in

@@ -129,6 +129,7 @@ dt_status read(const dt_kv_cache& c, int bits, int32_t batch, const int32_t* row
     const int esize = dtype == DT_BF16 ? 2 : 4;
     if (N < 1 || (rows && start) || !status) return DT_ERR_INVALID_ARG;
     if (!rows_apart(k, esize, batch, N, c.Hkv, c.D) || !rows_apart(v, esize, batch, N, c.Hkv, c.D)) return DT_ERR_INVALID_ARG;
+    if (k->ptr == v->ptr) return DT_ERR_INVALID_ARG;
     if (N > (1 << 30) || c.Hkv > 32767) return DT_ERR_UNSUPPORTED;
     if (count && (count_add < -(1 << 30) || count_add > (1 << 30))) return DT_ERR_INVALID_ARG;
     return cuda_status(dt_kn15_launch(c, bits, batch, rows, N, start, count, count_add, dtype, *k, *v, status,
@@ -209,6 +210,7 @@ dt_status dt_qk_norm(int32_t batch, int32_t M, int32_t Hq, int32_t Hk, int32_t D
     const int esize = dtype == DT_BF16 ? 2 : 4;
     if (Hq > 0 && (!rows_ok(q, esize) || !rows_apart(q_out, esize, batch, M, Hq, D))) return DT_ERR_INVALID_ARG;
     if (Hk > 0 && (!rows_ok(k, esize) || !rows_apart(k_out, esize, batch, M, Hk, D))) return DT_ERR_INVALID_ARG;
+    if (Hq > 0 && Hk > 0 && q_out->ptr == k_out->ptr) return DT_ERR_INVALID_ARG;
     if (!aligned16(q_weight) || !aligned16(k_weight)) return DT_ERR_INVALID_ARG;
     if ((q_weight_stride != 0 && q_weight_stride != D) || (k_weight_stride != 0 && k_weight_stride != D)) return DT_ERR_INVALID_ARG;
     if (!(eps >= 0.f) || !std::isfinite(eps) || !status) return DT_ERR_INVALID_ARG;

@@ -796,12 +796,7 @@ struct Soft {
             return;
         }
         uint32_t x[64];
-        float4 ks = sc->ks, lv = sc->lv, iv = sc->iv;
-        if constexpr (BITS == 4) {  // one scale for the tile
-            ks.y = ks.z = ks.w = ks.x;
-            lv.y = lv.z = lv.w = lv.x;
-            iv.y = iv.z = iv.w = iv.x;
-        }
+        const float4 ks = sc->ks, lv = sc->lv, iv = sc->iv;
         dt_tmem_ld64(ts, x);
         const float ka[4] = {at_factor(rowc, ks.x), at_factor(rowc, ks.y), at_factor(rowc, ks.z), at_factor(rowc, ks.w)};
         const float l4[4] = {lv.x, lv.y, lv.z, lv.w}, i4[4] = {iv.x, iv.y, iv.z, iv.w};
@@ -891,6 +886,53 @@ struct Soft {
         dt_tmem_st_wait();
     }
 
+    // The same with a mask: the context's last tile, and tiles of new rows with a scale for the
+    // tile: lv, iv are log2 and inverse of that of its values.
+    static DT_DI void half_masked(uint32_t ts, uint32_t to, bool has_o, float ka, float lv, float iv, uint2 mk, float& m,
+                                  float& l, uint64_t* other, uint32_t other_ph, int* fail) {
+        if (!__any_sync(0xffffffffu, mk.x | mk.y)) {  // none of the warp's rows sees any of them
+            const uint32_t z[16] = {};
+            dt_tmem_st16(ts, z);
+            dt_tmem_st16(ts + 16, z);
+            dt_tmem_st_wait();
+            return;
+        }
+        uint32_t x[64];
+        dt_tmem_ld64(ts, x);
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+            if (!(((i < 32 ? mk.x : mk.y) >> (i & 31)) & 1)) x[i] = 0xFF800000u;  // -infinity
+        float q[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            q[g] = fmaxf(__uint_as_float(x[16 * g]), __uint_as_float(x[16 * g + 1]));
+#pragma unroll
+            for (int i = 2; i < 16; i += 2) q[g] = max3(q[g], __uint_as_float(x[16 * g + i]), __uint_as_float(x[16 * g + i + 1]));
+        }
+        follow(__fmaf_rn(fmaxf(max3(q[0], q[1], q[2]), q[3]), ka, lv), m, l, to, has_o, other, other_ph, fail);
+        const float kb = __fsub_rn(lv, m == -__int_as_float(0x7F800000) ? 0.f : m);
+        const unsigned long long ka2 = dt_f2_pack(ka, ka), kb2 = dt_f2_pack(kb, kb);
+        unsigned long long sum[2] = {dt_f2_pack(0.f, 0.f), dt_f2_pack(0.f, 0.f)};
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                float e0, e1;
+                dt_f2_unpack(dt_f2_fma(dt_f2_pack(__uint_as_float(x[16 * g + i]), __uint_as_float(x[16 * g + i + 1])), ka2, kb2), e0, e1);
+                e0 = dt_ex2_approx(e0);
+                e1 = dt_ex2_approx(e1);
+                sum[(i >> 1) & 1] = dt_f2_add(sum[(i >> 1) & 1], dt_f2_pack(e0, e1));
+                p[i / 2] = f16x2(e0, e1);
+            }
+            dt_tmem_st16(ts + 8 * g, p);  // over columns that are in registers
+        }
+        float s0, s1;
+        dt_f2_unpack(dt_f2_add(sum[0], sum[1]), s0, s1);
+        l = __fmaf_rn(__fadd_rn(s0, s1), iv, l);
+        dt_tmem_st_wait();
+    }
+
     // The same for tokens with scales of their own: key exponents ek, value exponents ev.
     // Rare, so short: 16 tokens at a time, their scores read twice.
     static DT_DI void half_apart(const Apart* ap, int h, uint32_t ts, uint32_t to, bool has_o, float rowc,
@@ -957,9 +999,12 @@ struct Soft {
             const int clear = len / AT_TILE - u.t0;  // tiles before this one are wholly visible
             uint32_t pa = ph & 1;                    // phase of both halves' scores
             int lt = dual ? 0 : s;
-            const int node = BITS == 4 ? node_of(a, u, row) : 0;
+            // Cached tiles of a 4-bit cache need nothing but their scores, so nothing of them is
+            // waited for but those.  (That the barriers of the scales are passed over is safe:
+            // when a tile's are waited for, the converters are past those of RING tiles before.)
             if constexpr (BITS == 4) {
-                const float ka = at_factor(rowc, 1.f);
+                const float ka1 = at_factor(rowc, 1.f);
+                const int node = node_of(a, u, row);
                 const int last = min(clear, nt);
 #pragma unroll 1
                 for (; lt < last; lt += hop, pa ^= 1) {
@@ -968,45 +1013,68 @@ struct Soft {
                         wait(&sh->sfull[s][h], pa, &sh->fail);
                         __syncwarp();
                         dt_tc_fence_after();
-                        half_clear(ts + 64 * h, to, lt >= hop || h, ka, m, l, &sh->sfull[s][h ^ 1], pa ^ h, &sh->fail);
+                        half_clear(ts + 64 * h, to, lt >= hop || h, ka1, m, l, &sh->sfull[s][h ^ 1], pa ^ h, &sh->fail);
                         dt_tc_fence_before();
                         __syncwarp();
                         if ((tid & 31) == 0) dt_mbar_arrive(&sh->pfull[s][h]);
                     }
                 }
-            }
 #pragma unroll 1
-            for (; lt < nt; lt += hop, pa ^= 1) {
-                const uint32_t g = g0 + lt;
-                const Ring* ring = &sh->ring[g % RING];
-                uint2 mk2[2];  // of a 4-bit cache: both halves' masks, on their way while the scales are waited for
-                if constexpr (BITS == 4) {
-                    mk2[0] = mask_words(a, u, u.t0 + lt, 0, row, node);
-                    mk2[1] = mask_words(a, u, u.t0 + lt, 1, row, node);
-                }
-                wait(&sh->scfull[g % RING], (g / RING) & 1, &sh->fail);
-                // (under `clear`, known already: without it 16 trees of 257 nodes 1.14 ms instead of 1.13)
-                if (lt >= clear && u.t0 + lt >= u.ctx && (sh->apart[g % RING].yes[0] | sh->apart[g % RING].yes[1])) break;
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    uint64_t* other = &sh->sfull[s][h ^ 1];  // of half 0: waited for next; of half 1: of the next tile
-                    const uint32_t other_ph = pa ^ h, st = ts + 64 * h;
-                    const bool has_o = lt >= hop || h;
-                    const bool masked = lt >= clear;
-                    uint2 mk = make_uint2(0u, 0u);
-                    if (masked) {
-                        mk = BITS == 4 ? (h ? mk2[1] : mk2[0]) : mask_words(a, u, u.t0 + lt, h, row, node_of(a, u, row));
-                        if (u.t0 + lt >= u.ctx)
-                            poison |= ((mk.x & (ring->bad[0][2 * h] | ring->bad[1][2 * h])) |
-                                       (mk.y & (ring->bad[0][2 * h + 1] | ring->bad[1][2 * h + 1]))) != 0u;
+                for (; lt < nt; lt += hop, pa ^= 1) {
+                    float ka = ka1, lv = 0.f, iv = 1.f;
+                    const uint2 mk0 = mask_words(a, u, u.t0 + lt, 0, row, node);
+                    const uint2 mk1 = mask_words(a, u, u.t0 + lt, 1, row, node);
+                    if (u.t0 + lt >= u.ctx) {
+                        const uint32_t g = g0 + lt;
+                        const Ring* ring = &sh->ring[g % RING];
+                        wait(&sh->scfull[g % RING], (g / RING) & 1, &sh->fail);
+                        if (sh->apart[g % RING].yes[0] | sh->apart[g % RING].yes[1]) break;
+                        const uint4 bk = *(const uint4*)ring->bad[0], bv = *(const uint4*)ring->bad[1];
+                        poison |= ((mk0.x & (bk.x | bv.x)) | (mk0.y & (bk.y | bv.y)) | (mk1.x & (bk.z | bv.z)) | (mk1.y & (bk.w | bv.w))) != 0u;
+                        ka = at_factor(rowc, ring->half[0].ks.x);
+                        lv = ring->half[0].lv.x;
+                        iv = ring->half[0].iv.x;
                     }
-                    wait(&sh->sfull[s][h], pa, &sh->fail);
-                    __syncwarp();
-                    dt_tc_fence_after();
-                    half(&ring->half[h], st, to, has_o, rowc, masked, mk, m, l, other, other_ph, &sh->fail);
-                    dt_tc_fence_before();
-                    __syncwarp();
-                    if ((tid & 31) == 0) dt_mbar_arrive(&sh->pfull[s][h]);
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        wait(&sh->sfull[s][h], pa, &sh->fail);
+                        __syncwarp();
+                        dt_tc_fence_after();
+                        half_masked(ts + 64 * h, to, lt >= hop || h, ka, lv, iv, h ? mk1 : mk0, m, l, &sh->sfull[s][h ^ 1], pa ^ h, &sh->fail);
+                        dt_tc_fence_before();
+                        __syncwarp();
+                        if ((tid & 31) == 0) dt_mbar_arrive(&sh->pfull[s][h]);
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (; lt < nt; lt += hop, pa ^= 1) {
+                    const uint32_t g = g0 + lt;
+                    const Ring* ring = &sh->ring[g % RING];
+                    wait(&sh->scfull[g % RING], (g / RING) & 1, &sh->fail);
+                    // (under `clear`, known already: without it 16 trees of 257 nodes 1.14 ms instead of 1.13)
+                    if (lt >= clear && u.t0 + lt >= u.ctx && (sh->apart[g % RING].yes[0] | sh->apart[g % RING].yes[1])) break;
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        uint64_t* other = &sh->sfull[s][h ^ 1];  // of half 0: waited for next; of half 1: of the next tile
+                        const uint32_t other_ph = pa ^ h, st = ts + 64 * h;
+                        const bool has_o = lt >= hop || h;
+                        const bool masked = lt >= clear;
+                        uint2 mk = make_uint2(0u, 0u);
+                        if (masked) {
+                            mk = mask_words(a, u, u.t0 + lt, h, row, node_of(a, u, row));
+                            if (u.t0 + lt >= u.ctx)
+                                poison |= ((mk.x & (ring->bad[0][2 * h] | ring->bad[1][2 * h])) |
+                                           (mk.y & (ring->bad[0][2 * h + 1] | ring->bad[1][2 * h + 1]))) != 0u;
+                        }
+                        wait(&sh->sfull[s][h], pa, &sh->fail);
+                        __syncwarp();
+                        dt_tc_fence_after();
+                        half(&ring->half[h], st, to, has_o, rowc, masked, mk, m, l, other, other_ph, &sh->fail);
+                        dt_tc_fence_before();
+                        __syncwarp();
+                        if ((tid & 31) == 0) dt_mbar_arrive(&sh->pfull[s][h]);
+                    }
                 }
             }
             // new rows from a tile on whose rows have scales of their own (rare: short code, apart

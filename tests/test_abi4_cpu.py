@@ -26,15 +26,15 @@ def _attention4(cache=None, rope=None, batch=1, M=3, Hq=4, q=None, scale=1.0, ou
 def _read(four, cache=None, batch=1, rows=None, N=3, start=None, count=None, count_add=0, dtype=0, k=None, v=None,
           status=0x7000):
     call = dtree.lib().dt_kv_read4 if four else dtree.lib().dt_kv_read
-    return call(ref(cache or _cache()), batch, rows, N, start, count, count_add, dtype, ref(k or _rows()), ref(v or _rows()),
-                status, None)
+    return call(ref(cache or _cache()), batch, rows, N, start, count, count_add, dtype, ref(k or _rows()),
+                ref(v or _rows(ptr=0x9000)), status, None)
 
 
 def _norm(batch=1, M=3, Hq=4, Hk=2, D=64, dtype=0, q=None, k=None, qw=0x2000, qs=0, kw=0x3000, ks=0, eps=1e-6, rope=None,
           q_out=None, k_out=None, status=0x7000):
     return dtree.lib().dt_qk_norm(batch, M, Hq, Hk, D, dtype, ref(q or _rows()), ref(k or _rows()), qw, qs, kw, ks, eps,
                                   ref(rope) if rope else None, None, None, None, ref(q_out or _rows()),
-                                  ref(k_out or _rows()), status, None)
+                                  ref(k_out or _rows(ptr=0x9000)), status, None)
 
 
 @pytest.mark.parametrize("call", [_append4, _attention4, lambda **kw: _read(True, **kw), lambda **kw: _read(False, **kw)])
@@ -83,7 +83,7 @@ def test_attention():
 def test_read(four):
     for kw in (dict(batch=0), dict(N=0), dict(dtype=2), dict(status=None), dict(rows=0x8000, start=0x9000),
                dict(k=_rows(ptr=None)), dict(v=_rows(ptr=0x1008)), dict(v=_rows(stride_n=100)),
-               dict(k=_rows(stride_n=0)), dict(v=_rows(stride_h=56)), dict(k=_rows(stride_b=0), batch=2),
+               dict(v=_rows()), dict(k=_rows(stride_n=0)), dict(v=_rows(stride_h=56)), dict(k=_rows(stride_b=0), batch=2),
                dict(count=0x8000, count_add=-(1 << 30) - 1)):
         assert _read(four, **kw) == -1, kw
     assert _read(four, N=(1 << 30) + 1) == -2 and _read(four, cache=_cache(Hkv=32768)) == -2
@@ -94,7 +94,7 @@ def test_norm():
     for kw in (dict(batch=0), dict(M=0), dict(Hq=-1), dict(Hk=-1), dict(Hq=0, Hk=0), dict(D=0), dict(dtype=2),
                dict(eps=-1e-6), dict(eps=nan), dict(eps=inf), dict(status=None), dict(qw=0x2004), dict(qs=63), dict(ks=128),
                dict(q=_rows(ptr=None)), dict(k=_rows(ptr=0x1004)), dict(q_out=_rows(stride_h=60)),
-               dict(k_out=_rows(ptr=None)), dict(q_out=_rows(stride_h=0)), dict(k_out=_rows(stride_n=32)),
+               dict(k_out=_rows(ptr=None)), dict(k_out=_rows()), dict(q_out=_rows(stride_h=0)), dict(k_out=_rows(stride_n=32)),
                dict(q_out=_rows(stride_b=0), batch=2)):
         assert _norm(**kw) == -1, kw
     for kw in (dict(D=96), dict(D=256), dict(batch=65536), dict(M=(1 << 20) + 1), dict(Hq=65536), dict(batch=2048, M=1 << 20)):
