@@ -51,9 +51,10 @@
 // common loop and 0.90 with this.  Tiles of new rows and the context's last one take 6000
 // to 7500.  Rows without a rotation are read four at a time (queries 8 to 5 thousand clocks,
 // new rows 9 to 7), masks before the waits; with weights of its own for the division the
-// sixteen trees take 0.85 ms (68%), 64 trees of 61 nodes 128 us, 8 of 513 with D = 64 73 us.
+// sixteen trees take 0.85 ms (68%), 64 trees of 61 nodes 128 us, 8 of 513 with D = 64 70 us.
 // What did not help: new rows' loads or the next half's scores ahead (registers), waits that
-// look without sleeping (882 to 896 us), a short rolled loop for tiles with masks (961).
+// look without sleeping (882 to 896 us), a short rolled loop for tiles with masks (961), one
+// loop for tiles with and without masks (921), scores of a whole tile at a time (1077).
 #include <atomic>
 
 #include "dt_attend.cuh"

@@ -1,20 +1,21 @@
 // kn15_read.cu -- reading back tokens of the paged caches, in 4 bits and in e4m3
 // (dt_kv_read4, dt_kv_read).
 //
-// A thread turns 16 elements of a token's head (one scale of the 4-bit cache) into bf16 or
-// fp32 and writes them at once; a CTA keeps to one head, whose tokens lie together in a page.
+// A thread turns runs of 32 elements of a token's head (two scales of the 4-bit cache) into
+// bf16 or fp32; a CTA keeps to one head, whose tokens lie together in a page.
 //
 // Bound by HBM, mostly writes: 8 contexts of 500 to 8000 tokens of 8 heads of 128 to bf16,
-// 178 MB, 31 us, 5.8 TB/s (85% of a copy's rate).  With 1, 2, 4, 8 blocks in flight per
-// thread 61, 40, 33, 31 us at four CTAs to an SM; four at six CTAs 31.  Picked rows take the
-// latency of four dependent reads: 16 requests' 129 tokens of e4m3 4.5 us.
+// 178 MB, 30 us, 5.9 TB/s (87% of a copy's rate).  Runs of 16 took 31 us and issued in 81% of
+// the clocks, half of that for addresses; one, two, four runs of 32 in flight per thread take
+// 32, 30, 30 us.  Picked rows take the latency of four dependent reads: 16 requests' 129 tokens of
+// e4m3 4.5 us.
 #include "dt_cache.cuh"
 #include "dt_launch.h"
 
 namespace {
 
 constexpr int NT = 256;
-constexpr int U = 4;  // blocks of 16 in flight per thread
+constexpr int U = 2;  // runs of 32 in flight per thread
 
 DT_DI uint32_t bf16x2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -31,37 +32,37 @@ DT_DI void store16(void* p, const uint32_t (&w)[8]) {
 }
 
 template <int BITS>
-struct Raw {  // 16 codes and their scale
-    uint4 q;
-    float s;
-    DT_DI void load(const uint8_t* codes, const void* scales, size_t slot, size_t blk, int nb, int at) {
-        if (BITS == 4) {
-            const uint2 w = *(const uint2*)(codes + (slot * nb + at) * 8);
-            q = make_uint4(w.x, w.y, 0u, 0u);
-            s = __int_as_float(((const uint8_t*)scales)[slot * nb + at]);
-        } else {
-            q = *(const uint4*)(codes + (slot * nb + at) * 16);
-            s = ((const float*)scales)[blk];
-        }
+struct Raw {  // 32 codes and their scales
+    uint4 q[BITS / 4];
+    uint32_t s;  // two scale bytes, or an fp32 number's bits
+    DT_DI void load(const uint8_t* codes, const void* scales, size_t slot, size_t blk, int runs, int at) {
+        const uint4* p = (const uint4*)codes + (slot * runs + at) * (BITS / 4);
+#pragma unroll
+        for (int i = 0; i < BITS / 4; ++i) q[i] = p[i];
+        s = BITS == 4 ? ((const uint16_t*)scales)[slot * runs + at] : ((const uint32_t*)scales)[blk];
     }
-    DT_DI void values(float (&x)[16]) const {
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-        const float f = BITS == 4 ? dt_e5m3_to_f32(__float_as_int(s)) : s;
+    // Elements 16 half .. 16 half + 15, as pairs of fp32.
+    DT_DI void values(int half, float2 (&x)[8]) const {
+        const uint4 w = BITS == 4 ? q[0] : q[half & (BITS / 4 - 1)];
+        uint32_t h[8];
+        float f;
+        if constexpr (BITS == 4) {
+            uint32_t lo[4], hi[4];
+            dt_e2m1x8_to_f16x8(half ? w.z : w.x, lo);
+            dt_e2m1x8_to_f16x8(half ? w.w : w.y, hi);
 #pragma unroll
-        for (int i = 0; i < 4; i += (BITS == 4 ? 2 : 1)) {
-            uint32_t h[4];
-            if (BITS == 4) {
-                dt_e2m1x8_to_f16x8(w[i / 2], h);
-            } else {
-                dt_e4m3x4_to_f16x4(w[i], h[0], h[1]);
-            }
-#pragma unroll
-            for (int k = 0; k < (BITS == 4 ? 4 : 2); ++k) {
-                const float2 v = __half22float2(*(const __half2*)&h[k]);
-                x[4 * i + 2 * k] = __fmul_rn(v.x, f);
-                x[4 * i + 2 * k + 1] = __fmul_rn(v.y, f);
-            }
+            for (int i = 0; i < 4; ++i) h[i] = lo[i], h[4 + i] = hi[i];
+            f = dt_e5m3_to_f32(half ? s >> 8 : s & 255u);
+        } else {
+            dt_e4m3x4_to_f16x4(w.x, h[0], h[1]);
+            dt_e4m3x4_to_f16x4(w.y, h[2], h[3]);
+            dt_e4m3x4_to_f16x4(w.z, h[4], h[5]);
+            dt_e4m3x4_to_f16x4(w.w, h[6], h[7]);
+            f = __uint_as_float(s);
         }
+        const float2 f2 = make_float2(f, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(__half22float2(*(const __half2*)&h[i]), f2);
     }
 };
 
@@ -84,13 +85,13 @@ __global__ void __launch_bounds__(NT, 6) kn15_kernel(const __grid_constant__ dt_
         return;
     }
     const int n = (int)want;
-    const int sh = c.D == 128 ? 3 : 2, nb = 1 << sh, blk = tid & (nb - 1);  // blocks of a head
+    const int sh = c.D == 128 ? 2 : 1, runs = 1 << sh, run = tid & (runs - 1);  // runs of a head
     const int lp = 31 - __clz(c.page);
     const int32_t* table = c.table + (size_t)b * c.max_pages;
     const uint8_t* codes = keys ? c.k : c.v;
     const void* scales = keys ? c.k_scale : c.v_scale;
     const dt_rows& dst = keys ? ko : vo;
-    char* out = (char*)dst.ptr + (b * dst.stride_b + h * dst.stride_h + blk * 16) * OUT;
+    char* out = (char*)dst.ptr + (b * dst.stride_b + h * dst.stride_h + run * 32) * OUT;
     const int per = NT >> sh;  // tokens of a pass
     for (int j0 = (int)blockIdx.x * U * per + (tid >> sh); j0 < n; j0 += (int)gridDim.x * U * per) {
         Raw<BITS> raw[U];
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(NT, 6) kn15_kernel(const __grid_constant__ dt_
                 }
                 if (!off[i]) {
                     const size_t k = (size_t)id * c.Hkv + h;
-                    raw[i].load(codes, scales, (k << lp) + (tok & (c.page - 1)), k, nb, blk);
+                    raw[i].load(codes, scales, (k << lp) + (tok & (c.page - 1)), k, runs, run);
                 }
             }
         }
@@ -117,23 +118,24 @@ __global__ void __launch_bounds__(NT, 6) kn15_kernel(const __grid_constant__ dt_
         for (int i = 0; i < U; ++i) {
             const int j = j0 + i * per;
             if (j >= n) continue;
-            float x[16];
-            if (off[i]) {
-                atomicOr(&status[b], DT_DEV_BAD_CACHE);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = 0.f;
-            } else {
-                raw[i].values(x);
-            }
+            if (off[i]) atomicOr(&status[b], DT_DEV_BAD_CACHE);
             char* o = out + j * dst.stride_n * OUT;
 #pragma unroll
-            for (int part = 0; part < OUT / 2; ++part) {
-                uint32_t w[8];
+            for (int half = 0; half < 2; ++half) {
+                float2 x[8];
+                raw[i].values(half, x);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    w[e] = OUT == 2 ? bf16x2(x[2 * e], x[2 * e + 1]) : __float_as_uint(x[8 * part + e]);
-                if (WIDE) store32(o + 32 * part, w);
-                else store16(o + 32 * part, w);
+                for (int part = 0; part < OUT / 2; ++part) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (OUT == 2) w[e] = bf16x2(x[e].x, x[e].y);
+                        else w[e] = __float_as_uint(e & 1 ? x[4 * part + e / 2].y : x[4 * part + e / 2].x);
+                        if (off[i]) w[e] = 0u;
+                    }
+                    if (WIDE) store32(o + 16 * OUT * half + 32 * part, w);
+                    else store16(o + 16 * OUT * half + 32 * part, w);
+                }
             }
         }
     }
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(NT, 6) kn15_kernel(const __grid_constant__ dt_
 template <int BITS, int OUT, bool WIDE>
 cudaError_t launch(const dt_kv_cache& c, int batch, const int32_t* rows, int N, const int32_t* start, const int32_t* count,
                    int count_add, const dt_rows& k, const dt_rows& v, int32_t* status, cudaStream_t st) {
-    const int per = NT * 16 / c.D * U;  // tokens of a CTA
+    const int per = NT * 32 / c.D * U;  // tokens of a CTA
     DtLaunch lc(dim3((N + per - 1) / per, 2 * c.Hkv, batch), dim3(NT), 0, st);
     return cudaLaunchKernelEx(&lc.cfg, kn15_kernel<BITS, OUT, WIDE>, c, rows, N, start, count, count_add, k, v, status);
 }
