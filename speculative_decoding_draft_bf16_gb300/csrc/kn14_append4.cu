@@ -15,7 +15,8 @@
 //             half a step of fp32 away from it.
 //
 // Paths take a launch and three dependent reads: 64 paths of up to 17 rows 2.7 us.  Prompts are
-// bound by instructions (280 for 32 elements) and the rows in flight: 8 prompts of up to
+// bound by the rows in flight, not by issue (280 instructions for 32 elements, 44% of the
+// slots; most stalls wait for loads): 8 prompts of up to
 // 4000 bf16 rows, 8 heads of 128, 126 MB in all, 27.8 us, 4.5 TB/s (67% of a copy's rate);
 // fp32 45.7.  Four heads to a thread share a token's angles and the checks: with one each
 // 55 us.  CTAs of 128 threads start and end more evenly than of 256 (29.5 us); three of 256 to

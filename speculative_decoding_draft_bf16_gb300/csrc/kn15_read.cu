@@ -6,7 +6,7 @@
 //
 // Bound by HBM, mostly writes: 8 contexts of 500 to 8000 tokens of 8 heads of 128 to bf16,
 // 178 MB, 30 us, 5.9 TB/s (87% of a copy's rate).  Runs of 16 took 31 us and issued in 81% of
-// the clocks, half of that for addresses; one, two, four runs of 32 in flight per thread take
+// the clocks; one, two, four runs of 32 in flight per thread take
 // 32, 30, 30 us.  Picked rows take the latency of four dependent reads: 16 requests' 129 tokens of
 // e4m3 4.5 us.
 #include "dt_cache.cuh"
