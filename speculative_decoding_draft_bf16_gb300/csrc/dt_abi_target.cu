@@ -108,10 +108,11 @@ dt_status attend(const dt_kv_cache& c, int bits, const dt_rope* rope, int32_t ba
     if (s != DT_OK) return s;
     if (M < 1 || Hq < 1 || Hq % c.Hkv != 0) return DT_ERR_INVALID_ARG;
     if (Hq / c.Hkv > 128 || Hq > 65535 || M > (1 << 20)) return DT_ERR_UNSUPPORTED;
-    // the work division counts tiles in 32 bits
+    // the work division counts in 32 bits: a unit's tiles and its start, at the weights of AtPlan
     const long long rows = (long long)M * (Hq / c.Hkv);
     const double tiles = (double)c.max_pages * c.page / 128 + M / 128 + 2;
-    if ((double)batch * c.Hkv * (rows / 256 + 1) * (tiles * 6 + 30) > 4.2e9) return DT_ERR_UNSUPPORTED;
+    const double unit = rows <= kStreamRows ? tiles + 6 : bits == 4 ? tiles * 6 + 30 : tiles * 5 + 20;
+    if ((double)batch * c.Hkv * (rows / 256 + 1) * unit > 4.2e9) return DT_ERR_UNSUPPORTED;
     if (!rows_ok(q, 2) || !rows_ok(k, 2) || !rows_ok(v, 2)) return DT_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !std::isfinite(scale)) return DT_ERR_INVALID_ARG;
     if (!out || !aligned16(out) || !status) return DT_ERR_INVALID_ARG;

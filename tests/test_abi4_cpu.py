@@ -107,3 +107,19 @@ def test_null_caches():
     assert L.dt_kv_read4(None, 1, None, 1, None, None, 0, 0, ref(_rows()), ref(_rows()), 0x7000, None) == -1
     assert L.dt_kv_read(None, 1, None, 1, None, None, 0, 0, ref(_rows()), ref(_rows()), 0x7000, None) == -1
     assert L.dt_tree_attention4_workspace(None, 1, 1, 1) == 0
+
+
+def test_the_division_counts_each_form_with_its_own_weights():
+    """Refused (-2) where a form's units would leave 32 bits and not before; `status` is left out, so that
+    what passes is refused next (-1) and nothing is launched."""
+    def eight(cache, M):
+        return dtree.lib().dt_tree_attention(ref(cache), None, 65535, M, cache.Hkv, ref(_rows()), ref(_rows()), ref(_rows()),
+                                             None, None, None, 1.0, 0x8000, 0x9000, 1 << 40, None, None)
+
+    def four(cache, M):
+        return _attention4(cache=cache, batch=65535, M=M, Hq=cache.Hkv, status=None)
+
+    # two tiles and an eighth a unit at most: with 17 rows 42.75 (4 bits) and 30.625 a unit, with 3 rows 8.125
+    for Hkv, M, rc4, rc8 in ((1400, 17, -1, -1), (1800, 17, -2, -1), (2200, 17, -2, -2), (6000, 3, -1, -1), (8000, 3, -2, -2)):
+        cache = _cache(Hkv=Hkv, max_pages=1, page=16)
+        assert (four(cache, M), eight(cache, M)) == (rc4, rc8)
