@@ -7,9 +7,9 @@
 // first, so that the token's angles and the kind's weights are read once; steps of a few
 // heads are loaded while those before them are worked on.
 //
-// Bound by HBM: eight prompts of up to 4000 rows, 40 heads of 128 in bf16, 504 MB, 87 us, 5.8
-// TB/s (86% of a copy's rate); 4112 rows of 32 heads in fp32 with weights of each head, 102
-// MB, 23 us.  64 single tokens take 2.5 us, a launch and two dependent reads.  Persistent
+// Bound by HBM: eight prompts of up to 4000 rows, 40 heads of 128 in bf16, 504 MB, 86 us, 5.9
+// TB/s (87% of a copy's rate); 4112 rows of 32 heads in fp32 with weights of each head, 102
+// MB, 23 us.  64 single tokens take 2.4 us, a launch and two dependent reads.  Persistent
 // warps that copied rows ahead through shared memory took 91 us: the bookkeeping of such a
 // queue costs more instructions (260 a step) than the rows in flight gain.
 #include "dt_cache.cuh"
@@ -66,16 +66,31 @@ DT_DI float mean_square(const f2 (&x)[4], const f2 (&y)[4]) {
     for (int d = 1; d < PPR; d <<= 1) r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, d));
     return __fmul_rn(r, 1.f / (16 * PPR));
 }
-// 1 / sqrt(mean square + eps).  Squares that leave fp32's range are formed again of
-// numbers 2^-68 as large; such heads need no eps.
-template <int PPR>
-DT_DI float inverse_root(const f2 (&x)[4], const f2 (&y)[4], float eps) {
-    const float s = mean_square<PPR, false>(x, y);
-    if (__any_sync(0xffffffffu, s > 3e37f)) {  // all lanes go on together
+// 1 / sqrt(mean square + eps).  Squares that leave fp32's range upwards are formed again of
+// numbers 2^-68 as large; such heads need no eps.  With an eps below TINY squares may leave it
+// downwards, too: the head itself is scaled then, by 2^100, and eps by 2^200, because the root's
+// reciprocal of the smallest numbers would leave the range and its product with them does not.
+// Only one step at a time does that, and both ends alike: 3904 short rows take 10.7 us with it and
+// 10.9 without, but the prompts above, two steps at a time, 86 without and 89 to 92 with it.
+constexpr float TINY = 1e-30f;
+template <int PPR, int U>
+DT_DI float inverse_root(f2 (&x)[4], f2 (&y)[4], float eps) {
+    const float s = __fadd_rn(mean_square<PPR, false>(x, y), eps);
+    const bool big = s > 3e37f, tiny = U == 1 && s < TINY;
+    if (__any_sync(0xffffffffu, big || tiny)) {  // all lanes go on together
+        if (U == 1) {
+            const float k = big ? dt_pow2(-68) : tiny ? dt_pow2(100) : 1.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = mul2(x[i], make_float2(k, k));
+                y[i] = mul2(y[i], make_float2(k, k));
+            }
+            return rsqrtf(__fadd_rn(mean_square<PPR, false>(x, y), __fmul_rn(__fmul_rn(eps, k), k)));
+        }
         const float t = mean_square<PPR, true>(x, y);
-        if (s > 3e37f) return __fmul_rn(rsqrtf(t), dt_pow2(-68));
+        if (big) return __fmul_rn(rsqrtf(t), dt_pow2(-68));
     }
-    return rsqrtf(__fadd_rn(s, eps));
+    return rsqrtf(s);
 }
 
 // A token's angles for a lane's chunk pair; n: minus the sines.
@@ -171,7 +186,7 @@ DT_DI void run_heads(const T* in, long long in_stride, T* out, long long out_str
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             if (s + i >= s1) break;
-            const float f = inverse_root<PPR>(x[i], y[i], eps);
+            const float f = inverse_root<PPR, U>(x[i], y[i], eps);
             const f2 ff = make_float2(f, f);
             if (w_stride && now + i * VPW < H) {
                 load_pairs(w + (now + i * VPW) * w_stride + c0, g0);
@@ -243,9 +258,10 @@ cudaError_t launch(DtNorm a, int sms, cudaStream_t st) {
     a.parts = a.parts < most ? a.parts : most;
     a.per = (most + a.parts - 1) / a.parts;
     const long long units = tokens * a.parts, need = (units + NT / 32 - 1) / (NT / 32);
-    // whole tokens: two steps at a time (the prompts 87 us, one at a time 91); parts of
-    // tokens have few steps (3904 short rows 12.6 us with two, 10.9 with one)
-    return (a.parts == 1 ? launch_u<T, D, 2> : launch_u<T, D, 1>)(a, (unsigned)need, st);
+    // whole tokens: two steps at a time (the prompts 86 us, one at a time 89); parts of
+    // tokens have few steps (3904 short rows 12.6 us with two, 10.7 with one), and an eps below
+    // TINY needs one at a time
+    return (a.parts == 1 && a.eps >= TINY ? launch_u<T, D, 2> : launch_u<T, D, 1>)(a, (unsigned)need, st);
 }
 
 }  // namespace

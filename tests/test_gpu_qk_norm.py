@@ -86,6 +86,17 @@ def test_magnitudes(size):
     run(2, 7, 5, 1, 64, torch.bfloat16, size=size, eps=0.1, seed=4)
 
 
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -140, 2.0 ** -110])
+@pytest.mark.parametrize("size", [1e-14, 1e-16, 1e-19, 1e-25, 1e-38, 1e-43])
+def test_squares_below_the_range(size, eps):
+    """Heads whose squares, and eps, are below what fp32 holds, denormal numbers among them."""
+    run(2, 7, 5, 1, 128, torch.float32, size=size, eps=eps, seed=5)
+    run(2, 9, 7, 3, 64, torch.float32, size=size, eps=eps, heads=True, inplace=True, seed=6)
+    run(1, 5100, 9, 2, 64, torch.float32, size=size, eps=eps, seed=8)  # whole tokens to a warp
+    if size > 1e-39:  # numbers of bf16
+        run(2, 7, 5, 1, 64, torch.bfloat16, size=size, eps=eps, tree=True, seed=7)
+
+
 def test_values_that_are_not_finite_stay_in_their_head():
     g = torch.Generator().manual_seed(1)
     x = torch.randn((1, 3, 4, 128), generator=g).to(torch.bfloat16).cuda()
