@@ -608,6 +608,8 @@ class PagedCache:
             raise ValueError("table must be [batch, max_pages], got %s" % (tuple(table.shape),))
         self.batch, self.max_pages = table.shape
         _need(len, torch.int32, "len", numel=self.batch)
+        if {t.get_device() for t in (k, v, k_scale, v_scale, len)} != {table.get_device()}:
+            raise ValueError("a cache's tensors must be on one device")
         self.k, self.v, self.k_scale, self.v_scale, self.table, self.len = k, v, k_scale, v_scale, table, len
         self._struct = CacheStruct(self.n_pages, self.page, self.Hkv, self.D, self.max_pages, k.data_ptr(),
                                    v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
@@ -649,6 +651,8 @@ class PagedCache4:
             raise ValueError("table must be [batch, max_pages], got %s" % (tuple(table.shape),))
         self.batch, self.max_pages = table.shape
         _need(len, torch.int32, "len", numel=self.batch)
+        if {t.get_device() for t in (k, v, k_scale, v_scale, len)} != {table.get_device()}:
+            raise ValueError("a cache's tensors must be on one device")
         self.k, self.v, self.k_scale, self.v_scale, self.table, self.len = k, v, k_scale, v_scale, table, len
         self._struct = CacheStruct(self.n_pages, self.page, self.Hkv, self.D, self.max_pages, k.data_ptr(),
                                    v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
@@ -700,6 +704,12 @@ def _need_here(x, name, device):
         raise ValueError("%s must be on the current device" % name)
 
 
+def _need_all_here(device, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("every tensor of the call must be on the current device")
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -731,6 +741,7 @@ def kv_append(cache, k, v, rope=None, rows=None, count=None, count_add=0, len_ou
             status = torch.zeros((batch,), dtype=torch.int32, device=k.device)
     else:
         _need(status, torch.int32, "status", numel=batch)
+    _need_all_here(device, rows, count, len_out, status)
     call = lib().dt_kv_append4 if isinstance(cache, PagedCache4) else lib().dt_kv_append
     _check(call(cache._ref, rope._ref if rope is not None else None, batch, M, _dtype_code(k), kr, vr, _addr(rows), N,
                 _addr(count), int(count_add), _addr(len_out), status.data_ptr(),
@@ -781,6 +792,7 @@ def kv_read(cache, N=None, rows=None, start=None, count=None, count_add=0, dtype
         raise TypeError("k (%s) and v (%s) must share one dtype" % (k.dtype, v.dtype))
     shape = (batch, N, Hkv, D)
     kr, vr = _head_rows(k, shape, "k", device), _head_rows(v, shape, "v", device)
+    _need_all_here(device, rows, start, count, status)
     call = lib().dt_kv_read4 if isinstance(cache, PagedCache4) else lib().dt_kv_read
     _check(call(cache._ref, batch, _addr(rows), N, _addr(start), _addr(count), int(count_add), _dtype_code(k), kr, vr,
                 status.data_ptr(), _raw_stream(device) if stream is None else stream.cuda_stream), "dt_kv_read")
@@ -837,6 +849,7 @@ def qk_norm(q, k, q_weight=None, k_weight=None, eps=1e-6, rope=None, len=None, p
     _need(status, torch.int32, "status", numel=batch)
     qw, qs = _norm_weight(q_weight, Hq, D, "q_weight")
     kw, ks = _norm_weight(k_weight, Hk, D, "k_weight")
+    _need_all_here(device, q_weight, k_weight, len, pos, n_nodes, status)
     _check(lib().dt_qk_norm(batch, M, Hq, Hk, D, _dtype_code(q), qr, kr, qw, qs, kw, ks, eps,
                             rope._ref if rope is not None else None, _addr(len), _addr(pos), _addr(n_nodes), qo, ko,
                             status.data_ptr(), _raw_stream(device) if stream is None else stream.cuda_stream), "dt_qk_norm")
@@ -887,6 +900,7 @@ def tree_attention(cache, q, k, v, mask=None, pos=None, n_nodes=None, rope=None,
     ws, n = _need_workspace(workspace)
     if scale is None:
         scale = 1.0 / math.sqrt(cache.D)
+    _need_all_here(device, mask, pos, n_nodes, out, ws, status)
     call = lib().dt_tree_attention4 if isinstance(cache, PagedCache4) else lib().dt_tree_attention
     _check(call(cache._ref, rope._ref if rope is not None else None, batch, M, Hq, qr, kr, vr, _addr(mask), _addr(pos),
                 _addr(n_nodes), scale, out.data_ptr(), _addr(ws), n, status.data_ptr(),

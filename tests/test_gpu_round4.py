@@ -143,3 +143,36 @@ def test_calls_on_two_streams():
         assert torch.equal(q1, want[0]) and torch.equal(k1, want[1])
         for y, z in ((kr, k1), (vr, v)):
             assert torch.equal(y.double(), ref4.values4(*ref4.quantised(z.double())))
+
+
+class Elsewhere(torch.Tensor):
+    """A tensor that says it is on another device."""
+
+    def get_device(self):
+        return 1 + super().get_device()
+
+
+def test_tensors_on_another_device_are_refused():
+    B, M, H, D = 1, 2, 2, 64
+    x = torch.zeros((B, M, H, D), dtype=torch.bfloat16, device="cuda")
+    one, mask = torch.ones(B, **I32), torch.zeros((B, M, 1), **I32)
+    pos, w = torch.zeros((B, M), **I32), torch.ones(D, device="cuda")
+    away = lambda t: t.as_subclass(Elsewhere)  # noqa: E731
+    for kind in (dtree.PagedCache, dtree.PagedCache4):
+        cache = kind.empty(2, 16, H, D, B, 2)
+        ws, n = dtree.attention_workspace(cache, M, H)
+        calls = [(dtree.kv_append, (cache, x, x), dict(rows=pos, count=one, len_out=one.clone(), status=one)),
+                 (dtree.kv_read, (cache,), dict(rows=pos, count=one, status=one)),
+                 (dtree.kv_read, (cache, 2), dict(start=one)),
+                 (dtree.tree_attention, (cache, x, x, x), dict(mask=mask, pos=pos, n_nodes=one, out=x.clone(),
+                                                               workspace=(ws, n), status=one)),
+                 (dtree.qk_norm, (x, x), dict(q_weight=w, k_weight=w, len=one, pos=pos, n_nodes=one, status=one))]
+        for call, args, kw in calls:
+            for name, t in kw.items():
+                t = (away(ws), n) if name == "workspace" else away(t)
+                with pytest.raises(ValueError):
+                    call(*args, **{**kw, name: t})
+        f = dict(k=cache.k, v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale, table=cache.table, len=cache.len)
+        for name, t in f.items():
+            with pytest.raises(ValueError):
+                kind(**{**f, name: away(t)})
