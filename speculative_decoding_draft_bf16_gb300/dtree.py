@@ -704,10 +704,13 @@ def _need_here(x, name, device):
         raise ValueError("%s must be on the current device" % name)
 
 
-def _need_all_here(device, *tensors):
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError("every tensor of the call must be on the current device")
+def _need_at(t, device, dtype, name, numel=None):
+    """_need on the current device."""
+    if t.get_device() == device and t.is_contiguous() and t.dtype == dtype and (numel is None or t.numel() >= numel):
+        return t
+    if t.is_cuda and t.get_device() != device:
+        raise ValueError("%s must be on the current device" % name)
+    return _need(t, dtype, name, numel)
 
 
 def _addr(t):
@@ -728,20 +731,19 @@ def kv_append(cache, k, v, rope=None, rows=None, count=None, count_add=0, len_ou
     kr, vr = _head_rows(k, shape, "k", device), _head_rows(v, shape, "v", device)
     N = M
     if rows is not None:
-        _need(rows, torch.int32, "rows")
+        _need_at(rows, device, torch.int32, "rows")
         if rows.dim() != 2 or rows.shape[0] != batch:
             raise ValueError("rows must be [batch, N], got %s" % (tuple(rows.shape),))
         N = rows.shape[1]
     if count is not None:
-        _need(count, torch.int32, "count", numel=batch)
+        _need_at(count, device, torch.int32, "count", numel=batch)
     if len_out is not None:
-        _need(len_out, torch.int32, "len_out", numel=batch)
+        _need_at(len_out, device, torch.int32, "len_out", numel=batch)
     if status is None:
         with _on(stream):
             status = torch.zeros((batch,), dtype=torch.int32, device=k.device)
     else:
-        _need(status, torch.int32, "status", numel=batch)
-    _need_all_here(device, rows, count, len_out, status)
+        _need_at(status, device, torch.int32, "status", numel=batch)
     call = lib().dt_kv_append4 if isinstance(cache, PagedCache4) else lib().dt_kv_append
     _check(call(cache._ref, rope._ref if rope is not None else None, batch, M, _dtype_code(k), kr, vr, _addr(rows), N,
                 _addr(count), int(count_add), _addr(len_out), status.data_ptr(),
@@ -760,7 +762,7 @@ def kv_read(cache, N=None, rows=None, start=None, count=None, count_add=0, dtype
     batch, Hkv, D, device = cache.batch, cache.Hkv, cache.D, torch.cuda.current_device()
     _need_here(cache, "cache", device)
     if rows is not None:
-        _need(rows, torch.int32, "rows")
+        _need_at(rows, device, torch.int32, "rows")
         if rows.dim() != 2 or rows.shape[0] != batch:
             raise ValueError("rows must be [batch, N], got %s" % (tuple(rows.shape),))
         if start is not None:
@@ -775,9 +777,9 @@ def kv_read(cache, N=None, rows=None, start=None, count=None, count_add=0, dtype
     if N is None:
         raise ValueError("N is needed without rows and outputs")
     if start is not None:
-        _need(start, torch.int32, "start", numel=batch)
+        _need_at(start, device, torch.int32, "start", numel=batch)
     if count is not None:
-        _need(count, torch.int32, "count", numel=batch)
+        _need_at(count, device, torch.int32, "count", numel=batch)
     if k is None or v is None or status is None:
         with _on(stream):
             held = dict(dtype=dtype if k is None and v is None else (v if k is None else k).dtype, device=cache.k.device)
@@ -787,23 +789,22 @@ def kv_read(cache, N=None, rows=None, start=None, count=None, count_add=0, dtype
                 v = torch.zeros((batch, N, Hkv, D), **held)
             if status is None:
                 status = torch.zeros((batch,), dtype=torch.int32, device=cache.k.device)
-    _need(status, torch.int32, "status", numel=batch)
+    _need_at(status, device, torch.int32, "status", numel=batch)
     if k.dtype != v.dtype:
         raise TypeError("k (%s) and v (%s) must share one dtype" % (k.dtype, v.dtype))
     shape = (batch, N, Hkv, D)
     kr, vr = _head_rows(k, shape, "k", device), _head_rows(v, shape, "v", device)
-    _need_all_here(device, rows, start, count, status)
     call = lib().dt_kv_read4 if isinstance(cache, PagedCache4) else lib().dt_kv_read
     _check(call(cache._ref, batch, _addr(rows), N, _addr(start), _addr(count), int(count_add), _dtype_code(k), kr, vr,
                 status.data_ptr(), _raw_stream(device) if stream is None else stream.cuda_stream), "dt_kv_read")
     return k, v
 
 
-def _norm_weight(w, H, D, name):
+def _norm_weight(w, H, D, name, device):
     """(address, stride between heads) of weights [D] or [H, D]."""
     if w is None:
         return None, 0
-    _need(w, torch.float32, name)
+    _need_at(w, device, torch.float32, name)
     if w.shape not in ((D,), (H, D)):
         raise ValueError("%s must be %s or %s, got %s" % (name, (D,), (H, D), tuple(w.shape)))
     return w.data_ptr(), D if w.dim() == 2 else 0
@@ -841,15 +842,14 @@ def qk_norm(q, k, q_weight=None, k_weight=None, eps=1e-6, rope=None, len=None, p
         if k.dtype != dtype or k_out.dtype != dtype:
             raise TypeError("k and k_out must be %s, got %s and %s" % (dtype, k.dtype, k_out.dtype))
     if len is not None:
-        _need(len, torch.int32, "len", numel=batch)
+        _need_at(len, device, torch.int32, "len", numel=batch)
     if pos is not None:
-        _need(pos, torch.int32, "pos", numel=batch * M)
+        _need_at(pos, device, torch.int32, "pos", numel=batch * M)
     if n_nodes is not None:
-        _need(n_nodes, torch.int32, "n_nodes", numel=batch)
-    _need(status, torch.int32, "status", numel=batch)
-    qw, qs = _norm_weight(q_weight, Hq, D, "q_weight")
-    kw, ks = _norm_weight(k_weight, Hk, D, "k_weight")
-    _need_all_here(device, q_weight, k_weight, len, pos, n_nodes, status)
+        _need_at(n_nodes, device, torch.int32, "n_nodes", numel=batch)
+    _need_at(status, device, torch.int32, "status", numel=batch)
+    qw, qs = _norm_weight(q_weight, Hq, D, "q_weight", device)
+    kw, ks = _norm_weight(k_weight, Hk, D, "k_weight", device)
     _check(lib().dt_qk_norm(batch, M, Hq, Hk, D, _dtype_code(q), qr, kr, qw, qs, kw, ks, eps,
                             rope._ref if rope is not None else None, _addr(len), _addr(pos), _addr(n_nodes), qo, ko,
                             status.data_ptr(), _raw_stream(device) if stream is None else stream.cuda_stream), "dt_qk_norm")
@@ -880,15 +880,15 @@ def tree_attention(cache, q, k, v, mask=None, pos=None, n_nodes=None, rope=None,
     shape = (batch, M, cache.Hkv, cache.D)
     kr, vr = _head_rows(k, shape, "k", device), _head_rows(v, shape, "v", device)
     if mask is not None:
-        _need(mask, torch.int32, "mask", numel=batch * M * ((M + 31) // 32))
+        _need_at(mask, device, torch.int32, "mask", numel=batch * M * ((M + 31) // 32))
     if pos is not None:
-        _need(pos, torch.int32, "pos", numel=batch * M)
+        _need_at(pos, device, torch.int32, "pos", numel=batch * M)
     if n_nodes is not None:
-        _need(n_nodes, torch.int32, "n_nodes", numel=batch)
+        _need_at(n_nodes, device, torch.int32, "n_nodes", numel=batch)
     if out is not None:
-        _need(out, torch.bfloat16, "out", numel=batch * M * Hq * cache.D)
+        _need_at(out, device, torch.bfloat16, "out", numel=batch * M * Hq * cache.D)
     if status is not None:
-        _need(status, torch.int32, "status", numel=batch)
+        _need_at(status, device, torch.int32, "status", numel=batch)
     if out is None or status is None or workspace is None:
         with _on(stream):
             if out is None:
@@ -898,9 +898,10 @@ def tree_attention(cache, q, k, v, mask=None, pos=None, n_nodes=None, rope=None,
             if workspace is None:
                 workspace = attention_workspace(cache, M, Hq)
     ws, n = _need_workspace(workspace)
+    if ws is not None and ws.get_device() != device:
+        raise ValueError("workspace must be on the current device")
     if scale is None:
         scale = 1.0 / math.sqrt(cache.D)
-    _need_all_here(device, mask, pos, n_nodes, out, ws, status)
     call = lib().dt_tree_attention4 if isinstance(cache, PagedCache4) else lib().dt_tree_attention
     _check(call(cache._ref, rope._ref if rope is not None else None, batch, M, Hq, qr, kr, vr, _addr(mask), _addr(pos),
                 _addr(n_nodes), scale, out.data_ptr(), _addr(ws), n, status.data_ptr(),
