@@ -660,7 +660,9 @@ dt_status dt_tree_attention(const dt_kv_cache* c, const dt_rope* rope, int32_t b
                             size_t workspace_bytes, int32_t* status, dt_stream_t stream);
 
 /* The same over a 4-bit cache (codes times scales are exact in fp16, too); new values
- * below 2^-24 may count as zero.  A workspace serves calls of both kinds. */
+ * below 2^-24 may count as zero, and beside a new value of 2^100 or more the weights of other
+ * tokens may (such values cannot be appended: the cache holds 61440 at most).  A workspace
+ * serves calls of both kinds. */
 size_t dt_tree_attention4_workspace(const dt_kv_cache4* c, int32_t batch, int32_t M, int32_t Hq);
 dt_status dt_tree_attention4(const dt_kv_cache4* c, const dt_rope* rope, int32_t batch, int32_t M, int32_t Hq,
                              const dt_rows* q, const dt_rows* k, const dt_rows* v, const uint32_t* mask,

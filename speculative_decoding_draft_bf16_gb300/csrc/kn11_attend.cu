@@ -473,6 +473,9 @@ struct Stream {
     // The first of a warp's sums, from one new row that is not rotated: its score in fp32, its
     // weight 2^HEADROOM.  A single token's own row comes once to every unit and is work for one
     // warp, so this is short: fresh() takes 6000 clocks, most of them to fetch its instructions.
+    // Keys are summed 2^-8 as large, so that products that cancel do not leave the range, and a
+    // row with a value of 2^100 or more has the weight 2^-8, so that the product stays in it and
+    // the other tokens' weights, which the same sum counts, do too.
     DT_DI void fresh_one(const DtAttend& a, const Walk& u, int lane) {
         const int g = lane >> 2, t = lane & 3;
         const uint16_t* kp = (const uint16_t*)a.k.ptr + u.b * a.k.stride_b + u.h * a.k.stride_h;
@@ -482,7 +485,7 @@ struct Stream {
         for (int j = 0; j < 2 * L::KC; ++j) kw[j] = *(const uint4*)(kp + run_of(t, 0) * 16 + 8 * j);  // KC runs in a row
 #pragma unroll
         for (int j = 0; j < L::VB / 8; ++j) vw[j] = *(const uint4*)(vp + L::VB * g + 8 * j);
-        bool bad = false;
+        bool bad = false, far = false;
         float v[L::VB], dot[NR];
         auto finite = [&](float x) {  // zeros for what is not, which `bad` reports
             const bool odd = !(fabsf(x) < __int_as_float(0x7F800000));
@@ -494,7 +497,10 @@ struct Stream {
             float y[8];
             dt_vec_vals<uint16_t>(vw[j], y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[8 * j + e] = finite(y[e]);
+            for (int e = 0; e < 8; ++e) {
+                v[8 * j + e] = finite(y[e]);
+                far |= fabsf(v[8 * j + e]) >= dt_pow2(100);
+            }
         }
 #pragma unroll
         for (int i = 0; i < NR; ++i) dot[i] = 0.f;
@@ -503,7 +509,7 @@ struct Stream {
             float y[8];
             dt_vec_vals<uint16_t>(kw[j], y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = finite(y[e]);
+            for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(finite(y[e]), dt_pow2(-8));
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
                 uint32_t q[4];  // the row's elements 8 j on of the lane's run
@@ -516,6 +522,7 @@ struct Stream {
             }
         }
         bad = __any_sync(0xffffffffu, bad);
+        const float above = __any_sync(0xffffffffu, far) ? -8.f : HEADROOM;
         clear();
 #pragma unroll
         for (int i = 0; i < NR; ++i) {  // of row g + 8 i
@@ -523,11 +530,11 @@ struct Stream {
             dot[i] = __fadd_rn(dot[i], __shfl_xor_sync(0xffffffffu, dot[i], 2));
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float s = __fmul_rn(__shfl_sync(0xffffffffu, dot[i], 8 * t + 4 * e), rowc[i][e]);
+                const float s = __fmul_rn(__fmul_rn(__shfl_sync(0xffffffffu, dot[i], 8 * t + 4 * e), rowc[i][e]), dt_pow2(8));
                 const int r = 2 * t + e + 8 * i;
                 if (r >= u.rows || !(at_mask_word(a, u.b, r / a.G, 0, 1) & 1)) continue;
-                const float w = s == s ? 32.f : s;
-                m[i][e] = s == s ? s - HEADROOM : -__int_as_float(0x7F800000);
+                const float w = s == s ? dt_pow2((int)above) : s;
+                m[i][e] = s == s ? s - above : -__int_as_float(0x7F800000);
                 if (g == 0) l[i][e] = w;
                 if (bad) l[i][e] = __int_as_float(0x7FC00000);
 #pragma unroll
@@ -535,7 +542,7 @@ struct Stream {
             }
         }
     }
-    static_assert(HEADROOM == 5.f, "2^HEADROOM above");
+    static_assert(HEADROOM == (int)HEADROOM, "a power of two above");
 
     // The first of a warp's sums, from up to 16 new rows: rotated, each scaled by a power of
     // two to a largest magnitude below 4 (one of its own, so that what other rows hold does

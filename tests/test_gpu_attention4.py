@@ -197,6 +197,31 @@ def test_a_single_row_of_its_own(G):
     assert nan[0, 0, 0] and int(nan.sum()) == 1
 
 
+@pytest.mark.parametrize("G", [2, 12])
+@pytest.mark.parametrize("rot", [0, 64])
+def test_a_single_row_near_the_end_of_the_range(G, rot):
+    """Its values up to 3e38, and keys whose products with the query cancel, each far past fp32's range in
+    part.  With a rotation, position 0 (the empty context) turns nothing."""
+    cache = make_cache([100, 0, 30] if rot == 0 else [0, 0, 0], 32, 2, 64, 5)
+    g = torch.Generator().manual_seed(G)
+    q, k, v = (x.clone() for x in inputs(3, 1, 2 * G, 2, 64, g))
+    tabs = ref.rope_tables(200, rot, "cuda") if rot else None
+    rope = dtree.Rope(*tabs, False) if rot else None
+    see, at = [torch.ones((1, 1), dtype=torch.bool)] * 3, [torch.arange(1)] * 3
+    for size in (2.0 ** 90, 2.0 ** 99, 2.0 ** 101, 2.0 ** 110, 2.0 ** 122, 2.0 ** 125):
+        far = v * size
+        assert torch.isfinite(far).all()
+        out = dtree.tree_attention(cache, q, k, far, rope=rope)
+        check(cache, q, k, far, see, at, [1] * 3, (*tabs, False) if rot else None, 1 / math.sqrt(64), out)
+    # q of ones, keys of +x and -x in halves: every score is zero, whatever x, and the row's weight that of
+    # a key of zeros
+    one, zero = torch.ones_like(q), torch.zeros_like(k)
+    for x in (2.0 ** 100, 2.0 ** 124, 2.0 ** 127):
+        half = torch.cat((torch.full_like(k[..., :32], x), torch.full_like(k[..., :32], -x)), -1)
+        got = dtree.tree_attention(cache, one, half, v, rope=rope)
+        check(cache, one, zero, v, see, at, [1] * 3, (*tabs, False) if rot else None, 1 / math.sqrt(64), got)
+
+
 def test_long_contexts_are_split():
     run([9000, 5, 3001], 1, 16, 2, 128, 64, tree=False, seed=5)
     run([7001], 40, 16, 2, 128, 128, seed=6)
