@@ -277,10 +277,7 @@ DT_DI float at_factor(float row, float keys) {
 
 // Least exponent by which new rows are scaled: of keys down to where it is a normal
 // number; of values to 2^-57 (what lies below counts as small against 1), so that sums over
-// rows and pages keep their range.  Beside a 4-bit cache to 2^-13: its values have their
-// scales in them (from 2^-18 on), so P does not follow their magnitude, and a new row's P is
-// smaller by its scale.  With 2^-13 equal weights are 2^-8 at least, a normal number of
-// fp16, and values down to 2^-24 keep their bits.
+// rows and pages keep their range.  Beside a 4-bit cache, see at_value_exponent; kn11 to 2^-13.
 template <int BITS>
 DT_DI int at_least_exponent(bool keys) { return keys ? -126 : BITS == 4 ? -13 : -57; }
 // Exponent of a row from the bits of its largest magnitude; of a row of zeros, 0.
@@ -288,6 +285,22 @@ template <int BITS>
 DT_DI int at_row_exponent(uint32_t big, bool keys) {
     return big == 0u ? 0 : min(max((int)(big >> 23) - 127, at_least_exponent<BITS>(keys)), 126);
 }
+
+// Over 4 bits the values of new rows are scaled by 2^-e, one e for all that come together, and
+// their products join sums that are held 2^-e as large: P, in fp16, follows the weights alone,
+// and fp32 sums have the range that P has not.  (With e in P's exponent, tokens whose values need a
+// smaller e lose bits of their weights, and beside 2^30 all of them.)
+//   at_value_exponent: of rows whose largest magnitudes have the exponents lo to hi.  fp16 holds
+// them without a scale from 2^-8 (which keeps 2^-24) up to 2^15; else the largest comes to 2^14.
+//   at_value_row: a row's own, where it lies more than 18 octaves below the largest, of 2^15 or
+// more: 2^-4 then keeps what lies 2^-20 below its largest, and P takes the difference, not below
+// AT_LEAST_SHIFT, so that the weight itself stays a normal number.  Such a row's weight has all
+// its bits up to 2^37 below the largest value and some up to 2^48.
+//   AT_KEEP: how far a later e may be below an earlier one: sums of 2^20 rows of up to 2^128, with
+// weights of up to 2^13, then stay below 2^125.
+constexpr int AT_KEEP = 76, AT_LEAST_SHIFT = -60;
+DT_DI int at_value_exponent(int hi, int lo) { return hi < 15 && lo >= -8 ? 0 : max(hi - 14, -57); }
+DT_DI int at_value_row(int x, int e) { return e > 0 && max(x, -10) < e - 4 ? max(x, -10) + 4 : e; }
 
 // The bits of new rows [m0, m0 + 32) that row `node` sees, rows below n only.
 DT_DI uint32_t at_mask_word(const DtAttend& a, int b, int node, int m0, int n) {

@@ -19,11 +19,13 @@
 // of e2m1 codes go into the fp16 tiles, and these are 1 then).
 // Scores in base 2 are t = s * (row factor * ks); P holds p = 2^(t + log2 vs - m),
 // so the products need no scaling, and the row sum adds p / vs.  m is the running
-// maximum of t + log2 vs less 5 (fp16 then resolves probabilities down to 2^-29 of
-// the largest), moved -- and O rescaled -- only when the maximum has grown by
-// more than 8 since.  A tile of new rows has one scale, or, when the rows'
+// maximum of t + log2 vs less 5, moved -- and O rescaled -- only when the maximum has
+// grown by more than 8 since: of the largest p vs, fp16 then holds 11 bits of those down to
+// 2^-19 and something down to 2^-29.  A tile of new rows has one scale, or, when the rows'
 // magnitudes lie too far apart for fp16, one for each row: such tiles go through
 // a short loop of their own, and what a row does not see never matters to it.
+// Over 4 bits the scale of a tile's new values is not in P but in O, which is held 2^-e as
+// large while such a tile is worked on (follow): P is the weight alone, whatever the values.
 //
 // Roundings: codes are exact in fp16; q, new k and v are scaled by powers of two into
 // fp16's range and rounded to 11 bits (bf16 has 8, rotation gives them more); P to 11
@@ -128,6 +130,7 @@ struct Shared {
     int qpos[ROWS], kpos[AT_TILE];
     long long qoff[ROWS];
     float mrg_m[TQ], mrg_l[TQ];
+    int mrg_e[TQ];
     float wt[OWN_PARTS][ROWS];
     int emax[2][NC / 32], emin[2][NC / 32];
     uint64_t segfull[SEGS], segfree[SEGS];
@@ -342,11 +345,12 @@ struct Conv {
     // One tile of new rows, from row m0: keys rotated, and scaled by powers of two when
     // the rows' largest magnitudes are not all in [2^-4, 2^15), where fp16 is exact enough:
     // by one for the tile when that brings them there, else by one for each row, so that
-    // what other rows hold does not matter.  Pair: how chunk pairs are read (DtPair, Straight),
-    // U: rows in flight.
+    // what other rows hold does not matter.  Values over 4 bits: see at_value_exponent; top_e is the
+    // largest exponent of the segment's tiles so far.  Pair: how chunk pairs are read (DtPair,
+    // Straight), U: rows in flight.
     template <class Pair, int U>
     static DT_DI void fresh(const DtAttend& a, const Seg& u, bool keys, int m0, int ct, Shared* sh, uint32_t g,
-                            uint32_t tile) {
+                            uint32_t tile, int& top_e) {
         Ring* ring = &sh->ring[g % RING];
         Apart* ap = &sh->apart[g % RING];
         const int which = keys ? 0 : 1, b = u.b, n = u.n, len = u.len, left = min(AT_TILE, n - m0);
@@ -413,7 +417,7 @@ struct Conv {
                     if (pass == 0) {
 #pragma unroll
                         for (int d = 1; d < PPR; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        if (pr == 0 && top > 0.f && r < left) ap->e[which][r] = (int8_t)at_row_exponent<BITS>(__float_as_uint(top), keys);
+                        if (pr == 0 && top > 0.f && r < left) ap->e[which][r] = (int8_t)at_row_exponent<8>(__float_as_uint(top), keys);
                     }
                 }
             }
@@ -424,10 +428,18 @@ struct Conv {
             if ((ct & 31) == 0) sh->emax[which][ct >> 5] = hi, sh->emin[which][ct >> 5] = lo;
             group_sync(keys);
             for (int i = 0; i < NC / 32; ++i) hi = max(hi, sh->emax[which][i]), lo = min(lo, sh->emin[which][i]);
-            const bool apart = hi - lo > 18 && hi != -128;
-            const int e = apart || hi == -128 || (lo >= -4 && hi < 15) ? 0 : max(hi - 14, at_least_exponent<BITS>(keys));
-            if (!apart) ap->e[which][ct] = (int8_t)e;
-            else if (own == NONE) ap->e[which][ct] = 0;
+            bool apart = hi - lo > 18 && hi != -128;
+            int e = apart || hi == -128 || (lo >= -4 && hi < 15) ? 0 : max(hi - 14, at_least_exponent<8>(keys));
+            if (BITS == 4 && !keys) {
+                e = max(at_value_exponent(hi, lo), top_e - AT_KEEP);
+                top_e = max(top_e, e);
+                apart = at_value_row(lo, e) != e;
+                ap->e[which][ct] = (int8_t)(own == NONE ? e : at_value_row(own, e));
+            } else if (!apart) {
+                ap->e[which][ct] = (int8_t)e;
+            } else if (own == NONE) {
+                ap->e[which][ct] = 0;
+            }
             if (ct == 0) ap->yes[which] = apart;
             if (ct < 8) {
                 if (keys) {
@@ -504,6 +516,7 @@ struct Conv {
                 }
                 stored(s);
             }
+            int top_e = -128;
 #pragma unroll 1
             for (; j < t1; ++j, ++g) {
                 const int s = g % STAGES;
@@ -512,9 +525,9 @@ struct Conv {
                 // (rows loaded before these waits take registers that the loop over cached tiles
                 // needs: 16 trees of 257 nodes 881 us instead of 869)
                 if (BITS == 4 && (!keys || a.rope.rot == 0))
-                    fresh<Straight, 4>(a, u, keys, (j - u.ctx) * AT_TILE, ct, sh, g, base + s * L::TILE);
+                    fresh<Straight, 4>(a, u, keys, (j - u.ctx) * AT_TILE, ct, sh, g, base + s * L::TILE, top_e);
                 else  // two rotating rows in flight at D = 128 make that loop spill
-                    fresh<DtPair<uint16_t>, D == 64 ? 2 : 1>(a, u, keys, (j - u.ctx) * AT_TILE, ct, sh, g, base + s * L::TILE);
+                    fresh<DtPair<uint16_t>, D == 64 ? 2 : 1>(a, u, keys, (j - u.ctx) * AT_TILE, ct, sh, g, base + s * L::TILE, top_e);
                 if (ct == 0) dt_mbar_arrive(&sh->scfull[g % RING]);
                 stored(s);
             }
@@ -685,6 +698,8 @@ DT_DI void issue_slot(unsigned char* sm, Shared* sh, uint32_t tmem, int s) {
 template <int D, int BITS>
 struct Soft {
     using L = Lay<D>;
+    // Parts of a unit are held 2^-40 as large over 4 bits, where sums may pass fp32's range.
+    static constexpr int PART_E = BITS == 4 ? 40 : 0;
 
     // The block's rows, rotated, scaled by a power of two and converted.
     template <class Pair, int U>
@@ -756,11 +771,11 @@ struct Soft {
     }
 
     // A maximum that has grown moves the reference, and O when it has sums; rows of a
-    // warp do so together.
+    // warp do so together.  O comes out 2^d as large besides, |d| <= 252.
     static DT_DI void follow(float mx, float& m, float& l, uint32_t to, bool has_o, uint64_t* other, uint32_t other_ph,
-                             int* fail) {
+                             int* fail, int d = 0) {
         const bool grown = mx > m + (HEADROOM + LAZY);
-        if (__any_sync(0xffffffffu, grown)) {
+        if (__any_sync(0xffffffffu, grown) || d != 0) {
             const float to_m = grown ? mx - HEADROOM : m;
             const float f = grown ? dt_ex2_approx(m - to_m) : 1.f;  // m = -inf: 0
             m = to_m;
@@ -769,13 +784,14 @@ struct Soft {
                 wait(other, other_ph, fail);
                 __syncwarp();
                 dt_tc_fence_after();
+                const float f0 = __fmul_rn(f, dt_pow2(d / 2)), f1 = dt_pow2(d - d / 2);
 #pragma unroll 1
                 for (int c = 0; c < D / 16; ++c) {
                     uint32_t o[16];
                     dt_tmem_ld16_async(to + 16 * c, o);
                     dt_tmem_ld_wait(o);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__fmul_rn(__uint_as_float(o[i]), f));
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(o[i]), f0), f1));
                     dt_tmem_st16(to + 16 * c, o);
                 }
             }
@@ -888,8 +904,8 @@ struct Soft {
     }
 
     // The same with a mask: the context's last tile, and tiles of new rows with a scale for the
-    // tile: lv, iv are log2 and inverse of that of its values.
-    static DT_DI void half_masked(uint32_t ts, uint32_t to, bool has_o, float ka, float lv, float iv, uint2 mk, float& m,
+    // tile.  e: the exponent of the scale of its values, which O takes from here on (eo: so far).
+    static DT_DI void half_masked(uint32_t ts, uint32_t to, bool has_o, float ka, int e, int& eo, uint2 mk, float& m,
                                   float& l, uint64_t* other, uint32_t other_ph, int* fail) {
         if (!__any_sync(0xffffffffu, mk.x | mk.y)) {  // none of the warp's rows sees any of them
             const uint32_t z[16] = {};
@@ -910,8 +926,9 @@ struct Soft {
 #pragma unroll
             for (int i = 2; i < 16; i += 2) q[g] = max3(q[g], __uint_as_float(x[16 * g + i]), __uint_as_float(x[16 * g + i + 1]));
         }
-        follow(__fmaf_rn(fmaxf(max3(q[0], q[1], q[2]), q[3]), ka, lv), m, l, to, has_o, other, other_ph, fail);
-        const float kb = __fsub_rn(lv, m == -__int_as_float(0x7F800000) ? 0.f : m);
+        follow(__fmul_rn(fmaxf(max3(q[0], q[1], q[2]), q[3]), ka), m, l, to, has_o, other, other_ph, fail, eo - e);
+        eo = e;
+        const float kb = m == -__int_as_float(0x7F800000) ? 0.f : -m;
         const unsigned long long ka2 = dt_f2_pack(ka, ka), kb2 = dt_f2_pack(kb, kb);
         unsigned long long sum[2] = {dt_f2_pack(0.f, 0.f), dt_f2_pack(0.f, 0.f)};
 #pragma unroll
@@ -930,16 +947,17 @@ struct Soft {
         }
         float s0, s1;
         dt_f2_unpack(dt_f2_add(sum[0], sum[1]), s0, s1);
-        l = __fmaf_rn(__fadd_rn(s0, s1), iv, l);
+        l = __fadd_rn(__fadd_rn(s0, s1), l);
         dt_tmem_st_wait();
     }
 
-    // The same for tokens with scales of their own: key exponents ek, value exponents ev.
-    // Rare, so short: 16 tokens at a time, their scores read twice.
-    static DT_DI void half_apart(const Apart* ap, int h, uint32_t ts, uint32_t to, bool has_o, float rowc,
+    // The same for tokens with scales of their own: key exponents ek, value exponents ev, of which
+    // O takes e (over 4 bits; else 0).  Rare, so short: 16 tokens at a time, their scores read twice.
+    static DT_DI void half_apart(const Apart* ap, int e, int& eo, int h, uint32_t ts, uint32_t to, bool has_o, float rowc,
                                  uint2 mk, float& m, float& l, uint64_t* other, uint32_t other_ph, int* fail) {
         const float NEG_INF = -__int_as_float(0x7F800000);
         const int8_t *ek = ap->e[0] + 64 * h, *ev = ap->e[1] + 64 * h;
+        auto shift = [](int own, int e) { return BITS == 4 ? max(own - e, AT_LEAST_SHIFT) : own; };
         float mx = NEG_INF, mu = 0.f;
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {
@@ -953,7 +971,7 @@ struct Soft {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     y[i] = (bits >> i) & 1 ? __fmaf_rn(__uint_as_float(x[i]), at_factor(rowc, dt_pow2(ek[16 * g + i])),
-                                                       __fsub_rn((float)ev[16 * g + i], mu))
+                                                       __fsub_rn((float)shift(ev[16 * g + i], e), mu))
                                            : NEG_INF;
                 if (pass == 0) {
 #pragma unroll
@@ -962,7 +980,7 @@ struct Soft {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         y[i] = dt_ex2_approx(y[i]);
-                        l = __fmaf_rn(y[i], dt_pow2(-ev[16 * g + i]), l);
+                        l = __fmaf_rn(y[i], dt_pow2(-shift(ev[16 * g + i], e)), l);
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) p[i] = f16x2(y[2 * i], y[2 * i + 1]);
@@ -970,7 +988,8 @@ struct Soft {
                 }
             }
             if (pass == 0) {
-                follow(mx, m, l, to, has_o, other, other_ph, fail);
+                follow(mx, m, l, to, has_o, other, other_ph, fail, eo - e);
+                eo = e;
                 mu = m == NEG_INF ? 0.f : m;
             }
         }
@@ -1000,6 +1019,7 @@ struct Soft {
             const int clear = len / AT_TILE - u.t0;  // tiles before this one are wholly visible
             uint32_t pa = ph & 1;                    // phase of both halves' scores
             int lt = dual ? 0 : s;
+            int eo = 0;  // over 4 bits: O of the warp's rows is held 2^-eo as large
             // Cached tiles of a 4-bit cache need nothing but their scores, so nothing of them is
             // waited for but those.  (That the barriers of the scales are passed over is safe:
             // when a tile's are waited for, the converters are past those of RING tiles before.)
@@ -1022,7 +1042,8 @@ struct Soft {
                 }
 #pragma unroll 1
                 for (; lt < nt; lt += hop, pa ^= 1) {
-                    float ka = ka1, lv = 0.f, iv = 1.f;
+                    float ka = ka1;
+                    int e = 0;
                     const uint2 mk0 = mask_words(a, u, u.t0 + lt, 0, row, node);
                     const uint2 mk1 = mask_words(a, u, u.t0 + lt, 1, row, node);
                     if (u.t0 + lt >= u.ctx) {
@@ -1033,15 +1054,14 @@ struct Soft {
                         const uint4 bk = *(const uint4*)ring->bad[0], bv = *(const uint4*)ring->bad[1];
                         poison |= ((mk0.x & (bk.x | bv.x)) | (mk0.y & (bk.y | bv.y)) | (mk1.x & (bk.z | bv.z)) | (mk1.y & (bk.w | bv.w))) != 0u;
                         ka = at_factor(rowc, ring->half[0].ks.x);
-                        lv = ring->half[0].lv.x;
-                        iv = ring->half[0].iv.x;
+                        e = (int)ring->half[0].lv.x;
                     }
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         wait(&sh->sfull[s][h], pa, &sh->fail);
                         __syncwarp();
                         dt_tc_fence_after();
-                        half_masked(ts + 64 * h, to, lt >= hop || h, ka, lv, iv, h ? mk1 : mk0, m, l, &sh->sfull[s][h ^ 1], pa ^ h, &sh->fail);
+                        half_masked(ts + 64 * h, to, lt >= hop || h, ka, e, eo, h ? mk1 : mk0, m, l, &sh->sfull[s][h ^ 1], pa ^ h, &sh->fail);
                         dt_tc_fence_before();
                         __syncwarp();
                         if ((tid & 31) == 0) dt_mbar_arrive(&sh->pfull[s][h]);
@@ -1085,6 +1105,7 @@ struct Soft {
                 const uint32_t g = g0 + lt;
                 const Ring* ring = &sh->ring[g % RING];
                 wait(&sh->scfull[g % RING], (g / RING) & 1, &sh->fail);
+                const int e = BITS == 4 ? (int)ring->half[0].lv.x : 0;
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     const uint2 mk = mask_words(a, u, u.t0 + lt, h, row, node_of(a, u, row));
@@ -1093,7 +1114,7 @@ struct Soft {
                     wait(&sh->sfull[s][h], pa, &sh->fail);
                     __syncwarp();
                     dt_tc_fence_after();
-                    half_apart(&sh->apart[g % RING], h, ts + 64 * h, to, lt >= hop || h, rowc, mk, m, l, &sh->sfull[s][h ^ 1],
+                    half_apart(&sh->apart[g % RING], e, eo, h, ts + 64 * h, to, lt >= hop || h, rowc, mk, m, l, &sh->sfull[s][h ^ 1],
                                pa ^ h, &sh->fail);
                     dt_tc_fence_before();
                     __syncwarp();
@@ -1121,7 +1142,7 @@ struct Soft {
                 }
                 asm volatile("bar.sync 2, 256;" ::: "memory");
                 if (sh->last) {
-                    join_own(a, u, sh, part, cta - u.first, to, row, m, l, dt_smem_addr(sm + L::Q) + (tid >> 5) * (32 * D * 2),
+                    join_own(a, u, sh, part, cta - u.first, to, row, m, l, eo, dt_smem_addr(sm + L::Q) + (tid >> 5) * (32 * D * 2),
                              out_row(a, u, row));
                     continue;
                 }
@@ -1136,6 +1157,7 @@ struct Soft {
                 if (s == 1) {
                     sh->mrg_m[row] = m;
                     sh->mrg_l[row] = l;
+                    if (BITS == 4) sh->mrg_e[row] = eo;
                     if (any) {
 #pragma unroll 1
                         for (int c = 0; c < D / 16; ++c) {
@@ -1162,7 +1184,11 @@ struct Soft {
             }
             if (dual || s == 0) {
                 const float inv = l == 0.f ? 0.f : 1.0f / l;
-                const float w0 = whole ? __fmul_rn(f0, inv) : f0, w1 = whole ? __fmul_rn(f1, inv) : f1;
+                float w0 = whole ? __fmul_rn(f0, inv) : f0, w1 = whole ? __fmul_rn(f1, inv) : f1;
+                if constexpr (BITS == 4) {
+                    w0 = __fmul_rn(w0, dt_pow2(whole ? eo : eo - PART_E));
+                    if (!dual && nt > 1) w1 = __fmul_rn(w1, dt_pow2(sh->mrg_e[row] - (whole ? 0 : PART_E)));
+                }
                 uint16_t* out = out_row(a, u, row);
                 // a full block's rows go out by way of the query tiles, whole lines at a
                 // time: a warp's 32 rows in the place of its own slot's queries
@@ -1256,7 +1282,7 @@ struct Soft {
     // straight from tensor memory; same sums in the same order as join(), which writes
     // and reads all of them (64 trees of 61 nodes 174 us, this 166).
     static DT_DI void join_own(const DtAttend& a, const Seg& u, Shared* sh, const float* part, int own, uint32_t to, int row,
-                               float m, float l0, uint32_t stage, uint16_t* out) {
+                               float m, float l0, int eo, uint32_t stage, uint16_t* out) {
         const float NEG_INF = -__int_as_float(0x7F800000);
         const int first = u.first, segs = u.segs, lane = row & 31;
         auto slot = [&](int i) { return part + (size_t)(2 * (first + i) + (i == 0)) * ROWS * (D + 2); };
@@ -1273,7 +1299,9 @@ struct Soft {
         const float inv = l == 0.f ? 0.f : 1.0f / l;
         for (int i = 0; i < segs; ++i) {
             const float mi = sh->wt[i][row];
-            sh->wt[i][row] = mi == NEG_INF ? 0.f : __fmul_rn(dt_ex2_approx(mi - M), inv);
+            float w = mi == NEG_INF ? 0.f : __fmul_rn(dt_ex2_approx(mi - M), inv);
+            if constexpr (BITS == 4) w = __fmul_rn(w, dt_pow2(i == own ? eo : PART_E));
+            sh->wt[i][row] = w;
         }
 #pragma unroll 1
         for (int c = 0; c < D / 16; c += 2) {  // 32 columns
@@ -1351,7 +1379,8 @@ struct Soft {
 #pragma unroll 4
             for (int i = 0; i < np; ++i) {
                 const float mi = tid < rows ? __ldcg(slot(i0 + i) + tid) : NEG_INF;
-                wt[i * ROWS + tid] = mi == NEG_INF ? 0.f : __fmul_rn(dt_ex2_approx(mi - M), inv);
+                const float w = mi == NEG_INF ? 0.f : __fmul_rn(dt_ex2_approx(mi - M), inv);
+                wt[i * ROWS + tid] = __fmul_rn(w, dt_pow2(PART_E));
             }
             asm volatile("bar.sync 2, 256;" ::: "memory");
 #pragma unroll 1
