@@ -649,7 +649,10 @@ dt_status dt_qk_norm(int32_t batch, int32_t M, int32_t Hq, int32_t Hk, int32_t D
  * Products are taken in fp16 with fp32 accumulation (e4m3 codes are exact in
  * fp16; rows of q, new k and v are scaled by powers of two into its range, and
  * keep what lies within 2^-20 of the row's largest magnitude; new values below
- * 2^-57 may count as zero); softmax statistics are fp32.
+ * 2^-57 may count as zero); softmax statistics are fp32.  In a sum of values a token
+ * counts by its weight times its value scale, with 11 bits down to 2^-19 of the row's largest such
+ * product and not at all below 2^-30 (a new row's scale is 1, its largest
+ * magnitude, or 2^-14 of that of the 128 rows that it lies among).
  * A request whose len, n_nodes, pages or positions are out of range gets
  * DT_DEV_BAD_CACHE in status[b] (OR-ed) and undefined output rows; when a wait
  * of the kernel runs out, every request gets DT_DEV_TIMEOUT, and all rows are. */
@@ -659,10 +662,12 @@ dt_status dt_tree_attention(const dt_kv_cache* c, const dt_rope* rope, int32_t b
                             const int32_t* pos, const int32_t* n_nodes, float scale, void* out, void* workspace,
                             size_t workspace_bytes, int32_t* status, dt_stream_t stream);
 
-/* The same over a 4-bit cache (codes times scales are exact in fp16, too); new values
- * below 2^-24 may count as zero, and beside a new value of 2^100 or more the weights of other
- * tokens may (such values cannot be appended: the cache holds 61440 at most).  A workspace
- * serves calls of both kinds. */
+/* The same over a 4-bit cache (codes times scales are exact in fp16, too).  A token counts by its
+ * weight alone, with 11 bits down to 2^-19 of the row's largest, whatever the values.
+ * Limits: new values below 2^-24 may count as zero; beside a new value of 2^90 or more the other
+ * tokens may; and of a new row whose values all lie 2^30 below another one's, weights below 2^-7 of the
+ * largest lose bits, 2^48 below it all (the cache itself holds 61440 at most).  A workspace serves
+ * calls of both kinds. */
 size_t dt_tree_attention4_workspace(const dt_kv_cache4* c, int32_t batch, int32_t M, int32_t Hq);
 dt_status dt_tree_attention4(const dt_kv_cache4* c, const dt_rope* rope, int32_t batch, int32_t M, int32_t Hq,
                              const dt_rows* q, const dt_rows* k, const dt_rows* v, const uint32_t* mask,

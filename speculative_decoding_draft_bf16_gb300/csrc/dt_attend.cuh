@@ -275,15 +275,11 @@ DT_DI float at_factor(float row, float keys) {
     return f;
 }
 
-// Least exponent by which new rows are scaled: of keys down to where it is a normal
-// number; of values to 2^-57 (what lies below counts as small against 1), so that sums over
-// rows and pages keep their range.  Beside a 4-bit cache, see at_value_exponent; kn11 to 2^-13.
-template <int BITS>
-DT_DI int at_least_exponent(bool keys) { return keys ? -126 : BITS == 4 ? -13 : -57; }
-// Exponent of a row from the bits of its largest magnitude; of a row of zeros, 0.
-template <int BITS>
+// Exponent of a row from the bits of its largest magnitude; of a row of zeros, 0.  Least: of keys
+// down to where a scale is a normal number; of values to 2^-57 (what lies below counts as small
+// against 1), so that sums over rows and pages keep their range.
 DT_DI int at_row_exponent(uint32_t big, bool keys) {
-    return big == 0u ? 0 : min(max((int)(big >> 23) - 127, at_least_exponent<BITS>(keys)), 126);
+    return big == 0u ? 0 : min(max((int)(big >> 23) - 127, keys ? -126 : -57), 126);
 }
 
 // Over 4 bits the values of new rows are scaled by 2^-e, one e for all that come together, and

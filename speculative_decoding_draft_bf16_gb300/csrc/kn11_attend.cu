@@ -21,7 +21,8 @@
 // exponentials, a third of all instructions: 276 us instead of 233.
 //   Scales: P holds 2^(t + log2 vs - m) for scores t in base 2, the row sum adds p / vs
 // (value scales from 2^-100 on, or the sum leaves fp32), and m moves only when the maximum
-// has grown by more than 8.  The warps' sums are joined in shared memory, the CTAs' in the
+// has grown by more than 8.  Over 4 bits P holds the weights alone, and the new rows' sums, the
+// first that are formed, get back what their values were scaled by.  The warps' sums are joined in shared memory, the CTAs' in the
 // workspace.
 //
 // On the device (calls in a graph): 64 single tokens, 32 heads on 8, over contexts of 1001
@@ -546,8 +547,8 @@ struct Stream {
 
     // The first of a warp's sums, from up to 16 new rows: rotated, each scaled by a power of
     // two to a largest magnitude below 4 (one of its own, so that what other rows hold does
-    // not matter), elements that are not finite replaced by zeros and reported to the rows
-    // that see them.
+    // not matter; values over 4 bits: see at_value_exponent), elements that are not finite
+    // replaced by zeros and reported to the rows that see them.
     DT_DI void fresh(const DtAttend& a, const Walk& u, int lane) {
         const int g = lane >> 2, t = lane & 3, n = u.r.n;
         const uint16_t* kp = (const uint16_t*)a.k.ptr + u.b * a.k.stride_b + u.h * a.k.stride_h;
@@ -597,7 +598,7 @@ struct Stream {
             }
             big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            const int ek = at_row_exponent<BITS>(big, true);
+            const int ek = at_row_exponent(big, true);
             ks[i] = dt_pow2(ek), fk[i] = dt_pow2(-ek);
         }
 #pragma unroll
@@ -614,7 +615,7 @@ struct Stream {
         }
         if (BITS == 8) values();
         float fv[4];  // of rows as v's
-        int ev[4];
+        int ev[4], hi = -128, lo = 127;
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
             const int row = 2 * t + (k4 & 1) + 8 * (k4 >> 1);
@@ -632,8 +633,23 @@ struct Stream {
             }
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, d));
-            ev[k4] = at_row_exponent<BITS>(big, false);
-            fv[k4] = dt_pow2(-ev[k4]);
+            ev[k4] = at_row_exponent(big, false);
+            if (BITS == 4) {
+                if (big != 0u) hi = max(hi, ev[k4]), lo = min(lo, ev[k4]);
+                else ev[k4] = 127;  // of zeros: whatever the others have
+            }
+            if (BITS == 8) fv[k4] = dt_pow2(-ev[k4]);
+        }
+        int e = 0;  // over 4 bits: the sums are formed 2^-e as large, see at_value_exponent
+        if (BITS == 4) {
+            hi = __reduce_max_sync(0xffffffffu, hi);
+            e = at_value_exponent(hi, __reduce_min_sync(0xffffffffu, lo));
+#pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4) {
+                const int own = at_value_row(ev[k4], e);
+                fv[k4] = dt_pow2(-own);
+                ev[k4] = max(own - e, AT_LEAST_SHIFT);
+            }
         }
         float lv[2], iv[2];  // of rows g, g + 8, which lanes with t = g / 2 hold
 #pragma unroll
@@ -676,6 +692,20 @@ struct Stream {
             const uint32_t f[4] = {pair(0, 1, j), pair(0, 1, j + 1), pair(2, 3, j), pair(2, 3, j + 1)};
 #pragma unroll
             for (int i = 0; i < NR; ++i) mma(o[j / 2][i], f, p[i][0], p[i][1]);
+        }
+        if (BITS == 4 && e != 0) {
+            // sums proper; past 2^AT_KEEP the reference takes the rest
+            const float up = dt_pow2(min(e, AT_KEEP)), over = (float)max(e - AT_KEEP, 0), down = dt_pow2(-max(e - AT_KEEP, 0));
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    m[i][r] = __fadd_rn(m[i][r], over);
+                    l[i][r] = __fmul_rn(l[i][r], down);
+#pragma unroll
+                    for (int j = 0; j < NV; ++j) o[j / 2][i][2 * (j & 1) + r] = __fmul_rn(o[j / 2][i][2 * (j & 1) + r], up);
+                }
+            }
         }
     }
 };

@@ -417,7 +417,7 @@ struct Conv {
                     if (pass == 0) {
 #pragma unroll
                         for (int d = 1; d < PPR; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        if (pr == 0 && top > 0.f && r < left) ap->e[which][r] = (int8_t)at_row_exponent<8>(__float_as_uint(top), keys);
+                        if (pr == 0 && top > 0.f && r < left) ap->e[which][r] = (int8_t)at_row_exponent(__float_as_uint(top), keys);
                     }
                 }
             }
@@ -429,7 +429,7 @@ struct Conv {
             group_sync(keys);
             for (int i = 0; i < NC / 32; ++i) hi = max(hi, sh->emax[which][i]), lo = min(lo, sh->emin[which][i]);
             bool apart = hi - lo > 18 && hi != -128;
-            int e = apart || hi == -128 || (lo >= -4 && hi < 15) ? 0 : max(hi - 14, at_least_exponent<8>(keys));
+            int e = apart || hi == -128 || (lo >= -4 && hi < 15) ? 0 : max(hi - 14, keys ? -126 : -57);
             if (BITS == 4 && !keys) {
                 e = max(at_value_exponent(hi, lo), top_e - AT_KEEP);
                 top_e = max(top_e, e);
