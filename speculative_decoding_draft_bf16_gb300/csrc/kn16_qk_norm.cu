@@ -67,7 +67,7 @@ DT_DI float mean_square(const f2 (&x)[4], const f2 (&y)[4]) {
     return __fmul_rn(r, 1.f / (16 * PPR));
 }
 // 1 / sqrt(mean square + eps).  Squares that leave fp32's range upwards are formed again of
-// numbers 2^-68 as large; such heads need no eps.  With an eps below TINY squares may leave it
+// numbers 2^-68 as large, with eps 2^-136 as large.  With an eps below TINY squares may leave it
 // downwards, too: the head itself is scaled then, by 2^100, and eps by 2^200, because the root's
 // reciprocal of the smallest numbers would leave the range and its product with them does not.
 // Only one step at a time does that, and both ends alike: 3904 short rows take 10.7 us with it and
@@ -88,7 +88,7 @@ DT_DI float inverse_root(f2 (&x)[4], f2 (&y)[4], float eps) {
             return rsqrtf(__fadd_rn(mean_square<PPR, false>(x, y), __fmul_rn(__fmul_rn(eps, k), k)));
         }
         const float t = mean_square<PPR, true>(x, y);
-        if (big) return __fmul_rn(rsqrtf(t), dt_pow2(-68));
+        if (big) return __fmul_rn(rsqrtf(__fadd_rn(t, __fmul_rn(__fmul_rn(eps, dt_pow2(-68)), dt_pow2(-68)))), dt_pow2(-68));
     }
     return rsqrtf(s);
 }
