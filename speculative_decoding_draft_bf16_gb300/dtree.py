@@ -717,6 +717,18 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+class Pair(tuple):
+    """Two tensors that a call returns, and as `.status` the status words that it set: the caller's, or, when
+    it brought none, the call's own."""
+    status = None
+
+
+def _pair(a, b, status):
+    pair = Pair((a, b))
+    pair.status = status
+    return pair
+
+
 def kv_append(cache, k, v, rope=None, rows=None, count=None, count_add=0, len_out=None, status=None, stream=None):
     """Append rows of k, v [batch, M, Hkv, D] to the cache (dt_kv_append, dt_kv_append4): keys rotated to
     their position on the way, both stored in the cache's form.  rows [batch, N] int32 picks rows (the walk's acc_nodes),
@@ -757,8 +769,9 @@ def kv_read(cache, N=None, rows=None, start=None, count=None, count_add=0, dtype
     token rows[b, j] (rows [batch, N] int32), or start[b] + j (start [batch] int32; None: 0).
     count [batch] int32 + count_add says how many rows a request gets, in [0, N]; without it, all of `rows`,
     or all tokens from start on.  k, v: outputs [batch, N, Hkv, D] bf16 or fp32, any strides with dense heads
-    (None: zeros of `dtype`; N is needed then when there are no rows).  status [batch] int32 is OR-ed with
-    DT_DEV_BAD_CACHE for a request out of range.  Returns (k, v)."""
+    (None: zeros of `dtype`; N is needed then when there are no rows).  status [batch] int32 (None: made here) is
+    OR-ed with DT_DEV_BAD_CACHE for a request out of range, which is left alone as a whole: its rows stay zeros in
+    outputs made here.  Returns (k, v), with the status words as `.status`."""
     batch, Hkv, D, device = cache.batch, cache.Hkv, cache.D, torch.cuda.current_device()
     _need_here(cache, "cache", device)
     if rows is not None:
@@ -797,7 +810,7 @@ def kv_read(cache, N=None, rows=None, start=None, count=None, count_add=0, dtype
     call = lib().dt_kv_read4 if isinstance(cache, PagedCache4) else lib().dt_kv_read
     _check(call(cache._ref, batch, _addr(rows), N, _addr(start), _addr(count), int(count_add), _dtype_code(k), kr, vr,
                 status.data_ptr(), _raw_stream(device) if stream is None else stream.cuda_stream), "dt_kv_read")
-    return k, v
+    return _pair(k, v, status)
 
 
 def _norm_weight(w, H, D, name, device):
@@ -816,8 +829,9 @@ def qk_norm(q, k, q_weight=None, k_weight=None, eps=1e-6, rope=None, len=None, p
     k [batch, M, Hk, D] bf16 or fp32 (k None: queries alone); weights fp32 [D] or [heads, D] (None: ones).
     Row n of request b has position len[b] + pos[b, n] (len None: 0; pos None: n).  Outputs are like q and k and
     may be q and k themselves; rows from n_nodes[b] on are left alone in outputs that the caller brings, and
-    undefined in others.  tree_attention and kv_append then take the results with rope None.  status [batch]
-    int32 is OR-ed with DT_DEV_BAD_CACHE for a position or count out of range.  Returns (q_out, k_out)."""
+    undefined in others; so are rows whose position is out of range, and all of a request whose count is.
+    tree_attention and kv_append then take the results with rope None.  status [batch] int32 (None: made here) is
+    OR-ed with DT_DEV_BAD_CACHE for such a request.  Returns (q_out, k_out), with the status words as `.status`."""
     batch, M, Hq, D = q.shape
     Hk, device, dtype = 0 if k is None else k.shape[2], torch.cuda.current_device(), q.dtype
     _need_here(rope, "rope", device)
@@ -853,7 +867,7 @@ def qk_norm(q, k, q_weight=None, k_weight=None, eps=1e-6, rope=None, len=None, p
     _check(lib().dt_qk_norm(batch, M, Hq, Hk, D, _dtype_code(q), qr, kr, qw, qs, kw, ks, eps,
                             rope._ref if rope is not None else None, _addr(len), _addr(pos), _addr(n_nodes), qo, ko,
                             status.data_ptr(), _raw_stream(device) if stream is None else stream.cuda_stream), "dt_qk_norm")
-    return q_out, k_out
+    return _pair(q_out, k_out, status)
 
 
 def attention_workspace(cache, M, Hq):
