@@ -174,7 +174,7 @@ def _stream(stream):
     return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # None: torch without CUDA, which has no streams
 
 
 def _on(stream):
