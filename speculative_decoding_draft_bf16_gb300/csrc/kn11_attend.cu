@@ -874,8 +874,6 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
             for (int i = 0; i < n; ++i) {
                 issue();
                 asm volatile("cp.async.wait_group %0;" ::"n"(L::STAGES - 1) : "memory");
-                const int left = len - (u.t0 + i) * AT_TILE - w * 16, at = my_fifo + slot * L::BYTES;
-                slot = slot + 1 == L::STAGES ? 0 : slot + 1;
                 const bool odd = (i >> 5) & 1;
                 if ((i & 31) == 0) {
                     const float v = odd ? vs[1] : vs[0];
@@ -884,7 +882,9 @@ __global__ void __launch_bounds__(NT, 2) kn11_kernel(const __grid_constant__ DtA
                 }
                 const float k = __shfl_sync(0xffffffffu, odd ? ks[1] : ks[0], i & 31);
                 const float v = __shfl_sync(0xffffffffu, lv, i & 31), r = __shfl_sync(0xffffffffu, iv, i & 31);
-                if (left > 0) x.tile(at, lane, left, k, v, r);
+                const int left = len - (u.t0 + i) * AT_TILE - w * 16;
+                if (left > 0) x.tile(my_fifo + slot * L::BYTES, lane, left, k, v, r);
+                slot = slot + 1 == L::STAGES ? 0 : slot + 1;
             }
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
