@@ -428,6 +428,16 @@ struct Conv {
             if ((ct & 31) == 0) sh->emax[which][ct >> 5] = hi, sh->emin[which][ct >> 5] = lo;
             group_sync(keys);
             for (int i = 0; i < NC / 32; ++i) hi = max(hi, sh->emax[which][i]), lo = min(lo, sh->emin[which][i]);
+            // Values that need no scale, nearly always, by as few steps as that takes (8 prompts of 4000
+            // rows 1.83 ms; by way of the general case below 1.85).
+            if (BITS == 4 && !keys && top_e <= AT_KEEP && at_value_exponent(hi, lo) == 0) {
+                ap->e[which][ct] = 0;
+                top_e = max(top_e, 0);
+                if (ct == 0) ap->yes[which] = 0;
+                if (ct == 0) ring->half[0].lv.x = __int_as_float(0);
+                group_sync(keys);
+                return;
+            }
             bool apart = hi - lo > 18 && hi != -128;
             int e = apart || hi == -128 || (lo >= -4 && hi < 15) ? 0 : max(hi - 14, keys ? -126 : -57);
             if (BITS == 4 && !keys) {
@@ -445,7 +455,7 @@ struct Conv {
                 if (keys) {
                     *ring->ks(ct) = dt_pow2(e);
                 } else {
-                    *ring->lv(ct) = (float)e;
+                    *ring->lv(ct) = BITS == 4 ? __int_as_float(e) : (float)e;  // over 4 bits an integer
                     *ring->iv(ct) = dt_pow2(-e);
                 }
             }
@@ -775,7 +785,7 @@ struct Soft {
     static DT_DI void follow(float mx, float& m, float& l, uint32_t to, bool has_o, uint64_t* other, uint32_t other_ph,
                              int* fail, int d = 0) {
         const bool grown = mx > m + (HEADROOM + LAZY);
-        if (__any_sync(0xffffffffu, grown) || d != 0) {
+        if (__any_sync(0xffffffffu, grown || d != 0)) {
             const float to_m = grown ? mx - HEADROOM : m;
             const float f = grown ? dt_ex2_approx(m - to_m) : 1.f;  // m = -inf: 0
             m = to_m;
@@ -1054,7 +1064,7 @@ struct Soft {
                         const uint4 bk = *(const uint4*)ring->bad[0], bv = *(const uint4*)ring->bad[1];
                         poison |= ((mk0.x & (bk.x | bv.x)) | (mk0.y & (bk.y | bv.y)) | (mk1.x & (bk.z | bv.z)) | (mk1.y & (bk.w | bv.w))) != 0u;
                         ka = at_factor(rowc, ring->half[0].ks.x);
-                        e = (int)ring->half[0].lv.x;
+                        e = __float_as_int(ring->half[0].lv.x);
                     }
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
@@ -1105,7 +1115,7 @@ struct Soft {
                 const uint32_t g = g0 + lt;
                 const Ring* ring = &sh->ring[g % RING];
                 wait(&sh->scfull[g % RING], (g / RING) & 1, &sh->fail);
-                const int e = BITS == 4 ? (int)ring->half[0].lv.x : 0;
+                const int e = BITS == 4 ? __float_as_int(ring->half[0].lv.x) : 0;
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     const uint2 mk = mask_words(a, u, u.t0 + lt, h, row, node_of(a, u, row));
