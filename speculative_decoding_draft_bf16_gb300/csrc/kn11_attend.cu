@@ -143,7 +143,12 @@ struct Stream {
     using L = Lay<D, BITS>;
     using Walk = typename Division<BITS>::Walk;
     static constexpr int KS = D / 16;  // steps of K Q'
-    static constexpr int TP = NR == 1 ? 2 : 1;  // tiles at a time of a 4-bit cache (two groups of rows and two tiles spill)
+    // Tiles at a time of a 4-bit cache.  64 requests over 1001 to 16384, D = 128 (64): up to 8 rows with
+    // one 137 us (94), with two 127 (88); 9 to 16 rows with one 190 (118), with two 212 (115).  What ptxas
+    // spills of the forms that are kept (320 B of stores at D = 128 and up to 8 rows, 272 and 60 with more)
+    // lies beside the loop, but for D = 128 with more than 8 rows: 4 loads of the 520 instructions that
+    // 16 tokens take there (600 B, were it two tiles).
+    static constexpr int TP = NR == 1 ? 2 : 1;
     static constexpr int NV = D / 8;   // columns of a lane in V' P': NV * g + j; two to an MMA
 
     uint32_t qs;  // Q's fragments in shared memory, [KS / 2][NR][32 lanes][4 words]

@@ -37,7 +37,7 @@
 // 1300 to 1500 clocks for 64 elements of 32 rows, in which two softmax and two converter
 // warps share an SM quarter's issue slots, and the slots' chains (scores, softmax,
 // products) overlap but do not fill each other's gaps.  Sixteen trees of 257 nodes, 64
-// heads on 8, contexts of 5000 to 16384: 1.12 ms, 0.98 PFLOP/s (51% of the measured bf16
+// heads on 8, contexts of 5000 to 16384: 1.10 ms, 1.00 PFLOP/s (53% of the measured bf16
 // rate).  Scores of a whole tile at a time (fewer, wider MMAs, but a slot's softmax then
 // waits for all of them): 1.27 ms against 1.10 then.  Short contexts are bound by what a
 // unit costs beside its tiles, in thousands of clocks: queries (8), outputs (3 to 5), joins
@@ -53,7 +53,9 @@
 // common loop and 0.90 with this.  Tiles of new rows and the context's last one take 6000
 // to 7500.  Rows without a rotation are read four at a time (queries 8 to 5 thousand clocks,
 // new rows 9 to 7), masks before the waits; with weights of its own for the division the
-// sixteen trees take 0.85 ms (68%), 64 trees of 61 nodes 128 us, 8 of 513 with D = 64 70 us.
+// sixteen trees take 0.85 ms (68%), 64 trees of 61 nodes 127 us, 8 of 513 with D = 64 70 us.
+// Prompts, whose new rows every block converts again: eight of up to 4000 rows, 32 heads on 8,
+// 1.83 ms (21%), 3.56 with the rotation on the way.
 // What did not help: new rows' loads or the next half's scores ahead (registers), waits that
 // look without sleeping (882 to 896 us), a short rolled loop for tiles with masks (961), one
 // loop for tiles with and without masks (921), scores of a whole tile at a time (1077).
@@ -72,8 +74,10 @@ constexpr int NC = 128;         // converter threads for the keys, and as many f
 // walks the CTA's share of the work and a warp looks up pages.
 constexpr int NT = NS + 2 * NC + 128;
 // Registers per thread of the warpgroups (softmax, converters, MMA): over the
-// CTA they sum to what it is launched with, LAUNCH_REGS each.  No loop of a role may
-// spill: the shared memory in use leaves the L1 less than the spills need.
+// CTA they sum to what it is launched with, LAUNCH_REGS each.  Spills in the roles' loops
+// cost more than elsewhere: the shared memory in use leaves little L1.  What is left of them, of
+// a call over 16384 tokens and per tile of 256 rows: e4m3 60 local loads and 42 stores of 9000 warp
+// instructions (D = 64: 123 and 106 of 8100), 4 bits 20 and 2 of 8400 (18 and 2 of 7100).
 constexpr int LAUNCH_REGS = 65536 / NT / 8 * 8;
 constexpr int REG_SOFT = 120, REG_CONV = 96, REG_MMA = 48;
 static_assert(NS * REG_SOFT + 2 * NC * REG_CONV + 128 * REG_MMA == NT * LAUNCH_REGS, "register split");
@@ -145,9 +149,10 @@ struct Lay {
     static constexpr size_t SMEM = 1024 + SH + sizeof(Shared);
 };
 
-// Bounded wait: 2^18 tries of 3.8 us (measured, whatever the hint says), a second; once
-// one has run out, `fail` is set and later ones give up at their first look.  Short code: it
-// stands in every role.
+// Bounded wait: 2^18 tries of 3.8 us, a second (measured; they take as long with a hint of how
+// long to sleep, and with one of 1000 ns 16 trees of 257 nodes take 1.12 ms over e4m3 instead of 1.10 and
+// 866 us over 4 bits instead of 851); once one has run out, `fail` is set and later ones give up at
+// their first look.  Short code: it stands in every role.
 DT_DI void wait(uint64_t* bar, uint32_t phase, int* fail) {
     asm volatile(
         "{\n .reg .pred p;\n .reg .u32 n, f;\n mov.u32 n, 262144;\n"
